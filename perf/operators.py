@@ -302,7 +302,7 @@ def _own(s):
     if "cache" not in s:  # the handle and the workspace that a program keeps
         s["cache"] = kvq.KVCache.wrap(s["k"], s["v"], s["ks"], s["vs"])
         if op == "step":
-            need = kvq.kvq_step_accum_workspace_bytes(s["batch"], s["new"], s["hq"], s["hkv"], s["max_ctx"], s["d"])
+            need = kvq.kvq_step_accum_workspace_bytes(s["batch"], s["new"], s["hq"], s["max_ctx"], s["d"])
         elif op == "weights":
             need = kvq.kvq_chunk_weights_workspace_bytes(s["tokens"], s["hq"], s["hkv"], s["history"], s["d"])
         else:
