@@ -310,6 +310,150 @@ int kvq_decode_step_int8kv(const kvq_cache* cache, const void* k_new, const void
                            float softmax_scale, float* out, void* workspace, size_t workspace_bytes,
                            const kvq_decode_opts* opts, void* stream);
 
+/*
+ * A cache that forgets.  A sequence may hold fewer tokens than it has seen: kvq_cache_evict keeps,
+ * per (sequence, KV head), the tokens that the queries have attended to most, and the next tokens are
+ * appended behind them.  A token's slot is then not its position, and each KV head holds its own
+ * choice of tokens (equally many).  Beside the cache the caller keeps, per (sequence, KV head, slot):
+ *     acc       fp32  [batch][n_kv_heads][acc_stride]   the attention weight given to the token so far
+ *     slot_pos  int32 [batch][n_kv_heads][acc_stride]   the token's position
+ * The calls: kvq_rope_bf16 rotates q and k by position; kvq_decode_step_accum_int8kv appends,
+ * attends and adds up the weights of a decode step; kvq_attn_chunk_weights_int8kv adds up those of a
+ * chunk of prompt queries; kvq_cache_evict brings the sequences down to a budget.
+ */
+
+/* Workspace (bytes) of kvq_decode_step_accum_int8kv: the split route's partials
+ * (kvq_verify_workspace_bytes with force_route 2) and 4 bytes per (sequence, query row, query head,
+ * key).  0 if an argument is not positive. */
+size_t kvq_step_accum_workspace_bytes(int32_t batch, int32_t n_new, int32_t n_q_heads, int32_t max_ctx,
+                                      int32_t head_dim, const kvq_decode_opts* opts);
+
+/*
+ * kvq_decode_step_accum_int8kv — kvq_decode_step_int8kv (with k_new = v_new = NULL:
+ * kvq_attn_verify_int8kv) that also adds to every key the attention weight it was given:
+ *   acc[b][kvh][t] += sum over the call's rows i and the query heads h of KV head kvh of p[b][i][h][t],
+ *   p the softmax weights of the rows' scores over the keys they see (they sum to 1 over t; a row
+ *   with no key gives nothing).
+ * The n_new tokens written by the call start from zero: their entries are set to the sum, and with
+ * slot_pos their positions are set to slot_pos[b][kvh][c - n_new + j] = pos[b] + j (c = ctx_lens[b]).
+ * Entries at or past c are left as they are.  The sums are taken in a fixed order: the same call
+ * gives the same bits.
+ *   acc       : device fp32 [batch][n_kv_heads][acc_stride], acc_stride >= max_ctx
+ *   slot_pos  : device int32 [batch][n_kv_heads][acc_stride], or NULL (only with k_new)
+ *   pos       : device int32 [batch], or NULL; given exactly when slot_pos is
+ *   workspace : device, >= kvq_step_accum_workspace_bytes(...), 16-byte aligned
+ *   max_ctx   : > 0
+ *   other arguments as kvq_decode_step_int8kv; opts->force_route 1 is KVQ_ERR_UNSUPPORTED (the call
+ *   always takes the split route, with one split for a short context)
+ * A key whose page is outside the pool is skipped (KVQ_DEV_BAD_BLOCK) and gets no weight; when a
+ * sequence's new tokens are not written (KVQ_DEV_BAD_POS) no entry is set.  A row whose scores are
+ * not finite gives its keys the weights of its formula, NaN among them.
+ */
+int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
+                                 int32_t batch, int32_t n_new, int32_t n_q_heads, const int32_t* block_table,
+                                 int32_t max_blocks_per_seq, const int32_t* ctx_lens, int32_t max_ctx,
+                                 float softmax_scale, float* out, float* acc, int64_t acc_stride, int32_t* slot_pos,
+                                 const int32_t* pos, void* workspace, size_t workspace_bytes,
+                                 const kvq_decode_opts* opts, void* stream);
+
+/* Workspace (bytes) of kvq_cache_evict: per (sequence, KV head) the moves of the largest possible
+ * eviction (min(keep, max_ctx - keep) sources and destinations) and their index by page.  0 if an
+ * argument is not positive. */
+size_t kvq_evict_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max_ctx, int32_t keep);
+
+/*
+ * kvq_cache_evict — eviction by accumulated attention weight.  A (sequence, KV head) with
+ * c = ctx_lens[b] > keep tokens is brought down to exactly `keep` of them:
+ *   protected  : the tokens at positions below n_sink, and the n_recent newest positions (positions
+ *                above max slot_pos - n_recent);
+ *   kept       : the protected ones first, then the largest acc, ties to the lowest slot.  NaN
+ *                counts as less than every number;
+ *   moved      : the kept tokens in slots at or past keep (ascending) go into the slots below keep
+ *                that are given up (ascending): K and V codes, both scales, acc and slot_pos.  Kept
+ *                tokens in slots below keep stay where they are.  Slots at or past keep, and their
+ *                entries, are left as they are: ctx_lens no longer counts them.
+ * A sequence with c <= keep loses nothing.  new_lens[b] = min(c, keep) is the next call's ctx_lens;
+ * the pages past the last one it needs can go back to the pool.  The cache is changed in place, so
+ * the pages of a sequence that evicts must be its own.
+ *   acc, slot_pos          : device, [batch][n_kv_heads][acc_stride], acc_stride >= max_ctx
+ *   acc_out, slot_pos_out  : device, [batch][n_kv_heads][out_stride], out_stride >= min(keep, max_ctx):
+ *                            acc and slot_pos themselves (in place, out_stride == acc_stride), or
+ *                            other arrays, which receive entries 0 .. new_lens[b] - 1
+ *   keep > 0, n_sink >= 0, n_recent >= 0, n_sink + n_recent <= keep
+ *   new_lens               : device int32 [batch], not ctx_lens itself
+ *   max_ctx                : host bound of ctx_lens; a longer ctx (or one past what the block-table row
+ *                            maps) is clamped to it and sets KVQ_DEV_BAD_POS
+ *   workspace              : device, >= kvq_evict_workspace_bytes(...), 16-byte aligned
+ * A move whose source or destination page is outside the pool leaves the destination's codes and
+ * scales as they are (KVQ_DEV_BAD_BLOCK).
+ */
+int kvq_cache_evict(const kvq_cache* cache, int32_t batch, const int32_t* block_table, int32_t max_blocks_per_seq,
+                    const int32_t* ctx_lens, int32_t max_ctx, int32_t keep, int32_t n_sink, int32_t n_recent,
+                    const float* acc, const int32_t* slot_pos, int64_t acc_stride, float* acc_out,
+                    int32_t* slot_pos_out, int64_t out_stride, int32_t* new_lens, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Pairs of the rotation: dims (j, j + rotary_dim / 2), or (2j, 2j + 1), of the rotated part. */
+#define KVQ_ROPE_HALF 0
+#define KVQ_ROPE_INTERLEAVED 1
+
+/* Scalings of the rotary frequencies inv[j] = base^(-2j / rotary_dim) for contexts longer than the
+ * original one (L = original_len, s = factor):
+ *   LINEAR   : inv / s
+ *   NTK      : base * s^(r / (r - 2)) in place of base (r = rotary_dim > 2)
+ *   YARN     : inv / s * m + inv * (1 - m), m = clamp((j - lo) / (hi - lo), 0, 1) with
+ *              lo = max(floor(d(high)), 0), hi = min(ceil(d(low)), r - 1),
+ *              d(n) = r ln(L / (2 pi n)) / (2 ln base): frequencies of more than `high` turns over
+ *              the original context stay, those of fewer than `low` are interpolated; the factor on
+ *              cos and sin is 0.1 ln s + 1 (1 for s <= 1)
+ *   BANDS    : inv / s * (1 - m) + inv * m, m = clamp((L inv / (2 pi) - low) / (high - low), 0, 1)
+ *   DIVISORS : inv / divisors[j] */
+#define KVQ_ROPE_NONE 0
+#define KVQ_ROPE_LINEAR 1
+#define KVQ_ROPE_NTK 2
+#define KVQ_ROPE_YARN 3
+#define KVQ_ROPE_BANDS 4
+#define KVQ_ROPE_DIVISORS 5
+typedef struct kvq_rope_scaling {
+  int32_t kind;
+  double factor;
+  double original_len;
+  double low, high;
+  const double* divisors; /* host [rotary_dim / 2], DIVISORS only */
+} kvq_rope_scaling;
+
+/*
+ * kvq_rope_phases — the plan of kvq_rope_bf16: each frequency in turns per position as a 64-bit
+ * fraction, phases[j] = round(frac(inv[j] / 2 pi) * 2^64), and the factor on cos and sin
+ * (attn_factor, may be NULL).  Host only; the caller copies phases to the device once.
+ *   scaling: NULL for none
+ */
+int kvq_rope_phases(int32_t rotary_dim, double base, const kvq_rope_scaling* scaling, uint64_t* phases,
+                    float* attn_factor);
+
+/*
+ * kvq_rope_bf16 — rotary positions on bf16 rows ([DCU] §2.2 apply_rope, outside the quantising
+ * producer): what the decode steps and kvq_attn_prefill_first_bf16 take as q and k_new.  For the
+ * pair (x, y) of frequency j of every head of token i, with turns = frac(pos[i] * phases[j] / 2^64):
+ *   x' = x c - y s, y' = y c + x s, c = attn_factor cos(2 pi turns), s = attn_factor sin(2 pi turns)
+ * in fp32, rounded once to bf16.  Dims outside [rotary_offset, rotary_offset + rotary_dim) are
+ * copied.  The turns are exact for every position, negative ones too: -pos undoes a rotation, and is
+ * the rotation's gradient.
+ *   q, k      : device bf16 rows of n_q_heads (n_kv_heads) heads of head_dim, a token's row q_stride
+ *               (k_stride) elements after the one before: a view of a packed projection is taken as
+ *               it is.  n_q_heads or n_kv_heads may be 0 (its pointers are not used)
+ *   q_out, k_out : likewise; the rows themselves (in place), or rows that do not overlap the inputs
+ *   head_dim  : 1 .. 1024; rotary_dim even, rotary_offset + rotary_dim <= head_dim
+ *   pos       : device int32 [n_tokens]
+ *   phases    : device [rotary_dim / 2]
+ * Rows whose start, stride, halves and offset are multiples of 16 bytes move in 16-byte words,
+ * others in narrower ones.
+ */
+int kvq_rope_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                  const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_kv_heads,
+                  int32_t head_dim, int32_t n_tokens, const int32_t* pos, const uint64_t* phases, int32_t rotary_dim,
+                  int32_t rotary_offset, int32_t layout, float attn_factor, void* stream);
+
 /* Workspace (bytes) of kvq_attn_prefill_int8 for a chunk of n_tokens queries after
  * history_len keys: the int8 Q codes and their fp32 scales, and the K/V codes of every
  * (KV head, 128-key tile) of the history_len + n_tokens keys widened once to fp16 in the

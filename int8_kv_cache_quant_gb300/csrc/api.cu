@@ -280,12 +280,10 @@ int decode_plan(const kvq_cache* cache, int32_t batch, int32_t nq, int32_t n_q_h
 
 extern "C" {
 
-// Decode with nq query rows per sequence (nq = 1: plain decode); with k_new / v_new, the fused
-// step that first writes each sequence's nq newest tokens into the cache.
-static int decode_rows(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q, int32_t batch,
-                       int32_t nq, int32_t n_q_heads, const int32_t* block_table, int32_t max_blocks_per_seq,
-                       const int32_t* ctx_lens, int32_t max_ctx, float softmax_scale, float* out, void* workspace,
-                       size_t workspace_bytes, const kvq_decode_opts* opts, void* stream) {
+// What every decode call checks before it plans: pointers, sizes, GQA groups, alignment.
+static int check_decode(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q, int32_t batch,
+                        int32_t nq, int32_t n_q_heads, const int32_t* block_table, int32_t max_blocks_per_seq,
+                        const int32_t* ctx_lens, int32_t max_ctx, const float* out) {
   int st = check_cache(cache);
   if (st != KVQ_OK) return st;
   if (!q || !block_table || !ctx_lens || !out) return KVQ_ERR_INVALID_ARG;
@@ -299,15 +297,15 @@ static int decode_rows(const kvq_cache* cache, const void* k_new, const void* v_
   if (G > 16 || static_cast<long long>(G) * nq > KVQ_VERIFY_MAX_ROWS) return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out)) return KVQ_ERR_MISALIGNED;
   if (!aligned4(block_table) || !aligned4(ctx_lens)) return KVQ_ERR_MISALIGNED;
-  const int mc = max_ctx > 0 ? max_ctx : 1;
-  const kvq_decode_opts o = decode_defaults(opts);
-  if (o.split_rows % KVQ_BLOCK_SIZE != 0 || o.force_route < 0 || o.force_route > 2) return KVQ_ERR_INVALID_ARG;
-  // the workspace rule is pure host arithmetic (kvq_decode_workspace_bytes), checked before the GPU is asked
-  if (decode_split_route(o, mc) && !workspace) return KVQ_ERR_WORKSPACE;
-  kvq::DecodePlan plan;
-  st = kvq::decode_plan(cache, batch, nq, n_q_heads, mc, opts, &plan);
-  if (st != KVQ_OK) return st;
-  const bool split = plan.split;
+  return KVQ_OK;
+}
+
+// The kernels' arguments, but for the workspace.
+static kvq::DecodeArgs decode_args(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
+                                   int32_t batch, int32_t nq, int32_t n_q_heads, const int32_t* block_table,
+                                   int32_t max_blocks_per_seq, const int32_t* ctx_lens, int32_t mc,
+                                   float softmax_scale, float* out, const kvq_decode_opts& o,
+                                   const kvq::DecodePlan& plan) {
   kvq::DecodeArgs a{};
   a.k = cache->k;
   a.v = cache->v;
@@ -329,28 +327,50 @@ static int decode_rows(const kvq_cache* cache, const void* k_new, const void* v_
   a.v_new = v_new;
   a.out = out;
   a.split_rows = plan.split_rows;
+  a.n_split = plan.n_split;
   a.status = status_ptr();
   a.ev_begin = static_cast<cudaEvent_t>(o.stage1_event_begin);
   a.ev_end = static_cast<cudaEvent_t>(o.stage1_event_end);
   a.wait_budget = kvq::debug_wait_budget();
   a.fault = kvq::debug_fault_mode();
-  if (split) {
-    const long long n_split = plan.n_split;
+  return a;
+}
+
+// The split route's partials in the workspace: accumulators, then statistics on a 256-byte boundary.
+static void place_partials(kvq::DecodeArgs* a, void* workspace) {
+  const long long units = static_cast<long long>(a->batch) * a->nq * a->n_q_heads * a->n_split;
+  const long long acc_bytes = ((units * a->head_dim * 4 + 255) / 256) * 256;
+  a->part_acc = static_cast<float*>(workspace);
+  a->part_stats = reinterpret_cast<float*>(static_cast<char*>(workspace) + acc_bytes);
+}
+
+// Decode with nq query rows per sequence (nq = 1: plain decode); with k_new / v_new, the fused
+// step that first writes each sequence's nq newest tokens into the cache.
+static int decode_rows(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q, int32_t batch,
+                       int32_t nq, int32_t n_q_heads, const int32_t* block_table, int32_t max_blocks_per_seq,
+                       const int32_t* ctx_lens, int32_t max_ctx, float softmax_scale, float* out, void* workspace,
+                       size_t workspace_bytes, const kvq_decode_opts* opts, void* stream) {
+  int st = check_decode(cache, k_new, v_new, q, batch, nq, n_q_heads, block_table, max_blocks_per_seq, ctx_lens,
+                        max_ctx, out);
+  if (st != KVQ_OK) return st;
+  const int mc = max_ctx > 0 ? max_ctx : 1;
+  const kvq_decode_opts o = decode_defaults(opts);
+  if (o.split_rows % KVQ_BLOCK_SIZE != 0 || o.force_route < 0 || o.force_route > 2) return KVQ_ERR_INVALID_ARG;
+  // the workspace rule is pure host arithmetic (kvq_decode_workspace_bytes), checked before the GPU is asked
+  if (decode_split_route(o, mc) && !workspace) return KVQ_ERR_WORKSPACE;
+  kvq::DecodePlan plan;
+  st = kvq::decode_plan(cache, batch, nq, n_q_heads, mc, opts, &plan);
+  if (st != KVQ_OK) return st;
+  if (plan.split) {
     if (!workspace || workspace_bytes < plan.bytes) return KVQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
-    a.n_split = static_cast<int>(n_split);
-    const long long units = static_cast<long long>(batch) * nq * n_q_heads * n_split;
-    const long long acc_bytes = ((units * cache->head_dim * 4 + 255) / 256) * 256;
-    a.part_acc = static_cast<float*>(workspace);
-    a.part_stats = reinterpret_cast<float*>(static_cast<char*>(workspace) + acc_bytes);
-    int launched = 0;
-    const int rc = cuda_status(kvq::launch_decode(a, kvq::DecodeRoute::kSplit, static_cast<cudaStream_t>(stream), &launched));
-    if (o.launches) *o.launches = launched;
-    return rc;
   }
-  a.n_split = 1;
+  kvq::DecodeArgs a = decode_args(cache, k_new, v_new, q, batch, nq, n_q_heads, block_table, max_blocks_per_seq,
+                                  ctx_lens, mc, softmax_scale, out, o, plan);
+  if (plan.split) place_partials(&a, workspace);
   int launched = 0;
-  const int rc = cuda_status(kvq::launch_decode(a, kvq::DecodeRoute::kSingle, static_cast<cudaStream_t>(stream), &launched));
+  const int rc = cuda_status(kvq::launch_decode(a, plan.split ? kvq::DecodeRoute::kSplit : kvq::DecodeRoute::kSingle,
+                                                static_cast<cudaStream_t>(stream), &launched));
   if (o.launches) *o.launches = launched;
   return rc;
 }
@@ -381,6 +401,230 @@ int kvq_decode_step_int8kv(const kvq_cache* cache, const void* k_new, const void
   if (!k_new || !v_new) return KVQ_ERR_INVALID_ARG;
   return decode_rows(cache, k_new, v_new, q, batch, n_new, n_q_heads, block_table, max_blocks_per_seq, ctx_lens,
                      max_ctx, softmax_scale, out, workspace, workspace_bytes, opts, stream);
+}
+
+// The split route always: the weights are made from the scores of a finished stage 1.
+static kvq_decode_opts accum_opts(const kvq_decode_opts* opts) {
+  kvq_decode_opts o = decode_defaults(opts);
+  o.force_route = 2;
+  return o;
+}
+
+static long long accum_scores_bytes(int32_t batch, int32_t nq, int32_t n_q_heads, int32_t max_ctx) {
+  const long long stride = (static_cast<long long>(max_ctx) + KVQ_BLOCK_SIZE - 1) / KVQ_BLOCK_SIZE * KVQ_BLOCK_SIZE;
+  return static_cast<long long>(batch) * nq * n_q_heads * stride * 4;
+}
+
+size_t kvq_step_accum_workspace_bytes(int32_t batch, int32_t n_new, int32_t n_q_heads, int32_t max_ctx,
+                                      int32_t head_dim, const kvq_decode_opts* opts) {
+  const kvq_decode_opts o = accum_opts(opts);
+  const size_t part = kvq_verify_workspace_bytes(batch, n_new, n_q_heads, max_ctx, head_dim, &o);
+  if (part == 0) return 0;
+  return (part + 255) / 256 * 256 + static_cast<size_t>(accum_scores_bytes(batch, n_new, n_q_heads, max_ctx));
+}
+
+int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
+                                 int32_t batch, int32_t n_new, int32_t n_q_heads, const int32_t* block_table,
+                                 int32_t max_blocks_per_seq, const int32_t* ctx_lens, int32_t max_ctx,
+                                 float softmax_scale, float* out, float* acc, int64_t acc_stride, int32_t* slot_pos,
+                                 const int32_t* pos, void* workspace, size_t workspace_bytes,
+                                 const kvq_decode_opts* opts, void* stream) {
+  int st = check_decode(cache, k_new, v_new, q, batch, n_new, n_q_heads, block_table, max_blocks_per_seq, ctx_lens,
+                        max_ctx, out);
+  if (st != KVQ_OK) return st;
+  if (!acc || max_ctx <= 0 || acc_stride < max_ctx) return KVQ_ERR_INVALID_ARG;
+  if ((slot_pos == nullptr) != (pos == nullptr) || (slot_pos && !k_new)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(acc) || !aligned4(slot_pos) || !aligned4(pos)) return KVQ_ERR_MISALIGNED;
+  if (opts && opts->force_route == 1) return KVQ_ERR_UNSUPPORTED;
+  const kvq_decode_opts o = accum_opts(opts);
+  if (o.split_rows % KVQ_BLOCK_SIZE != 0 || (opts && (opts->force_route < 0 || opts->force_route > 2)))
+    return KVQ_ERR_INVALID_ARG;
+  if (!workspace) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
+  kvq::DecodePlan plan;
+  st = kvq::decode_plan(cache, batch, n_new, n_q_heads, max_ctx, &o, &plan);
+  if (st != KVQ_OK) return st;
+  const size_t part = (plan.bytes + 255) / 256 * 256;
+  if (workspace_bytes < part + static_cast<size_t>(accum_scores_bytes(batch, n_new, n_q_heads, max_ctx)))
+    return KVQ_ERR_WORKSPACE;
+  kvq::StepAccumArgs a{};
+  a.d = decode_args(cache, k_new, v_new, q, batch, n_new, n_q_heads, block_table, max_blocks_per_seq, ctx_lens,
+                    max_ctx, softmax_scale, out, o, plan);
+  place_partials(&a.d, workspace);
+  a.d.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + part);
+  a.d.scores_stride = (static_cast<long long>(max_ctx) + KVQ_BLOCK_SIZE - 1) / KVQ_BLOCK_SIZE * KVQ_BLOCK_SIZE;
+  a.acc = acc;
+  a.acc_stride = acc_stride;
+  a.slot_pos = slot_pos;
+  a.pos = pos;
+  int launched = 0;
+  const int rc = cuda_status(kvq::launch_step_accum(a, static_cast<cudaStream_t>(stream), &launched));
+  if (o.launches) *o.launches = launched;
+  return rc;
+}
+
+size_t kvq_evict_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max_ctx, int32_t keep) {
+  if (batch <= 0 || n_kv_heads <= 0 || max_ctx <= 0 || keep <= 0) return 0;
+  return static_cast<size_t>(kvq::evict_workspace(batch, n_kv_heads, max_ctx, keep).bytes);
+}
+
+int kvq_cache_evict(const kvq_cache* cache, int32_t batch, const int32_t* block_table, int32_t max_blocks_per_seq,
+                    const int32_t* ctx_lens, int32_t max_ctx, int32_t keep, int32_t n_sink, int32_t n_recent,
+                    const float* acc, const int32_t* slot_pos, int64_t acc_stride, float* acc_out,
+                    int32_t* slot_pos_out, int64_t out_stride, int32_t* new_lens, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!block_table || !ctx_lens || !acc || !slot_pos || !acc_out || !slot_pos_out || !new_lens)
+    return KVQ_ERR_INVALID_ARG;
+  if (batch <= 0 || max_blocks_per_seq <= 0 || max_ctx <= 0 || keep <= 0) return KVQ_ERR_INVALID_ARG;
+  if (n_sink < 0 || n_recent < 0 || static_cast<long long>(n_sink) + n_recent > keep) return KVQ_ERR_INVALID_ARG;
+  if (acc_stride < max_ctx || out_stride < std::min(keep, max_ctx)) return KVQ_ERR_INVALID_ARG;
+  // in place: both arrays, with the same rows
+  if ((acc_out == acc) != (slot_pos_out == slot_pos) || (acc_out == acc && out_stride != acc_stride))
+    return KVQ_ERR_INVALID_ARG;
+  if (new_lens == ctx_lens) return KVQ_ERR_INVALID_ARG;
+  if (batch > 65535 || cache->n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;  // grid y and z
+  if (!aligned4(block_table) || !aligned4(ctx_lens) || !aligned4(acc) || !aligned4(slot_pos) || !aligned4(acc_out) ||
+      !aligned4(slot_pos_out) || !aligned4(new_lens))
+    return KVQ_ERR_MISALIGNED;
+  const kvq::EvictWorkspace w = kvq::evict_workspace(batch, cache->n_kv_heads, max_ctx, keep);
+  if (!workspace || workspace_bytes < static_cast<size_t>(w.bytes)) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  kvq::EvictArgs a{};
+  a.k = cache->k;
+  a.v = cache->v;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.num_blocks = cache->num_blocks;
+  a.n_kv_heads = cache->n_kv_heads;
+  a.head_dim = cache->head_dim;
+  a.batch = batch;
+  a.block_table = block_table;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.ctx_lens = ctx_lens;
+  a.max_ctx = max_ctx;
+  a.keep = keep;
+  a.n_sink = n_sink;
+  a.n_recent = n_recent;
+  a.acc = acc;
+  a.slot_pos = slot_pos;
+  a.acc_stride = acc_stride;
+  a.acc_out = acc_out;
+  a.slot_pos_out = slot_pos_out;
+  a.out_stride = out_stride;
+  a.new_lens = new_lens;
+  char* base = static_cast<char*>(workspace);
+  a.max_moves = w.max_moves;
+  a.n_pages = w.n_pages;
+  a.move_src = reinterpret_cast<int32_t*>(base);
+  a.move_dst = reinterpret_cast<int32_t*>(base + w.off_dst);
+  a.page_first = reinterpret_cast<int32_t*>(base + w.off_first);
+  a.n_moves = reinterpret_cast<int32_t*>(base + w.off_count);
+  a.status = status_ptr();
+  return cuda_status(kvq::launch_evict(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int kvq_rope_phases(int32_t rotary_dim, double base, const kvq_rope_scaling* scaling, uint64_t* phases,
+                    float* attn_factor) {
+  if (!phases || rotary_dim <= 0 || rotary_dim % 2 != 0) return KVQ_ERR_INVALID_ARG;
+  if (!(base > 0.0) || !std::isfinite(base)) return KVQ_ERR_INVALID_ARG;
+  kvq_rope_scaling z = {KVQ_ROPE_NONE, 1.0, 0.0, 0.0, 0.0, nullptr};
+  if (scaling) z = *scaling;
+  if (z.kind < KVQ_ROPE_NONE || z.kind > KVQ_ROPE_DIVISORS) return KVQ_ERR_UNSUPPORTED;
+  if (z.kind != KVQ_ROPE_NONE && z.kind != KVQ_ROPE_DIVISORS && (!(z.factor > 0.0) || !std::isfinite(z.factor)))
+    return KVQ_ERR_INVALID_ARG;
+  constexpr double kTwoPi = 6.283185307179586476925;
+  const double r = rotary_dim;
+  double low = 0.0, high = 0.0, factor_attn = 1.0;
+  if (z.kind == KVQ_ROPE_NTK) {
+    if (rotary_dim <= 2) return KVQ_ERR_INVALID_ARG;
+    base *= std::pow(z.factor, r / (r - 2.0));
+  } else if (z.kind == KVQ_ROPE_YARN) {
+    if (!(z.original_len > 0.0) || !(z.low > 0.0) || !(z.high > z.low) || !(base > 1.0)) return KVQ_ERR_INVALID_ARG;
+    auto dim_of = [&](double turns) { return r * std::log(z.original_len / (turns * kTwoPi)) / (2.0 * std::log(base)); };
+    low = std::max(std::floor(dim_of(z.high)), 0.0);
+    high = std::min(std::ceil(dim_of(z.low)), r - 1.0);
+    if (z.factor > 1.0) factor_attn = 0.1 * std::log(z.factor) + 1.0;
+  } else if (z.kind == KVQ_ROPE_BANDS) {
+    if (!(z.original_len > 0.0) || !(z.low > 0.0) || !(z.high > z.low)) return KVQ_ERR_INVALID_ARG;
+  } else if (z.kind == KVQ_ROPE_DIVISORS) {
+    if (!z.divisors) return KVQ_ERR_INVALID_ARG;
+  }
+  for (int32_t j = 0; j < rotary_dim / 2; ++j) {
+    double inv = std::pow(base, -2.0 * j / r);
+    if (z.kind == KVQ_ROPE_LINEAR) {
+      inv /= z.factor;
+    } else if (z.kind == KVQ_ROPE_YARN) {
+      const double ramp = std::min(1.0, std::max(0.0, (j - low) / std::max(high - low, 1e-3)));
+      inv = inv / z.factor * ramp + inv * (1.0 - ramp);
+    } else if (z.kind == KVQ_ROPE_BANDS) {
+      const double turns = z.original_len * inv / kTwoPi;  // over the original context
+      const double mix = std::min(1.0, std::max(0.0, (turns - z.low) / (z.high - z.low)));
+      inv = inv / z.factor * (1.0 - mix) + inv * mix;
+    } else if (z.kind == KVQ_ROPE_DIVISORS) {
+      if (!(z.divisors[j] > 0.0)) return KVQ_ERR_INVALID_ARG;
+      inv /= z.divisors[j];
+    }
+    double turns = inv / kTwoPi;
+    turns -= std::floor(turns);
+    const double scaled = std::nearbyint(std::ldexp(turns, 64));
+    phases[j] = scaled >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(scaled);
+  }
+  if (attn_factor) *attn_factor = static_cast<float>(factor_attn);
+  return KVQ_OK;
+}
+
+int kvq_rope_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                  const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_kv_heads,
+                  int32_t head_dim, int32_t n_tokens, const int32_t* pos, const uint64_t* phases, int32_t rotary_dim,
+                  int32_t rotary_offset, int32_t layout, float attn_factor, void* stream) {
+  if (n_tokens < 0 || n_q_heads < 0 || n_kv_heads < 0 || head_dim <= 0) return KVQ_ERR_INVALID_ARG;
+  if (layout != KVQ_ROPE_HALF && layout != KVQ_ROPE_INTERLEAVED) return KVQ_ERR_UNSUPPORTED;
+  if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_offset < 0 ||
+      static_cast<long long>(rotary_offset) + rotary_dim > head_dim)
+    return KVQ_ERR_INVALID_ARG;
+  if (head_dim > 1024 || static_cast<long long>(n_q_heads) + n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0 || n_q_heads + n_kv_heads == 0) return KVQ_OK;
+  if (!pos || !phases) return KVQ_ERR_INVALID_ARG;
+  if (n_q_heads && (!q || !q_out)) return KVQ_ERR_INVALID_ARG;
+  if (n_kv_heads && (!k || !k_out)) return KVQ_ERR_INVALID_ARG;
+  // rows of different tokens do not overlap (one token has no next row)
+  const long long qd = static_cast<long long>(n_q_heads) * head_dim, kd = static_cast<long long>(n_kv_heads) * head_dim;
+  if (n_tokens > 1 && ((n_q_heads && (q_stride < qd || q_out_stride < qd)) ||
+                       (n_kv_heads && (k_stride < kd || k_out_stride < kd))))
+    return KVQ_ERR_INVALID_ARG;
+  // in place means the same rows
+  if (n_tokens > 1 && ((n_q_heads && q == q_out && q_stride != q_out_stride) ||
+                       (n_kv_heads && k == k_out && k_stride != k_out_stride)))
+    return KVQ_ERR_INVALID_ARG;
+  auto odd = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) != 0; };
+  if (odd(q) || odd(q_out) || odd(k) || odd(k_out) || !aligned4(pos) || reinterpret_cast<uintptr_t>(phases) % 8 != 0)
+    return KVQ_ERR_MISALIGNED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  kvq::RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.q_stride = n_tokens > 1 ? q_stride : qd;
+  a.q_out_stride = n_tokens > 1 ? q_out_stride : qd;
+  a.k_stride = n_tokens > 1 ? k_stride : kd;
+  a.k_out_stride = n_tokens > 1 ? k_out_stride : kd;
+  a.n_q_heads = n_q_heads;
+  a.n_kv_heads = n_kv_heads;
+  a.head_dim = head_dim;
+  a.n_tokens = n_tokens;
+  a.pos = pos;
+  a.phases = reinterpret_cast<const unsigned long long*>(phases);
+  a.rotary_dim = rotary_dim;
+  a.rotary_offset = rotary_offset;
+  a.interleaved = layout == KVQ_ROPE_INTERLEAVED;
+  a.attn_factor = attn_factor;
+  return cuda_status(kvq::launch_rope(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kvq_prefill_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,

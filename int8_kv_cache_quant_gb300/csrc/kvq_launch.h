@@ -74,6 +74,10 @@ struct DecodeArgs {
   // 1 = CTA 0's first team does not issue the copy of its second page
   long long wait_budget;
   int fault;
+  // step with accumulated weights only: the scores of every (sequence, KV head, query row) in log2
+  // units, fp32 [B][Hkv][G * nq][scores_stride]
+  float* scores;
+  long long scores_stride;
 };
 enum class DecodeRoute { kSingle = 1, kSplit = 2 };
 // Test-only fault injection and wait budget of the kernels launched next (kvq_debug_fault_inject).
@@ -92,6 +96,69 @@ int decode_plan(const kvq_cache* cache, int32_t batch, int32_t nq, int32_t n_q_h
 cudaError_t launch_decode(const DecodeArgs& a, DecodeRoute route, cudaStream_t stream, int* launched);
 // the stage-1 kernel's K/V stream alone, split route geometry (kvq_debug_stream_floor)
 cudaError_t launch_stream_floor(const DecodeArgs& a, cudaStream_t stream);
+
+// The split route's stage 1 that also writes the scores, the merge, and the pass that adds each key's
+// weight (summed over the rows of its KV head) to acc.
+struct StepAccumArgs {
+  DecodeArgs d;
+  float* acc;          // fp32 [B][Hkv][acc_stride]
+  long long acc_stride;
+  int32_t* slot_pos;   // int32 [B][Hkv][acc_stride] or nullptr: positions of the new tokens go here
+  const int32_t* pos;  // int32 [B]: position of each sequence's first new token
+};
+cudaError_t launch_step_accum(const StepAccumArgs& a, cudaStream_t stream, int* launched);
+// stage 2 alone (the split route's merge)
+cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
+
+// Eviction by accumulated weight.
+struct EvictArgs {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks, n_kv_heads, head_dim;
+  int batch;
+  const int32_t* block_table;
+  int max_blocks_per_seq;
+  const int32_t* ctx_lens;
+  int max_ctx, keep, n_sink, n_recent;
+  const float* acc;          // [B][Hkv][acc_stride]
+  const int32_t* slot_pos;   // [B][Hkv][acc_stride]
+  long long acc_stride;
+  float* acc_out;            // [B][Hkv][out_stride]
+  int32_t* slot_pos_out;
+  long long out_stride;
+  int32_t* new_lens;         // [B]
+  // workspace: per (sequence, KV head) the moves (ascending), the first move into each page, the count
+  int max_moves, n_pages;
+  int32_t* move_src;         // [units][max_moves]
+  int32_t* move_dst;
+  int32_t* page_first;       // [units][n_pages]
+  int32_t* n_moves;          // [units]
+  unsigned int* status;
+};
+struct EvictWorkspace {
+  int max_moves, n_pages;
+  long long off_dst, off_first, off_count, bytes;
+};
+EvictWorkspace evict_workspace(int batch, int n_kv_heads, int max_ctx, int keep);
+cudaError_t launch_evict(const EvictArgs& a, int n_sms, cudaStream_t stream);
+
+// Rotation of bf16 rows by position.
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements from a token to the next
+  int n_q_heads, n_kv_heads, head_dim, n_tokens;
+  const int32_t* pos;
+  const unsigned long long* phases;  // [rotary_dim / 2]: turns per position * 2^64
+  int rotary_dim, rotary_offset, interleaved;
+  float attn_factor;
+  int columns, head_groups;  // set by launch_rope
+};
+cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t stream);
 
 struct SparseArgs {
   const int8_t* k;

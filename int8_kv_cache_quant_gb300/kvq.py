@@ -41,6 +41,14 @@ class _DecodeOpts(ctypes.Structure):
                 ("stage1_event_end", ctypes.c_void_p), ("launches", ctypes.POINTER(ctypes.c_int32))]
 
 
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("divisors", ctypes.POINTER(ctypes.c_double))]
+
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4, "divisors": 5}
+
 _lib = None
 
 
@@ -80,6 +88,17 @@ def lib():
                                              ctypes.POINTER(_DecodeOpts), vp]
         L.kvq_decode_step_int8kv.argtypes = [cp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, vp, sz,
                                              ctypes.POINTER(_DecodeOpts), vp]
+        i64 = ctypes.c_int64
+        L.kvq_step_accum_workspace_bytes.restype = sz
+        L.kvq_step_accum_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(_DecodeOpts)]
+        L.kvq_decode_step_accum_int8kv.argtypes = [cp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, vp, i64,
+                                                   vp, vp, vp, sz, ctypes.POINTER(_DecodeOpts), vp]
+        L.kvq_evict_workspace_bytes.restype = sz
+        L.kvq_evict_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.kvq_cache_evict.argtypes = [cp, i32, vp, i32, vp, i32, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp, vp, sz, vp]
+        L.kvq_rope_phases.argtypes = [i32, ctypes.c_double, ctypes.POINTER(_RopeScaling),
+                                      ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_float)]
+        L.kvq_rope_bf16.argtypes = [vp, vp, i64, i64, i32, vp, vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, i32, f32, vp]
         L.kvq_prefill_first_workspace_bytes.restype = sz
         L.kvq_prefill_first_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.kvq_attn_prefill_first_bf16.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, f32, vp, vp, sz, vp]
@@ -163,6 +182,22 @@ class KVCache:
         self.k_scale = torch.zeros((num_blocks, n_kv_heads, BLOCK_SIZE), dtype=torch.float32,
                                    device=device)
         self.v_scale = torch.zeros_like(self.k_scale)
+
+    @classmethod
+    def wrap(cls, k, v, k_scale, v_scale):
+        """A cache over tensors that exist already, in the layout above (nothing is copied)."""
+        nb, hkv, chunks = k.shape[:3]
+        want = (("k", k, torch.int8, (nb, hkv, chunks, BLOCK_SIZE, 16)),
+                ("v", v, torch.int8, (nb, hkv, chunks * 16, BLOCK_SIZE)),
+                ("k_scale", k_scale, torch.float32, (nb, hkv, BLOCK_SIZE)),
+                ("v_scale", v_scale, torch.float32, (nb, hkv, BLOCK_SIZE)))
+        for name, t, dtype, shape in want:
+            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError("KVCache.wrap: %s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
+        c = cls.__new__(cls)
+        c.num_blocks, c.n_kv_heads, c.head_dim = int(nb), int(hkv), int(chunks) * 16
+        c.k, c.v, c.k_scale, c.v_scale = k, v, k_scale, v_scale
+        return c
 
     def struct(self):
         # every cache tensor goes through _p: a cache left in host memory is refused before any
@@ -424,6 +459,186 @@ def kvq_attn_sparse_int8kv(cache, q, cell_offsets, cells, block_table_row, softm
         ctypes.byref(c), _p(q), N, Hq, _p(cell_offsets), _p(cells), _p(block_table_row),
         nb, float(softmax_scale), _p(out), _p(workspace), workspace.numel(), _stream(stream)))
     return out
+
+
+def _need(fn, name, t, dtype, shape):
+    """t is a contiguous tensor of this type and shape on the current CUDA device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s: %s must be a contiguous %s tensor of shape %s (got %s %s)"
+                         % (fn, name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    _here(fn, name, t)
+
+
+def _here(fn, name, t):
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError("%s: %s must be on the current CUDA device (got %s)" % (fn, name, t.device))
+
+
+def _ws(workspace, need, device):
+    """(workspace tensor, its bytes): the caller's, or one of `need` bytes on the device."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _row_stride(fn, name, t, dtype, B, H):
+    """Elements from one (sequence, KV head) row of a [B][H][slots] tensor to the next: rows contiguous
+    and evenly spaced (a view of wider rows will do)."""
+    if t.dtype != dtype or t.dim() != 3 or tuple(t.shape[:2]) != (B, H) or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError("%s: %s must be a %s tensor [%d][%d][slots] with contiguous rows" % (fn, name, dtype, B, H))
+    stride = t.stride(1) if H > 1 else t.stride(0) if B > 1 else t.shape[2]
+    if stride < t.shape[2] or (B > 1 and t.stride(0) != H * stride):
+        raise ValueError("%s: the rows of %s must be evenly spaced" % (fn, name))
+    _here(fn, name, t)
+    return int(stride)
+
+
+def kvq_step_accum_workspace_bytes(batch, n_new, n_q_heads, max_ctx, head_dim, split_rows=0):
+    o = _decode_opts(split_rows, 0, 0)
+    return int(lib().kvq_step_accum_workspace_bytes(batch, n_new, n_q_heads, max_ctx, head_dim, ctypes.byref(o)))
+
+
+def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, max_ctx, softmax_scale, acc,
+                                 slot_pos=None, pos=None, out=None, workspace=None, split_rows=0, stream=None,
+                                 stage1_events=None, launches=None):
+    """kvq_decode_step_int8kv (k_new = v_new = None: kvq_attn_verify_int8kv) that also adds to
+    acc (fp32 [B][Hkv][>= max_ctx]) the attention weight each key was given, summed over the rows and
+    over the query heads of its KV head; the new tokens' entries start from zero.  slot_pos (int32,
+    shaped like acc) receives the new tokens' positions pos[b] + j (pos: int32 [B]).  Returns out
+    fp32 shaped like q."""
+    fn = "kvq_decode_step_accum_int8kv"
+    squeeze = q.dim() == 3
+    if squeeze:
+        q = q[:, None]
+    B, nq, Hq, D = q.shape
+    if out is None:
+        out = _new_out((B, nq, Hq, D), q)
+        ret = out[:, 0] if squeeze else out
+    else:
+        ret = out
+    for name, t, dtype, n in (("q", q, torch.bfloat16, B * nq * Hq * D), ("out", out, torch.float32, B * nq * Hq * D),
+                              ("k_new", k_new, torch.bfloat16, B * nq * cache.n_kv_heads * D),
+                              ("v_new", v_new, torch.bfloat16, B * nq * cache.n_kv_heads * D)):
+        if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+            raise ValueError("%s: %s must be a contiguous %s tensor of %d elements" % (fn, name, dtype, n))
+    if D != cache.head_dim:
+        raise ValueError("%s: q has head_dim %d, the cache %d" % (fn, D, cache.head_dim))
+    _host_ok(fn, q, k_new, v_new, out)
+    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,))
+    _need(fn, "block_table", block_table, torch.int32, (B, block_table.shape[1]))
+    stride = _row_stride(fn, "acc", acc, torch.float32, B, cache.n_kv_heads)
+    if acc.shape[-1] < max_ctx:
+        raise ValueError("%s: acc has %d slots, max_ctx is %d" % (fn, acc.shape[-1], max_ctx))
+    if slot_pos is not None:
+        if (slot_pos.shape[-1] < max_ctx
+                or _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, cache.n_kv_heads) != stride):
+            raise ValueError("%s: slot_pos must be shaped and laid out like acc" % fn)
+        if pos is None:
+            raise ValueError("%s: slot_pos needs pos" % fn)
+        _need(fn, "pos", pos, torch.int32, (B,))
+    o = _decode_opts(split_rows, 0, 0, stage1_events, launches)
+    need = 0
+    if workspace is None:
+        need = int(lib().kvq_step_accum_workspace_bytes(B, nq, Hq, int(max_ctx), D, ctypes.byref(o)))
+    workspace, wbytes = _ws(workspace, need, cache.k.device)
+    c = cache.struct()
+    _check(fn, lib().kvq_decode_step_accum_int8kv(
+        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, _p(block_table), int(block_table.shape[1]),
+        _p(ctx_lens), int(max_ctx), float(softmax_scale), _hp(out), _p(acc), stride, _p(slot_pos),
+        _p(pos) if slot_pos is not None else None, _p(workspace), wbytes, ctypes.byref(o), _stream(stream)))
+    return ret
+
+
+def kvq_evict_workspace_bytes(batch, n_kv_heads, max_ctx, keep):
+    return int(lib().kvq_evict_workspace_bytes(batch, n_kv_heads, max_ctx, keep))
+
+
+def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, n_sink=0, n_recent=0, acc_out=None,
+                    slot_pos_out=None, new_lens=None, workspace=None, stream=None):
+    """Brings every (sequence, KV head) down to `keep` tokens: those at positions below n_sink, the
+    n_recent newest, then those of the largest acc (ties to the lowest slot); kept tokens past the
+    budget move into the slots given up below it.  acc fp32 / slot_pos int32 [B][Hkv][>= max_ctx];
+    acc_out / slot_pos_out: None for in place, or tensors [B][Hkv][>= min(keep, max_ctx)].  Returns
+    (acc_out, slot_pos_out, new_lens int32 [B])."""
+    fn = "kvq_cache_evict"
+    B, H = int(ctx_lens.shape[0]), cache.n_kv_heads
+    if (acc_out is None) != (slot_pos_out is None):
+        raise ValueError("%s: acc_out and slot_pos_out go together" % fn)
+    if acc_out is None:
+        acc_out, slot_pos_out = acc, slot_pos
+    if new_lens is None:
+        new_lens = torch.empty_like(ctx_lens)
+    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,))
+    _need(fn, "new_lens", new_lens, torch.int32, (B,))
+    _need(fn, "block_table", block_table, torch.int32, (B, block_table.shape[1]))
+    stride, ostride = (_row_stride(fn, n, t, torch.float32, B, H) for n, t in (("acc", acc), ("acc_out", acc_out)))
+    if (_row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H) != stride
+            or _row_stride(fn, "slot_pos_out", slot_pos_out, torch.int32, B, H) != ostride):
+        raise ValueError("%s: slot_pos must be laid out like acc, slot_pos_out like acc_out" % fn)
+    if min(acc.shape[-1], slot_pos.shape[-1]) < max_ctx or min(acc_out.shape[-1], slot_pos_out.shape[-1]) < min(keep, max_ctx):
+        raise ValueError("%s: acc and slot_pos need max_ctx slots, the outputs min(keep, max_ctx)" % fn)
+    need = kvq_evict_workspace_bytes(B, H, int(max_ctx), int(keep)) if workspace is None else 0
+    workspace, wbytes = _ws(workspace, need, cache.k.device)
+    c = cache.struct()
+    _check(fn, lib().kvq_cache_evict(
+        ctypes.byref(c), B, _p(block_table), int(block_table.shape[1]), _p(ctx_lens), int(max_ctx), int(keep),
+        int(n_sink), int(n_recent), _p(acc), _p(slot_pos), stride, _p(acc_out), _p(slot_pos_out), ostride,
+        _p(new_lens), _p(workspace), wbytes, _stream(stream)))
+    return acc_out, slot_pos_out, new_lens
+
+
+def kvq_rope_phases(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=32.0,
+                    divisors=None, device="cuda"):
+    """The plan of kvq_rope_bf16: (phases, attn_factor), phases int64 [rotary_dim / 2] (the bits of the
+    64-bit fractions of a turn per position).  scaling: "none", "linear", "ntk", "yarn", "bands" or
+    "divisors"."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError("kvq_rope_phases: unknown scaling %r" % (scaling,))
+    n = max(int(rotary_dim), 0) // 2
+    div = None
+    if divisors is not None:
+        if len(divisors) != n:
+            raise ValueError("kvq_rope_phases: %d divisors for %d frequencies" % (len(divisors), n))
+        div = (ctypes.c_double * n)(*[float(x) for x in divisors])
+    z = _RopeScaling(_ROPE_SCALINGS[scaling], float(factor), float(original_len), float(low), float(high),
+                     ctypes.cast(div, ctypes.POINTER(ctypes.c_double)) if div is not None else None)
+    host = torch.empty(n, dtype=torch.int64)
+    af = ctypes.c_float(1.0)
+    _check("kvq_rope_phases", lib().kvq_rope_phases(
+        int(rotary_dim), float(base), ctypes.byref(z), ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_uint64)),
+        ctypes.byref(af)))
+    return host.to(device), af.value
+
+
+def kvq_rope_bf16(q, k, pos, phases, layout=ROPE_HALF, rotary_offset=0, attn_factor=1.0, q_out=None, k_out=None,
+                  stream=None):
+    """Rotates q bf16 [T][Hq][D] and k bf16 [T][Hkv][D] (either may be None) by pos int32 [T]; rows may be
+    views of a packed projection (token stride free, heads and dims contiguous).  q_out / k_out:
+    None for new tensors, or tensors like the inputs, the inputs themselves among them.  Returns
+    (q_out, k_out)."""
+    fn = "kvq_rope_bf16"
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("%s: q and k are both None" % fn)
+    T, _, D = ref.shape
+    args = []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            args += [None, None, 0, 0, 0, None]
+            continue
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        for n, t in ((name, x), (name + "_out", y)):
+            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.shape[1] != x.shape[1] \
+                    or (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and t.shape[1] > 1):
+                raise ValueError("%s: %s must be bf16 [%d][heads][%d] with contiguous heads" % (fn, n, T, D))
+            _here(fn, n, t)
+        args += [_p(x), _p(y), x.stride(0), y.stride(0), x.shape[1], y]
+    _need(fn, "pos", pos, torch.int32, (T,))
+    _need(fn, "phases", phases, torch.int64, (phases.numel(),))
+    _check(fn, lib().kvq_rope_bf16(*args[:5], *args[6:11], D, T, _p(pos), _p(phases), 2 * phases.numel(),
+                                   int(rotary_offset), int(layout), float(attn_factor), _stream(stream)))
+    return args[5], args[11]
 
 
 def kvq_debug_prefill_q_codes(q, stream=None):
