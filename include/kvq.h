@@ -356,6 +356,40 @@ int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, cons
                                  const int32_t* pos, void* workspace, size_t workspace_bytes,
                                  const kvq_decode_opts* opts, void* stream);
 
+/* Workspace (bytes) of kvq_attn_chunk_weights_int8kv: per (KV head, query, head of its group) the row's
+ * maximum and sum and their parts, per (KV head, key) the parts of its weight (no score and no
+ * widened key is kept).  It does not depend on the GPU.  0 if an argument is not positive
+ * (history_len may be 0), n_q_heads is no multiple of n_kv_heads, head_dim is not 128 / 256, or the
+ * sizes are past 2^30 (below). */
+size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,
+                                         int32_t head_dim);
+
+/*
+ * kvq_attn_chunk_weights_int8kv — the attention weights of a chunk of n_tokens causal queries of one
+ * sequence (as in kvq_attn_prefill_int8: query i at slot history_len + i sees the keys of slots
+ * t <= history_len + i, its own among them), added up per key:
+ *   acc[kvh][t] += sum over the queries i and the query heads h of KV head kvh of p[i][h][t],
+ *   p[i][h][:] = softmax over the visible t of softmax_scale * q[i][h] . k^[t].
+ * Scores from the bf16 queries and the int8 codes exactly as in decode (q is not quantised); statistics
+ * and sums in fp32, in a fixed order: the same call gives the same bits.  For all of a prompt's
+ * queries call it chunk by chunk; for an observation window, with the prompt's last queries only.
+ *   q              : device bf16 [n_tokens][n_q_heads][head_dim]
+ *   block_table_row: device int32 [n_blocks_row], covering history_len + n_tokens keys
+ *   acc            : device fp32 [n_kv_heads][acc_stride], acc_stride >= history_len + n_tokens; entries at
+ *                    or past history_len + n_tokens are left as they are
+ *   softmax_scale  : finite and > 0
+ *   workspace      : device, >= kvq_chunk_weights_workspace_bytes(n_tokens, n_q_heads, n_kv_heads,
+ *                    history_len, head_dim), 16-byte aligned; its contents on entry do not matter
+ * A key on a page outside the pool is skipped (KVQ_DEV_BAD_BLOCK) and gets no weight.  If a bounded wait
+ * runs out (KVQ_DEV_TIMEOUT), the rows and keys it leaves unfinished add nothing.  A row whose scores are
+ * not finite gives the keys it sees the weights of its formula, NaN among them.
+ * KVQ_ERR_UNSUPPORTED when n_tokens * (n_q_heads / n_kv_heads) or history_len + n_tokens reaches 2^30.
+ */
+int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
+                                  int32_t history_len, const int32_t* block_table_row, int32_t n_blocks_row,
+                                  float softmax_scale, float* acc, int64_t acc_stride, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Workspace (bytes) of kvq_cache_evict: per (sequence, KV head) the moves of the largest possible
  * eviction (min(keep, max_ctx - keep) sources and destinations) and their index by page.  0 if an
  * argument is not positive. */
@@ -633,11 +667,12 @@ int kvq_debug_stream_floor(const kvq_cache* cache, int32_t batch, const int32_t*
  * cycles (<= 0: the default, about 2 s), and with mode 1 the first team of decode stage-1 CTA 0
  * does not issue the copy of its second page, with mode 2 the producer of prefill attention CTA 0
  * does not issue its fourth piece, with mode 3 the sparse CTA of (query 0, KV head 0) does not
- * issue the copies of its second chunk (mode 0: no injection).  No copy is left in flight:
+ * issue the copies of its second chunk, with mode 4 the first CTA of the chunk weights' row pass does not
+ * announce the first piece of its second tile (mode 0: no injection).  No copy is left in flight:
  * the consumer's wait runs out, the kernel sets KVQ_DEV_TIMEOUT, waits (bounded) for the copies it
  * did issue, drops that CTA's result (decode single route: zero output rows; split route: an empty
  * partial that the merge skips; prefill: the unit's output rows are not written; sparse: the
- * query's rows are zeros) and returns; the device stays usable.  Process-wide, host only; kvq_debug_fault_inject(0, 0) restores the defaults.
+ * query's rows are zeros; chunk weights: the rows concerned give no weight) and returns; the device stays usable.  Process-wide, host only; kvq_debug_fault_inject(0, 0) restores the defaults.
  * KVQ_ERR_INVALID_ARG for an unknown mode.
  */
 int kvq_debug_fault_inject(int32_t mode, int64_t wait_budget_cycles);

@@ -92,7 +92,7 @@ const char* kvq_status_string(int s) {
 }
 
 int kvq_debug_fault_inject(int32_t mode, int64_t wait_budget_cycles) {
-  if (mode < 0 || mode > 3) return KVQ_ERR_INVALID_ARG;
+  if (mode < 0 || mode > 4) return KVQ_ERR_INVALID_ARG;
   g_wait_budget.store(wait_budget_cycles > 0 ? static_cast<long long>(wait_budget_cycles) : kvq::kWaitBudgetCycles);
   g_fault_mode.store(mode);
   return KVQ_OK;
@@ -461,6 +461,80 @@ int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, cons
   const int rc = cuda_status(kvq::launch_step_accum(a, static_cast<cudaStream_t>(stream), &launched));
   if (o.launches) *o.launches = launched;
   return rc;
+}
+
+// Largest number of CTAs a pass of the chunk weights runs: more than any GPU the library is built for has
+// SMs, so that the workspace size does not depend on the GPU.
+constexpr int kChunkWeightsMaxRuns = 160;
+
+static bool chunk_weights_sizes_ok(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len) {
+  if (n_tokens <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || history_len < 0 || n_q_heads % n_kv_heads != 0) return false;
+  // rows of a KV head and keys are counted in 32 bits, with room for a tile more
+  const long long limit = 1LL << 30;
+  return static_cast<long long>(n_tokens) * (n_q_heads / n_kv_heads) < limit &&
+         static_cast<long long>(history_len) + n_tokens < limit;
+}
+
+size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,
+                                         int32_t head_dim) {
+  if (!chunk_weights_sizes_ok(n_tokens, n_q_heads, n_kv_heads, history_len) || (head_dim != 128 && head_dim != 256)) return 0;
+  return static_cast<size_t>(
+      kvq::chunk_weights_plan(n_tokens, n_q_heads, n_kv_heads, history_len, kChunkWeightsMaxRuns).bytes);
+}
+
+int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
+                                  int32_t history_len, const int32_t* block_table_row, int32_t n_blocks_row,
+                                  float softmax_scale, float* acc, int64_t acc_stride, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  int st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!q || !block_table_row || !acc) return KVQ_ERR_INVALID_ARG;
+  if (n_tokens <= 0 || n_q_heads <= 0 || history_len < 0 || n_blocks_row <= 0) return KVQ_ERR_INVALID_ARG;
+  if (n_q_heads % cache->n_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  const long long n_keys = static_cast<long long>(history_len) + n_tokens;
+  if (n_keys > static_cast<long long>(n_blocks_row) * KVQ_BLOCK_SIZE || acc_stride < n_keys) return KVQ_ERR_INVALID_ARG;
+  if (!chunk_weights_sizes_ok(n_tokens, n_q_heads, cache->n_kv_heads, history_len) || cache->n_kv_heads > 65535)
+    return KVQ_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned4(acc) || !aligned4(block_table_row)) return KVQ_ERR_MISALIGNED;
+  if (!workspace) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
+  const int sms = std::min(device_sm_count(), kChunkWeightsMaxRuns);
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  const kvq::ChunkWeightsPlan p = kvq::chunk_weights_plan(n_tokens, n_q_heads, cache->n_kv_heads, history_len, sms);
+  if (workspace_bytes < static_cast<size_t>(p.bytes)) return KVQ_ERR_WORKSPACE;
+  kvq::ChunkWeightsArgs a{};
+  a.k = cache->k;
+  a.k_scale = cache->k_scale;
+  a.num_blocks = cache->num_blocks;
+  a.n_kv_heads = cache->n_kv_heads;
+  a.head_dim = cache->head_dim;
+  a.q = q;
+  a.n_q_heads = n_q_heads;
+  a.group = n_q_heads / cache->n_kv_heads;
+  a.history_len = history_len;
+  a.n_rows = n_tokens * a.group;
+  a.n_keys = static_cast<int>(n_keys);
+  a.block_table_row = block_table_row;
+  a.c2 = softmax_scale * 1.44269504088896341f;
+  a.acc = acc;
+  a.acc_stride = acc_stride;
+  a.row_tiles = p.row_tiles;
+  a.key_tiles = p.key_tiles;
+  for (int i = 0; i < 2; ++i) {
+    a.line[i] = p.line[i];
+    a.runs[i] = p.runs[i];
+    a.n_seg[i] = p.n_seg[i];
+  }
+  char* base = static_cast<char*>(workspace);
+  a.row_part = reinterpret_cast<float2*>(base);
+  a.row_nm = reinterpret_cast<float*>(base + p.off_nm);
+  a.row_il = reinterpret_cast<float*>(base + p.off_il);
+  a.col_part = reinterpret_cast<float*>(base + p.off_col);
+  a.status = status_ptr();
+  a.wait_budget = kvq::debug_wait_budget();
+  a.fault = kvq::debug_fault_mode();
+  return cuda_status(kvq::launch_chunk_weights(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kvq_evict_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max_ctx, int32_t keep) {

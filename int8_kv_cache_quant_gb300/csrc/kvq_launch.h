@@ -110,6 +110,37 @@ cudaError_t launch_step_accum(const StepAccumArgs& a, cudaStream_t stream, int* 
 // stage 2 alone (the split route's merge)
 cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 
+// Attention weights of a chunk of queries, summed per key.
+struct ChunkWeightsPlan {
+  int row_tiles, key_tiles;   // 128 (query, head) rows of a KV head; 128 keys
+  long long line[2];          // (A tile, B tile) pairs of one KV head in the row / column pass
+  int runs[2], n_seg[2];      // CTAs, and the most parts one A tile is cut into
+  long long off_nm, off_il, off_col, bytes;
+};
+ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads, int history_len, int n_sms);
+struct ChunkWeightsArgs {
+  const int8_t* k;
+  const float* k_scale;
+  int num_blocks, n_kv_heads, head_dim;
+  const void* q;  // bf16 [T][Hq][D]
+  int n_q_heads, group, history_len, n_rows, n_keys;  // n_rows = T * group
+  const int32_t* block_table_row;
+  float c2;       // softmax_scale * log2(e)
+  float* acc;     // fp32 [Hkv][acc_stride]
+  long long acc_stride;
+  int row_tiles, key_tiles;
+  long long line[2];
+  int runs[2], n_seg[2];
+  float2* row_part;  // workspace [Hkv * row_tiles][n_seg[0]][2][128]: (max, sum) parts, sum < 0: dropped
+  float* row_nm;     // workspace [Hkv * row_tiles][128]: minus the row's maximum
+  float* row_il;     // workspace: 1 / the row's sum, 0 for a row that gives nothing
+  float* col_part;   // workspace [Hkv * key_tiles][n_seg[1]][2][128]
+  unsigned int* status;
+  long long wait_budget;
+  int fault;
+};
+cudaError_t launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream);
+
 // Eviction by accumulated weight.
 struct EvictArgs {
   int8_t* k;

@@ -37,6 +37,7 @@
 #include "kvq_launch.h"
 #include "quant_rule.cuh"
 #include "tcgen05.cuh"
+#include "tile_dev.cuh"
 
 namespace kvq {
 
@@ -68,51 +69,6 @@ namespace {
 constexpr float kLog2eP = 1.44269504088896341f;
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 
-// Packed fp32 pairs (add / mul / fma .rn.f32x2): each lane is rounded exactly like the scalar
-// operation, so these give the same bits as __fadd_rn / __fmul_rn / __fmaf_rn per element with
-// half the instructions.
-struct f2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ f2 mk2(float x, float y) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-// one half of a pair: the unpacking mov names both halves and the other one is dropped
-#pragma nv_diag_suppress 550
-__device__ __forceinline__ float lo2(f2 a) {
-  float x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-  return x;
-}
-__device__ __forceinline__ float hi2(f2 a) {
-  float x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-  return y;
-}
-#pragma nv_diag_default 550
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 sub2(f2 a, f2 b) {
-  f2 r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
 // The specified exp2 of the P-code decisions (the same function, step for step, as the CPU
 // reference): the argument clamped to [-125, 125] (fmaxf / fminf: NaN becomes -125), Cody-Waite
 // reduction x = n + f with n = rint(x), 2^f by the degree-4 polynomial with constant term 1 whose
@@ -139,30 +95,6 @@ __device__ __forceinline__ f2 exp2_det2(f2 xin) {
   return mk2(__uint_as_float(r0), __uint_as_float(r1));
 }
 
-// 16 int8 codes (one int4) -> two 16-byte chunks of 8 fp16 (exact integer values).
-__device__ __forceinline__ void widen16(const int4 raw, uint4& c0, uint4& c1) {
-  uint32_t lo, hi;
-  i8x4_to_h2x2(static_cast<uint32_t>(raw.x), kSelB01, kSelB23, lo, hi);
-  c0.x = lo;
-  c0.y = hi;
-  i8x4_to_h2x2(static_cast<uint32_t>(raw.y), kSelB01, kSelB23, lo, hi);
-  c0.z = lo;
-  c0.w = hi;
-  i8x4_to_h2x2(static_cast<uint32_t>(raw.z), kSelB01, kSelB23, lo, hi);
-  c1.x = lo;
-  c1.y = hi;
-  i8x4_to_h2x2(static_cast<uint32_t>(raw.w), kSelB01, kSelB23, lo, hi);
-  c1.z = lo;
-  c1.w = hi;
-}
-
-__device__ __forceinline__ void sts128(uint8_t* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
-
-__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
-  const uint32_t s = smem_u32(p);
-  return p + (((s + 1023u) & ~1023u) - s);
-}
-
 }  // namespace
 
 // ============================================================================ K/V widening pre-pass
@@ -176,8 +108,6 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 //           dims 128dh .. 128dh+127 (rows = dims);
 // plus the tile's key and value scales (fp32 [128] each).  Keys at or past the context, and keys
 // on pages outside the pool, get zero codes and zero scales.
-constexpr int kPieceBytes = 16384;
-
 template <int D>
 __global__ void __launch_bounds__(256) kv_widen_kernel(PrefillArgs a) {
   grid_dep_wait();  // the chunk's own K/V were written by the previous kernels of the stream
@@ -270,14 +200,6 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(PrefillArgs a) {
 // of Q, K or V becomes x * 2^(14 - e) with e the exponent of max |x| (so max |x| * 2^(14 - e) lies
 // in [2^14, 2^15)), exact for every bf16 value within 2^29 of the row's maximum, and its scale
 // is 2^(e - 14).  The int8 codes and the fp16 operands are made by one pass over the chunk.
-
-// 2^(e - 14) and its inverse for a row maximum amax (1 for amax = 0), exponents clamped.
-__device__ __forceinline__ void pow2_scales(float amax, float& to_f16, float& back) {
-  int e = amax > 0.f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 127 : 14;
-  e = max(-100, min(e, 100));
-  to_f16 = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-  back = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23);
-}
 
 // P fp32 values (this lane's elements of a row) to fp16 after scaling, packed in pairs.
 template <int P>
@@ -509,30 +431,6 @@ constexpr int kSoftmaxThreads = 512;
 constexpr int kMmaWarp = kSoftmaxThreads / 32;
 constexpr int kPrefillThreads = kSoftmaxThreads + 64;
 
-// Bounded wait that also gives up as soon as another thread of the CTA has given up.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, unsigned int* status,
-                                              volatile int* abort_flag, long long budget) {
-  if (mbar_try_wait(bar, parity)) return true;
-  long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort_flag) return false;
-    if (clock64() - t0 > budget) {
-      set_status(status, KVQ_DEV_TIMEOUT);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r));
-  return r != 0;
-}
-
 __device__ __forceinline__ void named_bar(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
@@ -567,12 +465,6 @@ __device__ __forceinline__ void wait_flag(const unsigned int* flag, unsigned int
     }
     __nanosleep(64);
   }
-}
-
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 
 __device__ __forceinline__ float max4_col(const float* p, int row) {

@@ -93,6 +93,9 @@ def lib():
         L.kvq_step_accum_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(_DecodeOpts)]
         L.kvq_decode_step_accum_int8kv.argtypes = [cp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, vp, i64,
                                                    vp, vp, vp, sz, ctypes.POINTER(_DecodeOpts), vp]
+        L.kvq_chunk_weights_workspace_bytes.restype = sz
+        L.kvq_chunk_weights_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.kvq_attn_chunk_weights_int8kv.argtypes = [cp, vp, i32, i32, i32, vp, i32, f32, vp, i64, vp, sz, vp]
         L.kvq_evict_workspace_bytes.restype = sz
         L.kvq_evict_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.kvq_cache_evict.argtypes = [cp, i32, vp, i32, vp, i32, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp, vp, sz, vp]
@@ -547,6 +550,33 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
         _p(ctx_lens), int(max_ctx), float(softmax_scale), _hp(out), _p(acc), stride, _p(slot_pos),
         _p(pos) if slot_pos is not None else None, _p(workspace), wbytes, ctypes.byref(o), _stream(stream)))
     return ret
+
+
+def kvq_chunk_weights_workspace_bytes(n_tokens, n_q_heads, n_kv_heads, history_len, head_dim):
+    return int(lib().kvq_chunk_weights_workspace_bytes(n_tokens, n_q_heads, n_kv_heads, history_len, head_dim))
+
+
+def kvq_attn_chunk_weights_int8kv(cache, q, history_len, block_table_row, softmax_scale, acc, workspace=None,
+                                  stream=None):
+    """Adds to acc (fp32 [Hkv][>= history_len + T]) the attention weights that the causal queries q (bf16
+    [T][Hq][D], at slots history_len ..) give to every key of the sequence, summed over the queries and
+    over the query heads of each KV head.  block_table_row int32 [n].  Returns acc."""
+    fn = "kvq_attn_chunk_weights_int8kv"
+    T, Hq, D = q.shape
+    _need(fn, "q", q, torch.bfloat16, (T, Hq, cache.head_dim))
+    _need(fn, "block_table_row", block_table_row, torch.int32, (block_table_row.numel(),))
+    if acc.dim() != 2 or acc.shape[1] < history_len + T:
+        raise ValueError("%s: acc must be [%d][>= %d]" % (fn, cache.n_kv_heads, history_len + T))
+    stride = _row_stride(fn, "acc", acc[None], torch.float32, 1, cache.n_kv_heads)
+    need = 0
+    if workspace is None:
+        need = kvq_chunk_weights_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), D)
+    workspace, wbytes = _ws(workspace, need, q.device)
+    c = cache.struct()
+    _check(fn, lib().kvq_attn_chunk_weights_int8kv(
+        ctypes.byref(c), _p(q), T, Hq, int(history_len), _p(block_table_row), int(block_table_row.numel()),
+        float(softmax_scale), _p(acc), stride, _p(workspace), wbytes, _stream(stream)))
+    return acc
 
 
 def kvq_evict_workspace_bytes(batch, n_kv_heads, max_ctx, keep):

@@ -57,6 +57,33 @@ def test_step_workspace(L):
     assert step(L, wb=need - 1, **kw) == WORKSPACE
 
 
+def weights(L, c=None, q=A, n=10, hq=24, hist=20, bt=A, nb=8, scale=0.1, acc=A, stride=64, ws=A, wb=1 << 30):
+    return L.kvq_attn_chunk_weights_int8kv(ctypes.byref(c or cache()), q, n, hq, hist, bt, nb, scale, acc, stride, ws, wb, None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(q=None)), (INVALID, dict(bt=None)), (INVALID, dict(acc=None)), (INVALID, dict(n=0)), (INVALID, dict(hq=0)),
+    (INVALID, dict(hq=26)), (INVALID, dict(hist=-1)), (INVALID, dict(nb=0)), (INVALID, dict(nb=1)), (INVALID, dict(stride=29)),
+    (INVALID, dict(scale=0.0)), (INVALID, dict(scale=-0.1)), (INVALID, dict(scale=float("nan"))), (INVALID, dict(scale=float("inf"))),
+    (UNSUPPORTED, dict(n=1 << 28, hist=0, nb=1 << 24, stride=1 << 28)), (UNSUPPORTED, dict(hist=(1 << 30) - 10, nb=1 << 27, stride=1 << 31)),
+    (UNSUPPORTED, dict(c=cache(hkv=65536), hq=65536)), (UNSUPPORTED, dict(c=cache(d=64))), (MISALIGNED, dict(q=A + 8)),
+    (MISALIGNED, dict(acc=A + 1)), (MISALIGNED, dict(ws=A + 8)), (WORKSPACE, dict(ws=None))])
+def test_chunk_weights_refusals(L, status, kw):
+    assert weights(L, **kw) == status
+
+
+def test_chunk_weights_workspace():
+    # 10 queries x 6 heads: one row tile and one key tile per KV head, one part each (two halves)
+    r = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, 20, 256) == r(4 * 128 * 2 * 2 * 8) + 2 * r(4 * 128 * 4) + 4 * 128 * 2 * 2 * 4
+    assert k.kvq_chunk_weights_workspace_bytes(0, 24, 4, 20, 256) == 0
+    assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, -1, 256) == 0
+    assert k.kvq_chunk_weights_workspace_bytes(10, 23, 4, 20, 256) == 0
+    assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, 20, 192) == 0
+    # no scores: far below 4 bytes per (query, head, key)
+    assert k.kvq_chunk_weights_workspace_bytes(2048, 24, 4, 30720, 256) < 16 << 20
+
+
 def evict(L, c=None, batch=2, bt=A, mb=8, ctx=A, max_ctx=100, keep=64, sink=0, recent=0, acc=A, sp=A + 1024, stride=128,
           ao=A + 2048, po=A + 4096, ostride=64, nl=A + 16, ws=A, wb=1 << 30):
     return L.kvq_cache_evict(ctypes.byref(c or cache()), batch, bt, mb, ctx, max_ctx, keep, sink, recent, acc, sp, stride,
