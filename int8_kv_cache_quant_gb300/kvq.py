@@ -120,9 +120,16 @@ def lib():
     return _lib
 
 
+# A call's host time is a few microseconds of the kernel's at decode sizes, so the marshalling below
+# stays on attribute reads that cost under 0.1 us each (a torch.cuda.Stream object alone is 3 us).
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """cudaStream_t of the stream, or of the current device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(_current_device())
 
 
 def _p(t):
@@ -130,9 +137,9 @@ def _p(t):
     handed a host pointer would fault."""
     if t is None:
         return None
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("the library takes CUDA tensors here (got a %s tensor)" % t.device.type)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _hp(t):
@@ -140,10 +147,10 @@ def _hp(t):
     or page-locked host memory mapped into the device's address space."""
     if t is None:
         return None
-    if t.device.type != "cuda" and not kvq_device_accessible(t):
+    if not t.is_cuda and not kvq_device_accessible(t):
         raise ValueError("a host tensor must be page-locked memory mapped into the device's address space "
                          "(e.g. tensor.pin_memory())")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _check(fn, status):
@@ -161,7 +168,7 @@ def _host_ok(fn, *tensors):
     """Host tensors passed to a decode call must be mapped page-locked memory (zero-copy): the
     kernels read and write them across the host link.  Anything else is refused before launch."""
     for t in tensors:
-        if t is not None and t.device.type == "cpu" and not kvq_device_accessible(t):
+        if t is not None and not t.is_cuda and not kvq_device_accessible(t):
             raise ValueError(fn + ": a host tensor must be page-locked memory mapped into the device's "
                              "address space (e.g. tensor.pin_memory())")
 
@@ -205,8 +212,8 @@ class KVCache:
     def struct(self):
         # every cache tensor goes through _p: a cache left in host memory is refused before any
         # launch (a kernel handed its pageable pointers would fault)
-        ptrs = [_p(t).value for t in (self.k, self.v, self.k_scale, self.v_scale)]
-        return _Cache(*ptrs, self.num_blocks, BLOCK_SIZE, self.n_kv_heads, self.head_dim)
+        return _Cache(_p(self.k), _p(self.v), _p(self.k_scale), _p(self.v_scale), self.num_blocks, BLOCK_SIZE,
+                      self.n_kv_heads, self.head_dim)
 
 
 def kvq_version():
@@ -464,17 +471,24 @@ def kvq_attn_sparse_int8kv(cache, q, cell_offsets, cells, block_table_row, softm
     return out
 
 
-def _need(fn, name, t, dtype, shape):
-    """t is a contiguous tensor of this type and shape on the current CUDA device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _need(fn, name, t, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on the current CUDA device, number dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: %s must be a contiguous %s tensor of shape %s (got %s %s)"
                          % (fn, name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    _here(fn, name, t)
+    if t.get_device() != dev:
+        _elsewhere(fn, name, t)
 
 
-def _here(fn, name, t):
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError("%s: %s must be on the current CUDA device (got %s)" % (fn, name, t.device))
+def _elsewhere(fn, name, t):
+    raise ValueError("%s: %s must be on the current CUDA device (it is on %s)" % (fn, name, t.device))
+
+
+def _cache_struct(fn, cache, dev):
+    """The cache's C struct; its tensors are on the current device."""
+    if cache.k.get_device() != dev:
+        _elsewhere(fn, "the cache", cache.k)
+    return cache.struct()
 
 
 def _ws(workspace, need, device):
@@ -484,16 +498,19 @@ def _ws(workspace, need, device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _row_stride(fn, name, t, dtype, B, H):
-    """Elements from one (sequence, KV head) row of a [B][H][slots] tensor to the next: rows contiguous
-    and evenly spaced (a view of wider rows will do)."""
-    if t.dtype != dtype or t.dim() != 3 or tuple(t.shape[:2]) != (B, H) or (t.stride(2) != 1 and t.shape[2] > 1):
+def _row_stride(fn, name, t, dtype, B, H, dev):
+    """(elements from one (sequence, KV head) row of a [B][H][slots] tensor to the next, slots): rows
+    contiguous and evenly spaced (a view of wider rows will do)."""
+    shape, st = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) != 3 or shape[0] != B or shape[1] != H or (st[2] != 1 and shape[2] > 1):
         raise ValueError("%s: %s must be a %s tensor [%d][%d][slots] with contiguous rows" % (fn, name, dtype, B, H))
-    stride = t.stride(1) if H > 1 else t.stride(0) if B > 1 else t.shape[2]
-    if stride < t.shape[2] or (B > 1 and t.stride(0) != H * stride):
+    slots = shape[2]
+    stride = st[1] if H > 1 else st[0] if B > 1 else slots
+    if stride < slots or (B > 1 and st[0] != H * stride):
         raise ValueError("%s: the rows of %s must be evenly spaced" % (fn, name))
-    _here(fn, name, t)
-    return int(stride)
+    if t.get_device() != dev:
+        _elsewhere(fn, name, t)
+    return stride, slots
 
 
 def kvq_step_accum_workspace_bytes(batch, n_new, n_q_heads, max_ctx, head_dim, split_rows=0):
@@ -519,35 +536,38 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
         ret = out[:, 0] if squeeze else out
     else:
         ret = out
+    H, dev = cache.n_kv_heads, _current_device()
     for name, t, dtype, n in (("q", q, torch.bfloat16, B * nq * Hq * D), ("out", out, torch.float32, B * nq * Hq * D),
-                              ("k_new", k_new, torch.bfloat16, B * nq * cache.n_kv_heads * D),
-                              ("v_new", v_new, torch.bfloat16, B * nq * cache.n_kv_heads * D)):
-        if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
-            raise ValueError("%s: %s must be a contiguous %s tensor of %d elements" % (fn, name, dtype, n))
+                              ("k_new", k_new, torch.bfloat16, B * nq * H * D),
+                              ("v_new", v_new, torch.bfloat16, B * nq * H * D)):
+        if t is not None:
+            if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+                raise ValueError("%s: %s must be a contiguous %s tensor of %d elements" % (fn, name, dtype, n))
+            if t.get_device() != dev and t.is_cuda:  # host memory: zero-copy, checked by _hp
+                _elsewhere(fn, name, t)
     if D != cache.head_dim:
         raise ValueError("%s: q has head_dim %d, the cache %d" % (fn, D, cache.head_dim))
-    _host_ok(fn, q, k_new, v_new, out)
-    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,))
-    _need(fn, "block_table", block_table, torch.int32, (B, block_table.shape[1]))
-    stride = _row_stride(fn, "acc", acc, torch.float32, B, cache.n_kv_heads)
-    if acc.shape[-1] < max_ctx:
-        raise ValueError("%s: acc has %d slots, max_ctx is %d" % (fn, acc.shape[-1], max_ctx))
+    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
+    n_blocks = block_table.shape[-1]
+    _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
+    stride, slots = _row_stride(fn, "acc", acc, torch.float32, B, H, dev)
+    if slots < max_ctx:
+        raise ValueError("%s: acc has %d slots, max_ctx is %d" % (fn, slots, max_ctx))
     if slot_pos is not None:
-        if (slot_pos.shape[-1] < max_ctx
-                or _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, cache.n_kv_heads) != stride):
+        pstride, slots = _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H, dev)
+        if pstride != stride or slots < max_ctx:
             raise ValueError("%s: slot_pos must be shaped and laid out like acc" % fn)
         if pos is None:
             raise ValueError("%s: slot_pos needs pos" % fn)
-        _need(fn, "pos", pos, torch.int32, (B,))
+        _need(fn, "pos", pos, torch.int32, (B,), dev)
     o = _decode_opts(split_rows, 0, 0, stage1_events, launches)
     need = 0
     if workspace is None:
         need = int(lib().kvq_step_accum_workspace_bytes(B, nq, Hq, int(max_ctx), D, ctypes.byref(o)))
     workspace, wbytes = _ws(workspace, need, cache.k.device)
-    c = cache.struct()
+    c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_decode_step_accum_int8kv(
-        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, _p(block_table), int(block_table.shape[1]),
-        _p(ctx_lens), int(max_ctx), float(softmax_scale), _hp(out), _p(acc), stride, _p(slot_pos),
+        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, _p(block_table), n_blocks, _p(ctx_lens), int(max_ctx), float(softmax_scale), _hp(out), _p(acc), stride, _p(slot_pos),
         _p(pos) if slot_pos is not None else None, _p(workspace), wbytes, ctypes.byref(o), _stream(stream)))
     return ret
 
@@ -563,18 +583,19 @@ def kvq_attn_chunk_weights_int8kv(cache, q, history_len, block_table_row, softma
     over the query heads of each KV head.  block_table_row int32 [n].  Returns acc."""
     fn = "kvq_attn_chunk_weights_int8kv"
     T, Hq, D = q.shape
-    _need(fn, "q", q, torch.bfloat16, (T, Hq, cache.head_dim))
-    _need(fn, "block_table_row", block_table_row, torch.int32, (block_table_row.numel(),))
+    dev, n_blocks = _current_device(), block_table_row.numel()
+    _need(fn, "q", q, torch.bfloat16, (T, Hq, cache.head_dim), dev)
+    _need(fn, "block_table_row", block_table_row, torch.int32, (n_blocks,), dev)
     if acc.dim() != 2 or acc.shape[1] < history_len + T:
         raise ValueError("%s: acc must be [%d][>= %d]" % (fn, cache.n_kv_heads, history_len + T))
-    stride = _row_stride(fn, "acc", acc[None], torch.float32, 1, cache.n_kv_heads)
+    stride, _ = _row_stride(fn, "acc", acc[None], torch.float32, 1, cache.n_kv_heads, dev)
     need = 0
     if workspace is None:
         need = kvq_chunk_weights_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), D)
     workspace, wbytes = _ws(workspace, need, q.device)
-    c = cache.struct()
+    c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_attn_chunk_weights_int8kv(
-        ctypes.byref(c), _p(q), T, Hq, int(history_len), _p(block_table_row), int(block_table_row.numel()),
+        ctypes.byref(c), _p(q), T, Hq, int(history_len), _p(block_table_row), n_blocks,
         float(softmax_scale), _p(acc), stride, _p(workspace), wbytes, _stream(stream)))
     return acc
 
@@ -598,22 +619,25 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
         acc_out, slot_pos_out = acc, slot_pos
     if new_lens is None:
         new_lens = torch.empty_like(ctx_lens)
-    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,))
-    _need(fn, "new_lens", new_lens, torch.int32, (B,))
-    _need(fn, "block_table", block_table, torch.int32, (B, block_table.shape[1]))
-    stride, ostride = (_row_stride(fn, n, t, torch.float32, B, H) for n, t in (("acc", acc), ("acc_out", acc_out)))
-    if (_row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H) != stride
-            or _row_stride(fn, "slot_pos_out", slot_pos_out, torch.int32, B, H) != ostride):
+    dev, n_blocks = _current_device(), block_table.shape[-1]
+    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
+    _need(fn, "new_lens", new_lens, torch.int32, (B,), dev)
+    _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
+    stride, slots = _row_stride(fn, "acc", acc, torch.float32, B, H, dev)
+    pstride, pslots = _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H, dev)
+    ostride, oslots = _row_stride(fn, "acc_out", acc_out, torch.float32, B, H, dev)
+    qstride, qslots = _row_stride(fn, "slot_pos_out", slot_pos_out, torch.int32, B, H, dev)
+    if pstride != stride or qstride != ostride:
         raise ValueError("%s: slot_pos must be laid out like acc, slot_pos_out like acc_out" % fn)
-    if min(acc.shape[-1], slot_pos.shape[-1]) < max_ctx or min(acc_out.shape[-1], slot_pos_out.shape[-1]) < min(keep, max_ctx):
+    if min(slots, pslots) < max_ctx or min(oslots, qslots) < min(keep, max_ctx):
         raise ValueError("%s: acc and slot_pos need max_ctx slots, the outputs min(keep, max_ctx)" % fn)
     need = kvq_evict_workspace_bytes(B, H, int(max_ctx), int(keep)) if workspace is None else 0
     workspace, wbytes = _ws(workspace, need, cache.k.device)
-    c = cache.struct()
+    c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_cache_evict(
-        ctypes.byref(c), B, _p(block_table), int(block_table.shape[1]), _p(ctx_lens), int(max_ctx), int(keep),
-        int(n_sink), int(n_recent), _p(acc), _p(slot_pos), stride, _p(acc_out), _p(slot_pos_out), ostride,
-        _p(new_lens), _p(workspace), wbytes, _stream(stream)))
+        ctypes.byref(c), B, _p(block_table), n_blocks, _p(ctx_lens), int(max_ctx), int(keep), int(n_sink),
+        int(n_recent), _p(acc), _p(slot_pos), stride, _p(acc_out), _p(slot_pos_out), ostride, _p(new_lens),
+        _p(workspace), wbytes, _stream(stream)))
     return acc_out, slot_pos_out, new_lens
 
 
@@ -651,24 +675,43 @@ def kvq_rope_bf16(q, k, pos, phases, layout=ROPE_HALF, rotary_offset=0, attn_fac
     if ref is None:
         raise ValueError("%s: q and k are both None" % fn)
     T, _, D = ref.shape
-    args = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            args += [None, None, 0, 0, 0, None]
-            continue
-        if y is None:
-            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        for n, t in ((name, x), (name + "_out", y)):
-            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.shape[1] != x.shape[1] \
-                    or (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and t.shape[1] > 1):
-                raise ValueError("%s: %s must be bf16 [%d][heads][%d] with contiguous heads" % (fn, n, T, D))
-            _here(fn, n, t)
-        args += [_p(x), _p(y), x.stride(0), y.stride(0), x.shape[1], y]
-    _need(fn, "pos", pos, torch.int32, (T,))
-    _need(fn, "phases", phases, torch.int64, (phases.numel(),))
-    _check(fn, lib().kvq_rope_bf16(*args[:5], *args[6:11], D, T, _p(pos), _p(phases), 2 * phases.numel(),
-                                   int(rotary_offset), int(layout), float(attn_factor), _stream(stream)))
-    return args[5], args[11]
+    dev = _current_device()
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        hq, qs = _heads(fn, "q", q, T, D, dev)
+        ho, qos = _heads(fn, "q_out", q_out, T, D, dev)
+        if ho != hq:
+            raise ValueError("%s: q_out has %d heads, q %d" % (fn, ho, hq))
+    else:
+        q_out, hq, qs, qos = None, 0, 0, 0
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        hk, ks = _heads(fn, "k", k, T, D, dev)
+        ho, kos = _heads(fn, "k_out", k_out, T, D, dev)
+        if ho != hk:
+            raise ValueError("%s: k_out has %d heads, k %d" % (fn, ho, hk))
+    else:
+        k_out, hk, ks, kos = None, 0, 0, 0
+    n = phases.numel()
+    _need(fn, "pos", pos, torch.int32, (T,), dev)
+    _need(fn, "phases", phases, torch.int64, (n,), dev)
+    _check(fn, lib().kvq_rope_bf16(_p(q), _p(q_out), qs, qos, hq, _p(k), _p(k_out), ks, kos, hk, D, T, _p(pos),
+                                   _p(phases), 2 * n, int(rotary_offset), int(layout), float(attn_factor),
+                                   _stream(stream)))
+    return q_out, k_out
+
+
+def _heads(fn, name, t, T, D, dev):
+    """(heads, token stride) of bf16 rows [T][heads][D], heads and dims contiguous, tokens any stride apart."""
+    shape, st = t.shape, t.stride()
+    if (t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[0] != T or shape[2] != D
+            or (st[2] != 1 and D > 1) or (st[1] != D and shape[1] > 1)):
+        raise ValueError("%s: %s must be bf16 [%d][heads][%d] with contiguous heads" % (fn, name, T, D))
+    if t.get_device() != dev:
+        _elsewhere(fn, name, t)
+    return shape[1], st[0]
 
 
 def kvq_debug_prefill_q_codes(q, stream=None):
