@@ -594,8 +594,7 @@ int kvq_cache_evict(const kvq_cache* cache, int32_t batch, const int32_t* block_
   a.max_moves = w.max_moves;
   a.n_pages = w.n_pages;
   a.move_src = reinterpret_cast<int32_t*>(base);
-  a.move_dst = reinterpret_cast<int32_t*>(base + w.off_dst);
-  a.page_first = reinterpret_cast<int32_t*>(base + w.off_first);
+  a.slot_map = reinterpret_cast<int32_t*>(base + w.off_map);
   a.n_moves = reinterpret_cast<int32_t*>(base + w.off_count);
   a.status = status_ptr();
   return cuda_status(kvq::launch_evict(a, sms, static_cast<cudaStream_t>(stream)));

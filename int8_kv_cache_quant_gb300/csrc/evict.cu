@@ -12,13 +12,18 @@
 // Two kernels.
 // * evict_select_kernel: a cluster of CTAs per (sequence, KV head), each CTA a contiguous range of
 //   slots with its order keys in shared memory.  The keep-th largest key is found by a radix select
-//   (digits of 11, 11 and 10 bits: a histogram per CTA in shared memory, summed over the cluster
-//   through distributed shared memory); then each warp walks its own run of slots with ballots, which
-//   gives ties, holes and movers their ranks without a barrier a step.  The weight and position of
-//   every slot are read once.
+//   (four digits of 8 bits): a histogram per CTA in shared memory, lanes with the same digit adding
+//   once (equal weights are common, and every lane of a warp adding to one bin is 32 additions), the
+//   bins that are not zero pushed into every other CTA's total, and each warp finding the digit by
+//   itself, so that a digit costs one barrier.  Then each warp walks its own run of slots with ballots,
+//   which gives ties, holes and movers their ranks without a barrier a step.  The kernel also moves
+//   weights and positions, and leaves for every slot below the budget the physical slot that moves into
+//   it, if any.
 // * evict_move_kernel: a CTA per (page below the budget, KV head, sequence) fills that page's holes.
 //   The cache stores V as [dim][16 slots], so a token's V is one byte of every 16: a whole page's
 //   rows are rebuilt in registers and stored as 16-byte words.
+// When at most kFewMoves tokens can move (a serving batch that evicts one token a step), the select
+// kernel's warps move the codes too, and the second launch falls away.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -34,10 +39,15 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kDigits = 4;
 constexpr int kMaxCluster = 8;
 // Order keys a CTA keeps in shared memory (64 KB); slots of its range past them are read again.
 constexpr int kKeyCap = 16384;
+constexpr int kPosRegs = 8;  // positions a thread keeps in registers between their maximum and the keys
+constexpr int kFewMoves = 16;
+// What the move kernel finds for a slot below the budget: the physical slot (page * 16 + slot) that
+// moves into it, or one of these.
+constexpr int32_t kStays = -1, kBadMove = -2;
 
 // Order-preserving image of a weight: NaN lowest, then -inf .. +inf (-0 as +0); protected slots are
 // 0xFFFFFFFF, above +inf.
@@ -49,11 +59,11 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 struct SelShared {
-  uint32_t hist[2][kBins];
-  uint32_t warp_a[kSelWarps], warp_b[kSelWarps];  // per-warp counts
-  uint32_t cta_a, cta_b;                          // this CTA's totals, read by the cluster
-  int cta_max;
-  uint32_t pick_digit, pick_above;
+  uint32_t own[kDigits][256];    // this CTA's histograms
+  uint32_t total[kDigits][256];  // the cluster's
+  uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
+  uint32_t ties[kMaxCluster], holes[kMaxCluster], movers[kMaxCluster];  // by rank, pushed by each CTA
+  int newest;
 };
 
 // Exclusive prefix of the CTA's warp counts; returns the CTA's total.
@@ -69,8 +79,41 @@ __device__ __forceinline__ uint32_t warp_prefix(const uint32_t* counts, int warp
   return t;
 }
 
+// hist[digit] += 1 for every lane with `in`, one addition per distinct digit of the warp.
+__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit, bool in, int lane) {
+  const uint32_t peers = __match_any_sync(0xffffffffu, in ? digit : 256u);
+  if (in && lane == __ffs(peers) - 1) atomicAdd(hist + digit, __popc(peers));
+}
+
+// One token's codes and scales, slot s to slot t of the sequence (a warp).
+__device__ __forceinline__ void move_token(const EvictArgs& a, const int32_t* bt, int kvh, int s, int t, int lane) {
+  const int sp = bt[s / KVQ_BLOCK_SIZE], dp = bt[t / KVQ_BLOCK_SIZE];
+  if (sp < 0 || sp >= a.num_blocks || dp < 0 || dp >= a.num_blocks) {
+    if (lane == 0) set_status(a.status, KVQ_DEV_BAD_BLOCK);
+    return;
+  }
+  const int D = a.head_dim, so = s % KVQ_BLOCK_SIZE, to = t % KVQ_BLOCK_SIZE;
+  const long long sph = static_cast<long long>(sp) * a.n_kv_heads + kvh, dph = static_cast<long long>(dp) * a.n_kv_heads + kvh;
+  // every load before the first store: K 16 dims a lane, V bytes of dims lane, lane + 32, ..
+  uint4 kc = make_uint4(0, 0, 0, 0);
+  if (lane < D / 16) kc = *reinterpret_cast<const uint4*>(a.k + ((sph * (D / 16) + lane) * KVQ_BLOCK_SIZE + so) * 16);
+  int8_t vb[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < D / 32) vb[i] = a.v[(sph * D + lane + 32 * i) * KVQ_BLOCK_SIZE + so];
+  float sc = 0.f;
+  if (lane < 2) sc = (lane ? a.v_scale : a.k_scale)[sph * KVQ_BLOCK_SIZE + so];
+  if (lane < D / 16) *reinterpret_cast<uint4*>(a.k + ((dph * (D / 16) + lane) * KVQ_BLOCK_SIZE + to) * 16) = kc;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < D / 32) a.v[(dph * D + lane + 32 * i) * KVQ_BLOCK_SIZE + to] = vb[i];
+  if (lane < 2) (lane ? a.v_scale : a.k_scale)[dph * KVQ_BLOCK_SIZE + to] = sc;
+}
+
 }  // namespace
 
+// FEW: at most kFewMoves tokens can move; the codes are moved here.
+template <bool FEW>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), n_cta = static_cast<int>(cluster.num_blocks());
@@ -78,9 +121,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ SelShared sh;
   extern __shared__ uint32_t keys[];  // [min(range, kKeyCap)]
+  auto barrier = [&] {  // of the cluster
+    if (n_cta > 1) cluster.sync();
+    else __syncthreads();
+  };
+  auto peer = [&](auto* p, int r) { return cluster.map_shared_rank(p, r); };
   grid_dep_wait();
+  grid_dep_trigger();
   int ctx = a.ctx_lens[b];
-  const int cap = min(a.max_blocks_per_seq > 0x7FFFFFF ? 0x7FFFFFF0 : a.max_blocks_per_seq * KVQ_BLOCK_SIZE, a.max_ctx);
+  const int cap = static_cast<int>(min(static_cast<long long>(a.max_blocks_per_seq) * KVQ_BLOCK_SIZE, static_cast<long long>(a.max_ctx)));
   if (ctx > cap) {
     if (tid == 0 && rank == 0) set_status(a.status, KVQ_DEV_BAD_POS);
     ctx = cap;
@@ -92,10 +141,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   const int32_t* pos = a.slot_pos + unit * a.acc_stride;
   float* acc_out = a.acc_out + unit * a.out_stride;
   int32_t* pos_out = a.slot_pos_out + unit * a.out_stride;
+  const int32_t* bt = a.block_table + static_cast<long long>(b) * a.max_blocks_per_seq;
   const bool in_place = a.acc_out == a.acc;
   if (kvh == 0 && rank == 0 && tid == 0) a.new_lens[b] = new_len;
+  if (rank == 0 && tid == 0) a.n_moves[unit] = ctx > keep;  // read by the move kernel: anything to do
   if (ctx <= keep) {  // nothing goes (the same in every CTA of the cluster)
-    if (rank == 0 && tid == 0) a.n_moves[unit] = 0;
     if (!in_place)
       for (int t = rank * kSelThreads + tid; t < ctx; t += n_cta * kSelThreads) {
         acc_out[t] = acc[t];
@@ -109,93 +159,127 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   const int run = ((range + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int w0 = min(t1, t0 + warp * run), w1 = min(t1, w0 + run);
 
-  // ---- the newest position, then the order keys
+  // ---- positions and weights, the newest position
+  const bool in_regs = range <= kPosRegs * kSelThreads;  // the same in every CTA
+  int32_t p_reg[kPosRegs];
+  float w_reg[kPosRegs];
   int pmax = INT32_MIN;
-  for (int t = t0 + tid; t < t1; t += kSelThreads) pmax = max(pmax, pos[t]);
-  pmax = __reduce_max_sync(0xffffffffu, pmax);
-  if (tid == 0) sh.cta_max = INT32_MIN;
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0u;
-  __syncthreads();
-  if (lane == 0) atomicMax(&sh.cta_max, pmax);
-  cluster.sync();
-  for (int r = 0; r < n_cta; ++r) pmax = max(pmax, *cluster.map_shared_rank(&sh.cta_max, r));
-  const long long recent_from = static_cast<long long>(pmax) - a.n_recent;  // protected above it
-  auto make_key = [&](int t) {
-    const int p = pos[t];
-    return (p < a.n_sink || p > recent_from) ? 0xFFFFFFFFu : order_key(acc[t]);
-  };
-  for (int t = t0 + tid; t < t1; t += kSelThreads) {
-    const uint32_t k = make_key(t);
-    if (t - t0 < kKeyCap) keys[t - t0] = k;
-    atomicAdd(&sh.hist[0][k >> 21], 1u);
+  if (in_regs) {
+#pragma unroll
+    for (int i = 0; i < kPosRegs; ++i) {
+      const int t = t0 + tid + i * kSelThreads;
+      if (t < t1) {
+        p_reg[i] = pos[t];
+        w_reg[i] = acc[t];
+        pmax = max(pmax, p_reg[i]);
+      }
+    }
+  } else {
+#pragma unroll 8
+    for (int t = t0 + tid; t < t1; t += kSelThreads) pmax = max(pmax, pos[t]);
   }
-  auto key_of = [&](int t) { return t - t0 < kKeyCap ? keys[t - t0] : make_key(t); };
+  pmax = __reduce_max_sync(0xffffffffu, pmax);
+  if (tid == 0) sh.newest = INT32_MIN;
+  for (int i = tid; i < 2 * kDigits * 256; i += kSelThreads) (&sh.own[0][0])[i] = 0u;
+  barrier();
+  if (lane < n_cta) atomicMax(peer(&sh.newest, lane), pmax);
+  barrier();
+  const long long recent_from = static_cast<long long>(sh.newest) - a.n_recent;  // protected above it
+  auto key_from = [&](int p, float w) { return (p < a.n_sink || p > recent_from) ? 0xFFFFFFFFu : order_key(w); };
+  auto key_of = [&](int t) { return t - t0 < kKeyCap ? keys[t - t0] : key_from(pos[t], acc[t]); };
+
+  // ---- order keys, and the first digit's histogram
+  if (in_regs) {
+#pragma unroll
+    for (int i = 0; i < kPosRegs; ++i) {
+      const int t = t0 + tid + i * kSelThreads;
+      if (t - tid + warp * 32 >= t1) break;  // warp-uniform
+      const uint32_t k = t < t1 ? key_from(p_reg[i], w_reg[i]) : 0u;
+      if (t < t1) keys[t - t0] = k;
+      count_digit(sh.own[0], k >> 24, t < t1, lane);
+    }
+  } else {
+#pragma unroll 4
+    for (int t = t0 + tid; t - lane < t1; t += kSelThreads) {
+      const uint32_t k = t < t1 ? key_from(pos[t], acc[t]) : 0u;
+      if (t < t1 && t - t0 < kKeyCap) keys[t - t0] = k;
+      count_digit(sh.own[0], k >> 24, t < t1, lane);
+    }
+  }
 
   // ---- radix select: the prefix of the keep-th largest key, digit by digit
   uint32_t prefix = 0, need = static_cast<uint32_t>(keep);  // still wanted among keys that start with prefix
+  uint32_t equal = 0;                                       // keys that do
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    uint32_t* hist = sh.hist[pass & 1];
-    cluster.sync();  // every CTA's histogram of this digit is complete
-    // bins 4 tid .. 4 tid + 3, from the top: sums over the cluster, suffix sums over the CTA
-    uint32_t bin[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = kBins - 1 - (4 * tid + i);
-      uint32_t v = 0;
-      for (int r = 0; r < n_cta; ++r) v += cluster.map_shared_rank(hist, r)[d];
-      bin[i] = v;
-      sum += v;
+  for (int d = 0; d < kDigits; ++d) {
+    const uint32_t* hist = sh.own[d];
+    __syncthreads();
+    if (n_cta > 1) {
+      for (int i = tid; i < 256 * n_cta; i += kSelThreads) {
+        const uint32_t v = sh.own[d][i & 255];
+        if (v) atomicAdd(peer(&sh.total[d][i & 255], i >> 8), v);
+      }
+      cluster.sync();
+      hist = sh.total[d];
     }
-    uint32_t incl = sum;
+    // every warp: lane l has bins 255 - 8 l down to 248 - 8 l
+    uint32_t bin[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bin[i] = hist[255 - 8 * lane - i];
+      sum += bin[i];
+    }
+    uint32_t above = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
+      const uint32_t o = __shfl_up_sync(0xffffffffu, above, off);
+      if (lane >= off) above += o;
     }
-    if (lane == 31) sh.warp_a[warp] = incl;
-    __syncthreads();
-    uint32_t before;
-    warp_prefix(sh.warp_a, warp, before);
-    uint32_t above = before + incl - sum;  // keys in higher bins than this thread's first
+    const uint32_t here = __ballot_sync(0xffffffffu, above >= need);
+    above -= sum;  // keys in the bins above this lane's
+    const int l = __ffs(here) - 1;  // the lane whose bins hold the keep-th key
+    uint32_t digit = 0, left = need, count = 0;
+    bool found = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (above < need && need <= above + bin[i]) {
-        sh.pick_digit = kBins - 1 - (4 * tid + i);
-        sh.pick_above = above;
+    for (int i = 0; i < 8; ++i) {
+      if (!found && need <= above + bin[i]) {
+        found = true;
+        digit = 255 - 8 * lane - i;
+        left = need - above;
+        count = bin[i];
       }
       above += bin[i];
     }
-    __syncthreads();
-    const uint32_t digit = sh.pick_digit;
-    need -= sh.pick_above;
+    digit = __shfl_sync(0xffffffffu, digit, l);
+    need = __shfl_sync(0xffffffffu, left, l);
+    equal = __shfl_sync(0xffffffffu, count, l);
+    const int shift = 24 - 8 * d;
     prefix |= digit << shift;
-    if (pass == 2) break;
-    // the next digit's histogram, of the keys that share the prefix
-    uint32_t* next = sh.hist[(pass + 1) & 1];
-    if (pass == 1) {  // its buffer held the first digit, which every CTA read before the last cluster barrier
-      for (int i = tid; i < kBins; i += kSelThreads) next[i] = 0u;
-      __syncthreads();
-    }
-    for (int t = t0 + tid; t < t1; t += kSelThreads) {
-      const uint32_t k = key_of(t);
-      if ((k >> shift) == (prefix >> shift)) atomicAdd(&next[pass == 0 ? (k >> 10) & 2047u : k & 1023u], 1u);
+    if (d + 1 == kDigits) break;
+    for (int t = t0 + tid; t - lane < t1; t += kSelThreads) {
+      const uint32_t k = t < t1 ? key_of(t) : 0u;
+      count_digit(sh.own[d + 1], (k >> (shift - 8)) & 255u, t < t1 && (k >> shift) == (prefix >> shift), lane);
     }
   }
-  const uint32_t thr = prefix;  // kept: keys above thr, and the first `need` that equal it
+  const uint32_t thr = prefix;  // kept: keys above thr, and the first `need` of the `equal` that are thr
 
-  // ---- ranks of the ties, in slot order: over the warp's run, the CTA, the cluster
-  uint32_t ties = 0;
-  for (int t = w0 + lane; t - lane < w1; t += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, t < w1 && key_of(t) == thr));
-  if (lane == 0) sh.warp_b[warp] = ties;
-  __syncthreads();
-  uint32_t tie_before;
-  const uint32_t cta_ties = warp_prefix(sh.warp_b, warp, tie_before);
-  if (tid == 0) sh.cta_a = cta_ties;
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) tie_before += *cluster.map_shared_rank(&sh.cta_a, r);
+  // ---- ranks of the ties, in slot order: over the warp's run, the CTA, the cluster (when some of them go)
+  uint32_t tie_before = 0;
+  if (equal != need) {
+    uint32_t ties = 0;
+    for (int t = w0 + lane; t - lane < w1; t += 32)
+      ties += __popc(__ballot_sync(0xffffffffu, t < w1 && key_of(t) == thr));
+    if (lane == 0) sh.warp_a[warp] = ties;
+    __syncthreads();
+    const uint32_t cta_ties = warp_prefix(sh.warp_a, warp, tie_before);
+    if (n_cta > 1) {
+      if (tid < n_cta) *peer(&sh.ties[rank], tid) = cta_ties;
+      cluster.sync();
+      for (int r = 0; r < rank; ++r) tie_before += sh.ties[r];
+    } else {
+      __syncthreads();  // warp_a is free again
+    }
+  }
 
   // ---- kept or not, and the counts of holes (below keep) and movers (at or past it) of the run
   const uint32_t lt = (1u << lane) - 1u;
@@ -216,7 +300,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
     holes += __popc(__ballot_sync(0xffffffffu, live && !kept && t < keep));
     movers += __popc(__ballot_sync(0xffffffffu, kept && t >= keep));
   });
-  __syncthreads();  // warp_a, warp_b are free again
   if (lane == 0) {
     sh.warp_a[warp] = holes;
     sh.warp_b[warp] = movers;
@@ -224,100 +307,106 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   __syncthreads();
   uint32_t hole_at, mover_at;
   const uint32_t cta_holes = warp_prefix(sh.warp_a, warp, hole_at), cta_movers = warp_prefix(sh.warp_b, warp, mover_at);
-  cluster.sync();  // every CTA has read the tie counts
-  if (tid == 0) {
-    sh.cta_a = cta_holes;
-    sh.cta_b = cta_movers;
-  }
-  cluster.sync();
-  uint32_t total = 0;
-  for (int r = 0; r < n_cta; ++r) {
-    const uint32_t h = *cluster.map_shared_rank(&sh.cta_a, r);
-    if (r < rank) {
-      hole_at += h;
-      mover_at += *cluster.map_shared_rank(&sh.cta_b, r);
+  if (n_cta > 1) {
+    if (tid < n_cta) {
+      *peer(&sh.holes[rank], tid) = cta_holes;
+      *peer(&sh.movers[rank], tid) = cta_movers;
     }
-    total += h;
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      hole_at += sh.holes[r];
+      mover_at += sh.movers[r];
+    }
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
 
-  // ---- the lists, the first hole of every page, and what stays where it is
+  // ---- the movers, by rank; then each hole takes the mover of its rank
   int32_t* src = a.move_src + unit * a.max_moves;
-  int32_t* dst = a.move_dst + unit * a.max_moves;
-  int32_t* first = a.page_first + unit * a.n_pages;
-  if (rank == 0 && tid == 0) a.n_moves[unit] = static_cast<int32_t>(total);
+  int32_t* map = a.slot_map + unit * a.n_pages * KVQ_BLOCK_SIZE;
   walk([&](int t, bool live, bool kept) {
-    const bool hole = live && !kept && t < keep, mover = kept && t >= keep;
-    const uint32_t hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-    if (hole) dst[hole_at + __popc(hm & lt)] = t;
+    const bool mover = kept && t >= keep;
+    const uint32_t mm = __ballot_sync(0xffffffffu, mover);
     if (mover) src[mover_at + __popc(mm & lt)] = t;
-    if (live && t < keep && t % KVQ_BLOCK_SIZE == 0) first[t / KVQ_BLOCK_SIZE] = static_cast<int32_t>(hole_at + __popc(hm & lt));
-    if (kept && t < keep && !in_place) {
-      acc_out[t] = acc[t];
-      pos_out[t] = pos[t];
+    mover_at += __popc(mm);
+  });
+  barrier();  // no CTA touches another's shared memory after this one
+  walk([&](int t, bool live, bool kept) {
+    const bool hole = live && !kept && t < keep;
+    const uint32_t hm = __ballot_sync(0xffffffffu, hole);
+    if (hole) {
+      const int s = src[hole_at + __popc(hm & lt)];
+      const int page = bt[s / KVQ_BLOCK_SIZE];
+      if (!FEW) {
+        const bool ok = page >= 0 && page < a.num_blocks;  // page * 16 + 15 < 2^31: a pool is far smaller
+        if (!ok) set_status(a.status, KVQ_DEV_BAD_BLOCK);
+        map[t] = ok ? page * KVQ_BLOCK_SIZE + s % KVQ_BLOCK_SIZE : kBadMove;
+      }
+      acc_out[t] = acc[s];
+      pos_out[t] = pos[s];
+    } else if (kept && t < keep) {
+      if (!FEW) map[t] = kStays;
+      if (!in_place) {
+        acc_out[t] = acc[t];
+        pos_out[t] = pos[t];
+      }
+    }
+    if (FEW) {  // warp-wide, hole by hole: the codes
+      uint32_t left = hm, j = hole_at;
+      for (; left; left &= left - 1, ++j) move_token(a, bt, kvh, src[j], t - lane + __ffs(left) - 1, lane);
     }
     hole_at += __popc(hm);
-    mover_at += __popc(mm);
   });
 }
 
-// The moves into one page below the budget.  Holes of the page are entries page_first[p] .. up to the
-// next page's first; their movers are the same entries of move_src.
+// The moves into one page below the budget.
 template <int D>
 __global__ void __launch_bounds__(D) evict_move_kernel(EvictArgs a) {
   const int p = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  __shared__ long long src_ph[KVQ_BLOCK_SIZE];  // source page * n_kv_heads + kvh, -1: none
-  __shared__ int src_slot[KVQ_BLOCK_SIZE];      // by destination slot
-  grid_dep_wait();
+  __shared__ int32_t from[KVQ_BLOCK_SIZE];  // by destination slot: physical slot, or negative
+  __shared__ int any;
   const long long unit = static_cast<long long>(b) * a.n_kv_heads + kvh;
-  const int total = a.n_moves[unit];
-  if (total == 0) return;
-  const int32_t* first = a.page_first + unit * a.n_pages;
-  const int j0 = first[p], j1 = p + 1 < a.n_pages ? first[p + 1] : total;
-  if (j0 == j1) return;
-  const int32_t* bt = a.block_table + static_cast<long long>(b) * a.max_blocks_per_seq;
-  const int dpage = bt[p];
-  const bool dst_ok = dpage >= 0 && dpage < a.num_blocks;
+  grid_dep_wait();
+  const int moves = a.n_moves[unit];
+  const int dpage = a.block_table[static_cast<long long>(b) * a.max_blocks_per_seq + p];
+  if (tid < 32) {
+    int32_t f = kStays;
+    const int t = p * KVQ_BLOCK_SIZE + tid;
+    if (tid < KVQ_BLOCK_SIZE && t < a.keep && moves) f = a.slot_map[unit * a.n_pages * KVQ_BLOCK_SIZE + t];
+    const bool moving = f != kStays;
+    const bool dst_ok = dpage >= 0 && dpage < a.num_blocks;
+    if (moving && !dst_ok) set_status(a.status, KVQ_DEV_BAD_BLOCK);
+    if (tid < KVQ_BLOCK_SIZE) from[tid] = f;
+    const uint32_t m = __ballot_sync(0xffffffffu, f >= 0 && dst_ok);
+    if (tid == 0) any = m != 0;
+  }
+  __syncthreads();
+  if (!any) return;
   const long long dph = static_cast<long long>(dpage) * a.n_kv_heads + kvh;
-  if (tid < KVQ_BLOCK_SIZE) src_ph[tid] = -1;
-  __syncthreads();
-  if (tid < j1 - j0) {
-    const int s = a.move_src[unit * a.max_moves + j0 + tid], t = a.move_dst[unit * a.max_moves + j0 + tid];
-    const int page = bt[s / KVQ_BLOCK_SIZE];
-    const bool ok = dst_ok && page >= 0 && page < a.num_blocks;
-    if (!ok) set_status(a.status, KVQ_DEV_BAD_BLOCK);
-    const long long ph = static_cast<long long>(page) * a.n_kv_heads + kvh;
-    src_ph[t % KVQ_BLOCK_SIZE] = ok ? ph : -1;
-    src_slot[t % KVQ_BLOCK_SIZE] = s % KVQ_BLOCK_SIZE;
-    if (ok) {
-      const int so = s % KVQ_BLOCK_SIZE, dz = t % KVQ_BLOCK_SIZE;
-      a.k_scale[dph * KVQ_BLOCK_SIZE + dz] = a.k_scale[ph * KVQ_BLOCK_SIZE + so];
-      a.v_scale[dph * KVQ_BLOCK_SIZE + dz] = a.v_scale[ph * KVQ_BLOCK_SIZE + so];
-    }
-    a.acc_out[unit * a.out_stride + t] = a.acc[unit * a.acc_stride + s];
-    a.slot_pos_out[unit * a.out_stride + t] = a.slot_pos[unit * a.acc_stride + s];
-  }
-  __syncthreads();
-  if (!dst_ok) return;
-  // K: a token's chunk of 16 dims is one 16-byte word
-  for (int i = tid; i < KVQ_BLOCK_SIZE * (D / 16); i += D) {
-    const int slot = i % KVQ_BLOCK_SIZE, ch = i / KVQ_BLOCK_SIZE;
-    const long long ph = src_ph[slot];
-    if (ph >= 0)
-      *reinterpret_cast<uint4*>(a.k + ((dph * (D / 16) + ch) * KVQ_BLOCK_SIZE + slot) * 16) =
-          *reinterpret_cast<const uint4*>(a.k + ((ph * (D / 16) + ch) * KVQ_BLOCK_SIZE + src_slot[slot]) * 16);
-  }
+  auto ph_of = [&](int f) { return static_cast<long long>(f / KVQ_BLOCK_SIZE) * a.n_kv_heads + kvh; };
   // V: thread = dim; its 16 slots are one 16-byte word, into which the movers' bytes go
   uint4* row = reinterpret_cast<uint4*>(a.v + (dph * D + tid) * KVQ_BLOCK_SIZE);
-  uint4 w = *row;
-  uint32_t word[4] = {w.x, w.y, w.z, w.w};
+  const uint4 w = *row;
+  uint32_t byte[KVQ_BLOCK_SIZE];
 #pragma unroll
   for (int slot = 0; slot < KVQ_BLOCK_SIZE; ++slot) {
-    const long long ph = src_ph[slot];
-    if (ph >= 0) {
-      const uint32_t byte = static_cast<uint8_t>(a.v[(ph * D + tid) * KVQ_BLOCK_SIZE + src_slot[slot]]);
-      const uint32_t sh = 8u * (slot % 4);
-      word[slot / 4] = (word[slot / 4] & ~(0xFFu << sh)) | (byte << sh);
+    const int f = from[slot];
+    if (f >= 0) byte[slot] = static_cast<uint8_t>(a.v[(ph_of(f) * D + tid) * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE]);
+  }
+  // K: a token's chunk of 16 dims is one 16-byte word; thread = (chunk tid / 16, slot tid % 16)
+  const int slot = tid % KVQ_BLOCK_SIZE, ch = tid / KVQ_BLOCK_SIZE;
+  const int f = from[slot];
+  if (f >= 0) {
+    const long long ph = ph_of(f);
+    *reinterpret_cast<uint4*>(a.k + ((dph * (D / 16) + ch) * KVQ_BLOCK_SIZE + slot) * 16) =
+        *reinterpret_cast<const uint4*>(a.k + ((ph * (D / 16) + ch) * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE) * 16);
+    if (ch == 0) a.k_scale[dph * KVQ_BLOCK_SIZE + slot] = a.k_scale[ph * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE];
+    if (ch == 1) a.v_scale[dph * KVQ_BLOCK_SIZE + slot] = a.v_scale[ph * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE];
+  }
+  uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int s = 0; s < KVQ_BLOCK_SIZE; ++s) {
+    if (from[s] >= 0) {
+      const uint32_t sh = 8u * (s % 4);
+      word[s / 4] = (word[s / 4] & ~(0xFFu << sh)) | (byte[s] << sh);
     }
   }
   *row = make_uint4(word[0], word[1], word[2], word[3]);
@@ -337,9 +426,8 @@ EvictWorkspace evict_workspace(int batch, int n_kv_heads, int max_ctx, int keep)
   const long long units = static_cast<long long>(batch) * n_kv_heads;
   w.max_moves = max_ctx > keep ? std::min(keep, max_ctx - keep) : 0;
   w.n_pages = max_ctx > keep ? (keep + KVQ_BLOCK_SIZE - 1) / KVQ_BLOCK_SIZE : 0;
-  w.off_dst = (units * w.max_moves * 4 + 255) / 256 * 256;
-  w.off_first = 2 * w.off_dst;
-  w.off_count = w.off_first + (units * w.n_pages * 4 + 255) / 256 * 256;
+  w.off_map = (units * w.max_moves * 4 + 255) / 256 * 256;
+  w.off_count = w.off_map + units * w.n_pages * KVQ_BLOCK_SIZE * 4;
   w.bytes = w.off_count + units * 4;
   return w;
 }
@@ -348,8 +436,14 @@ cudaError_t launch_evict(const EvictArgs& a, int n_sms, cudaStream_t stream) {
   const int c = select_cluster(a, n_sms);
   const int range = ((a.max_ctx + c - 1) / c + 31) / 32 * 32;
   const size_t smem = static_cast<size_t>(std::min(range, kKeyCap)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
-  if (e != cudaSuccess) return e;
+  // Few moves in the select kernel's warps, each a few hundred bytes in dozens of small pieces; a page at
+  // a time in a kernel of their own when there are more.
+  const bool few = a.max_moves <= kFewMoves;
+  auto kern = few ? evict_select_kernel<true> : evict_select_kernel<false>;
+  cudaError_t e;
+  if (smem > 32 * 1024 &&
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4)) != cudaSuccess)
+    return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c, a.n_kv_heads, a.batch);
   cfg.blockDim = dim3(kSelThreads);
@@ -364,9 +458,10 @@ cudaError_t launch_evict(const EvictArgs& a, int n_sms, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if ((e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a)) != cudaSuccess) return e;
-  if (a.max_moves == 0) return cudaSuccess;
-  const dim3 grid(a.n_pages, a.n_kv_heads, a.batch);
+  if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return e;
+  if (few) return cudaSuccess;
+  // (a budget past the block table's pages never evicts)
+  const dim3 grid(std::min(a.n_pages, a.max_blocks_per_seq), a.n_kv_heads, a.batch);
   return a.head_dim == 256 ? launch_pdl(evict_move_kernel<256>, grid, dim3(256), 0, stream, a)
                            : launch_pdl(evict_move_kernel<128>, grid, dim3(128), 0, stream, a);
 }

@@ -160,17 +160,17 @@ struct EvictArgs {
   int32_t* slot_pos_out;
   long long out_stride;
   int32_t* new_lens;         // [B]
-  // workspace: per (sequence, KV head) the moves (ascending), the first move into each page, the count
+  // workspace: per (sequence, KV head) the slots that move (ascending), for every slot of the pages below
+  // the budget the physical slot that moves into it, and whether anything moves
   int max_moves, n_pages;
   int32_t* move_src;         // [units][max_moves]
-  int32_t* move_dst;
-  int32_t* page_first;       // [units][n_pages]
+  int32_t* slot_map;         // [units][16 * n_pages]
   int32_t* n_moves;          // [units]
   unsigned int* status;
 };
 struct EvictWorkspace {
   int max_moves, n_pages;
-  long long off_dst, off_first, off_count, bytes;
+  long long off_map, off_count, bytes;
 };
 EvictWorkspace evict_workspace(int batch, int n_kv_heads, int max_ctx, int keep);
 cudaError_t launch_evict(const EvictArgs& a, int n_sms, cudaStream_t stream);
