@@ -202,19 +202,19 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
   if (warp == kCwMmaWarp) tc::tmem_alloc(tmem_slot, L::kTmemCols);
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(&bars[L::full + s], 128);
+      mbar_init(&bars[L::full + s], 4);  // a lane of each producer warp arrives: a thread's arrival costs as much as a warp's
       mbar_init(&bars[L::empty + s], 1);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars[L::sFull + s], 1);
-      mbar_init(&bars[L::sFree + s], kSoftThreads);
+      mbar_init(&bars[L::sFree + s], kSoftThreads / 32);
     }
     for (int s = 0; s < kParBufs; ++s) {
-      mbar_init(&bars[L::parFull + s], 128);
-      mbar_init(&bars[L::parFree + s], kSoftThreads);
+      mbar_init(&bars[L::parFull + s], 4);
+      mbar_init(&bars[L::parFree + s], kSoftThreads / 32);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars[L::aFull + s], 128);
+      mbar_init(&bars[L::aFull + s], 4);
       mbar_init(&bars[L::aFree + s], 1);
     }
     mbar_init(&bars[L::drain], 1);
@@ -227,6 +227,10 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
   const uint32_t tmem = *tmem_slot;
   auto wait = [&](int bar, uint32_t parity) {
     return wait_or_abort(&bars[bar], parity & 1u, a.status, abort_flag, a.wait_budget);
+  };
+  auto arrive_warp = [&](int bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[bar]);
   };
   auto wait_warp = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
         tc::wait_ld();
         if (ch == 1) {
           tc::fence_before_sync();
-          mbar_arrive(&bars[L::sFree + sb]);  // this half of S is in registers
+          arrive_warp(L::sFree + sb);  // this warp's part of S is in registers
         }
         const int c0 = 64 * part + 32 * ch;  // first column of the chunk
         const float4* p0 = reinterpret_cast<const float4*>(par + (pb * 2 + 0) * 128 + c0);
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
           }
         }
       }
-      mbar_arrive(&bars[L::parFree + pb]);
+      arrive_warp(L::parFree + pb);
       l += PASS == 2 ? tile_sum : 0.f;
       if (w.b + 1 == w.n || f + 1 == n_tiles) {  // the A tile, or this CTA's part of it, is done
         if (PASS == 1) a.row_part[out_index(w)] = make_float2(m, l);
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
         par[(pb * 2 + 0) * 128 + n] = ks;
         const uint32_t bits = __ballot_sync(0xffffffffu, real);
         if (lane == 0) valid[pb * 4 + (n >> 5)] = bits;
-        mbar_arrive(&bars[L::parFull + pb]);
+        arrive_warp(L::parFull + pb);
         step<1>(a, w);
         const bool more = f + 1 < n_tiles;
         if (more) seek(w);
@@ -429,9 +433,8 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
             sts128(piece + tc::sw128_off(n, 2 * i + 1), c1);
             if (more) fetch(4 * p + i);
           }
-          tc::fence_proxy_async_smem();
           // test-only fault injection: the first piece of CTA 0's second tile is never announced
-          if (!(a.fault == 4 && blockIdx.x == 0 && f == 1 && p == 0)) mbar_arrive(&bars[L::full + s]);
+          if (!(a.fault == 4 && blockIdx.x == 0 && f == 1 && p == 0)) arrive_warp(L::full + s);
           ++fill;
         }
       }
@@ -440,8 +443,7 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
       const int cc = n & 7, r8 = n >> 3;
       int done = 0;
       auto announce = [&]() {
-        tc::fence_proxy_async_smem();
-        mbar_arrive(&bars[L::full + done % kRing]);
+        arrive_warp(L::full + done % kRing);
         ++done;
       };
       auto stats = [&](const Walk& x, float& nm, float& il) {
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
         if (!ok) break;
         par[(pb * 2 + 0) * 128 + n] = nm;
         par[(pb * 2 + 1) * 128 + n] = il;
-        mbar_arrive(&bars[L::parFull + pb]);
+        arrive_warp(L::parFull + pb);
         const int r0 = 128 * (b_first<2>(a, w.t) + w.b);
         const uint16_t* base = static_cast<const uint16_t*>(a.q) + static_cast<long long>(w.kvh) * a.group * D + 8 * cc;
         long long off[8];
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
       tc::wait_st();
       consts[(at % kConstBufs) * 128 + n] = cst;
       tc::fence_before_sync();
-      mbar_arrive(&bars[L::aFull + (at & 1)]);
+      arrive_warp(L::aFull + (at & 1));
       // the next A tile of the run
       f += w.n - w.b;
       w.b = w.n - 1;
@@ -583,6 +585,9 @@ __global__ void __launch_bounds__(kCwThreads, 1) chunk_weights_kernel(ChunkWeigh
         ok = wait_warp(L::full + s, used / kRing);
         if (!ok) break;
         if (elect_one()) {
+          // The producers' stores come before the tensor core's reads.  The fence is taken here, on the thread that
+          // has acquired them, and not by the producers: there it waits for every load they have in flight.
+          tc::fence_proxy_async_smem();
           tc::fence_after_sync();
           const uint64_t bd = rd0 + static_cast<uint64_t>((s * kPieceBytes) >> 4);
 #pragma unroll
