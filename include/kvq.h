@@ -668,7 +668,7 @@ int kvq_debug_stream_floor(const kvq_cache* cache, int32_t batch, const int32_t*
  * does not issue the copy of its second page, with mode 2 the producer of prefill attention CTA 0
  * does not issue its fourth piece, with mode 3 the sparse CTA of (query 0, KV head 0) does not
  * issue the copies of its second chunk, with mode 4 the first CTA of the chunk weights' row pass does not
- * announce the first piece of its second tile (mode 0: no injection).  No copy is left in flight:
+ * announce its first key tile (mode 0: no injection).  No copy is left in flight:
  * the consumer's wait runs out, the kernel sets KVQ_DEV_TIMEOUT, waits (bounded) for the copies it
  * did issue, drops that CTA's result (decode single route: zero output rows; split route: an empty
  * partial that the merge skips; prefill: the unit's output rows are not written; sparse: the

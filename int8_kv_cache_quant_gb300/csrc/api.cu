@@ -479,7 +479,7 @@ size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, in
                                          int32_t head_dim) {
   if (!chunk_weights_sizes_ok(n_tokens, n_q_heads, n_kv_heads, history_len) || (head_dim != 128 && head_dim != 256)) return 0;
   return static_cast<size_t>(
-      kvq::chunk_weights_plan(n_tokens, n_q_heads, n_kv_heads, history_len, kChunkWeightsMaxRuns).bytes);
+      kvq::chunk_weights_plan(n_tokens, n_q_heads, n_kv_heads, history_len, head_dim, kChunkWeightsMaxRuns).bytes);
 }
 
 int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
@@ -501,7 +501,7 @@ int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t
   if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
   const int sms = std::min(device_sm_count(), kChunkWeightsMaxRuns);
   if (sms <= 0) return KVQ_ERR_CUDA;
-  const kvq::ChunkWeightsPlan p = kvq::chunk_weights_plan(n_tokens, n_q_heads, cache->n_kv_heads, history_len, sms);
+  const kvq::ChunkWeightsPlan p = kvq::chunk_weights_plan(n_tokens, n_q_heads, cache->n_kv_heads, history_len, cache->head_dim, sms);
   if (workspace_bytes < static_cast<size_t>(p.bytes)) return KVQ_ERR_WORKSPACE;
   kvq::ChunkWeightsArgs a{};
   a.k = cache->k;
@@ -522,14 +522,17 @@ int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t
   a.row_tiles = p.row_tiles;
   a.key_tiles = p.key_tiles;
   for (int i = 0; i < 2; ++i) {
+    a.a_rows[i] = p.a_rows[i];
+    a.units[i] = p.units[i];
     a.line[i] = p.line[i];
     a.runs[i] = p.runs[i];
-    a.n_seg[i] = p.n_seg[i];
+    a.n_part[i] = p.n_part[i];
   }
   char* base = static_cast<char*>(workspace);
   a.row_part = reinterpret_cast<float2*>(base);
   a.row_nm = reinterpret_cast<float*>(base + p.off_nm);
   a.row_il = reinterpret_cast<float*>(base + p.off_il);
+  a.q_tiles = reinterpret_cast<uint8_t*>(base + p.off_q);
   a.col_part = reinterpret_cast<float*>(base + p.off_col);
   a.status = status_ptr();
   a.wait_budget = kvq::debug_wait_budget();

@@ -110,14 +110,16 @@ cudaError_t launch_step_accum(const StepAccumArgs& a, cudaStream_t stream, int* 
 // stage 2 alone (the split route's merge)
 cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 
-// Attention weights of a chunk of queries, summed per key.
+// Attention weights of a chunk of queries, summed per key.  [0]: the row pass, [1]: the column pass.
 struct ChunkWeightsPlan {
   int row_tiles, key_tiles;   // 128 (query, head) rows of a KV head; 128 keys
-  long long line[2];          // (A tile, B tile) pairs of one KV head in the row / column pass
-  int runs[2], n_seg[2];      // CTAs, and the most parts one A tile is cut into
-  long long off_nm, off_il, off_col, bytes;
+  int a_rows[2], units[2];    // rows of an A unit (128 or 256), A units of a KV head
+  long long line[2];          // (A unit, B tile) pairs of one KV head
+  int runs[2], n_part[2];     // CTAs, and the most parts one 128-row A tile is cut into
+  long long off_nm, off_il, off_q, off_col, bytes;
 };
-ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads, int history_len, int n_sms);
+ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads, int history_len, int head_dim,
+                                    int n_sms);
 struct ChunkWeightsArgs {
   const int8_t* k;
   const float* k_scale;
@@ -129,12 +131,14 @@ struct ChunkWeightsArgs {
   float* acc;     // fp32 [Hkv][acc_stride]
   long long acc_stride;
   int row_tiles, key_tiles;
+  int a_rows[2], units[2];
   long long line[2];
-  int runs[2], n_seg[2];
-  float2* row_part;  // workspace [Hkv * row_tiles][n_seg[0]][2][128]: (max, sum) parts, sum < 0: dropped
+  int runs[2], n_part[2];
+  float2* row_part;  // workspace [Hkv][A tiles][n_part[0]][128]: (max, sum) parts, sum < 0: dropped
   float* row_nm;     // workspace [Hkv * row_tiles][128]: minus the row's maximum
   float* row_il;     // workspace: 1 / the row's sum, 0 for a row that gives nothing
-  float* col_part;   // workspace [Hkv * key_tiles][n_seg[1]][2][128]
+  uint8_t* q_tiles;  // workspace [Hkv * row_tiles][D / 64 pieces of 16 KB]: the queries, bf16, in tile order
+  float* col_part;   // workspace [Hkv][A tiles][n_part[1]][128]
   unsigned int* status;
   long long wait_budget;
   int fault;

@@ -38,7 +38,8 @@ CASES = [  # tokens, history, hkv, G, d
     (1, 0, 1, 1, 128), (1, 0, 2, 6, 256), (2, 0, 1, 16, 256), (1, 127, 1, 4, 128), (1, 128, 2, 3, 256), (7, 121, 1, 1, 256),
     (128, 0, 1, 1, 128), (129, 0, 1, 1, 256), (22, 500, 4, 6, 256), (21, 1, 1, 6, 128), (128, 128, 2, 1, 256),
     (100, 413, 2, 4, 128), (333, 47, 1, 5, 256), (513, 0, 2, 2, 128), (64, 1999, 8, 4, 128), (40, 3000, 1, 12, 256),
-    (5, 700, 3, 20, 128), (777, 600, 1, 3, 256)]
+    (5, 700, 3, 20, 128), (777, 600, 1, 3, 256),
+    (1, 40000, 3, 1, 128), (1, 30000, 2, 1, 256), (129, 20000, 1, 1, 256)]
 
 
 @pytest.mark.parametrize("T,hist,hkv,G,d", CASES)
@@ -144,7 +145,7 @@ def test_a_row_that_is_not_finite_reaches_only_the_keys_it_sees(kvq):
 
 
 def test_a_wait_that_ran_out(kvq):
-    """The first run of the row pass stops at its second tile (host-injected): the call returns, the rows it
+    """The first run of the row pass stops at its first tile (host-injected): the call returns, the rows it
     left unfinished give no weight, and the next call is right again."""
     import torch
     from int8_kv_cache_quant_gb300.kvq import DEV_TIMEOUT
@@ -166,8 +167,8 @@ def test_a_wait_that_ran_out(kvq):
     finally:
         kvq.kvq_debug_fault_inject(0, 0)
     s = float(acc2.double().sum())
-    # the 128 rows of the first row tile are gone, the others give 1 each
-    assert abs(s - (T2 * G - 128)) < 0.1, s
+    # the 256 rows of the first run's row tiles are gone, the others give 1 each
+    assert abs(s - (T2 * G - 256)) < 0.1, s
     kvq.kvq_attn_chunk_weights_int8kv(cache, qt[:T], hist, bt, 0.09, acc)
     assert kvq.kvq_device_status() == 0
     check(pool, table[0], hist, q[:T], np.zeros((1, hist + T), np.float32), acc.cpu().numpy(), 0.09)
