@@ -534,6 +534,11 @@ int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t
   a.row_il = reinterpret_cast<float*>(base + p.off_il);
   a.q_tiles = reinterpret_cast<uint8_t*>(base + p.off_q);
   a.col_part = reinterpret_cast<float*>(base + p.off_col);
+  if (p.widen_once) {
+    a.k_tiles = reinterpret_cast<uint8_t*>(base + p.off_k);
+    a.k_par = reinterpret_cast<float*>(base + p.off_kpar);
+    a.k_valid = reinterpret_cast<uint32_t*>(base + p.off_kvalid);
+  }
   a.status = status_ptr();
   a.wait_budget = kvq::debug_wait_budget();
   a.fault = kvq::debug_fault_mode();

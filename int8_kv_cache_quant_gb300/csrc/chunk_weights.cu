@@ -14,29 +14,27 @@
 //                sum over the columns (rows) of 2^(s - M) / l.
 // The rows of a KV head are r = i * G + g (G heads a group), so a row tile is a run of queries.
 //
-// Operands.  sm_103a has no integer tcgen05 kind, and the codes are exact in 16 bits: the row pass widens
-// K to fp16 and scales each query row by a power of two (exact for bf16 values within 2^29 of the row's
-// largest); the column pass takes the bf16 queries as they are and widens the codes to bf16 (exact:
-// |code| < 2^8).  Either way every product is exact and the sums are fp32.  The row pass widens in the
-// producer warps, from global memory through registers into the swizzled shared-memory tile: the codes
-// are read as bytes (half of what a widened copy would move) and no copy of K is ever written.  The
-// queries, far smaller, are laid out once in the swizzled tile order by the row pass, on its way
-// through them, so that the column pass brings a tile in with one bulk copy.
+// Operands.  sm_103a has no integer tcgen05 kind, and the codes are exact in bf16 (|code| < 2^8), so both
+// passes take the bf16 queries as they are and widen the codes to bf16: every product is exact and the
+// sums are fp32.  The key tiles of the row pass come in one of two ways: widened by producer warps, from
+// global memory through registers into the swizzled shared-memory tile (WIDEN; the codes are read as
+// bytes and no copy of K is written), or, when many row tiles read them, widened once by a pass of
+// their own into a workspace from which a tile is one bulk copy.  The queries are laid out in the same
+// tile order by the row pass, on its way through them, so that the column pass brings them in by bulk
+// copies too.
 //
 // Schedule.  One CTA per SM; the (A unit, B tile) pairs of all KV heads are one line, cut into equal
 // runs, one per CTA, so that causal and ragged shapes balance to a tile.  An A unit is one 128-row tile
-// (MT = 1, held twice: the next one loads while this one is in use) or two of them (MT = 2), which
-// share every B tile: a 128 x 128 tile pair at head_dim 256 takes 1024 cycles of the tensor core, in
-// which one SM would have to take in 64 KB of queries, more than all SMs together get out of L2;
-// with two A tiles it is half of that.  An A unit that two CTAs share leaves one partial each, and the
-// partials are added in the order of the line: the same result every time.  Roles of a CTA's warps:
-//   warps 0-7    softmax: group w / 4 takes every second 128 x 128 tile of scores (MT = 2: its A tile's),
-//                thread = tensor-memory lane 32 (w % 4) + lane
-//   warps 8-11   row pass: B producers (128 threads); column pass: warp 8 issues the bulk copies, warp 9
-//                the MMAs
-//   warps 12-15  A loaders (128 threads)
-//   warp 16      row pass: MMA issue
-// Tensor memory: A tiles (head_dim / 2 columns each) | two score tiles, one a softmax group.
+// (MT = 1) or two of them (MT = 2), which share every B tile: a 128 x 128 tile pair at head_dim 256
+// takes 1024 cycles of the tensor core, in which one SM would have to take in 64 KB, more than all SMs
+// together get out of L2; with two A tiles it is half of that.  An A unit that two CTAs share leaves
+// one partial each, and the partials are added in the order of the line: the same result every time.
+// Roles of a CTA's warps:
+//   warps 0-15   softmax: thread = tensor-memory lane 32 (w % 4) + lane, columns 32 (w / 4) .. of every
+//                128 x 128 score tile; four warps a scheduler hide each other's latencies
+//   WIDEN        warps 16-19 B producers (128 threads), 20-23 A loaders (128 threads), 24 MMA issue
+//   else         warp 16 bulk copies (one lane), 17 MMA issue, 20-23 A loaders
+// Tensor memory: A tiles (head_dim / 2 columns each) | two score tiles, filled in turn.
 //
 // What bounds it: at head_dim 256 the tensor core (1024 cycles a 128 x 128 tile at 4096 multiply-adds a
 // cycle and SM; its 16384 exponentials take 512 at 32 a cycle), at head_dim 128 both alike.
@@ -53,18 +51,22 @@ namespace kvq {
 
 namespace {
 
-constexpr int kSoftWarps = 8, kProdWarp = 8, kLoadWarp = 12;
+constexpr int kSoftWarps = 16, kProdWarp = 16, kLoadWarp = 20;
 constexpr int kParBufs = 4;    // column parameters, by B tile
-// Row constants, by A unit.  A softmax group can lag behind the A loaders by five units (of one B tile
-// each: the other group's tiles go on until the MMA needs this group's score tile), so the constants
-// have more buffers than the A tiles, and barriers of their own, whose phases cannot pass the reader.
+// Column pass: key constants, by A unit.  The softmax warps can lag behind the A loaders by several units
+// (of one B tile each), so the constants have more buffers than the A tiles, and barriers of their own,
+// whose phases cannot pass the reader.
 constexpr int kConstBufs = 8;
-constexpr float kRefSlack = 8.0f;  // a running maximum stays until it is exceeded by 2^8
+// Row pass: the reference that stands for a row's maximum is the largest score of the first chunk the row
+// sees, and moves only when a chunk's sum of 2^(s - reference) reaches this: fp32 holds the sums as exactly
+// whatever their exponent, and without a maximum to take a score costs one multiply-add, one
+// exponential and one addition.
+constexpr float kSumLimit = 1.8446744e19f;  // 2^64
 
-template <int D, int PASS, int MT>
+template <int D, int PASS, int MT, bool WIDEN>
 struct Cw {
-  static constexpr int kThreads = PASS == 1 ? 17 * 32 : 16 * 32;
-  static constexpr int kMmaWarp = PASS == 1 ? 16 : 9;
+  static constexpr int kThreads = WIDEN ? 25 * 32 : 24 * 32;
+  static constexpr int kMmaWarp = WIDEN ? 24 : 17;
   static constexpr int kRows = 128 * MT;                   // rows of an A unit
   static constexpr int kTileBytes = D * 256;               // one B tile: 128 rows x D 16-bit values
   static constexpr int kStages = 196608 / kTileBytes;      // 3 at head_dim 256, 6 at 128
@@ -81,9 +83,10 @@ struct Cw {
   static constexpr int kAlloc = offFlag + 16 + 1024;
   static_assert(MT * kABufs * kACols <= kSCol && kSCol + 256 <= kTmemCols, "tensor memory");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  // barriers: B stages, score tiles (one a softmax group), column parameters, A units
+  // barriers: B stages, score tiles, column parameters, A units, key constants
   static constexpr int full = 0, empty = full + kStages, sFull = empty + kStages, sFree = sFull + 2, parFull = sFree + 2,
-                       parFree = parFull + kParBufs, aFull = parFree + kParBufs, aFree = aFull + 2, constFull = aFree + 2, drain = constFull + kConstBufs;
+                       parFree = parFull + kParBufs, aFull = parFree + kParBufs, aFree = aFull + 2, constFull = aFree + 2,
+                       drain = constFull + kConstBufs;
 };
 
 // B tiles of A unit t, and the first of them.
@@ -179,9 +182,50 @@ __device__ __forceinline__ long long key_ph(const ChunkWeightsArgs& a, int kvh, 
 
 }  // namespace
 
-template <int D, int PASS, int MT>
-__global__ void __launch_bounds__(Cw<D, PASS, MT>::kThreads, 1) chunk_weights_kernel(ChunkWeightsArgs a) {
-  using L = Cw<D, PASS, MT>;
+// The key tiles widened once: (key tile, KV head) to the bf16 operand tile, the keys' score factors and
+// which of them exist.  Four adjacent lanes fill one 128-byte row of a piece.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_widen_kernel(ChunkWeightsArgs a) {
+  const int j = blockIdx.x, kvh = blockIdx.y, tid = threadIdx.x;
+  __shared__ long long ph_s[8];
+  grid_dep_wait();
+  if (tid < 8) ph_s[tid] = key_ph(a, kvh, 128 * j + KVQ_BLOCK_SIZE * tid);
+  __syncthreads();
+  const long long u = static_cast<long long>(kvh) * a.key_tiles + j;
+  uint8_t* tile = a.k_tiles + u * (D * 256);
+  uint4 raw[D / 32];
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) {
+    const int i = tid + 256 * x, n = (i >> 2) & 127, c16 = ((i >> 9) << 2) | (i & 3);
+    const long long ph = ph_s[n >> 4];
+    raw[x] = make_uint4(0, 0, 0, 0);
+    if (ph >= 0 && 128 * j + n < a.n_keys)
+      raw[x] = __ldg(reinterpret_cast<const uint4*>(a.k + (ph * (D / 16) + c16) * 256 + (n & 15) * 16));
+  }
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) {
+    const int i = tid + 256 * x, n = (i >> 2) & 127, c16 = ((i >> 9) << 2) | (i & 3);
+    uint32_t h[8];
+    widen16_bf16(raw[x], h);
+    uint8_t* piece = tile + (c16 >> 2) * kPieceBytes;
+    const int cc = (c16 & 3) * 2;
+    sts128(piece + tc::sw128_off(n, cc), make_uint4(h[0], h[1], h[2], h[3]));  // global stores
+    sts128(piece + tc::sw128_off(n, cc + 1), make_uint4(h[4], h[5], h[6], h[7]));
+  }
+  if (tid < 128) {
+    const long long ph = ph_s[tid >> 4];
+    const bool real = ph >= 0 && 128 * j + tid < a.n_keys;
+    a.k_par[u * 128 + tid] = real ? a.k_scale[ph * KVQ_BLOCK_SIZE + (tid & 15)] * a.c2 : 0.f;
+    const uint32_t bits = __ballot_sync(0xffffffffu, real);
+    if ((tid & 31) == 0) a.k_valid[u * 4 + (tid >> 5)] = bits;
+  }
+  grid_dep_trigger();
+}
+
+template <int D, int PASS, int MT, bool WIDEN>
+__global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_weights_kernel(ChunkWeightsArgs a) {
+  static_assert(PASS == 1 || !WIDEN, "the column pass streams queries");
+  using L = Cw<D, PASS, MT, WIDEN>;
   constexpr int NP = D / 64;  // 16 KB pieces of a B tile
   constexpr int ST = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -204,18 +248,18 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT>::kThreads, 1) chunk_weights_ke
   if (tid == 0) {
     // a lane of each warp arrives for its warp: a thread's arrival costs as much as a warp's
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&bars[L::full + s], PASS == 1 ? 4 : 1);
+      mbar_init(&bars[L::full + s], WIDEN ? 4 : 1);
       mbar_init(&bars[L::empty + s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars[L::sFull + s], 1);
-      mbar_init(&bars[L::sFree + s], 4);
+      mbar_init(&bars[L::sFree + s], kSoftWarps);
       mbar_init(&bars[L::aFull + s], 4);
       mbar_init(&bars[L::aFree + s], 1);
     }
     for (int s = 0; s < kParBufs; ++s) {
-      mbar_init(&bars[L::parFull + s], PASS == 1 ? 4 : 1);
-      mbar_init(&bars[L::parFree + s], 4 * MT);  // MT = 1: only the group whose tile it is reads them
+      mbar_init(&bars[L::parFull + s], WIDEN ? 4 : 1);
+      mbar_init(&bars[L::parFree + s], kSoftWarps);
     }
     for (int s = 0; s < kConstBufs; ++s) mbar_init(&bars[L::constFull + s], 4);
     mbar_init(&bars[L::drain], 1);
@@ -237,135 +281,141 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT>::kThreads, 1) chunk_weights_ke
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
-    const int grp = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t tm_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::kSCol + 128 * grp;
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane, c0 = 32 * part;
+    const uint32_t tm_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::kSCol + c0;
     // where this CTA's partial of the A unit at the walk goes: slot 0 unless an earlier run began it
     int slot = w.b == 0 ? 0 : static_cast<int>(blockIdx.x) - run_of(f0 - w.b, total, P);
-    // parts of a 128-row tile: [slot] (MT = 2), or [slot][group] (MT = 1)
-    auto out_index = [&](const Walk& x) {
-      const long long u = (static_cast<long long>(x.kvh) * a.units[PASS - 1] + x.t) * MT + (MT == 2 ? grp : 0);
-      return (u * a.n_part[PASS - 1] + (MT == 2 ? slot : 2 * slot + grp)) * 128 + row;
+    auto out_index = [&](const Walk& x, int i) {
+      const long long u = (static_cast<long long>(x.kvh) * a.units[PASS - 1] + x.t) * MT + i;
+      return (u * a.n_part[PASS - 1] + 4 * slot + part) * 128 + row;
     };
-    const int arow = (MT == 2 ? 128 * grp : 0) + row;  // row of the A unit
     bool ok = true;
-    int at = -1;       // ordinal of the current A unit in this CTA
-    int mine = 0;      // score tiles this group has taken
-    float cst = 0.f;   // row pass: the row's score factor; column pass: the key's
-    float m = -INFINITY, l = 0.f;
-    int bound = 0;     // row pass: last visible key; column pass: first row that sees the key
+    int at = -1;    // ordinal of the current A unit in this CTA
+    int first = 0;  // its first B tile
+    // per A tile of the unit.  Row pass: reference and sum of the row, its last visible key.  Column pass: the
+    // key's sum, its score factor, the first row that sees it.
+    float m[MT], l[MT], cst[MT];
+    int bound[MT];
     for (int f = 0; f < n_tiles; ++f) {
       if (f == 0 || w.b == 0) {
         ++at;
-        ok = wait_warp(L::constFull + at % kConstBufs, at / kConstBufs);
-        if (!ok) break;
-        cst = consts[(at % kConstBufs) * L::kRows + arow];
-        m = -INFINITY;
-        l = 0.f;
-        const int r = L::kRows * w.t + arow;
-        if (PASS == 1) bound = r < a.n_rows ? a.history_len + r / a.group : -1;
-        else bound = max(0, r - a.history_len) * a.group;
+        if (PASS == 2) {
+          ok = wait_warp(L::constFull + at % kConstBufs, at / kConstBufs);
+          if (!ok) break;
+        }
+        first = b_first<PASS>(a, w.t);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const int r = L::kRows * w.t + 128 * i + row;
+          cst[i] = PASS == 2 ? consts[(at % kConstBufs) * L::kRows + 128 * i + row] : 0.f;
+          m[i] = -INFINITY;
+          l[i] = 0.f;
+          bound[i] = PASS == 1 ? (r < a.n_rows ? a.history_len + r / a.group : -1) : max(0, r - a.history_len) * a.group;
+        }
       }
-      if (MT == 2 || (f & 1) == grp) {
-        const int pb = f % kParBufs;
-        ok = wait_warp(L::sFull + grp, mine) && wait_warp(L::parFull + pb, f / kParBufs);
+      const int pb = f % kParBufs;
+      ok = wait_warp(L::parFull + pb, f / kParBufs);
+      if (!ok) break;
+      const float4* p0 = reinterpret_cast<const float4*>(par + (pb * 2 + 0) * 128 + c0);
+      const float4* p1 = reinterpret_cast<const float4*>(par + (pb * 2 + 1) * 128 + c0);
+      const uint32_t exist = PASS == 1 ? valid[pb * 4 + part] : 0u;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int g = MT * f + i, sg = g & 1;
+        ok = wait_warp(L::sFull + sg, g >> 1);
         if (!ok) break;
         tc::fence_after_sync();
-        float tile_sum = 0.f;
-        uint32_t buf[2][32];
-        tc::ld_32x32b_x32(tm_s, buf[0]);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t (&sv)[32] = buf[ch & 1];
-          tc::wait_ld();
-          if (ch < 3) {
-            tc::ld_32x32b_x32(tm_s + 32 * (ch + 1), buf[(ch + 1) & 1]);  // on its way while this chunk is worked on
-          } else {
-            tc::fence_before_sync();
-            arrive_warp(L::sFree + grp);  // the tile is in registers
-          }
-          const int c0 = 32 * ch;  // first column of the chunk
-          const float4* p0 = reinterpret_cast<const float4*>(par + (pb * 2 + 0) * 128 + c0);
-          const float4* p1 = reinterpret_cast<const float4*>(par + (pb * 2 + 1) * 128 + c0);
-          // columns of the chunk that count, as bits
-          uint32_t vis;
-          if (PASS == 1) {
-            const int n = bound - 128 * w.b + 1 - c0;
-            vis = (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u) & valid[pb * 4 + ch];
-          } else {
-            const int r0 = 128 * (b_first<2>(a, w.t) + w.b) + c0;
-            const int lo = bound - r0, hi = a.n_rows - r0;
-            vis = (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1u)) &
-                  (hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u);
-          }
-          const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
-          if (PASS == 1) {
-            float ym0 = -INFINITY, ym1 = -INFINITY;
+        uint32_t sv[32];
+        tc::ld_32x32b_x32(tm_s + 128 * sg, sv);
+        // columns of the chunk that count, as bits
+        uint32_t vis;
+        if (PASS == 1) {
+          const int n = bound[i] - 128 * w.b + 1 - c0;
+          vis = (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u) & exist;
+        } else {
+          const int r0 = 128 * (first + w.b) + c0, lo = bound[i] - r0, hi = a.n_rows - r0;
+          vis = (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1u)) &
+                (hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u);
+        }
+        const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
+        tc::wait_ld();
+        tc::fence_before_sync();
+        arrive_warp(L::sFree + sg);  // this warp's part of the score tile is in registers
+        if (PASS == 1) {
+          // sum of 2^(s - ref) over the chunk, s = S * (k_scale c2)
+          auto sum_from = [&](float ref) {
+            const f2 nm2 = mk2(-ref, -ref);
+            f2 sa = mk2(0.f, 0.f), sb = mk2(0.f, 0.f);
 #pragma unroll
             for (int n = 0; n < 32; n += 4) {
               const float4 k4 = p0[n >> 2];
-              const f2 ya = mul2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), mk2(k4.x, k4.y));
-              const f2 yb = mul2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), mk2(k4.z, k4.w));
-              sv[n] = __float_as_uint(lo2(ya));
-              sv[n + 1] = __float_as_uint(hi2(ya));
-              sv[n + 2] = __float_as_uint(lo2(yb));
-              sv[n + 3] = __float_as_uint(hi2(yb));
-              ym0 = fmax3(ym0, lo2(ya), hi2(ya));
-              ym1 = fmax3(ym1, lo2(yb), hi2(yb));
+              const f2 xa = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), mk2(k4.x, k4.y), nm2);
+              const f2 xb = fma2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), mk2(k4.z, k4.w), nm2);
+              sa = add2(sa, mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))));
+              sb = add2(sb, mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb))));
             }
-            float ym = fmaxf(ym0, ym1);
-            if (masked) {
-              ym = -INFINITY;
+            return (lo2(sa) + lo2(sb)) + (hi2(sa) + hi2(sb));
+          };
+          float s = 0.f;
+          bool plain = !masked && !__any_sync(0xffffffffu, m[i] == -INFINITY);
+          if (plain) {
+            s = sum_from(m[i]);
+            plain = !__any_sync(0xffffffffu, !(s < kSumLimit));  // true for NaN
+          }
+          if (!plain) {  // masks, a first chunk, or a score far above the reference: scores, maximum, sum
+            const float* k1 = par + (pb * 2 + 0) * 128 + c0;
+            float cm = -INFINITY;
 #pragma unroll
-              for (int n = 0; n < 32; ++n) {
-                if (!((vis >> n) & 1u)) sv[n] = 0xFF800000u;  // -inf
-                ym = fmaxf(ym, __uint_as_float(sv[n]));
-              }
+            for (int n = 0; n < 32; ++n) {
+              const float y = ((vis >> n) & 1u) ? __uint_as_float(sv[n]) * k1[n] : -INFINITY;
+              sv[n] = __float_as_uint(y);
+              cm = fmaxf(cm, y);
             }
-            const float cm = ym * cst;
-            if (cm > m + kRefSlack) {
-              l *= fast_exp2(m - cm);
-              m = cm;
+            // a first chunk, or more than 2^32 above the reference: the reference moves up
+            if (m[i] == -INFINITY || cm > m[i] + 32.f) {
+              if (m[i] != -INFINITY) l[i] *= fast_exp2(m[i] - cm);
+              m[i] = cm;
             }
-            const float ref = m == -INFINITY ? 0.f : m;
-            const f2 c2 = mk2(cst, cst), nm2 = mk2(-ref, -ref);
-            f2 s = mk2(0.f, 0.f);
+            const float ref = m[i] == -INFINITY ? 0.f : m[i];
+            s = 0.f;
 #pragma unroll
-            for (int n = 0; n < 32; n += 2) {
-              const f2 x = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), c2, nm2);
-              s = add2(s, mk2(fast_exp2(lo2(x)), fast_exp2(hi2(x))));
+            for (int n = 0; n < 32; ++n) s += fast_exp2(__uint_as_float(sv[n]) - ref);
+          }
+          l[i] += s;
+        } else {
+          const f2 c2 = mk2(cst[i], cst[i]);
+          float tile_sum = 0.f;
+          if (!masked) {
+            f2 sa = mk2(0.f, 0.f), sb = mk2(0.f, 0.f);
+#pragma unroll
+            for (int n = 0; n < 32; n += 4) {
+              const float4 nm = p0[n >> 2], il = p1[n >> 2];
+              const f2 xa = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), c2, mk2(nm.x, nm.y));
+              const f2 xb = fma2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), c2, mk2(nm.z, nm.w));
+              sa = fma2(mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))), mk2(il.x, il.y), sa);
+              sb = fma2(mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb))), mk2(il.z, il.w), sb);
             }
-            l += lo2(s) + hi2(s);
+            tile_sum = (lo2(sa) + lo2(sb)) + (hi2(sa) + hi2(sb));
           } else {
-            const f2 c2 = mk2(cst, cst);
-            f2 s = mk2(0.f, 0.f);
-            if (!masked) {
+            const float* nm = par + (pb * 2 + 0) * 128 + c0;
+            const float* il = par + (pb * 2 + 1) * 128 + c0;
 #pragma unroll
-              for (int n = 0; n < 32; n += 4) {
-                const float4 nm = p0[n >> 2], il = p1[n >> 2];
-                const f2 xa = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), c2, mk2(nm.x, nm.y));
-                const f2 xb = fma2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), c2, mk2(nm.z, nm.w));
-                s = fma2(mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))), mk2(il.x, il.y), s);
-                s = fma2(mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb))), mk2(il.z, il.w), s);
-              }
-              tile_sum += lo2(s) + hi2(s);
-            } else {
-              const float* nm = par + (pb * 2 + 0) * 128 + c0;
-              const float* il = par + (pb * 2 + 1) * 128 + c0;
-#pragma unroll
-              for (int n = 0; n < 32; ++n) {
-                const float p = fast_exp2(fmaf(__uint_as_float(sv[n]), cst, nm[n])) * il[n];
-                tile_sum += ((vis >> n) & 1u) ? p : 0.f;  // a row that does not see the key adds nothing, NaN neither
-              }
+            for (int n = 0; n < 32; ++n) {
+              const float p = fast_exp2(fmaf(__uint_as_float(sv[n]), cst[i], nm[n])) * il[n];
+              tile_sum += ((vis >> n) & 1u) ? p : 0.f;  // a row that does not see the key adds nothing, NaN neither
             }
           }
+          l[i] += tile_sum;
         }
-        arrive_warp(L::parFree + pb);
-        if (PASS == 2) l += tile_sum;
-        ++mine;
       }
+      if (!ok) break;
+      arrive_warp(L::parFree + pb);
       if (w.b + 1 == w.n || f + 1 == n_tiles) {  // the A unit, or this CTA's part of it, is done
-        if (PASS == 1) a.row_part[out_index(w)] = make_float2(m, l);
-        else a.col_part[out_index(w)] = l;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          if (PASS == 1) a.row_part[out_index(w, i)] = make_float2(m[i], l[i]);
+          else a.col_part[out_index(w, i)] = l[i];
+        }
         slot = 0;
       }
       step<PASS>(a, w);
@@ -378,74 +428,96 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT>::kThreads, 1) chunk_weights_ke
         slot = x.b == 0 ? 0 : static_cast<int>(blockIdx.x) - run_of(f - x.b, total, P);
         const long long end = min(f1, f + (x.n - x.b));
         if (x.kvh > w.kvh || (x.kvh == w.kvh && x.t >= w.t)) {
-          if (PASS == 1) a.row_part[out_index(x)] = make_float2(0.f, -1.f);
-          else a.col_part[out_index(x)] = 0.f;
+          for (int i = 0; i < MT; ++i) {
+            if (PASS == 1) a.row_part[out_index(x, i)] = make_float2(0.f, -1.f);
+            else a.col_part[out_index(x, i)] = 0.f;
+          }
         }
         f = end;
       }
     }
-  } else if (PASS == 1 && warp < kLoadWarp) {
-    // ================================================================ row pass: B producers, thread = key of the tile
+  } else if (WIDEN && warp < kLoadWarp) {
+    // ================================================================ B producers, thread = key of the tile
     const int n = tid - 32 * kProdWarp;
-    constexpr int NI = D / 16;
-    int4 raw[NI];  // the codes of the whole head dimension, one tile ahead
-    float ks = 0.f;
-    bool real = false, ok = true;
-    const int8_t* src = nullptr;
-    auto fetch = [&](const Walk& x) {
-      const int t = 128 * x.b + n;
-      const long long ph = key_ph(a, x.kvh, t);
-      real = ph >= 0;
-      src = a.k + (real ? ph : 0) * (D * KVQ_BLOCK_SIZE) + (t % KVQ_BLOCK_SIZE) * 16;
-      ks = real ? __ldg(a.k_scale + ph * KVQ_BLOCK_SIZE + t % KVQ_BLOCK_SIZE) : 0.f;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        raw[i] = make_int4(0, 0, 0, 0);
-        if (real) raw[i] = __ldg(reinterpret_cast<const int4*>(src + i * 256));
-      }
+    constexpr int NI = D / 16;   // 16-byte words of a key
+    uint4 raw[8];                // eight words ahead, across tiles
+    bool ok = true;
+    struct Key {
+      long long ph;
+      const int8_t* src;
     };
-    fetch(w);
+    auto key_at = [&](const Walk& x) {
+      Key k;
+      const int t = 128 * x.b + n;
+      k.ph = key_ph(a, x.kvh, t);
+      k.src = a.k + (k.ph < 0 ? 0 : k.ph) * (D * KVQ_BLOCK_SIZE) + (t % KVQ_BLOCK_SIZE) * 16;
+      return k;
+    };
+    auto fetch = [&](const Key& k, int i) {
+      return k.ph < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(k.src + i * 256));
+    };
+    Key now = key_at(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = fetch(now, i);
     for (int f = 0; f < n_tiles; ++f) {
       const int pb = f % kParBufs, s = f % ST;
+      step<1>(a, w);
+      const bool more = f + 1 < n_tiles;
+      Key next{-1, a.k};
+      if (more) next = key_at(w);
+      const float ks = now.ph < 0 ? 0.f : __ldg(a.k_scale + now.ph * KVQ_BLOCK_SIZE + n % KVQ_BLOCK_SIZE) * a.c2;
       if (f >= kParBufs) ok = wait_warp(L::parFree + pb, f / kParBufs - 1);
       if (ok && f >= ST) ok = wait_warp(L::empty + s, f / ST - 1);
       if (!ok) break;
-      par[(pb * 2 + 0) * 128 + n] = ks;
-      const uint32_t bits = __ballot_sync(0xffffffffu, real);
-      if (lane == 0) valid[pb * 4 + (n >> 5)] = bits;
-      arrive_warp(L::parFull + pb);
       uint8_t* tile = sm + s * L::kTileBytes;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        uint4 c0, c1;
-        widen16(raw[i], c0, c1);
+        uint32_t h[8];
+        widen16_bf16(raw[i & 7], h);
+        raw[i & 7] = i + 8 < NI ? fetch(now, i + 8) : fetch(next, i + 8 - NI);
         uint8_t* piece = tile + (i >> 2) * kPieceBytes;
-        sts128(piece + tc::sw128_off(n, 2 * (i & 3)), c0);
-        sts128(piece + tc::sw128_off(n, 2 * (i & 3) + 1), c1);
+        sts128(piece + tc::sw128_off(n, 2 * (i & 3)), make_uint4(h[0], h[1], h[2], h[3]));
+        sts128(piece + tc::sw128_off(n, 2 * (i & 3) + 1), make_uint4(h[4], h[5], h[6], h[7]));
       }
       // test-only fault injection: CTA 0's first tile is never announced
       if (!(a.fault == 4 && blockIdx.x == 0 && f == 0)) arrive_warp(L::full + s);
-      step<1>(a, w);
-      if (f + 1 < n_tiles) fetch(w);
+      par[(pb * 2 + 0) * 128 + n] = ks;
+      const uint32_t bits = __ballot_sync(0xffffffffu, now.ph >= 0);
+      if (lane == 0) valid[pb * 4 + (n >> 5)] = bits;
+      arrive_warp(L::parFull + pb);
+      now = next;
     }
-  } else if (PASS == 2 && warp == kProdWarp) {
-    // ================================================================ column pass: bulk copies (one lane)
+  } else if (!WIDEN && warp == kProdWarp) {
+    // ================================================================ bulk copies (one lane)
     if (lane == 0) {
       int f = 0;
+      const bool skip_one = PASS == 1 && a.fault == 4 && blockIdx.x == 0;  // test-only: the first tile is not copied
       for (; f < n_tiles; ++f) {
         const int pb = f % kParBufs, s = f % ST;
         if (f >= kParBufs && !wait(L::parFree + pb, f / kParBufs - 1)) break;
         if (f >= ST && !wait(L::empty + s, f / ST - 1)) break;
-        const long long u = static_cast<long long>(w.kvh) * a.row_tiles + b_first<2>(a, w.t) + w.b;
-        mbar_arrive_expect_tx(&bars[L::parFull + pb], 1024);
-        bulk_g2s(par + (pb * 2 + 0) * 128, a.row_nm + u * 128, 512, &bars[L::parFull + pb]);
-        bulk_g2s(par + (pb * 2 + 1) * 128, a.row_il + u * 128, 512, &bars[L::parFull + pb]);
-        mbar_arrive_expect_tx(&bars[L::full + s], L::kTileBytes);
-        bulk_g2s(sm + s * L::kTileBytes, a.q_tiles + u * L::kTileBytes, L::kTileBytes, &bars[L::full + s]);
-        step<2>(a, w);
+        if (PASS == 1) {
+          const long long u = static_cast<long long>(w.kvh) * a.key_tiles + w.b;
+          mbar_arrive_expect_tx(&bars[L::parFull + pb], 512 + 16);
+          bulk_g2s(par + (pb * 2 + 0) * 128, a.k_par + u * 128, 512, &bars[L::parFull + pb]);
+          bulk_g2s(valid + pb * 4, a.k_valid + u * 4, 16, &bars[L::parFull + pb]);
+          if (!(skip_one && f == 0)) {
+            mbar_arrive_expect_tx(&bars[L::full + s], L::kTileBytes);
+            bulk_g2s(sm + s * L::kTileBytes, a.k_tiles + u * L::kTileBytes, L::kTileBytes, &bars[L::full + s]);
+          }
+        } else {
+          const long long u = static_cast<long long>(w.kvh) * a.row_tiles + b_first<2>(a, w.t) + w.b;
+          mbar_arrive_expect_tx(&bars[L::parFull + pb], 1024);
+          bulk_g2s(par + (pb * 2 + 0) * 128, a.row_nm + u * 128, 512, &bars[L::parFull + pb]);
+          bulk_g2s(par + (pb * 2 + 1) * 128, a.row_il + u * 128, 512, &bars[L::parFull + pb]);
+          mbar_arrive_expect_tx(&bars[L::full + s], L::kTileBytes);
+          bulk_g2s(sm + s * L::kTileBytes, a.q_tiles + u * L::kTileBytes, L::kTileBytes, &bars[L::full + s]);
+        }
+        step<PASS>(a, w);
       }
       // copies still in flight (after an abort) land before the CTA exits
-      for (int g = max(0, f - ST); g < f; ++g) mbar_wait(&bars[L::full + g % ST], (g / ST) & 1, a.status, a.wait_budget);
+      for (int g = max(0, f - ST); g < f; ++g)
+        if (!(skip_one && g == 0)) mbar_wait(&bars[L::full + g % ST], (g / ST) & 1, a.status, a.wait_budget);
       for (int g = max(0, f - kParBufs); g < f; ++g)
         mbar_wait(&bars[L::parFull + g % kParBufs], (g / kParBufs) & 1, a.status, a.wait_budget);
     }
@@ -453,91 +525,93 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT>::kThreads, 1) chunk_weights_ke
     // ================================================================ A loaders: thread = row n of each A tile
     const int n = tid - 32 * kLoadWarp;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    constexpr int kAhead = 8;  // 16-byte words in flight
     bool ok = true;
+    long long ph = PASS == 2 ? key_ph(a, w.kvh, L::kRows * w.t + n) : 0;  // column pass: the next A tile's key
     for (int f = 0, at = 0; ok && f < n_tiles; ++at) {
       const int ab = at % L::kABufs;
+      Walk nw = w;  // the next A unit of the run
+      nw.b = nw.n - 1;
+      step<PASS>(a, nw);
+      const bool more = f + (w.n - w.b) < n_tiles;
 #pragma unroll 1
       for (int i = 0; ok && i < MT; ++i) {
         const uint32_t tm_a = tmem + lane_base + (ab * MT + i) * L::kACols;
-        float cst = 0.f;
         const int r = L::kRows * w.t + 128 * i + n;
+        auto slot_free = [&] {  // the MMAs of the unit that held this buffer are done
+          if (i == 0 && at >= L::kABufs) ok = wait_warp(L::aFree + ab, at / L::kABufs - 1);
+          if (ok) tc::fence_after_sync();
+          return ok;
+        };
         if (PASS == 1) {
           const bool real = r < a.n_rows;
           const int q = r / a.group;
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(a.q) +
               (real ? (static_cast<long long>(q) * a.n_q_heads + w.kvh * a.group + (r - q * a.group)) * D : 0));
-          // the row's largest magnitude; on the way the run that begins the A unit lays the row out for the
-          // column pass
+          // the run that begins the A unit also lays the row out for the column pass
           const int tile = MT * w.t + i;
           uint8_t* image = w.b == 0 && tile < a.row_tiles
                                ? a.q_tiles + (static_cast<long long>(w.kvh) * a.row_tiles + tile) * L::kTileBytes
                                : nullptr;
-          float amax = 0.f;
-#pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              amax = fmax3(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
-            if (image) sts128(image + (c >> 3) * kPieceBytes + tc::sw128_off(n, c & 7), v);  // a global store
+          for (int p = 0; p < D / 8 / kAhead; ++p) {
+            uint4 v[kAhead];
+            uint32_t h[32];
+#pragma unroll
+            for (int c = 0; c < kAhead; ++c) {
+              v[c] = real ? __ldg(src + kAhead * p + c) : make_uint4(0, 0, 0, 0);
+              h[4 * c] = v[c].x;
+              h[4 * c + 1] = v[c].y;
+              h[4 * c + 2] = v[c].z;
+              h[4 * c + 3] = v[c].w;
+            }
+            if (p == 0 && !slot_free()) break;
+            tc::st_32x32b_x32(tm_a + 32 * p, h);
+            if (image) {
+#pragma unroll
+              for (int c = 0; c < kAhead; ++c) sts128(image + p * kPieceBytes + tc::sw128_off(n, c), v[c]);  // global stores
+            }
           }
-          float to_f16, back;
-          pow2_scales(amax, to_f16, back);
-          cst = real ? back * a.c2 : 0.f;
-          if (i == 0 && at >= L::kABufs) ok = wait_warp(L::aFree + ab, at / L::kABufs - 1);
           if (!ok) break;
-          tc::fence_after_sync();
+        } else {
+          const long long cur = ph;
+          const uint4* src = reinterpret_cast<const uint4*>(a.k + (cur < 0 ? 0 : cur) * (D * KVQ_BLOCK_SIZE) +
+                                                            (r % KVQ_BLOCK_SIZE) * 16);
+          const float ks = cur < 0 ? 0.f : __ldg(a.k_scale + cur * KVQ_BLOCK_SIZE + r % KVQ_BLOCK_SIZE);
+          uint4 raw[kAhead];
+#pragma unroll
+          for (int c = 0; c < kAhead; ++c) raw[c] = cur < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + c * 16);
+          // the page of the A tile after this one
+          if (i + 1 < MT) ph = key_ph(a, w.kvh, r + 128);
+          else if (more) ph = key_ph(a, nw.kvh, L::kRows * nw.t + n);
+          if (!slot_free()) break;
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             uint32_t h[32];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 v = real ? __ldg(src + 8 * p + c) : make_uint4(0, 0, 0, 0);
-              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                h[4 * c + e] = pack_half2(__uint_as_float(x[e] << 16) * to_f16, __uint_as_float(x[e] & 0xFFFF0000u) * to_f16);
+            for (int c = 0; c < 4; ++c) {
+              const int x = 4 * p + c;
+              widen16_bf16(raw[x % kAhead], h + 8 * c);
+              if (x + kAhead < D / 16) raw[x % kAhead] = cur < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + (x + kAhead) * 16);
             }
             tc::st_32x32b_x32(tm_a + 32 * p, h);
           }
-        } else {
-          constexpr int NI = D / 16;
-          const long long ph = key_ph(a, w.kvh, r);
-          const uint4* src = reinterpret_cast<const uint4*>(a.k + (ph < 0 ? 0 : ph) * (D * KVQ_BLOCK_SIZE) +
-                                                            (r % KVQ_BLOCK_SIZE) * 16);
-          uint4 raw[NI];
-#pragma unroll
-          for (int c = 0; c < NI; ++c) raw[c] = ph < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + c * 16);
-          cst = ph < 0 ? 0.f : __ldg(a.k_scale + ph * KVQ_BLOCK_SIZE + r % KVQ_BLOCK_SIZE) * a.c2;
-          if (i == 0 && at >= L::kABufs) ok = wait_warp(L::aFree + ab, at / L::kABufs - 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            uint32_t h[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) widen16_bf16(raw[4 * p + c], h + 8 * c);
-            tc::st_32x32b_x32(tm_a + 32 * p, h);
-          }
+          consts[(at % kConstBufs) * L::kRows + 128 * i + n] = ks * a.c2;
         }
-        consts[(at % kConstBufs) * L::kRows + 128 * i + n] = cst;
       }
       if (!ok) break;
       tc::wait_st();
       tc::fence_before_sync();
       arrive_warp(L::aFull + ab);
-      arrive_warp(L::constFull + at % kConstBufs);
-      // the next A unit of the run
+      if (PASS == 2) arrive_warp(L::constFull + at % kConstBufs);
       f += w.n - w.b;
-      w.b = w.n - 1;
-      step<PASS>(a, w);
+      w = nw;
     }
   } else if (warp == L::kMmaWarp) {
     // ================================================================ MMA issue
     const uint64_t rd0 = tc::sdesc_sw128(smem_u32(sm));
-    constexpr uint32_t idesc = PASS == 1 ? tc::idesc_f16_f32(128, 128) : tc::idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(128, 128);
     bool ok = true;
     int at = -1;
     for (int f = 0; ok && f < n_tiles; ++f) {
@@ -551,13 +625,13 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT>::kThreads, 1) chunk_weights_ke
       const uint64_t bd0 = rd0 + static_cast<uint64_t>((s * L::kTileBytes) >> 4);
 #pragma unroll 1
       for (int i = 0; ok && i < MT; ++i) {
-        const int g = MT * f + i, sg = g & 1;  // score tile g belongs to softmax group g % 2
-        if (g >= 2) ok = wait_warp(L::sFree + sg, g / 2 - 1);
+        const int g = MT * f + i, sg = g & 1;
+        if (g >= 2) ok = wait_warp(L::sFree + sg, (g >> 1) - 1);
         if (!ok) break;
         if (elect_one()) {
           // The producers' stores come before the tensor core's reads.  The fence is taken here, on the thread that
           // has acquired them, and not by the producers: there it would wait for every load they have in flight.
-          if (PASS == 1 && i == 0) tc::fence_proxy_async_smem();
+          if (WIDEN && i == 0) tc::fence_proxy_async_smem();
           tc::fence_after_sync();
           const uint32_t tm_a = tmem + ((at % L::kABufs) * MT + i) * L::kACols, tm_s = tmem + L::kSCol + 128 * sg;
 #pragma unroll
@@ -606,39 +680,49 @@ __device__ int segments_of(const ChunkWeightsArgs& a, int kvh, int t) {
   return run_of(f + b_count<PASS>(a, t) - 1, total, runs) - run_of(f, total, runs) + 1;
 }
 
-// Row statistics of the column pass: -M and 1 / l from the parts of the row pass.
+// Row statistics of the column pass: minus the reference and 1 / l, from the parts of the row pass.  A CTA
+// takes 32 rows, a lane each; warp w takes parts w, w + 4, .. (a row cut over a whole GPU has dozens).
 __global__ void __launch_bounds__(128) chunk_rows_kernel(ChunkWeightsArgs a) {
-  const int t = blockIdx.x, kvh = blockIdx.y, n = threadIdx.x;
+  __shared__ float2 part_s[4][32];
+  const int t = blockIdx.x / 4, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = (blockIdx.x % 4) * 32 + lane;
   const int mt = a.a_rows[0] / 128;
-  const int parts = segments_of<1>(a, kvh, t / mt) * (mt == 2 ? 1 : 2);
+  const int parts = 4 * segments_of<1>(a, kvh, t / mt);  // four column quarters a run
   grid_dep_wait();
   const float2* p = a.row_part + (static_cast<long long>(kvh) * a.units[0] * mt + t) * a.n_part[0] * 128 + n;
-  float m = -INFINITY;
-  bool dropped = false;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const float2 v = p[i * 128];
-    m = fmaxf(m, v.x);
-    dropped |= v.y < 0.f;
+  // (m, l) of several (m, l): the largest m, the sums moved onto it; a sum below zero marks a dropped part
+  float m = -INFINITY, l = 0.f;
+  auto merge = [&](const float2& v) {
+    if (v.y < 0.f || l < 0.f) {
+      l = -1.f;
+    } else if (v.x != -INFINITY) {
+      const float x = fmaxf(m, v.x);
+      l = (m == -INFINITY ? 0.f : l * fast_exp2(m - x)) + v.y * fast_exp2(v.x - x);
+      m = x;
+    }
+  };
+  for (int i0 = warp; i0 < parts; i0 += 32) {
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i0 + 4 * i < parts ? p[(i0 + 4 * i) * 128] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) merge(v[i]);
   }
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const float2 v = p[i * 128];
-    if (v.x != -INFINITY) l += v.y * fast_exp2(v.x - ref);
-  }
+  part_s[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  if (warp != 0) return;
+  for (int i = 1; i < 4; ++i) merge(part_s[i][lane]);
   // a row with no key (or without its sum) gives no weight
-  const long long u = static_cast<long long>(kvh) * a.row_tiles + t;
-  a.row_nm[u * 128 + n] = -ref;
-  a.row_il[u * 128 + n] = dropped || l == 0.f ? 0.f : __fdiv_rn(1.0f, l);
+  const long long r = (static_cast<long long>(kvh) * a.row_tiles + t) * 128 + n;
+  a.row_nm[r] = m == -INFINITY ? 0.f : -m;
+  a.row_il[r] = l < 0.f || l == 0.f ? 0.f : __fdiv_rn(1.0f, l);
 }
 
 // acc += the parts of the column pass, in the order of the line.
 __global__ void __launch_bounds__(128) chunk_acc_kernel(ChunkWeightsArgs a) {
   const int t = blockIdx.x, kvh = blockIdx.y, n = threadIdx.x;
   const int mt = a.a_rows[1] / 128;
-  const int parts = segments_of<2>(a, kvh, t / mt) * (mt == 2 ? 1 : 2);
+  const int parts = 4 * segments_of<2>(a, kvh, t / mt);
   grid_dep_wait();
   const int key = 128 * t + n;
   if (key >= a.n_keys) return;
@@ -683,9 +767,8 @@ ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads,
     // an A unit of n pairs lies in at most ceil(n / floor(total / runs)) + 1 runs, and in no more than there are
     const long long shortest = total / p.runs[i];
     const long long seg = std::min<long long>(p.runs[i], (most[i] + shortest - 1) / shortest + 1);
-    const int mt = p.a_rows[i] / 128;
-    p.n_part[i] = static_cast<int>(mt == 2 ? seg : 2 * seg);
-    part[i] = static_cast<long long>(n_kv_heads) * p.units[i] * mt * p.n_part[i] * 128;
+    p.n_part[i] = static_cast<int>(4 * seg);
+    part[i] = static_cast<long long>(n_kv_heads) * p.units[i] * p.a_rows[i] * p.n_part[i];
   }
   auto round = [](long long x) { return (x + 255) / 256 * 256; };
   const long long row_n = static_cast<long long>(n_kv_heads) * p.row_tiles * 128;
@@ -694,13 +777,21 @@ ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads,
   p.off_q = p.off_il + round(row_n * 4);
   p.off_col = p.off_q + row_n * head_dim * 2;
   p.bytes = p.off_col + part[1] * 4;
+  p.widen_once = p.units[0] >= 8;
+  if (p.widen_once) {
+    const long long key_n = static_cast<long long>(n_kv_heads) * p.key_tiles * 128;
+    p.off_k = round(p.bytes);
+    p.off_kpar = p.off_k + key_n * head_dim * 2;
+    p.off_kvalid = p.off_kpar + key_n * 4;
+    p.bytes = p.off_kvalid + key_n / 8;
+  }
   return p;
 }
 
-template <int D, int PASS, int MT>
+template <int D, int PASS, int MT, bool WIDEN>
 static cudaError_t launch_pass(const ChunkWeightsArgs& a, cudaStream_t stream) {
-  using L = Cw<D, PASS, MT>;
-  auto kern = chunk_weights_kernel<D, PASS, MT>;
+  using L = Cw<D, PASS, MT, WIDEN>;
+  auto kern = chunk_weights_kernel<D, PASS, MT, WIDEN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(a.runs[PASS - 1]), dim3(L::kThreads), L::kAlloc, stream, a);
@@ -708,10 +799,16 @@ static cudaError_t launch_pass(const ChunkWeightsArgs& a, cudaStream_t stream) {
 
 template <int D>
 static cudaError_t launch_chunk_weights_d(const ChunkWeightsArgs& a, cudaStream_t stream) {
-  cudaError_t e = a.a_rows[0] == 256 ? launch_pass<D, 1, 2>(a, stream) : launch_pass<D, 1, 1>(a, stream);
+  cudaError_t e;
+  if (a.k_tiles) {
+    e = launch_pdl(chunk_widen_kernel<D>, dim3(a.key_tiles, a.n_kv_heads), dim3(256), 0, stream, a);
+    if (e == cudaSuccess) e = launch_pass<D, 1, 2, false>(a, stream);
+  } else {
+    e = a.a_rows[0] == 256 ? launch_pass<D, 1, 2, true>(a, stream) : launch_pass<D, 1, 1, true>(a, stream);
+  }
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(chunk_rows_kernel, dim3(a.row_tiles, a.n_kv_heads), dim3(128), 0, stream, a)) != cudaSuccess) return e;
-  e = a.a_rows[1] == 256 ? launch_pass<D, 2, 2>(a, stream) : launch_pass<D, 2, 1>(a, stream);
+  if ((e = launch_pdl(chunk_rows_kernel, dim3(4 * a.row_tiles, a.n_kv_heads), dim3(128), 0, stream, a)) != cudaSuccess) return e;
+  e = a.a_rows[1] == 256 ? launch_pass<D, 2, 2, false>(a, stream) : launch_pass<D, 2, 1, false>(a, stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(chunk_acc_kernel, dim3(a.key_tiles, a.n_kv_heads), dim3(128), 0, stream, a);
 }

@@ -116,7 +116,8 @@ struct ChunkWeightsPlan {
   int a_rows[2], units[2];    // rows of an A unit (128 or 256), A units of a KV head
   long long line[2];          // (A unit, B tile) pairs of one KV head
   int runs[2], n_part[2];     // CTAs, and the most parts one 128-row A tile is cut into
-  long long off_nm, off_il, off_q, off_col, bytes;
+  bool widen_once;            // the key tiles are widened by a pass of their own
+  long long off_nm, off_il, off_q, off_col, off_k, off_kpar, off_kvalid, bytes;
 };
 ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads, int history_len, int head_dim,
                                     int n_sms);
@@ -139,6 +140,10 @@ struct ChunkWeightsArgs {
   float* row_il;     // workspace: 1 / the row's sum, 0 for a row that gives nothing
   uint8_t* q_tiles;  // workspace [Hkv * row_tiles][D / 64 pieces of 16 KB]: the queries, bf16, in tile order
   float* col_part;   // workspace [Hkv][A tiles][n_part[1]][128]
+  // workspace, when the key tiles are widened once (else nullptr): bf16 in tile order, score factors, key bits
+  uint8_t* k_tiles;   // [Hkv * key_tiles][D / 64 pieces of 16 KB]
+  float* k_par;       // [Hkv * key_tiles][128]
+  uint32_t* k_valid;  // [Hkv * key_tiles][4]
   unsigned int* status;
   long long wait_budget;
   int fault;

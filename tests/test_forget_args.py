@@ -73,16 +73,16 @@ def test_chunk_weights_refusals(L, status, kw):
 
 
 def test_chunk_weights_workspace():
-    # 10 queries x 6 heads: one row tile and one key tile per KV head, up to two runs of two groups each; the
-    # row statistics; the queries in bf16
+    # 10 queries x 6 heads: one row tile and one key tile per KV head, up to two runs of four column quarters
+    # each; the row statistics; the queries in bf16
     rows = 4 * 128
-    assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, 20, 256) == rows * 4 * 8 + 2 * rows * 4 + rows * 256 * 2 + rows * 4 * 4
+    assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, 20, 256) == rows * 8 * 8 + 2 * rows * 4 + rows * 256 * 2 + rows * 8 * 4
     assert k.kvq_chunk_weights_workspace_bytes(0, 24, 4, 20, 256) == 0
     assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, -1, 256) == 0
     assert k.kvq_chunk_weights_workspace_bytes(10, 23, 4, 20, 256) == 0
     assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, 20, 192) == 0
-    # no scores: the queries once more and little else, where the scores would be 6.4 GB
-    assert k.kvq_chunk_weights_workspace_bytes(2048, 24, 4, 30720, 256) < 2048 * 24 * 256 * 2 + (16 << 20)
+    # no scores: the queries and the keys in bf16 and little else, where the scores would be 6.4 GB
+    assert k.kvq_chunk_weights_workspace_bytes(2048, 24, 4, 30720, 256) < (2048 * 24 + 32768 * 4) * 256 * 2 + (16 << 20)
 
 
 def evict(L, c=None, batch=2, bt=A, mb=8, ctx=A, max_ctx=100, keep=64, sink=0, recent=0, acc=A, sp=A + 1024, stride=128,
