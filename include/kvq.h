@@ -358,8 +358,8 @@ int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, cons
 
 /* Workspace (bytes) of kvq_attn_chunk_weights_int8kv: the queries in the tensor core's tile order (2 bytes
  * an element), per (KV head, query, head of its group) the row's maximum and sum and their parts, per
- * (KV head, key) the parts of its weight, and for a chunk of at least eight row pairs (1793 (query, head)
- * rows a KV head) the keys widened to bf16 (2 * head_dim bytes per key and KV head).  No score is kept.
+ * (KV head, key) the parts of its weight, and for a chunk of more than 896 such rows the
+ * keys widened to bf16 (2 * head_dim bytes per key and KV head).  No score is kept.
  * It does not depend on the GPU.  0 if an argument is not positive (history_len may be 0), n_q_heads is
  * no multiple of n_kv_heads, head_dim is not 128 / 256, or the sizes are past 2^30 (below). */
 size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,

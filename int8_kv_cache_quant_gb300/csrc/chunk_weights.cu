@@ -16,24 +16,30 @@
 //
 // Operands.  sm_103a has no integer tcgen05 kind, and the codes are exact in bf16 (|code| < 2^8), so both
 // passes take the bf16 queries as they are and widen the codes to bf16: every product is exact and the
-// sums are fp32.  The key tiles of the row pass come in one of two ways: widened by producer warps, from
-// global memory through registers into the swizzled shared-memory tile (WIDEN; the codes are read as
-// bytes and no copy of K is written), or, when many row tiles read them, widened once by a pass of
-// their own into a workspace from which a tile is one bulk copy.  The queries are laid out in the same
-// tile order by the row pass, on its way through them, so that the column pass brings them in by bulk
-// copies too.
+// sums are fp32.  A pass before them lays the queries out in the swizzled order of an operand tile, so
+// that a tile is one bulk copy; when there are eight row tiles or more to read them, it does the same
+// with the widened keys.  With fewer row tiles (WIDEN) that copy would be most of the call's traffic:
+// then the pages come into a ring of their own as bytes, by bulk copies, and warps of the CTA widen them
+// from there, into the B tile (row pass) or into tensor memory (column pass).
 //
 // Schedule.  One CTA per SM; the (A unit, B tile) pairs of all KV heads are one line, cut into equal
 // runs, one per CTA, so that causal and ragged shapes balance to a tile.  An A unit is one 128-row tile
 // (MT = 1) or two of them (MT = 2), which share every B tile: a 128 x 128 tile pair at head_dim 256
 // takes 1024 cycles of the tensor core, in which one SM would have to take in 64 KB, more than all SMs
-// together get out of L2; with two A tiles it is half of that.  An A unit that two CTAs share leaves
-// one partial each, and the partials are added in the order of the line: the same result every time.
-// Roles of a CTA's warps:
+// together get out of L2; with two A tiles it is half of that.  With few row tiles the column pass keeps
+// all of them in shared memory instead.  An A unit that two CTAs share leaves one partial each, and the
+// partials are added in the order of the line: the same result every time.  Roles of a CTA's warps:
 //   warps 0-15   softmax: thread = tensor-memory lane 32 (w % 4) + lane, columns 32 (w / 4) .. of every
 //                128 x 128 score tile; four warps a scheduler hide each other's latencies
-//   WIDEN        warps 16-19 B producers (128 threads), 20-23 A loaders (128 threads), 24 MMA issue
-//   else         warp 16 bulk copies (one lane), 17 MMA issue, 20-23 A loaders
+//   warps 16-19  WIDEN row pass: B producers (128 threads); else warp 16 copies tiles, 17 issues the MMAs,
+//                18 copies pages (WIDEN)
+//   warps 20-23  A loaders (128 threads): an A tile from shared memory to tensor memory
+//   warps 24-25  WIDEN row pass: MMA issue, page copies
+// Shared memory: a ring of tiles | WIDEN: a ring of pages.  A tiles take their turn before the first B tile of
+// their unit in the ring of tiles, or (WIDEN row pass) as halves in the ring of pages; the WIDEN column
+// pass's A tiles are the pages.  A wait on a barrier tells a phase only from the one before it, so every
+// role that waits on a barrier visits all its phases in order: each ring is filled by one role, and A tiles
+// that share a ring announce themselves on barriers of their own.
 // Tensor memory: A tiles (head_dim / 2 columns each) | two score tiles, filled in turn.
 //
 // What bounds it: at head_dim 256 the tensor core (1024 cycles a 128 x 128 tile at 4096 multiply-adds a
@@ -65,28 +71,53 @@ constexpr float kSumLimit = 1.8446744e19f;  // 2^64
 
 template <int D, int PASS, int MT, bool WIDEN>
 struct Cw {
-  static constexpr int kThreads = WIDEN ? 25 * 32 : 24 * 32;
-  static constexpr int kMmaWarp = WIDEN ? 24 : 17;
+  static constexpr bool kProduce = PASS == 1 && WIDEN;     // B tiles made by producer warps
+  static constexpr bool kARing = !WIDEN;                   // A tiles come through the ring of tiles
+  static constexpr int kThreads = kProduce ? 26 * 32 : 24 * 32;
+  static constexpr int kMmaWarp = kProduce ? 24 : 17, kPageWarp = kProduce ? 25 : 18, kTileWarp = 16;
   static constexpr int kRows = 128 * MT;                   // rows of an A unit
-  static constexpr int kTileBytes = D * 256;               // one B tile: 128 rows x D 16-bit values
-  static constexpr int kStages = 196608 / kTileBytes;      // 3 at head_dim 256, 6 at 128
+  static constexpr int kTileBytes = D * 256;               // one tile: 128 rows x D 16-bit values
+  static constexpr int kStages = (WIDEN ? 131072 : 196608) / kTileBytes;  // tiles in the ring
+  static constexpr int kPageBytes = 8 * (D * KVQ_BLOCK_SIZE + 64);        // a key tile's codes, then its scales
+  static constexpr int kPages = WIDEN ? 65536 / (D * 128) : 1;            // key tiles in the ring of pages
   static constexpr uint32_t kACols = D / 2;                // tensor-memory columns of an A tile
   static constexpr uint32_t kSCol = 256;                   // score tiles at 256 and 384
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kABufs = MT * 2 * kACols <= kSCol ? 2 : 1;  // A units held at a time
-  static constexpr int offPar = kStages * kTileBytes;      // [buf][2][128] fp32
+  static constexpr int offPages = kStages * kTileBytes;
+  static constexpr int offPar = offPages + (WIDEN ? kPages * kPageBytes : 0);  // [buf][2][128] fp32
   static constexpr int offConst = offPar + kParBufs * 2 * 128 * 4;
   static constexpr int offValid = offConst + kConstBufs * kRows * 4;  // [buf][4] key bits
-  static constexpr int offBar = offValid + kParBufs * 16;
-  static constexpr int kNumBars = 2 * kStages + 4 + 2 * kParBufs + 4 + kConstBufs + 1;
+  static constexpr int offPageOk = offValid + kParBufs * 16;          // [page ring] bits of the pages that exist
+  // phase of the last bulk copy into each tile, parameter buffer and page slot, -1: none
+  static constexpr int offLast = offPageOk + 16;
+  // Copies of an A unit (kARing, kProduce), a barrier each; four sets of them, since a slow loader warp may be
+  // waiting for a unit when the copies of the second one after it have landed.
+  static constexpr int kAParts = kProduce ? 2 * MT : MT;
+  static constexpr int kASets = 4;
+  static constexpr int kLasts = kStages + kParBufs + kPages + kAParts;
+  static constexpr int offBar = offLast + 20 * 4;
+  static constexpr int kNumBars = 2 * kStages + 4 + 2 * kParBufs + 4 + kConstBufs + 2 * kPages + kASets * kAParts + 1;
+  static_assert(offBar % 8 == 0, "barriers");
   static constexpr int offFlag = offBar + kNumBars * 8;    // abort flag, TMEM base
   static constexpr int kAlloc = offFlag + 16 + 1024;
   static_assert(MT * kABufs * kACols <= kSCol && kSCol + 256 <= kTmemCols, "tensor memory");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  // barriers: B stages, score tiles, column parameters, A units, key constants
+  static_assert(kPages <= 4 && kLasts <= 20, "page bits, last copies");
+  static_assert(!kProduce || kTileBytes / 2 <= kPageBytes, "half an A tile fits in a page slot");
+  // barriers: tiles, score tiles, column parameters, A units, key constants, pages
   static constexpr int full = 0, empty = full + kStages, sFull = empty + kStages, sFree = sFull + 2, parFull = sFree + 2,
                        parFree = parFull + kParBufs, aFull = parFree + kParBufs, aFree = aFull + 2, constFull = aFree + 2,
-                       drain = constFull + kConstBufs;
+                       pageFull = constFull + kConstBufs, pageFree = pageFull + kPages, aTile = pageFree + kPages, drain = aTile + kASets * kAParts;
+  // Place in the ring of tiles of B tile f of the run, in its at-th A unit; the unit's A tile i (kARing) comes
+  // MT - i places before its first B tile.
+  __device__ static int entry(int f, int at) { return f + (kARing ? MT * (at + 1) : 0); }
+  // barrier and phase of copy i of the at-th A unit
+  __device__ static int a_tile(int at, int i) { return aTile + (at % kASets) * kAParts + i; }
+  __device__ static int a_phase(int at) { return at / kASets; }
+  // WIDEN row pass: place in the ring of pages of the key tile of B tile f; half h of the unit's A tile i comes
+  // 2 (MT - i) - h places before its first key tile.
+  __device__ static int page_entry(int f, int at) { return f + (kProduce ? 2 * MT * (at + 1) : 0); }
 };
 
 // B tiles of A unit t, and the first of them.
@@ -182,20 +213,36 @@ __device__ __forceinline__ long long key_ph(const ChunkWeightsArgs& a, int kvh, 
 
 }  // namespace
 
-// The key tiles widened once: (key tile, KV head) to the bf16 operand tile, the keys' score factors and
-// which of them exist.  Four adjacent lanes fill one 128-byte row of a piece.
+// Operand tiles: blocks x < row_tiles lay 128 query rows of a KV head out (a row is G heads of a query in
+// turn), the blocks after them widen 128 keys and leave their score factors and which of them exist.
 template <int D>
-__global__ void __launch_bounds__(256) chunk_widen_kernel(ChunkWeightsArgs a) {
-  const int j = blockIdx.x, kvh = blockIdx.y, tid = threadIdx.x;
+__global__ void __launch_bounds__(256) chunk_tiles_kernel(ChunkWeightsArgs a) {
+  const int kvh = blockIdx.y, tid = threadIdx.x;
   __shared__ long long ph_s[8];
   grid_dep_wait();
+  if (static_cast<int>(blockIdx.x) < a.row_tiles) {
+    const int t = blockIdx.x;
+    uint8_t* tile = a.q_tiles + (static_cast<long long>(kvh) * a.row_tiles + t) * (D * 256);
+    constexpr int W = D / 8;  // 16-byte words of a row
+#pragma unroll 8
+    for (int x = 0; x < W / 2; ++x) {
+      const int i = tid + 256 * x, n = i / W, c = i % W, r = 128 * t + n, q = r / a.group;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < a.n_rows)
+        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                 (static_cast<long long>(q) * a.n_q_heads + kvh * a.group + (r - q * a.group)) * D) + c);
+      sts128(tile + (c >> 3) * kPieceBytes + tc::sw128_off(n, c & 7), v);  // a global store
+    }
+    return;
+  }
+  const int j = blockIdx.x - a.row_tiles;
   if (tid < 8) ph_s[tid] = key_ph(a, kvh, 128 * j + KVQ_BLOCK_SIZE * tid);
   __syncthreads();
   const long long u = static_cast<long long>(kvh) * a.key_tiles + j;
   uint8_t* tile = a.k_tiles + u * (D * 256);
   uint4 raw[D / 32];
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) {
+  for (int x = 0; x < D / 32; ++x) {  // four adjacent lanes fill one 128-byte row of a piece
     const int i = tid + 256 * x, n = (i >> 2) & 127, c16 = ((i >> 9) << 2) | (i & 3);
     const long long ph = ph_s[n >> 4];
     raw[x] = make_uint4(0, 0, 0, 0);
@@ -219,12 +266,10 @@ __global__ void __launch_bounds__(256) chunk_widen_kernel(ChunkWeightsArgs a) {
     const uint32_t bits = __ballot_sync(0xffffffffu, real);
     if ((tid & 31) == 0) a.k_valid[u * 4 + (tid >> 5)] = bits;
   }
-  grid_dep_trigger();
 }
 
 template <int D, int PASS, int MT, bool WIDEN>
 __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_weights_kernel(ChunkWeightsArgs a) {
-  static_assert(PASS == 1 || !WIDEN, "the column pass streams queries");
   using L = Cw<D, PASS, MT, WIDEN>;
   constexpr int NP = D / 64;  // 16 KB pieces of a B tile
   constexpr int ST = L::kStages;
@@ -233,6 +278,8 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
   float* par = reinterpret_cast<float*>(sm + L::offPar);
   float* consts = reinterpret_cast<float*>(sm + L::offConst);
   uint32_t* valid = reinterpret_cast<uint32_t*>(sm + L::offValid);
+  volatile int* last_copy = reinterpret_cast<volatile int*>(sm + L::offLast);
+  volatile uint32_t* page_ok = reinterpret_cast<volatile uint32_t*>(sm + L::offPageOk);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::offBar);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::offFlag);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::offFlag + 4);
@@ -248,8 +295,8 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
   if (tid == 0) {
     // a lane of each warp arrives for its warp: a thread's arrival costs as much as a warp's
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&bars[L::full + s], WIDEN ? 4 : 1);
-      mbar_init(&bars[L::empty + s], 1);
+      mbar_init(&bars[L::full + s], L::kProduce ? 4 : 1);
+      mbar_init(&bars[L::empty + s], 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars[L::sFull + s], 1);
@@ -258,11 +305,17 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
       mbar_init(&bars[L::aFree + s], 1);
     }
     for (int s = 0; s < kParBufs; ++s) {
-      mbar_init(&bars[L::parFull + s], WIDEN ? 4 : 1);
+      mbar_init(&bars[L::parFull + s], L::kProduce ? 4 : 1);
       mbar_init(&bars[L::parFree + s], kSoftWarps);
     }
     for (int s = 0; s < kConstBufs; ++s) mbar_init(&bars[L::constFull + s], 4);
+    for (int s = 0; s < L::kPages; ++s) {
+      mbar_init(&bars[L::pageFull + s], 1);
+      mbar_init(&bars[L::pageFree + s], 4);
+    }
     mbar_init(&bars[L::drain], 1);
+    for (int s = 0; s < L::kASets * L::kAParts; ++s) mbar_init(&bars[L::aTile + s], 1);
+    for (int s = 0; s < L::kLasts; ++s) last_copy[s] = -1;
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -278,6 +331,9 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[bar]);
   };
+  // WIDEN column pass with all row tiles in the ring at once: B tile j stays in stage (and parameter buffer) j
+  // for all A units of a KV head, an epoch
+  const bool resident = PASS == 2 && WIDEN && a.row_tiles <= min(ST, kParBufs);
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
@@ -292,6 +348,7 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
     bool ok = true;
     int at = -1;    // ordinal of the current A unit in this CTA
     int first = 0;  // its first B tile
+    int epoch = 0;
     // per A tile of the unit.  Row pass: reference and sum of the row, its last visible key.  Column pass: the
     // key's sum, its score factor, the first row that sees it.
     float m[MT], l[MT], cst[MT];
@@ -313,8 +370,8 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
           bound[i] = PASS == 1 ? (r < a.n_rows ? a.history_len + r / a.group : -1) : max(0, r - a.history_len) * a.group;
         }
       }
-      const int pb = f % kParBufs;
-      ok = wait_warp(L::parFull + pb, f / kParBufs);
+      const int pb = resident ? first + w.b : f % kParBufs;
+      ok = wait_warp(L::parFull + pb, resident ? epoch : f / kParBufs);
       if (!ok) break;
       const float4* p0 = reinterpret_cast<const float4*>(par + (pb * 2 + 0) * 128 + c0);
       const float4* p1 = reinterpret_cast<const float4*>(par + (pb * 2 + 1) * 128 + c0);
@@ -409,7 +466,7 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
         }
       }
       if (!ok) break;
-      arrive_warp(L::parFree + pb);
+      if (!resident) arrive_warp(L::parFree + pb);
       if (w.b + 1 == w.n || f + 1 == n_tiles) {  // the A unit, or this CTA's part of it, is done
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -418,7 +475,16 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
         }
         slot = 0;
       }
+      const int kvh = w.kvh;
       step<PASS>(a, w);
+      if (resident && (w.kvh != kvh || f + 1 == n_tiles)) {  // every tile of the epoch, seen by a unit or not
+        for (int j = 0; ok && j < a.row_tiles; ++j) {
+          ok = wait_warp(L::parFull + j, epoch);
+          if (ok && w.kvh != kvh) arrive_warp(L::parFree + j);
+        }
+        ++epoch;
+        if (!ok) break;
+      }
     }
     if (!ok) {
       // A wait ran out (KVQ_DEV_TIMEOUT is set): the rows of the A units from here on are marked as having
@@ -436,192 +502,250 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
         f = end;
       }
     }
-  } else if (WIDEN && warp < kLoadWarp) {
-    // ================================================================ B producers, thread = key of the tile
+  } else if (L::kProduce && warp < kLoadWarp) {
+    // ================================================================ B producers: thread = key of the tile
     const int n = tid - 32 * kProdWarp;
-    constexpr int NI = D / 16;   // 16-byte words of a key
-    uint4 raw[8];                // eight words ahead, across tiles
     bool ok = true;
-    struct Key {
-      long long ph;
-      const int8_t* src;
-    };
-    auto key_at = [&](const Walk& x) {
-      Key k;
-      const int t = 128 * x.b + n;
-      k.ph = key_ph(a, x.kvh, t);
-      k.src = a.k + (k.ph < 0 ? 0 : k.ph) * (D * KVQ_BLOCK_SIZE) + (t % KVQ_BLOCK_SIZE) * 16;
-      return k;
-    };
-    auto fetch = [&](const Key& k, int i) {
-      return k.ph < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(k.src + i * 256));
-    };
-    Key now = key_at(w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = fetch(now, i);
+    int at = -1;
+    uint32_t phases = 0;  // per page slot: parity of its next key tile
     for (int f = 0; f < n_tiles; ++f) {
-      const int pb = f % kParBufs, s = f % ST;
-      step<1>(a, w);
-      const bool more = f + 1 < n_tiles;
-      Key next{-1, a.k};
-      if (more) next = key_at(w);
-      const float ks = now.ph < 0 ? 0.f : __ldg(a.k_scale + now.ph * KVQ_BLOCK_SIZE + n % KVQ_BLOCK_SIZE) * a.c2;
-      if (f >= kParBufs) ok = wait_warp(L::parFree + pb, f / kParBufs - 1);
+      if (f == 0 || w.b == 0) ++at;
+      const int pb = f % kParBufs, s = f % ST, x = L::page_entry(f, at), ps = x % L::kPages;
+      ok = wait_warp(L::pageFull + ps, phases >> ps);
+      phases ^= 1u << ps;
+      if (ok && f >= kParBufs) ok = wait_warp(L::parFree + pb, f / kParBufs - 1);
       if (ok && f >= ST) ok = wait_warp(L::empty + s, f / ST - 1);
       if (!ok) break;
+      const uint8_t* page = sm + L::offPages + ps * L::kPageBytes;
+      const uint8_t* src = page + (n >> 4) * (D * KVQ_BLOCK_SIZE) + (n & 15) * 16;
       uint8_t* tile = sm + s * L::kTileBytes;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
+      for (int i = 0; i < D / 16; ++i) {
         uint32_t h[8];
-        widen16_bf16(raw[i & 7], h);
-        raw[i & 7] = i + 8 < NI ? fetch(now, i + 8) : fetch(next, i + 8 - NI);
+        widen16_bf16(*reinterpret_cast<const uint4*>(src + i * 256), h);
         uint8_t* piece = tile + (i >> 2) * kPieceBytes;
         sts128(piece + tc::sw128_off(n, 2 * (i & 3)), make_uint4(h[0], h[1], h[2], h[3]));
         sts128(piece + tc::sw128_off(n, 2 * (i & 3) + 1), make_uint4(h[4], h[5], h[6], h[7]));
       }
+      const bool real = ((page_ok[ps] >> (n >> 4)) & 1u) && 128 * w.b + n < a.n_keys;
+      const float ks = reinterpret_cast<const float*>(page + 8 * D * KVQ_BLOCK_SIZE)[n];
+      tc::fence_proxy_async_smem();  // each writer's stores come before the tensor core's reads
       // test-only fault injection: CTA 0's first tile is never announced
       if (!(a.fault == 4 && blockIdx.x == 0 && f == 0)) arrive_warp(L::full + s);
-      par[(pb * 2 + 0) * 128 + n] = ks;
-      const uint32_t bits = __ballot_sync(0xffffffffu, now.ph >= 0);
+      par[(pb * 2 + 0) * 128 + n] = real ? ks * a.c2 : 0.f;
+      const uint32_t bits = __ballot_sync(0xffffffffu, real);
       if (lane == 0) valid[pb * 4 + (n >> 5)] = bits;
       arrive_warp(L::parFull + pb);
-      now = next;
+      arrive_warp(L::pageFree + ps);
+      step<1>(a, w);
     }
-  } else if (!WIDEN && warp == kProdWarp) {
-    // ================================================================ bulk copies (one lane)
+  } else if (WIDEN && warp == L::kPageWarp) {
+    // ================================================================ page copies: lane = page of the key tile
+    // the key tiles of the run's B tiles (row pass), each unit's A tiles before them, or of its A units (column pass)
+    auto page_at = [&](const Walk& v) {
+      return lane < 8 ? key_ph(a, v.kvh, 128 * (PASS == 1 ? v.b : v.t) + KVQ_BLOCK_SIZE * lane) : -1;
+    };
+    long long ph = page_at(w);
+    bool ok = true;
+    int x = 0, at = -1;   // entries of the ring filled, A unit
+    uint32_t phases = 0;  // per page slot: parity of its next key tile
+    auto slot_free = [&] { return x < L::kPages || wait_warp(L::pageFree + x % L::kPages, x / L::kPages - 1); };
+    for (int f = 0; f < n_tiles;) {
+      if (L::kProduce && (f == 0 || w.b == 0)) {
+        ++at;
+        for (int i = 0; ok && i < 2 * MT; ++i) {
+          ok = slot_free();
+          if (!ok) break;
+          if (lane == 0) {
+            const int ps = x % L::kPages;
+            // the second tile of the last unit may not exist: any tile will do, its rows count for nothing
+            const long long u = static_cast<long long>(w.kvh) * a.row_tiles + min(MT * w.t + i / 2, a.row_tiles - 1);
+            last_copy[ST + kParBufs + L::kPages + i] = at;
+            mbar_arrive_expect_tx(&bars[L::a_tile(at, i)], L::kTileBytes / 2);
+            bulk_g2s(sm + L::offPages + ps * L::kPageBytes, a.q_tiles + u * L::kTileBytes + (i & 1) * (L::kTileBytes / 2),
+                     L::kTileBytes / 2, &bars[L::a_tile(at, i)]);
+          }
+          __syncwarp();
+          ++x;
+        }
+      }
+      ok = ok && slot_free();
+      if (!ok) break;
+      const int ps = x % L::kPages;
+      const uint32_t exist = __ballot_sync(0xffffffffu, ph >= 0);
+      if (lane == 0) {
+        page_ok[ps] = exist;
+        last_copy[ST + kParBufs + ps] = (phases >> ps) & 1u;
+        mbar_arrive_expect_tx(&bars[L::pageFull + ps], __popc(exist) * (D * KVQ_BLOCK_SIZE + 64));
+      }
+      __syncwarp();
+      if (ph >= 0) {  // codes of pages that do not exist are whatever was there: finite once widened, and masked
+        uint8_t* page = sm + L::offPages + ps * L::kPageBytes;
+        bulk_g2s(page + lane * (D * KVQ_BLOCK_SIZE), a.k + ph * (D * KVQ_BLOCK_SIZE), D * KVQ_BLOCK_SIZE, &bars[L::pageFull + ps]);
+        bulk_g2s(page + 8 * D * KVQ_BLOCK_SIZE + lane * 64, a.k_scale + ph * KVQ_BLOCK_SIZE, 64, &bars[L::pageFull + ps]);
+      }
+      phases ^= 1u << ps;
+      ++x;
+      f += PASS == 1 ? 1 : w.n - w.b;
+      if (PASS == 2) w.b = w.n - 1;
+      step<PASS>(a, w);
+      if (f < n_tiles) ph = page_at(w);  // the next tile's pages, while this one's copies run
+    }
+  } else if (!L::kProduce && warp == L::kTileWarp) {
+    // ================================================================ tile copies (one lane)
     if (lane == 0) {
-      int f = 0;
-      const bool skip_one = PASS == 1 && a.fault == 4 && blockIdx.x == 0;  // test-only: the first tile is not copied
-      for (; f < n_tiles; ++f) {
-        const int pb = f % kParBufs, s = f % ST;
-        if (f >= kParBufs && !wait(L::parFree + pb, f / kParBufs - 1)) break;
-        if (f >= ST && !wait(L::empty + s, f / ST - 1)) break;
+      int e = 0;  // ring entries filled
+      // test-only fault injection: CTA 0's first key tile is not copied
+      const bool skip_one = PASS == 1 && !WIDEN && a.fault == 4 && blockIdx.x == 0;
+      auto copy_tile = [&](int s, int bar, int last, int phase, const uint8_t* src) {
+        last_copy[last] = phase;
+        mbar_arrive_expect_tx(&bars[bar], L::kTileBytes);
+        bulk_g2s(sm + s * L::kTileBytes, src, L::kTileBytes, &bars[bar]);
+      };
+      uint32_t phases = 0;  // per stage: parity of its next B tile
+      // the next entry of the ring: A tile i of unit at, or (i < 0) a B tile
+      auto put = [&](const uint8_t* src, int i, int at, bool skip) {
+        const int s = e % ST;
+        if (e >= ST && !wait(L::empty + s, e / ST - 1)) return false;
+        if (i >= 0) {
+          copy_tile(s, L::a_tile(at, i), ST + kParBufs + L::kPages + i, at, src);
+        } else {
+          if (!skip) copy_tile(s, L::full + s, s, (phases >> s) & 1u, src);
+          phases ^= 1u << s;
+        }
+        ++e;
+        return true;
+      };
+      auto copy_columns = [&](int pb, int phase, long long u) {
+        last_copy[ST + pb] = phase;
         if (PASS == 1) {
-          const long long u = static_cast<long long>(w.kvh) * a.key_tiles + w.b;
           mbar_arrive_expect_tx(&bars[L::parFull + pb], 512 + 16);
           bulk_g2s(par + (pb * 2 + 0) * 128, a.k_par + u * 128, 512, &bars[L::parFull + pb]);
           bulk_g2s(valid + pb * 4, a.k_valid + u * 4, 16, &bars[L::parFull + pb]);
-          if (!(skip_one && f == 0)) {
-            mbar_arrive_expect_tx(&bars[L::full + s], L::kTileBytes);
-            bulk_g2s(sm + s * L::kTileBytes, a.k_tiles + u * L::kTileBytes, L::kTileBytes, &bars[L::full + s]);
-          }
         } else {
-          const long long u = static_cast<long long>(w.kvh) * a.row_tiles + b_first<2>(a, w.t) + w.b;
           mbar_arrive_expect_tx(&bars[L::parFull + pb], 1024);
           bulk_g2s(par + (pb * 2 + 0) * 128, a.row_nm + u * 128, 512, &bars[L::parFull + pb]);
           bulk_g2s(par + (pb * 2 + 1) * 128, a.row_il + u * 128, 512, &bars[L::parFull + pb]);
-          mbar_arrive_expect_tx(&bars[L::full + s], L::kTileBytes);
-          bulk_g2s(sm + s * L::kTileBytes, a.q_tiles + u * L::kTileBytes, L::kTileBytes, &bars[L::full + s]);
         }
-        step<PASS>(a, w);
+      };
+      bool ok = true;
+      if (resident) {
+        int epoch = 0;
+        for (int f = 0; ok && f < n_tiles; ++epoch) {
+          for (int j = 0; j < a.row_tiles; ++j) {
+            if (epoch > 0) ok = wait(L::parFree + j, epoch - 1) && wait(L::empty + j, epoch - 1);
+            if (!ok) break;
+            const long long u = static_cast<long long>(w.kvh) * a.row_tiles + j;
+            copy_columns(j, epoch, u);
+            copy_tile(j, L::full + j, j, epoch, a.q_tiles + u * L::kTileBytes);
+          }
+          for (const int kvh = w.kvh; f < n_tiles && w.kvh == kvh; ++f) step<PASS>(a, w);
+        }
+      } else {
+        for (int f = 0, at = -1; ok && f < n_tiles; ++f) {
+          if (L::kARing && (f == 0 || w.b == 0)) {
+            ++at;
+            const uint8_t* tiles = PASS == 1 ? a.q_tiles : a.k_tiles;
+            const int n = PASS == 1 ? a.row_tiles : a.key_tiles;
+            // the second tile of the last unit may not exist: any tile will do, its rows count for nothing
+            for (int i = 0; ok && i < MT; ++i)
+              ok = put(tiles + (static_cast<long long>(w.kvh) * n + min(MT * w.t + i, n - 1)) * L::kTileBytes, i, at, false);
+          }
+          if (!ok) break;
+          const int pb = f % kParBufs;
+          if (f >= kParBufs && !wait(L::parFree + pb, f / kParBufs - 1)) break;
+          const long long u = PASS == 1 ? static_cast<long long>(w.kvh) * a.key_tiles + w.b
+                                        : static_cast<long long>(w.kvh) * a.row_tiles + b_first<2>(a, w.t) + w.b;
+          copy_columns(pb, f / kParBufs, u);
+          ok = put((PASS == 1 ? a.k_tiles : a.q_tiles) + u * L::kTileBytes, -1, 0, skip_one && f == 0);
+          step<PASS>(a, w);
+        }
       }
-      // copies still in flight (after an abort) land before the CTA exits
-      for (int g = max(0, f - ST); g < f; ++g)
-        if (!(skip_one && g == 0)) mbar_wait(&bars[L::full + g % ST], (g / ST) & 1, a.status, a.wait_budget);
-      for (int g = max(0, f - kParBufs); g < f; ++g)
-        mbar_wait(&bars[L::parFull + g % kParBufs], (g / kParBufs) & 1, a.status, a.wait_budget);
     }
+    __syncwarp();  // the lanes go to the CTA's barrier together
   } else if (warp >= kLoadWarp && warp < kLoadWarp + 4) {
     // ================================================================ A loaders: thread = row n of each A tile
     const int n = tid - 32 * kLoadWarp;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    constexpr int kAhead = 8;  // 16-byte words in flight
     bool ok = true;
-    long long ph = PASS == 2 ? key_ph(a, w.kvh, L::kRows * w.t + n) : 0;  // column pass: the next A tile's key
     for (int f = 0, at = 0; ok && f < n_tiles; ++at) {
       const int ab = at % L::kABufs;
-      Walk nw = w;  // the next A unit of the run
-      nw.b = nw.n - 1;
-      step<PASS>(a, nw);
-      const bool more = f + (w.n - w.b) < n_tiles;
 #pragma unroll 1
       for (int i = 0; ok && i < MT; ++i) {
         const uint32_t tm_a = tmem + lane_base + (ab * MT + i) * L::kACols;
-        const int r = L::kRows * w.t + 128 * i + n;
-        auto slot_free = [&] {  // the MMAs of the unit that held this buffer are done
-          if (i == 0 && at >= L::kABufs) ok = wait_warp(L::aFree + ab, at / L::kABufs - 1);
-          if (ok) tc::fence_after_sync();
-          return ok;
-        };
-        if (PASS == 1) {
-          const bool real = r < a.n_rows;
-          const int q = r / a.group;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const uint16_t*>(a.q) +
-              (real ? (static_cast<long long>(q) * a.n_q_heads + w.kvh * a.group + (r - q * a.group)) * D : 0));
-          // the run that begins the A unit also lays the row out for the column pass
-          const int tile = MT * w.t + i;
-          uint8_t* image = w.b == 0 && tile < a.row_tiles
-                               ? a.q_tiles + (static_cast<long long>(w.kvh) * a.row_tiles + tile) * L::kTileBytes
-                               : nullptr;
+        float cst = 0.f;
+        if (PASS == 2 && !WIDEN) {
+          const int t = min(MT * w.t + i, a.key_tiles - 1);
+          cst = __ldg(a.k_par + (static_cast<long long>(w.kvh) * a.key_tiles + t) * 128 + n);
+        }
+        // kARing: a tile of the ring.  Row pass: two halves of a tile in the ring of pages.  Column pass: pages.
+        constexpr int kParts = L::kProduce ? 2 : 1;
 #pragma unroll
-          for (int p = 0; p < D / 8 / kAhead; ++p) {
-            uint4 v[kAhead];
-            uint32_t h[32];
-#pragma unroll
-            for (int c = 0; c < kAhead; ++c) {
-              v[c] = real ? __ldg(src + kAhead * p + c) : make_uint4(0, 0, 0, 0);
-              h[4 * c] = v[c].x;
-              h[4 * c + 1] = v[c].y;
-              h[4 * c + 2] = v[c].z;
-              h[4 * c + 3] = v[c].w;
-            }
-            if (p == 0 && !slot_free()) break;
-            tc::st_32x32b_x32(tm_a + 32 * p, h);
-            if (image) {
-#pragma unroll
-              for (int c = 0; c < kAhead; ++c) sts128(image + p * kPieceBytes + tc::sw128_off(n, c), v[c]);  // global stores
-            }
-          }
+        for (int half = 0; half < kParts; ++half) {
+          const int e = L::entry(f, at) - MT + i;
+          const int x = L::kProduce ? L::page_entry(f, at) - 2 * (MT - i) + half : at;
+          const int s = L::kARing ? e % ST : x % L::kPages;
+          ok = L::kARing      ? wait_warp(L::a_tile(at, i), L::a_phase(at))
+               : L::kProduce ? wait_warp(L::a_tile(at, 2 * i + half), L::a_phase(at))
+                             : wait_warp(L::pageFull + s, x / L::kPages);
+          // the MMAs of the unit that held this buffer are done
+          if (ok && i == 0 && half == 0 && at >= L::kABufs) ok = wait_warp(L::aFree + ab, at / L::kABufs - 1);
           if (!ok) break;
-        } else {
-          const long long cur = ph;
-          const uint4* src = reinterpret_cast<const uint4*>(a.k + (cur < 0 ? 0 : cur) * (D * KVQ_BLOCK_SIZE) +
-                                                            (r % KVQ_BLOCK_SIZE) * 16);
-          const float ks = cur < 0 ? 0.f : __ldg(a.k_scale + cur * KVQ_BLOCK_SIZE + r % KVQ_BLOCK_SIZE);
-          uint4 raw[kAhead];
+          tc::fence_after_sync();
+          const uint8_t* src = L::kARing ? sm + s * L::kTileBytes : sm + L::offPages + s * L::kPageBytes;
 #pragma unroll
-          for (int c = 0; c < kAhead; ++c) raw[c] = cur < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + c * 16);
-          // the page of the A tile after this one
-          if (i + 1 < MT) ph = key_ph(a, w.kvh, r + 128);
-          else if (more) ph = key_ph(a, nw.kvh, L::kRows * nw.t + n);
-          if (!slot_free()) break;
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
+          for (int p = 0; p < NP / kParts; ++p) {
             uint32_t h[32];
+            if (PASS == 1 || !WIDEN) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int x = 4 * p + c;
-              widen16_bf16(raw[x % kAhead], h + 8 * c);
-              if (x + kAhead < D / 16) raw[x % kAhead] = cur < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + (x + kAhead) * 16);
+              for (int c = 0; c < 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src + p * kPieceBytes + tc::sw128_off(n, c));
+                h[4 * c] = v.x;
+                h[4 * c + 1] = v.y;
+                h[4 * c + 2] = v.z;
+                h[4 * c + 3] = v.w;
+              }
+            } else {
+              const uint8_t* key = src + (n >> 4) * (D * KVQ_BLOCK_SIZE) + (n & 15) * 16;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) widen16_bf16(*reinterpret_cast<const uint4*>(key + (4 * p + c) * 256), h + 8 * c);
             }
-            tc::st_32x32b_x32(tm_a + 32 * p, h);
+            tc::st_32x32b_x32(tm_a + 32 * (half * (NP / kParts) + p), h);
           }
-          consts[(at % kConstBufs) * L::kRows + 128 * i + n] = ks * a.c2;
+          if (PASS == 2 && WIDEN) cst = reinterpret_cast<const float*>(src + 8 * D * KVQ_BLOCK_SIZE)[n] * a.c2;
+          if (PASS == 2) consts[(at % kConstBufs) * L::kRows + 128 * i + n] = cst;
+          arrive_warp(L::kARing ? L::empty + s : L::pageFree + s);
         }
       }
+      tc::wait_st();  // also when a wait ran out: nothing is on its way to tensor memory when it is given back
       if (!ok) break;
-      tc::wait_st();
       tc::fence_before_sync();
       arrive_warp(L::aFull + ab);
       if (PASS == 2) arrive_warp(L::constFull + at % kConstBufs);
       f += w.n - w.b;
-      w = nw;
+      w.b = w.n - 1;
+      step<PASS>(a, w);
     }
   } else if (warp == L::kMmaWarp) {
     // ================================================================ MMA issue
     const uint64_t rd0 = tc::sdesc_sw128(smem_u32(sm));
     constexpr uint32_t idesc = tc::idesc_bf16_f32(128, 128);
     bool ok = true;
-    int at = -1;
+    int at = -1, epoch = 0, first = 0;
+    uint32_t phases = 0;  // per stage: parity of its next B tile
     for (int f = 0; ok && f < n_tiles; ++f) {
       if (f == 0 || w.b == 0) {
         ++at;
+        first = b_first<PASS>(a, w.t);
         ok = wait_warp(L::aFull + at % L::kABufs, at / L::kABufs);
       }
-      const int s = f % ST;
-      if (ok) ok = wait_warp(L::full + s, f / ST);
+      const int s = resident ? first + w.b : L::entry(f, at) % ST;
+      if (ok) ok = wait_warp(L::full + s, resident ? epoch : phases >> s);
+      phases ^= 1u << s;
       const bool last = w.b + 1 == w.n || f + 1 == n_tiles;
+      const int kvh = w.kvh;
+      step<PASS>(a, w);
+      const bool epoch_end = resident && w.kvh != kvh;
       const uint64_t bd0 = rd0 + static_cast<uint64_t>((s * L::kTileBytes) >> 4);
 #pragma unroll 1
       for (int i = 0; ok && i < MT; ++i) {
@@ -629,9 +753,6 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
         if (g >= 2) ok = wait_warp(L::sFree + sg, (g >> 1) - 1);
         if (!ok) break;
         if (elect_one()) {
-          // The producers' stores come before the tensor core's reads.  The fence is taken here, on the thread that
-          // has acquired them, and not by the producers: there it would wait for every load they have in flight.
-          if (WIDEN && i == 0) tc::fence_proxy_async_smem();
           tc::fence_after_sync();
           const uint32_t tm_a = tmem + ((at % L::kABufs) * MT + i) * L::kACols, tm_s = tmem + L::kSCol + 128 * sg;
 #pragma unroll
@@ -639,13 +760,28 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
             tc::mma_f16_ts(tm_s, tm_a + 8 * k, bd0 + (k >> 2) * (kPieceBytes >> 4) + 2 * (k & 3), idesc, k ? 1u : 0u);
           tc::commit(&bars[L::sFull + sg]);
           if (i == MT - 1) {
-            tc::commit(&bars[L::empty + s]);
+            // a stage is released by four arrivals (an A tile's are the four loader warps): three now, the last one
+            // when the MMAs are done
+            if (!resident) {
+              for (int x = 0; x < 3; ++x) mbar_arrive(&bars[L::empty + s]);
+              tc::commit(&bars[L::empty + s]);
+            }
             if (last) tc::commit(&bars[L::aFree + at % L::kABufs]);
           }
         }
         __syncwarp();
       }
-      step<PASS>(a, w);
+      // the epoch's tiles that no unit of this run saw (their phases are visited all the same)
+      if (resident && (epoch_end || f + 1 == n_tiles))
+        for (int j = 0; ok && j < a.row_tiles; ++j) ok = wait_warp(L::full + j, epoch);
+      if (ok && epoch_end && elect_one()) {
+        for (int j = 0; j < a.row_tiles; ++j) {
+          for (int x = 0; x < 3; ++x) mbar_arrive(&bars[L::empty + j]);
+          tc::commit(&bars[L::empty + j]);
+        }
+      }
+      __syncwarp();
+      epoch += epoch_end;
     }
     if (elect_one()) {
       tc::commit(&bars[L::drain]);
@@ -657,6 +793,20 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
   grid_dep_trigger();
   tc::fence_before_sync();
   __syncthreads();
+  // After an abort copies may still be in flight: they land before the CTA exits (within microseconds, so the
+  // waits are short).
+  if (*abort_flag && tid == 0) {
+    for (int s = 0; s < L::kLasts; ++s) {
+      const int at = last_copy[s], i = s - ST - kParBufs - L::kPages;
+      const int bar = s < ST                             ? L::full + s
+                      : s < ST + kParBufs              ? L::parFull + (s - ST)
+                      : s < ST + kParBufs + L::kPages ? L::pageFull + (s - ST - kParBufs)
+                                                       : L::a_tile(max(at, 0), i);
+      if (at >= 0) mbar_wait(&bars[bar], (i < 0 ? at : L::a_phase(at)) & 1, nullptr, 1000000);
+      // (the A unit before that one too: its copies may be as young)
+      if (i >= 0 && at > 0) mbar_wait(&bars[L::a_tile(at - 1, i)], L::a_phase(at - 1) & 1, nullptr, 1000000);
+    }
+  }
   if (warp == L::kMmaWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, L::kTmemCols);
@@ -746,7 +896,8 @@ ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads,
   // many B tiles a unit, so it takes two wherever there are two; the column pass does when the rows are
   // many enough to outweigh the loads.
   p.a_rows[0] = p.row_tiles > 1 ? 256 : 128;
-  p.a_rows[1] = p.row_tiles >= 8 ? 256 : 128;
+  p.widen_once = p.row_tiles >= 8;
+  p.a_rows[1] = p.widen_once ? 256 : 128;
   long long most[2] = {0, 0};
   p.units[0] = static_cast<int>((rows + p.a_rows[0] - 1) / p.a_rows[0]);
   p.units[1] = static_cast<int>((keys + p.a_rows[1] - 1) / p.a_rows[1]);
@@ -777,7 +928,6 @@ ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads,
   p.off_q = p.off_il + round(row_n * 4);
   p.off_col = p.off_q + row_n * head_dim * 2;
   p.bytes = p.off_col + part[1] * 4;
-  p.widen_once = p.units[0] >= 8;
   if (p.widen_once) {
     const long long key_n = static_cast<long long>(n_kv_heads) * p.key_tiles * 128;
     p.off_k = round(p.bytes);
@@ -799,16 +949,15 @@ static cudaError_t launch_pass(const ChunkWeightsArgs& a, cudaStream_t stream) {
 
 template <int D>
 static cudaError_t launch_chunk_weights_d(const ChunkWeightsArgs& a, cudaStream_t stream) {
-  cudaError_t e;
-  if (a.k_tiles) {
-    e = launch_pdl(chunk_widen_kernel<D>, dim3(a.key_tiles, a.n_kv_heads), dim3(256), 0, stream, a);
-    if (e == cudaSuccess) e = launch_pass<D, 1, 2, false>(a, stream);
-  } else {
-    e = a.a_rows[0] == 256 ? launch_pass<D, 1, 2, true>(a, stream) : launch_pass<D, 1, 1, true>(a, stream);
-  }
+  const bool once = a.k_tiles != nullptr;
+  cudaError_t e = launch_pdl(chunk_tiles_kernel<D>, dim3(a.row_tiles + (once ? a.key_tiles : 0), a.n_kv_heads), dim3(256), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  e = once                  ? launch_pass<D, 1, 2, false>(a, stream)
+      : a.a_rows[0] == 256 ? launch_pass<D, 1, 2, true>(a, stream)
+                           : launch_pass<D, 1, 1, true>(a, stream);
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(chunk_rows_kernel, dim3(4 * a.row_tiles, a.n_kv_heads), dim3(128), 0, stream, a)) != cudaSuccess) return e;
-  e = a.a_rows[1] == 256 ? launch_pass<D, 2, 2, false>(a, stream) : launch_pass<D, 2, 1, false>(a, stream);
+  e = once ? launch_pass<D, 2, 2, false>(a, stream) : launch_pass<D, 2, 1, true>(a, stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(chunk_acc_kernel, dim3(a.key_tiles, a.n_kv_heads), dim3(128), 0, stream, a);
 }

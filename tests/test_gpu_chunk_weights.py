@@ -39,7 +39,8 @@ CASES = [  # tokens, history, hkv, G, d
     (128, 0, 1, 1, 128), (129, 0, 1, 1, 256), (22, 500, 4, 6, 256), (21, 1, 1, 6, 128), (128, 128, 2, 1, 256),
     (100, 413, 2, 4, 128), (333, 47, 1, 5, 256), (513, 0, 2, 2, 128), (64, 1999, 8, 4, 128), (40, 3000, 1, 12, 256),
     (5, 700, 3, 20, 128), (777, 600, 1, 3, 256),
-    (1, 40000, 3, 1, 128), (1, 30000, 2, 1, 256), (129, 20000, 1, 1, 256)]
+    (1, 40000, 3, 1, 128), (1, 30000, 2, 1, 256), (129, 20000, 1, 1, 256), (30, 2500, 3, 8, 256), (100, 1500, 2, 5, 128),
+    (120, 900, 2, 6, 128), (110, 900, 2, 6, 256), (150, 900, 2, 6, 128), (150, 5000, 3, 6, 256)]
 
 
 @pytest.mark.parametrize("T,hist,hkv,G,d", CASES)
