@@ -31,10 +31,10 @@
 // partials are added in the order of the line: the same result every time.  Roles of a CTA's warps:
 //   warps 0-15   softmax: thread = tensor-memory lane 32 (w % 4) + lane, columns 32 (w / 4) .. of every
 //                128 x 128 score tile; four warps a scheduler hide each other's latencies
-//   warps 16-19  WIDEN row pass: B producers (128 threads); else warp 16 copies tiles, 17 issues the MMAs,
-//                18 copies pages (WIDEN)
-//   warps 20-23  A loaders (128 threads): an A tile from shared memory to tensor memory
-//   warps 24-25  WIDEN row pass: MMA issue, page copies
+//   warps 16-19  A loaders (128 threads): an A tile from shared memory to tensor memory; in the WIDEN column
+//                pass, where they widen it, two groups (warps 16-23) take every second unit
+//   WIDEN row pass: warps 20-27 B producers, two groups of 128 threads that take every second tile
+//   the last warps: MMA issue, tile copies, page copies (WIDEN)
 // Shared memory: a ring of tiles | WIDEN: a ring of pages.  A tiles take their turn before the first B tile of
 // their unit in the ring of tiles, or (WIDEN row pass) as halves in the ring of pages; the WIDEN column
 // pass's A tiles are the pages.  A wait on a barrier tells a phase only from the one before it, so every
@@ -57,7 +57,7 @@ namespace kvq {
 
 namespace {
 
-constexpr int kSoftWarps = 16, kProdWarp = 16, kLoadWarp = 20;
+constexpr int kSoftWarps = 16, kLoadWarp = 16, kProdWarp = 20;
 constexpr int kParBufs = 4;    // column parameters, by B tile
 // Column pass: key constants, by A unit.  The softmax warps can lag behind the A loaders by several units
 // (of one B tile each), so the constants have more buffers than the A tiles, and barriers of their own,
@@ -73,8 +73,10 @@ template <int D, int PASS, int MT, bool WIDEN>
 struct Cw {
   static constexpr bool kProduce = PASS == 1 && WIDEN;     // B tiles made by producer warps
   static constexpr bool kARing = !WIDEN;                   // A tiles come through the ring of tiles
-  static constexpr int kThreads = kProduce ? 26 * 32 : 24 * 32;
-  static constexpr int kMmaWarp = kProduce ? 24 : 17, kPageWarp = kProduce ? 25 : 18, kTileWarp = 16;
+  static constexpr int kLoadGroups = PASS == 2 && WIDEN ? 2 : 1;
+  static constexpr int kMmaWarp = kProduce ? kProdWarp + 8 : kLoadWarp + 4 * kLoadGroups;
+  static constexpr int kPageWarp = kMmaWarp + 1, kTileWarp = kMmaWarp + (WIDEN ? 2 : 1);
+  static constexpr int kThreads = 32 * (kProduce ? kPageWarp + 1 : kTileWarp + 1);
   static constexpr int kRows = 128 * MT;                   // rows of an A unit
   static constexpr int kTileBytes = D * 256;               // one tile: 128 rows x D 16-bit values
   static constexpr int kStages = (WIDEN ? 131072 : 196608) / kTileBytes;  // tiles in the ring
@@ -105,6 +107,7 @@ struct Cw {
   static_assert(kAlloc <= 227 * 1024, "shared memory");
   static_assert(kPages <= 4 && kLasts <= 20, "page bits, last copies");
   static_assert(!kProduce || kTileBytes / 2 <= kPageBytes, "half an A tile fits in a page slot");
+  static_assert(!WIDEN || (kStages % 2 == 0 && kPages % 2 == 0 && kParBufs % 2 == 0), "a slot belongs to one group");
   // barriers: tiles, score tiles, column parameters, A units, key constants, pages
   static constexpr int full = 0, empty = full + kStages, sFull = empty + kStages, sFree = sFull + 2, parFull = sFree + 2,
                        parFree = parFull + kParBufs, aFull = parFree + kParBufs, aFree = aFull + 2, constFull = aFree + 2,
@@ -213,19 +216,23 @@ __device__ __forceinline__ long long key_ph(const ChunkWeightsArgs& a, int kvh, 
 
 }  // namespace
 
-// Operand tiles: blocks x < row_tiles lay 128 query rows of a KV head out (a row is G heads of a query in
-// turn), the blocks after them widen 128 keys and leave their score factors and which of them exist.
+// Operand tiles: the first blocks lay the query rows of a KV head out (a row is G heads of a query in turn),
+// kRowParts blocks a tile, the blocks after them widen 128 keys and leave their score factors and which of them exist.
+constexpr int kRowParts = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) chunk_tiles_kernel(ChunkWeightsArgs a) {
   const int kvh = blockIdx.y, tid = threadIdx.x;
   __shared__ long long ph_s[8];
+  grid_dep_trigger();  // the row pass may take its place; it waits for this grid before it reads
   grid_dep_wait();
-  if (static_cast<int>(blockIdx.x) < a.row_tiles) {
-    const int t = blockIdx.x;
+  if (static_cast<int>(blockIdx.x) < kRowParts * a.row_tiles) {
+    const int t = blockIdx.x / kRowParts, part = blockIdx.x % kRowParts;
     uint8_t* tile = a.q_tiles + (static_cast<long long>(kvh) * a.row_tiles + t) * (D * 256);
     constexpr int W = D / 8;  // 16-byte words of a row
-#pragma unroll 8
-    for (int x = 0; x < W / 2; ++x) {
+    static_assert(W / 2 % kRowParts == 0, "whole passes of the block");
+#pragma unroll
+    for (int x = part * (W / 2 / kRowParts); x < (part + 1) * (W / 2 / kRowParts); ++x) {
       const int i = tid + 256 * x, n = i / W, c = i % W, r = 128 * t + n, q = r / a.group;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < a.n_rows)
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(256) chunk_tiles_kernel(ChunkWeightsArgs a) {
     }
     return;
   }
-  const int j = blockIdx.x - a.row_tiles;
+  const int j = blockIdx.x - kRowParts * a.row_tiles;
   if (tid < 8) ph_s[tid] = key_ph(a, kvh, 128 * j + KVQ_BLOCK_SIZE * tid);
   __syncthreads();
   const long long u = static_cast<long long>(kvh) * a.key_tiles + j;
@@ -285,7 +292,6 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::offFlag + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  grid_dep_wait();
   const long long total = a.line[PASS - 1] * a.n_kv_heads;
   const int P = static_cast<int>(gridDim.x);
   const long long f0 = total * blockIdx.x / P, f1 = total * (blockIdx.x + 1) / P;
@@ -323,6 +329,7 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();  // everything above depends on the arguments alone
   auto wait = [&](int bar, uint32_t parity) {
     return wait_or_abort(&bars[bar], parity & 1u, a.status, abort_flag, a.wait_budget);
   };
@@ -502,14 +509,18 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
         f = end;
       }
     }
-  } else if (L::kProduce && warp < kLoadWarp) {
+  } else if (L::kProduce && warp >= kProdWarp && warp < kProdWarp + 8) {
     // ================================================================ B producers: thread = key of the tile
-    const int n = tid - 32 * kProdWarp;
+    const int n = (tid - 32 * kProdWarp) & 127, group = (warp - kProdWarp) >> 2;
     bool ok = true;
     int at = -1;
     uint32_t phases = 0;  // per page slot: parity of its next key tile
     for (int f = 0; f < n_tiles; ++f) {
       if (f == 0 || w.b == 0) ++at;
+      if ((f & 1) != group) {  // the other group's; its stage, page slot and parameter buffer too
+        step<1>(a, w);
+        continue;
+      }
       const int pb = f % kParBufs, s = f % ST, x = L::page_entry(f, at), ps = x % L::kPages;
       ok = wait_warp(L::pageFull + ps, phases >> ps);
       phases ^= 1u << ps;
@@ -663,13 +674,19 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
       }
     }
     __syncwarp();  // the lanes go to the CTA's barrier together
-  } else if (warp >= kLoadWarp && warp < kLoadWarp + 4) {
+  } else if (warp >= kLoadWarp && warp < kLoadWarp + 4 * L::kLoadGroups) {
     // ================================================================ A loaders: thread = row n of each A tile
-    const int n = tid - 32 * kLoadWarp;
+    const int n = (tid - 32 * kLoadWarp) & 127, group = (warp - kLoadWarp) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     bool ok = true;
     for (int f = 0, at = 0; ok && f < n_tiles; ++at) {
       const int ab = at % L::kABufs;
+      if (L::kLoadGroups == 2 && (at & 1) != group) {  // the other group's unit, buffer and page slot
+        f += w.n - w.b;
+        w.b = w.n - 1;
+        step<PASS>(a, w);
+        continue;
+      }
 #pragma unroll 1
       for (int i = 0; ok && i < MT; ++i) {
         const uint32_t tm_a = tmem + lane_base + (ab * MT + i) * L::kACols;
@@ -814,29 +831,33 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
 }
 
 // Runs that hold a part of A unit t of KV head kvh: the number of them (block-wide; the prefix of the
-// units before it is summed by the block's 128 threads).
+// units before it is summed by the block's threads, 256 at most).
 template <int PASS>
 __device__ int segments_of(const ChunkWeightsArgs& a, int kvh, int t) {
-  __shared__ long long warp_sum[4];
+  __shared__ long long warp_sum[8];
   long long s = 0;
-  for (int x = threadIdx.x; x < t; x += 128) s += b_count<PASS>(a, x);
+  for (int x = threadIdx.x; x < t; x += blockDim.x) s += b_count<PASS>(a, x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
   __syncthreads();
   const long long line = a.line[PASS - 1], total = line * a.n_kv_heads;
   const int runs = a.runs[PASS - 1];
-  const long long f = kvh * line + warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
+  long long f = kvh * line;
+  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) f += warp_sum[i];
   return run_of(f + b_count<PASS>(a, t) - 1, total, runs) - run_of(f, total, runs) + 1;
 }
 
 // Row statistics of the column pass: minus the reference and 1 / l, from the parts of the row pass.  A CTA
-// takes 32 rows, a lane each; warp w takes parts w, w + 4, .. (a row cut over a whole GPU has dozens).
-__global__ void __launch_bounds__(128) chunk_rows_kernel(ChunkWeightsArgs a) {
-  __shared__ float2 part_s[4][32];
+// takes 32 rows, a lane each; its warps share the parts (a row cut over a whole GPU has dozens).
+constexpr int kRowWarps = 8;
+
+__global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeightsArgs a) {
+  __shared__ float2 part_s[kRowWarps][32];
   const int t = blockIdx.x / 4, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = (blockIdx.x % 4) * 32 + lane;
   const int mt = a.a_rows[0] / 128;
+  grid_dep_trigger();
   const int parts = 4 * segments_of<1>(a, kvh, t / mt);  // four column quarters a run
   grid_dep_wait();
   const float2* p = a.row_part + (static_cast<long long>(kvh) * a.units[0] * mt + t) * a.n_part[0] * 128 + n;
@@ -851,17 +872,18 @@ __global__ void __launch_bounds__(128) chunk_rows_kernel(ChunkWeightsArgs a) {
       m = x;
     }
   };
-  for (int i0 = warp; i0 < parts; i0 += 32) {
+  for (int i0 = warp; i0 < parts; i0 += 8 * kRowWarps) {
     float2 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i0 + 4 * i < parts ? p[(i0 + 4 * i) * 128] : make_float2(-INFINITY, 0.f);
+    for (int i = 0; i < 8; ++i)
+      v[i] = i0 + kRowWarps * i < parts ? p[(i0 + kRowWarps * i) * 128] : make_float2(-INFINITY, 0.f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) merge(v[i]);
   }
   part_s[warp][lane] = make_float2(m, l);
   __syncthreads();
   if (warp != 0) return;
-  for (int i = 1; i < 4; ++i) merge(part_s[i][lane]);
+  for (int i = 1; i < kRowWarps; ++i) merge(part_s[i][lane]);
   // a row with no key (or without its sum) gives no weight
   const long long r = (static_cast<long long>(kvh) * a.row_tiles + t) * 128 + n;
   a.row_nm[r] = m == -INFINITY ? 0.f : -m;
@@ -950,13 +972,13 @@ static cudaError_t launch_pass(const ChunkWeightsArgs& a, cudaStream_t stream) {
 template <int D>
 static cudaError_t launch_chunk_weights_d(const ChunkWeightsArgs& a, cudaStream_t stream) {
   const bool once = a.k_tiles != nullptr;
-  cudaError_t e = launch_pdl(chunk_tiles_kernel<D>, dim3(a.row_tiles + (once ? a.key_tiles : 0), a.n_kv_heads), dim3(256), 0, stream, a);
+  cudaError_t e = launch_pdl(chunk_tiles_kernel<D>, dim3(kRowParts * a.row_tiles + (once ? a.key_tiles : 0), a.n_kv_heads), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   e = once                  ? launch_pass<D, 1, 2, false>(a, stream)
       : a.a_rows[0] == 256 ? launch_pass<D, 1, 2, true>(a, stream)
                            : launch_pass<D, 1, 1, true>(a, stream);
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(chunk_rows_kernel, dim3(4 * a.row_tiles, a.n_kv_heads), dim3(128), 0, stream, a)) != cudaSuccess) return e;
+  if ((e = launch_pdl(chunk_rows_kernel, dim3(4 * a.row_tiles, a.n_kv_heads), dim3(kRowWarps * 32), 0, stream, a)) != cudaSuccess) return e;
   e = once ? launch_pass<D, 2, 2, false>(a, stream) : launch_pass<D, 2, 1, true>(a, stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(chunk_acc_kernel, dim3(a.key_tiles, a.n_kv_heads), dim3(128), 0, stream, a);
