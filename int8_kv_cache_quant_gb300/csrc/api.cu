@@ -604,6 +604,8 @@ int kvq_cache_evict(const kvq_cache* cache, int32_t batch, const int32_t* block_
   a.move_src = reinterpret_cast<int32_t*>(base);
   a.slot_map = reinterpret_cast<int32_t*>(base + w.off_map);
   a.n_moves = reinterpret_cast<int32_t*>(base + w.off_count);
+  a.n_words = w.n_words;
+  a.words = reinterpret_cast<uint32_t*>(base + w.off_words);
   a.status = status_ptr();
   return cuda_status(kvq::launch_evict(a, sms, static_cast<cudaStream_t>(stream)));
 }

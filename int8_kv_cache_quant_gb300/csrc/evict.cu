@@ -25,6 +25,7 @@
 // When at most kFewMoves tokens can move (a serving batch that evicts one token a step), the select
 // kernel's warps move the codes too, and the second launch falls away.
 #include <algorithm>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -45,6 +46,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kKeyCap = 16384;
 constexpr int kPosRegs = 8;  // positions a thread keeps in registers between their maximum and the keys
 constexpr int kFewMoves = 16;
+constexpr int kBatch = 4;  // slots a thread has in flight
 // What the move kernel finds for a slot below the budget: the physical slot (page * 16 + slot) that
 // moves into it, or one of these.
 constexpr int32_t kStays = -1, kBadMove = -2;
@@ -64,7 +66,9 @@ struct SelShared {
   uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
   uint32_t ties[kMaxCluster], holes[kMaxCluster], movers[kMaxCluster];  // by rank, pushed by each CTA
   int newest;
+  int n_few, few_src[kFewMoves], few_dst[kFewMoves];  // FEW: this CTA's moves
 };
+static_assert(2 * (kKeyCap / 32) <= kDigits * 256, "a CTA's kept bits and ranks fit in place of its histograms");
 
 // Exclusive prefix of the CTA's warp counts; returns the CTA's total.
 __device__ __forceinline__ uint32_t warp_prefix(const uint32_t* counts, int warp, uint32_t& before) {
@@ -79,10 +83,15 @@ __device__ __forceinline__ uint32_t warp_prefix(const uint32_t* counts, int warp
   return t;
 }
 
-// hist[digit] += 1 for every lane with `in`, one addition per distinct digit of the warp.
+// hist[digit] += 1 for every lane with `in`.  Lanes with the first one's digit add once together.
 __device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit, bool in, int lane) {
-  const uint32_t peers = __match_any_sync(0xffffffffu, in ? digit : 256u);
-  if (in && lane == __ffs(peers) - 1) atomicAdd(hist + digit, __popc(peers));
+  const uint32_t m = __ballot_sync(0xffffffffu, in);
+  if (m == 0) return;
+  const int leader = __ffs(m) - 1;
+  const uint32_t first = __shfl_sync(0xffffffffu, digit, leader);
+  const uint32_t same = __ballot_sync(0xffffffffu, in && digit == first);
+  if (lane == leader) atomicAdd(hist + first, __popc(same));
+  else if (in && digit != first) atomicAdd(hist + digit, 1u);
 }
 
 // One token's codes and scales, slot s to slot t of the sequence (a warp).
@@ -114,13 +123,13 @@ __device__ __forceinline__ void move_token(const EvictArgs& a, const int32_t* bt
 
 // FEW: at most kFewMoves tokens can move; the codes are moved here.
 template <bool FEW>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(EvictArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), n_cta = static_cast<int>(cluster.num_blocks());
   const int kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ SelShared sh;
-  extern __shared__ uint32_t keys[];  // [min(range, kKeyCap)]
+  extern __shared__ __align__(16) uint32_t keys[];  // [min(range, kKeyCap)]
   auto barrier = [&] {  // of the cluster
     if (n_cta > 1) cluster.sync();
     else __syncthreads();
@@ -164,44 +173,45 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   int32_t p_reg[kPosRegs];
   float w_reg[kPosRegs];
   int pmax = INT32_MIN;
-  if (in_regs) {
+  auto load = [&](int from) {  // kPosRegs of the thread's slots, from `from` on, all in flight at once
 #pragma unroll
     for (int i = 0; i < kPosRegs; ++i) {
-      const int t = t0 + tid + i * kSelThreads;
+      const int t = from + tid + i * kSelThreads;
       if (t < t1) {
         p_reg[i] = pos[t];
         w_reg[i] = acc[t];
-        pmax = max(pmax, p_reg[i]);
       }
     }
+  };
+  if (in_regs) {
+    load(t0);
+#pragma unroll
+    for (int i = 0; i < kPosRegs; ++i)
+      if (t0 + tid + i * kSelThreads < t1) pmax = max(pmax, p_reg[i]);
   } else {
 #pragma unroll 8
     for (int t = t0 + tid; t < t1; t += kSelThreads) pmax = max(pmax, pos[t]);
   }
   pmax = __reduce_max_sync(0xffffffffu, pmax);
   if (tid == 0) sh.newest = INT32_MIN;
+  if (tid == 0) sh.n_few = 0;
   for (int i = tid; i < 2 * kDigits * 256; i += kSelThreads) (&sh.own[0][0])[i] = 0u;
   barrier();
   if (lane < n_cta) atomicMax(peer(&sh.newest, lane), pmax);
   barrier();
   const long long recent_from = static_cast<long long>(sh.newest) - a.n_recent;  // protected above it
   auto key_from = [&](int p, float w) { return (p < a.n_sink || p > recent_from) ? 0xFFFFFFFFu : order_key(w); };
+  const bool in_smem = range <= kKeyCap;
   auto key_of = [&](int t) { return t - t0 < kKeyCap ? keys[t - t0] : key_from(pos[t], acc[t]); };
 
   // ---- order keys, and the first digit's histogram
-  if (in_regs) {
+  for (int from = t0; from < t1; from += kPosRegs * kSelThreads) {
+    if (!in_regs) load(from);
 #pragma unroll
     for (int i = 0; i < kPosRegs; ++i) {
-      const int t = t0 + tid + i * kSelThreads;
-      if (t - tid + warp * 32 >= t1) break;  // warp-uniform
+      const int t = from + tid + i * kSelThreads;
+      if (t - lane >= t1) break;  // the same for a warp's lanes
       const uint32_t k = t < t1 ? key_from(p_reg[i], w_reg[i]) : 0u;
-      if (t < t1) keys[t - t0] = k;
-      count_digit(sh.own[0], k >> 24, t < t1, lane);
-    }
-  } else {
-#pragma unroll 4
-    for (int t = t0 + tid; t - lane < t1; t += kSelThreads) {
-      const uint32_t k = t < t1 ? key_from(pos[t], acc[t]) : 0u;
       if (t < t1 && t - t0 < kKeyCap) keys[t - t0] = k;
       count_digit(sh.own[0], k >> 24, t < t1, lane);
     }
@@ -256,9 +266,24 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
     const int shift = 24 - 8 * d;
     prefix |= digit << shift;
     if (d + 1 == kDigits) break;
-    for (int t = t0 + tid; t - lane < t1; t += kSelThreads) {
-      const uint32_t k = t < t1 ? key_of(t) : 0u;
-      count_digit(sh.own[d + 1], (k >> (shift - 8)) & 255u, t < t1 && (k >> shift) == (prefix >> shift), lane);
+    auto starts = [&](uint32_t k) { return (k >> shift) == (prefix >> shift); };
+    auto tally = [&](uint32_t k, bool in) { count_digit(sh.own[d + 1], (k >> (shift - 8)) & 255u, in, lane); };
+    if (in_smem) {  // four keys a lane; from the third digit on few of them start with the prefix
+      for (int i0 = 128 * warp; i0 < t1 - t0; i0 += 4 * kSelThreads) {
+        const int i = i0 + 4 * lane, n = t1 - t0 - i;
+        const uint4 k = n > 0 ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0, 0, 0, 0);
+        const bool in0 = n > 0 && starts(k.x), in1 = n > 1 && starts(k.y), in2 = n > 2 && starts(k.z), in3 = n > 3 && starts(k.w);
+        if (!__any_sync(0xffffffffu, in0 || in1 || in2 || in3)) continue;
+        tally(k.x, in0);
+        tally(k.y, in1);
+        tally(k.z, in2);
+        tally(k.w, in3);
+      }
+    } else {
+      for (int t = t0 + tid; t - lane < t1; t += kSelThreads) {
+        const uint32_t k = t < t1 ? key_of(t) : 0u;
+        tally(k, t < t1 && starts(k));
+      }
     }
   }
   const uint32_t thr = prefix;  // kept: keys above thr, and the first `need` of the `equal` that are thr
@@ -281,25 +306,43 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
     }
   }
 
-  // ---- kept or not, and the counts of holes (below keep) and movers (at or past it) of the run
+  // ---- kept or not, as bits, with the holes (below keep) or movers (at or past it) before each word of 32
+  // slots: first in the warp's run, then in the sequence
+  uint32_t* kept_bits = n_cta > 1 ? &sh.own[0][0] : &sh.total[0][0];  // histograms that are not read any more
+  uint32_t* ranks = kept_bits + kKeyCap / 32;
+  if (!in_smem) {
+    kept_bits = a.words + (unit * a.n_words + t0 / 32) * 2;
+    ranks = kept_bits + (t1 - t0 + 31) / 32;
+  }
   const uint32_t lt = (1u << lane) - 1u;
-  auto walk = [&](auto&& visit) {
-    uint32_t tb = tie_before;
+  uint32_t holes = 0, movers = 0;
+  auto mark = [&](auto keys_near, auto some_ties_go) {
+#pragma unroll 4
     for (int t = w0 + lane; t - lane < w1; t += 32) {
       const bool live = t < w1;
-      const uint32_t k = live ? key_of(t) : 0u;
-      const bool tie = live && k == thr;
-      const uint32_t tm = __ballot_sync(0xffffffffu, tie);
-      const bool kept = live && (k > thr || (tie && tb + __popc(tm & lt) < need));
-      tb += __popc(tm);
-      visit(t, live, kept);
+      const uint32_t k = !live ? 0u : keys_near.value ? keys[t - t0] : key_of(t);
+      bool keeps = live && k >= thr;
+      if (some_ties_go.value) {
+        const uint32_t tm = __ballot_sync(0xffffffffu, live && k == thr);
+        keeps = keeps && (k > thr || tie_before + __popc(tm & lt) < need);
+        tie_before += __popc(tm);
+      }
+      const uint32_t kept = __ballot_sync(0xffffffffu, keeps);
+      if (lane == 0) {
+        kept_bits[(t - t0) / 32] = kept;
+        ranks[(t - t0) / 32] = t < keep ? holes : movers;
+      }
+      const int below = min(32, max(0, keep - (t - lane)));  // slots of the word below keep
+      const uint32_t bm = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+      holes += below - __popc(kept & bm);  // ctx > keep: slots below keep all live
+      movers += __popc(kept & ~bm);
     }
   };
-  uint32_t holes = 0, movers = 0;
-  walk([&](int t, bool live, bool kept) {
-    holes += __popc(__ballot_sync(0xffffffffu, live && !kept && t < keep));
-    movers += __popc(__ballot_sync(0xffffffffu, kept && t >= keep));
-  });
+  using std::false_type;
+  using std::true_type;
+  if (in_smem && equal == need) mark(true_type{}, false_type{});
+  else if (in_smem) mark(true_type{}, true_type{});
+  else mark(false_type{}, true_type{});
   if (lane == 0) {
     sh.warp_a[warp] = holes;
     sh.warp_b[warp] = movers;
@@ -318,43 +361,71 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
       mover_at += sh.movers[r];
     }
   }
+  for (int t = w0 + 32 * lane; t < w1; t += 32 * 32) ranks[(t - t0) / 32] += t < keep ? hole_at : mover_at;
+  __syncthreads();
 
-  // ---- the movers, by rank; then each hole takes the mover of its rank
+  // ---- the movers, by rank; then each hole takes the mover of its rank.  Any thread can take any slot now.
   int32_t* src = a.move_src + unit * a.max_moves;
   int32_t* map = a.slot_map + unit * a.n_pages * KVQ_BLOCK_SIZE;
-  walk([&](int t, bool live, bool kept) {
-    const bool mover = kept && t >= keep;
-    const uint32_t mm = __ballot_sync(0xffffffffu, mover);
-    if (mover) src[mover_at + __popc(mm & lt)] = t;
-    mover_at += __popc(mm);
-  });
+#pragma unroll 4
+  for (int t = max(t0, keep / 32 * 32) + tid; t < t1; t += kSelThreads) {
+    const int w = (t - t0) / 32, base = t / 32 * 32;
+    const uint32_t bits = kept_bits[w];
+    const uint32_t past = base < keep ? ~((1u << (keep - base)) - 1u) : 0xffffffffu;  // of a word across keep
+    if (t >= keep && ((bits >> lane) & 1u)) src[(base < keep ? 0u : ranks[w]) + __popc(bits & past & lt)] = t;
+  }
   barrier();  // no CTA touches another's shared memory after this one
-  walk([&](int t, bool live, bool kept) {
-    const bool hole = live && !kept && t < keep;
-    const uint32_t hm = __ballot_sync(0xffffffffu, hole);
-    if (hole) {
-      const int s = src[hole_at + __popc(hm & lt)];
-      const int page = bt[s / KVQ_BLOCK_SIZE];
-      if (!FEW) {
-        const bool ok = page >= 0 && page < a.num_blocks;  // page * 16 + 15 < 2^31: a pool is far smaller
-        if (!ok) set_status(a.status, KVQ_DEV_BAD_BLOCK);
-        map[t] = ok ? page * KVQ_BLOCK_SIZE + s % KVQ_BLOCK_SIZE : kBadMove;
-      }
-      acc_out[t] = acc[s];
-      pos_out[t] = pos[s];
-    } else if (kept && t < keep) {
-      if (!FEW) map[t] = kStays;
-      if (!in_place) {
-        acc_out[t] = acc[t];
-        pos_out[t] = pos[t];
+  const int h1 = min(t1, keep);
+  for (int tb = t0 + tid; tb < h1; tb += kBatch * kSelThreads) {
+    int s[kBatch], page[kBatch], p[kBatch];  // s: the slot that comes here (the slot itself: it stays)
+    float w[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = tb + i * kSelThreads;
+      s[i] = t;
+      if (t < h1) {
+        const uint32_t bits = kept_bits[(t - t0) / 32];
+        if (!((bits >> lane) & 1u)) s[i] = src[ranks[(t - t0) / 32] + __popc(~bits & lt)];
       }
     }
-    if (FEW) {  // warp-wide, hole by hole: the codes
-      uint32_t left = hm, j = hole_at;
-      for (; left; left &= left - 1, ++j) move_token(a, bt, kvh, src[j], t - lane + __ffs(left) - 1, lane);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = tb + i * kSelThreads;
+      if (t < h1 && (s[i] != t || !in_place)) {
+        page[i] = !FEW && s[i] != t ? bt[s[i] / KVQ_BLOCK_SIZE] : 0;
+        w[i] = acc[s[i]];
+        p[i] = pos[s[i]];
+      }
     }
-    hole_at += __popc(hm);
-  });
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = tb + i * kSelThreads;
+      if (t >= h1) break;
+      if (s[i] != t || !in_place) {
+        acc_out[t] = w[i];
+        pos_out[t] = p[i];
+      }
+      if (FEW) {
+        if (s[i] != t) {
+          const int n = atomicAdd(&sh.n_few, 1);
+          sh.few_src[n] = s[i];
+          sh.few_dst[n] = t;
+        }
+      } else {
+        int32_t m = kStays;
+        if (s[i] != t) {
+          const bool ok = page[i] >= 0 && page[i] < a.num_blocks;  // page * 16 + 15 < 2^31: a pool is far smaller
+          if (!ok) set_status(a.status, KVQ_DEV_BAD_BLOCK);
+          m = ok ? page[i] * KVQ_BLOCK_SIZE + s[i] % KVQ_BLOCK_SIZE : kBadMove;
+        }
+        map[t] = m;
+      }
+    }
+  }
+  if (FEW) {  // the codes, a warp a token; no two moves touch the same slot
+    __syncthreads();
+    for (int i = warp; i < sh.n_few; i += kSelWarps) move_token(a, bt, kvh, sh.few_src[i], sh.few_dst[i], lane);
+  }
 }
 
 // The moves into one page below the budget.
@@ -428,7 +499,9 @@ EvictWorkspace evict_workspace(int batch, int n_kv_heads, int max_ctx, int keep)
   w.n_pages = max_ctx > keep ? (keep + KVQ_BLOCK_SIZE - 1) / KVQ_BLOCK_SIZE : 0;
   w.off_map = (units * w.max_moves * 4 + 255) / 256 * 256;
   w.off_count = w.off_map + units * w.n_pages * KVQ_BLOCK_SIZE * 4;
-  w.bytes = w.off_count + units * 4;
+  w.n_words = max_ctx > keep && max_ctx > kKeyCap ? (max_ctx + 31) / 32 : 0;
+  w.off_words = w.off_count + units * 4;
+  w.bytes = w.off_words + units * w.n_words * 8;
   return w;
 }
 

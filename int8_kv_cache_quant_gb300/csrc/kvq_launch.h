@@ -170,16 +170,18 @@ struct EvictArgs {
   long long out_stride;
   int32_t* new_lens;         // [B]
   // workspace: per (sequence, KV head) the slots that move (ascending), for every slot of the pages below
-  // the budget the physical slot that moves into it, and whether anything moves
+  // the budget the physical slot that moves into it, whether anything moves, and which slots are kept
   int max_moves, n_pages;
   int32_t* move_src;         // [units][max_moves]
   int32_t* slot_map;         // [units][16 * n_pages]
   int32_t* n_moves;          // [units]
+  int n_words;               // > 0: words of 32 slots, when a CTA's range can pass what it keeps in shared memory
+  uint32_t* words;           // [units][n_words][2]
   unsigned int* status;
 };
 struct EvictWorkspace {
-  int max_moves, n_pages;
-  long long off_map, off_count, bytes;
+  int max_moves, n_pages, n_words;
+  long long off_map, off_count, off_words, bytes;
 };
 EvictWorkspace evict_workspace(int batch, int n_kv_heads, int max_ctx, int keep);
 cudaError_t launch_evict(const EvictArgs& a, int n_sms, cudaStream_t stream);

@@ -111,6 +111,8 @@ def test_long_contexts_past_the_keys_in_shared_memory(kvq):
     """160 units take one CTA each: 17000 slots are more than a CTA keeps in shared memory."""
     rng = np.random.default_rng(3)
     assert run(kvq, rng, [17000] + [20] * 159, 1, 128, 9001, 4, 300, "coarse", in_place=False) == 0
+    assert run(kvq, rng, [40000, 16385] + [0] * 158, 1, 128, 20, 4, 10, "spread", in_place=True) == 0
+    assert run(kvq, rng, [17001] + [16400] * 2 + [3] * 157, 1, 256, 16390, 4, 300, "zeros", in_place=True) == 0
 
 
 def test_rows_of_wider_arrays(kvq):
