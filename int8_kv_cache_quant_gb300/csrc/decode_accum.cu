@@ -10,6 +10,9 @@
 // and V, and accum_kernel turns them into weights.  Its reads mostly hit L2: the scores of a call
 // were just written.  A thread owns four keys and sums the rows in a fixed order: no atomics, the
 // same result every time.
+#include <cstdint>
+
+#include "decode_merge.cuh"
 #include "decode_stage1.cuh"
 
 namespace kvq {
@@ -17,61 +20,87 @@ namespace kvq {
 namespace {
 
 constexpr int kAccumThreads = 256;
-constexpr int kAccumKeys = 4 * kAccumThreads;  // keys per CTA
+constexpr int kKeysPerThread = 4;
+constexpr int kAccumKeys = kKeysPerThread * kAccumThreads;  // keys per CTA
+constexpr int kRowsAhead = 8;                               // rows whose scores a thread loads before their statistics are known
+constexpr int kRowLanes = 8;                                // lanes that share a row's statistics
+static_assert(kAccumThreads == kMergeThreads && kAccumThreads == 256, "one launch does both");
 
-}  // namespace
-
-__global__ void __launch_bounds__(kAccumThreads) accum_kernel(StepAccumArgs sa) {
+// The weights of kAccumKeys keys of one (sequence, KV head).
+__device__ __forceinline__ void accum_block(const StepAccumArgs& sa, int chunk, int kvh, int b) {
   const DecodeArgs& a = sa.d;
   __shared__ float row_m[KVQ_VERIFY_MAX_ROWS], row_il[KVQ_VERIFY_MAX_ROWS];
-  const int kvh = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int Hq = a.n_q_heads, G = Hq / a.n_kv_heads, nq = a.nq, R = G * nq;
   grid_dep_wait();
   const int raw = a.ctx_lens[b];
   const int cap = min(a.max_blocks_per_seq * KVQ_BLOCK_SIZE, a.max_ctx);
   const int ctx = max(0, min(raw, cap));
-  const int t = static_cast<int>(blockIdx.x) * kAccumKeys + 4 * tid;
-  if (static_cast<int>(blockIdx.x) * kAccumKeys >= ctx) return;
+  if (chunk * kAccumKeys >= ctx) return;
+  const int t = chunk * kAccumKeys + kKeysPerThread * tid;
   const int n = min(a.n_split, (ctx + a.split_rows - 1) / a.split_rows);
-  // each row's maximum and 1 / l over the splits' statistics
-  for (int r = warp; r < R; r += kAccumThreads / 32) {
-    const long long orow = (static_cast<long long>(b) * nq + r / G) * Hq + kvh * G + r % G;
-    const float4* st = reinterpret_cast<const float4*>(a.part_stats) + orow * a.n_split;
-    float m = -INFINITY;
-    for (int s = lane; s < n; s += 32) m = fmaxf(m, st[s].x);
+  // rows of scores start on 16 bytes and hold whole groups of 16 keys
+  const float* sc = a.scores + (static_cast<long long>(b) * a.n_kv_heads + kvh) * R * a.scores_stride + t;
+  float4 ahead[kRowsAhead];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float mr = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int s = lane; s < n; s += 32) {
-      const float4 v = st[s];
-      if (v.x != -INFINITY) l += v.z * fast_exp2(v.x - mr);
+  for (int r = 0; r < kRowsAhead; ++r)
+    if (r < R && t < ctx) ahead[r] = __ldcg(reinterpret_cast<const float4*>(sc + r * a.scores_stride));
+  const long long at = (static_cast<long long>(b) * a.n_kv_heads + kvh) * sa.acc_stride + t;
+  const int first_new = a.k_new != nullptr && raw >= nq && raw <= cap ? ctx - nq : ctx;  // new tokens start from zero
+  const bool whole = t + kKeysPerThread <= first_new && (reinterpret_cast<uintptr_t>(sa.acc + at) & 15) == 0;
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (whole) old = *reinterpret_cast<const float4*>(sa.acc + at);
+  // each row's maximum and 1 / l over the splits' statistics, in one pass of eight lanes
+  for (int r = tid / kRowLanes; r < (R + 3) / 4 * 4; r += kAccumThreads / kRowLanes) {  // whole warps
+    const int rr = min(r, R - 1);
+    const long long orow = (static_cast<long long>(b) * nq + rr / G) * Hq + kvh * G + rr % G;
+    const float4* st = reinterpret_cast<const float4*>(a.part_stats) + orow * a.n_split;
+    float m = -INFINITY, l = 0.f;
+    auto join = [&](float om, float ol) {
+      const float top = fmaxf(m, om);
+      if (top == -INFINITY) return;
+      l = l * fast_exp2(m - top) + ol * fast_exp2(om - top);
+      m = top;
+    };
+    for (int s0 = tid % kRowLanes; s0 < n; s0 += 4 * kRowLanes) {
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = s0 + i * kRowLanes < n ? st[s0 + i * kRowLanes] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) join(v[i].x, v[i].x == -INFINITY ? 0.f : v[i].z);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    if (lane == 0) {
-      row_m[r] = mr;
+    for (int off = kRowLanes / 2; off > 0; off >>= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m, off), ol = __shfl_xor_sync(0xffffffffu, l, off);
+      join(om, ol);
+    }
+    if (tid % kRowLanes == 0 && r < R) {
+      row_m[r] = m == -INFINITY ? 0.f : m;
       row_il[r] = l == 0.f ? 0.f : __fdiv_rn(1.0f, l);  // a row with no key gives no weight
     }
   }
   __syncthreads();
   if (t >= ctx) return;
-  // scores rows start on 16 bytes and hold whole groups of 16 keys
-  const float* sc = a.scores + (static_cast<long long>(b) * a.n_kv_heads + kvh) * R * a.scores_stride + t;
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int r = 0; r < R; ++r) {
-    const float4 s4 = __ldcg(reinterpret_cast<const float4*>(sc + static_cast<long long>(r) * a.scores_stride));
+  auto add = [&](const float4& s4, int r) {
     const float m = row_m[r], il = row_il[r];
     w[0] = fmaf(fast_exp2(s4.x - m), il, w[0]);
     w[1] = fmaf(fast_exp2(s4.y - m), il, w[1]);
     w[2] = fmaf(fast_exp2(s4.z - m), il, w[2]);
     w[3] = fmaf(fast_exp2(s4.w - m), il, w[3]);
+  };
+  for (int r0 = 0; r0 < R; r0 += kRowsAhead) {
+#pragma unroll
+    for (int i = 0; i < kRowsAhead; ++i) {
+      if (r0 + i < R) add(ahead[i], r0 + i);
+      if (r0 + kRowsAhead + i < R)
+        ahead[i] = __ldcg(reinterpret_cast<const float4*>(sc + static_cast<long long>(r0 + kRowsAhead + i) * a.scores_stride));
+    }
   }
-  // new tokens (when they were written) start from zero
-  const bool wrote = a.k_new != nullptr && raw >= nq && raw <= cap;
-  const int first_new = wrote ? ctx - nq : ctx;
-  const long long at = (static_cast<long long>(b) * a.n_kv_heads + kvh) * sa.acc_stride + t;
+  if (whole) {
+    *reinterpret_cast<float4*>(sa.acc + at) = make_float4(old.x + w[0], old.y + w[1], old.z + w[2], old.w + w[3]);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (t + i < first_new) {
@@ -81,6 +110,47 @@ __global__ void __launch_bounds__(kAccumThreads) accum_kernel(StepAccumArgs sa) 
       if (sa.slot_pos) sa.slot_pos[at + i] = sa.pos[b] + (t + i - first_new);
     }
   }
+}
+
+}  // namespace
+
+// Stage 2: the first CTAs merge the splits into the output, the others make the weights.  Both need
+// stage 1 alone, so they share a launch.
+template <int D, bool WARPS>
+__global__ void __launch_bounds__(kAccumThreads, D == 256 && WARPS ? 2 : 3) step_tail_kernel(StepAccumArgs sa) {
+  extern __shared__ float wts[];
+  int x = blockIdx.x;
+  if (x < sa.merge_blocks) {
+    if (WARPS) {
+      decode_merge_warps<D>(sa.d, x);
+    } else {
+      constexpr int kCols = D / kMergeCols;
+      decode_merge_block<D>(sa.d, x / kCols % sa.d.n_q_heads, x / kCols / sa.d.n_q_heads, x % kCols, wts);
+    }
+    return;
+  }
+  x -= sa.merge_blocks;
+  const int unit = x / sa.key_blocks;
+  accum_block(sa, x % sa.key_blocks, unit % sa.d.n_kv_heads, unit / sa.d.n_kv_heads);
+}
+
+template <int D>
+static cudaError_t launch_tail(StepAccumArgs a, cudaStream_t stream) {
+  const DecodeArgs& d = a.d;
+  const long long rows = static_cast<long long>(d.batch) * d.nq * d.n_q_heads, units = static_cast<long long>(d.batch) * d.n_kv_heads;
+  const bool warps = decode_merge_by_warps(d);
+  const long long mb = warps ? (rows + 7) / 8 : rows * (D / kMergeCols);
+  a.key_blocks = (d.max_ctx + kAccumKeys - 1) / kAccumKeys;
+  if (mb + units * a.key_blocks > INT32_MAX) return cudaErrorInvalidValue;
+  a.merge_blocks = static_cast<int>(mb);
+  const dim3 grid(static_cast<unsigned>(mb + units * a.key_blocks));
+  if (warps) return launch_pdl(step_tail_kernel<D, true>, grid, dim3(kAccumThreads), 0, stream, a);
+  const size_t smem = static_cast<size_t>(d.n_split) * sizeof(float);
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(step_tail_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(step_tail_kernel<D, false>, grid, dim3(kAccumThreads), smem, stream, a);
 }
 
 template <int D>
@@ -102,14 +172,12 @@ static cudaError_t launch_stage1_scores(const DecodeArgs& a, dim3 grid, cudaStre
 }
 
 cudaError_t launch_step_accum(const StepAccumArgs& a, cudaStream_t stream, int* launched) {
-  *launched = 3;
+  *launched = 2;
   const dim3 grid(a.d.n_split, a.d.n_kv_heads, a.d.batch);
-  cudaError_t e = a.d.head_dim == 256 ? launch_stage1_scores<256>(a.d, grid, stream)
-                                      : launch_stage1_scores<128>(a.d, grid, stream);
+  const cudaError_t e = a.d.head_dim == 256 ? launch_stage1_scores<256>(a.d, grid, stream)
+                                            : launch_stage1_scores<128>(a.d, grid, stream);
   if (e != cudaSuccess) return e;
-  if ((e = launch_decode_merge(a.d, stream)) != cudaSuccess) return e;
-  const dim3 ga((a.d.max_ctx + kAccumKeys - 1) / kAccumKeys, a.d.n_kv_heads, a.d.batch);
-  return launch_pdl(accum_kernel, ga, dim3(kAccumThreads), 0, stream, a);
+  return a.d.head_dim == 256 ? launch_tail<256>(a, stream) : launch_tail<128>(a, stream);
 }
 
 }  // namespace kvq

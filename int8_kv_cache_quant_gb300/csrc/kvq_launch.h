@@ -97,18 +97,17 @@ cudaError_t launch_decode(const DecodeArgs& a, DecodeRoute route, cudaStream_t s
 // the stage-1 kernel's K/V stream alone, split route geometry (kvq_debug_stream_floor)
 cudaError_t launch_stream_floor(const DecodeArgs& a, cudaStream_t stream);
 
-// The split route's stage 1 that also writes the scores, the merge, and the pass that adds each key's
-// weight (summed over the rows of its KV head) to acc.
+// The split route's stage 1 that also writes the scores, then one launch that merges the splits and adds
+// each key's weight (summed over the rows of its KV head) to acc.
 struct StepAccumArgs {
   DecodeArgs d;
   float* acc;          // fp32 [B][Hkv][acc_stride]
   long long acc_stride;
   int32_t* slot_pos;   // int32 [B][Hkv][acc_stride] or nullptr: positions of the new tokens go here
   const int32_t* pos;  // int32 [B]: position of each sequence's first new token
+  int merge_blocks, key_blocks;  // set by launch_step_accum: CTAs that merge, CTAs of keys per (sequence, KV head)
 };
 cudaError_t launch_step_accum(const StepAccumArgs& a, cudaStream_t stream, int* launched);
-// stage 2 alone (the split route's merge)
-cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 
 // Attention weights of a chunk of queries, summed per key.  [0]: the row pass, [1]: the column pass.
 struct ChunkWeightsPlan {
