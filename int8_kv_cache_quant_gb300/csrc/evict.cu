@@ -26,6 +26,7 @@
 // kernel's warps move the codes too, and the second launch falls away.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include <cooperative_groups.h>
 
@@ -47,6 +48,7 @@ constexpr int kKeyCap = 16384;
 constexpr int kPosRegs = 8;  // positions a thread keeps in registers between their maximum and the keys
 constexpr int kFewMoves = 16;
 constexpr int kBatch = 4;  // slots a thread has in flight
+constexpr int kCands = 256;  // keys that are compared with each other
 // What the move kernel finds for a slot below the budget: the physical slot (page * 16 + slot) that
 // moves into it, or one of these.
 constexpr int32_t kStays = -1, kBadMove = -2;
@@ -65,7 +67,10 @@ struct SelShared {
   uint32_t total[kDigits][256];  // the cluster's
   uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
   uint32_t ties[kMaxCluster], holes[kMaxCluster], movers[kMaxCluster];  // by rank, pushed by each CTA
-  int newest;
+  int newest[kMaxCluster];                     // by rank
+  int n_cand, cand_base, thr_slot;
+  uint32_t n_cands, thr_key;
+  unsigned long long own_cand[kCands], cand[kCands];  // this CTA's, the cluster's: the keys that the last selection is among, with ~slot below
   int n_few, few_src[kFewMoves], few_dst[kFewMoves];  // FEW: this CTA's moves
 };
 static_assert(2 * (kKeyCap / 32) <= kDigits * 256, "a CTA's kept bits and ranks fit in place of its histograms");
@@ -83,15 +88,23 @@ __device__ __forceinline__ uint32_t warp_prefix(const uint32_t* counts, int warp
   return t;
 }
 
-// hist[digit] += 1 for every lane with `in`.  Lanes with the first one's digit add once together.
-__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit, bool in, int lane) {
-  const uint32_t m = __ballot_sync(0xffffffffu, in);
-  if (m == 0) return;
-  const int leader = __ffs(m) - 1;
-  const uint32_t first = __shfl_sync(0xffffffffu, digit, leader);
-  const uint32_t same = __ballot_sync(0xffffffffu, in && digit == first);
-  if (lane == leader) atomicAdd(hist + first, __popc(same));
-  else if (in && digit != first) atomicAdd(hist + digit, 1u);
+// hist[digit] += 1 for every lane with `in`, N digits a lane (all in flight together).  Lanes with the first
+// one's digit add once: equal weights are common, and 32 additions to one bin would run one after another.
+template <int N>
+__device__ __forceinline__ void count_digits(uint32_t* hist, const uint32_t (&digit)[N], const bool (&in)[N], int lane) {
+  int leader[N];
+  uint32_t first[N], same[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) leader[i] = __ffs(__ballot_sync(0xffffffffu, in[i])) - 1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) first[i] = __shfl_sync(0xffffffffu, digit[i], leader[i] & 31);
+#pragma unroll
+  for (int i = 0; i < N; ++i) same[i] = __ballot_sync(0xffffffffu, in[i] && digit[i] == first[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool leads = lane == leader[i];
+    if (leads || (in[i] && digit[i] != first[i])) atomicAdd(hist + digit[i], leads ? __popc(same[i]) : 1);
+  }
 }
 
 // One token's codes and scales, slot s to slot t of the sequence (a warp).
@@ -162,6 +175,8 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
       }
     return;
   }
+  cg::cluster_group::arrival_token started{};
+  if (n_cta > 1) started = cluster.barrier_arrive();
   // This CTA's slots [t0, t1), and each warp's run of them (whole ballots of 32, whole pages).
   const int range = ((ctx + n_cta - 1) / n_cta + 31) / 32 * 32;
   const int t0 = min(ctx, rank * range), t1 = min(ctx, t0 + range);
@@ -193,13 +208,20 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
     for (int t = t0 + tid; t < t1; t += kSelThreads) pmax = max(pmax, pos[t]);
   }
   pmax = __reduce_max_sync(0xffffffffu, pmax);
-  if (tid == 0) sh.newest = INT32_MIN;
-  if (tid == 0) sh.n_few = 0;
+  if (lane == 0) sh.warp_a[warp] = static_cast<uint32_t>(pmax);
+  if (tid == 0) sh.n_few = sh.n_cand = 0, sh.n_cands = 0;
   for (int i = tid; i < 2 * kDigits * 256; i += kSelThreads) (&sh.own[0][0])[i] = 0u;
-  barrier();
-  if (lane < n_cta) atomicMax(peer(&sh.newest, lane), pmax);
-  barrier();
-  const long long recent_from = static_cast<long long>(sh.newest) - a.n_recent;  // protected above it
+  __syncthreads();
+  int newest = INT32_MIN;
+#pragma unroll
+  for (int i = 0; i < kSelWarps; ++i) newest = max(newest, static_cast<int>(sh.warp_a[i]));
+  if (n_cta > 1) {
+    cluster.barrier_wait(std::move(started));  // every CTA of the cluster runs
+    if (tid < n_cta) *peer(&sh.newest[rank], tid) = newest;
+    cluster.sync();
+    for (int r = 0; r < n_cta; ++r) newest = max(newest, sh.newest[r]);
+  }
+  const long long recent_from = static_cast<long long>(newest) - a.n_recent;  // protected above it
   auto key_from = [&](int p, float w) { return (p < a.n_sink || p > recent_from) ? 0xFFFFFFFFu : order_key(w); };
   const bool in_smem = range <= kKeyCap;
   auto key_of = [&](int t) { return t - t0 < kKeyCap ? keys[t - t0] : key_from(pos[t], acc[t]); };
@@ -208,18 +230,26 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
   for (int from = t0; from < t1; from += kPosRegs * kSelThreads) {
     if (!in_regs) load(from);
 #pragma unroll
-    for (int i = 0; i < kPosRegs; ++i) {
-      const int t = from + tid + i * kSelThreads;
-      if (t - lane >= t1) break;  // the same for a warp's lanes
-      const uint32_t k = t < t1 ? key_from(p_reg[i], w_reg[i]) : 0u;
-      if (t < t1 && t - t0 < kKeyCap) keys[t - t0] = k;
-      count_digit(sh.own[0], k >> 24, t < t1, lane);
+    for (int i0 = 0; i0 < kPosRegs; i0 += 4) {
+      if (from + warp * 32 + i0 * kSelThreads >= t1) break;  // the same for a warp's lanes
+      uint32_t digit[4];
+      bool in[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = from + tid + (i0 + i) * kSelThreads;
+        in[i] = t < t1;
+        const uint32_t k = in[i] ? key_from(p_reg[i0 + i], w_reg[i0 + i]) : 0u;
+        if (in[i] && t - t0 < kKeyCap) keys[t - t0] = k;
+        digit[i] = k >> 24;
+      }
+      count_digits(sh.own[0], digit, in, lane);
     }
   }
 
   // ---- radix select: the prefix of the keep-th largest key, digit by digit
   uint32_t prefix = 0, need = static_cast<uint32_t>(keep);  // still wanted among keys that start with prefix
   uint32_t equal = 0;                                       // keys that do
+  bool chosen = false;                                      // the last key kept is known, with its slot
 #pragma unroll 1
   for (int d = 0; d < kDigits; ++d) {
     const uint32_t* hist = sh.own[d];
@@ -265,32 +295,82 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
     equal = __shfl_sync(0xffffffffu, count, l);
     const int shift = 24 - 8 * d;
     prefix |= digit << shift;
-    if (d + 1 == kDigits) break;
+    if (d + 1 == kDigits || equal == need) break;
     auto starts = [&](uint32_t k) { return (k >> shift) == (prefix >> shift); };
-    auto tally = [&](uint32_t k, bool in) { count_digit(sh.own[d + 1], (k >> (shift - 8)) & 255u, in, lane); };
-    if (in_smem) {  // four keys a lane; from the third digit on few of them start with the prefix
-      for (int i0 = 128 * warp; i0 < t1 - t0; i0 += 4 * kSelThreads) {
-        const int i = i0 + 4 * lane, n = t1 - t0 - i;
-        const uint4 k = n > 0 ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0, 0, 0, 0);
-        const bool in0 = n > 0 && starts(k.x), in1 = n > 1 && starts(k.y), in2 = n > 2 && starts(k.z), in3 = n > 3 && starts(k.w);
-        if (!__any_sync(0xffffffffu, in0 || in1 || in2 || in3)) continue;
-        tally(k.x, in0);
-        tally(k.y, in1);
-        tally(k.z, in2);
-        tally(k.w, in3);
+    chosen = equal <= kCands;  // few keys left: they are compared with each other
+    auto scan = [&](auto&& visit) {  // visit(keys, first slot, is it one of them) for four keys a lane
+      if (in_smem) {
+        for (int i0 = 128 * warp; i0 < t1 - t0; i0 += 4 * kSelThreads) {
+          const int i = i0 + 4 * lane, n = t1 - t0 - i;
+          const uint4 q = n > 0 ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+          const bool in[4] = {n > 0 && starts(q.x), n > 1 && starts(q.y), n > 2 && starts(q.z), n > 3 && starts(q.w)};
+          if (__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) visit(k, t0 + i, in);
+        }
+      } else {
+        for (int i0 = 128 * warp; i0 < t1 - t0; i0 += 4 * kSelThreads) {
+          const int t = t0 + i0 + 4 * lane;
+          uint32_t k[4];
+          bool in[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            k[i] = t + i < t1 ? key_of(t + i) : 0u;
+            in[i] = t + i < t1 && starts(k[i]);
+          }
+          visit(k, t, in);
+        }
       }
-    } else {
-      for (int t = t0 + tid; t - lane < t1; t += kSelThreads) {
-        const uint32_t k = t < t1 ? key_of(t) : 0u;
-        tally(k, t < t1 && starts(k));
+    };
+    if (chosen) {
+      scan([&](const uint32_t (&k)[4], int t, const bool (&in)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (in[i]) sh.own_cand[atomicAdd(&sh.n_cand, 1)] = static_cast<unsigned long long>(k[i]) << 32 | ~static_cast<uint32_t>(t + i);
+      });
+      break;
+    }
+    scan([&](const uint32_t (&k)[4], int, const bool (&in)[4]) {
+      uint32_t digit[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) digit[i] = (k[i] >> (shift - 8)) & 255u;
+      count_digits(sh.own[d + 1], digit, in, lane);
+    });
+  }
+  // Kept: keys above thr, and those that are thr up to slot thr_slot (chosen), or the first `need` of the
+  // `equal` that are thr.
+  uint32_t thr = prefix;
+  int thr_slot = INT32_MAX;
+  if (chosen) {
+    // Every CTA gets all of them (key, and ~slot so that the lower of equal keys is the larger), in no
+    // particular order: the one with need - 1 above it is the last that stays.
+    __syncthreads();
+    const int mine = sh.n_cand;
+    if (n_cta > 1) {
+      if (tid == 0 && mine) sh.cand_base = static_cast<int>(atomicAdd(peer(&sh.n_cands, 0), static_cast<uint32_t>(mine)));
+      __syncthreads();
+      for (int i = tid; i < mine * n_cta; i += kSelThreads) *peer(&sh.cand[sh.cand_base + i / n_cta], i % n_cta) = sh.own_cand[i / n_cta];
+      cluster.sync();
+    }
+    const unsigned long long* cand = n_cta > 1 ? sh.cand : sh.own_cand;
+    if (tid < static_cast<int>(equal)) {
+      const unsigned long long c = cand[tid];
+      uint32_t above = 0;
+#pragma unroll 8
+      for (uint32_t i = 0; i < equal; ++i) above += cand[i] > c;
+      if (above == need - 1) {
+        sh.thr_key = static_cast<uint32_t>(c >> 32);
+        sh.thr_slot = static_cast<int>(~static_cast<uint32_t>(c));
       }
     }
+    __syncthreads();
+    thr = sh.thr_key;
+    thr_slot = sh.thr_slot;
   }
-  const uint32_t thr = prefix;  // kept: keys above thr, and the first `need` of the `equal` that are thr
 
   // ---- ranks of the ties, in slot order: over the warp's run, the CTA, the cluster (when some of them go)
   uint32_t tie_before = 0;
-  if (equal != need) {
+  const bool count_ties = equal != need && !chosen;
+  if (count_ties) {
     uint32_t ties = 0;
     for (int t = w0 + lane; t - lane < w1; t += 32)
       ties += __popc(__ballot_sync(0xffffffffu, t < w1 && key_of(t) == thr));
@@ -321,7 +401,7 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
     for (int t = w0 + lane; t - lane < w1; t += 32) {
       const bool live = t < w1;
       const uint32_t k = !live ? 0u : keys_near.value ? keys[t - t0] : key_of(t);
-      bool keeps = live && k >= thr;
+      bool keeps = live && (k > thr || (k == thr && t <= thr_slot));
       if (some_ties_go.value) {
         const uint32_t tm = __ballot_sync(0xffffffffu, live && k == thr);
         keeps = keeps && (k > thr || tie_before + __popc(tm & lt) < need);
@@ -340,8 +420,9 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
   };
   using std::false_type;
   using std::true_type;
-  if (in_smem && equal == need) mark(true_type{}, false_type{});
+  if (in_smem && !count_ties) mark(true_type{}, false_type{});
   else if (in_smem) mark(true_type{}, true_type{});
+  else if (!count_ties) mark(false_type{}, false_type{});
   else mark(false_type{}, true_type{});
   if (lane == 0) {
     sh.warp_a[warp] = holes;
