@@ -848,19 +848,25 @@ __device__ int segments_of(const ChunkWeightsArgs& a, int kvh, int t) {
   return run_of(f + b_count<PASS>(a, t) - 1, total, runs) - run_of(f, total, runs) + 1;
 }
 
-// Row statistics of the column pass: minus the reference and 1 / l, from the parts of the row pass.  A CTA
-// takes 32 rows, a lane each; its warps share the parts (a row cut over a whole GPU has dozens).
+// Row statistics of the column pass: minus the reference and 1 / l, from the parts of the row pass.  A lane
+// takes a row; WARPS warps share a row's parts (a row cut over a whole GPU has dozens) and a CTA of 8 warps
+// has 8 / WARPS times 32 rows.
 constexpr int kRowWarps = 8;
+constexpr int kFewParts = 16;  // parts a row, up to which a warp takes them all
 
+template <int WARPS>
 __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeightsArgs a) {
   __shared__ float2 part_s[kRowWarps][32];
-  const int t = blockIdx.x / 4, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = (blockIdx.x % 4) * 32 + lane;
+  constexpr int kRows = kRowWarps / WARPS * 32;
+  const int kvh = blockIdx.y, warp = threadIdx.x / 32 % WARPS, group = threadIdx.x / 32 / WARPS, lane = threadIdx.x & 31;
+  const int t = static_cast<int>(blockIdx.x) * kRows / 128, n_all = static_cast<int>(blockIdx.x) * kRows + 32 * group + lane;
   const int mt = a.a_rows[0] / 128;
   grid_dep_trigger();
   const int parts = 4 * segments_of<1>(a, kvh, t / mt);  // four column quarters a run
   grid_dep_wait();
-  const float2* p = a.row_part + (static_cast<long long>(kvh) * a.units[0] * mt + t) * a.n_part[0] * 128 + n;
+  const int tile = n_all / 128, n = n_all % 128;  // a CTA's rows are of one A unit
+  if (tile >= a.row_tiles) return;
+  const float2* p = a.row_part + (static_cast<long long>(kvh) * a.units[0] * mt + tile) * a.n_part[0] * 128 + n;
   // (m, l) of several (m, l): the largest m, the sums moved onto it; a sum below zero marks a dropped part
   float m = -INFINITY, l = 0.f;
   auto merge = [&](const float2& v) {
@@ -872,20 +878,23 @@ __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeights
       m = x;
     }
   };
-  for (int i0 = warp; i0 < parts; i0 += 8 * kRowWarps) {
+  for (int i0 = warp; i0 < parts; i0 += 8 * WARPS) {
     float2 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      v[i] = i0 + kRowWarps * i < parts ? p[(i0 + kRowWarps * i) * 128] : make_float2(-INFINITY, 0.f);
+      v[i] = i0 + WARPS * i < parts ? p[(i0 + WARPS * i) * 128] : make_float2(-INFINITY, 0.f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) merge(v[i]);
   }
-  part_s[warp][lane] = make_float2(m, l);
-  __syncthreads();
-  if (warp != 0) return;
-  for (int i = 1; i < kRowWarps; ++i) merge(part_s[i][lane]);
+  if (WARPS > 1) {
+    static_assert(WARPS == 1 || WARPS == kRowWarps, "a block barrier joins one group");
+    part_s[warp][lane] = make_float2(m, l);
+    __syncthreads();
+    if (warp != 0) return;
+    for (int i = 1; i < WARPS; ++i) merge(part_s[i][lane]);
+  }
   // a row with no key (or without its sum) gives no weight
-  const long long r = (static_cast<long long>(kvh) * a.row_tiles + t) * 128 + n;
+  const long long r = (static_cast<long long>(kvh) * a.row_tiles + tile) * 128 + n;
   a.row_nm[r] = m == -INFINITY ? 0.f : -m;
   a.row_il[r] = l < 0.f || l == 0.f ? 0.f : __fdiv_rn(1.0f, l);
 }
@@ -978,7 +987,10 @@ static cudaError_t launch_chunk_weights_d(const ChunkWeightsArgs& a, cudaStream_
       : a.a_rows[0] == 256 ? launch_pass<D, 1, 2, true>(a, stream)
                            : launch_pass<D, 1, 1, true>(a, stream);
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(chunk_rows_kernel, dim3(4 * a.row_tiles, a.n_kv_heads), dim3(kRowWarps * 32), 0, stream, a)) != cudaSuccess) return e;
+  e = a.n_part[0] > kFewParts
+          ? launch_pdl(chunk_rows_kernel<kRowWarps>, dim3(4 * a.row_tiles, a.n_kv_heads), dim3(kRowWarps * 32), 0, stream, a)
+          : launch_pdl(chunk_rows_kernel<1>, dim3((a.row_tiles + 1) / 2, a.n_kv_heads), dim3(kRowWarps * 32), 0, stream, a);
+  if (e != cudaSuccess) return e;
   e = once ? launch_pass<D, 2, 2, false>(a, stream) : launch_pass<D, 2, 1, true>(a, stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(chunk_acc_kernel, dim3(a.key_tiles, a.n_kv_heads), dim3(128), 0, stream, a);
