@@ -69,6 +69,10 @@ constexpr int kConstBufs = 8;
 // exponential and one addition.
 constexpr float kSumLimit = 1.8446744e19f;  // 2^64
 
+// Parts that a run leaves of each A tile of its units: a tile's columns are halved between warps, and with one
+// tile a unit its B tiles are halved between two groups of warps as well.
+__host__ __device__ constexpr int parts_of_run(int a_tiles) { return a_tiles == 2 ? 2 : 4; }
+
 template <int D, int PASS, int MT, bool WIDEN>
 struct Cw {
   static constexpr bool kProduce = PASS == 1 && WIDEN;     // B tiles made by producer warps
@@ -292,6 +296,9 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::offFlag + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  // WIDEN column pass with all row tiles in the ring at once: B tile j stays in stage (and parameter buffer) j
+  // for all A units of a KV head, an epoch
+  const bool resident = PASS == 2 && WIDEN && a.row_tiles <= min(ST, kParBufs);
   const long long total = a.line[PASS - 1] * a.n_kv_heads;
   const int P = static_cast<int>(gridDim.x);
   const long long f0 = total * blockIdx.x / P, f1 = total * (blockIdx.x + 1) / P;
@@ -306,13 +313,13 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars[L::sFull + s], 1);
-      mbar_init(&bars[L::sFree + s], kSoftWarps);
+      mbar_init(&bars[L::sFree + s], kSoftWarps / 2);
       mbar_init(&bars[L::aFull + s], 4);
       mbar_init(&bars[L::aFree + s], 1);
     }
     for (int s = 0; s < kParBufs; ++s) {
       mbar_init(&bars[L::parFull + s], L::kProduce ? 4 : 1);
-      mbar_init(&bars[L::parFree + s], kSoftWarps);
+      mbar_init(&bars[L::parFree + s], MT == 2 || resident ? kSoftWarps : kSoftWarps / 2);
     }
     for (int s = 0; s < kConstBufs; ++s) mbar_init(&bars[L::constFull + s], 4);
     for (int s = 0; s < L::kPages; ++s) {
@@ -338,28 +345,26 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[bar]);
   };
-  // WIDEN column pass with all row tiles in the ring at once: B tile j stays in stage (and parameter buffer) j
-  // for all A units of a KV head, an epoch
-  const bool resident = PASS == 2 && WIDEN && a.row_tiles <= min(ST, kParBufs);
-
   if (warp < kSoftWarps) {
     // ================================================================ softmax
-    const int part = warp >> 2, row = (warp & 3) * 32 + lane, c0 = 32 * part;
-    const uint32_t tm_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::kSCol + c0;
+    // Score tile g of the run is group g % 2's: with two A tiles a unit, one of them is; else every second B tile.
+    const int group = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+    const int tile = MT == 2 ? group : 0, part = MT == 2 ? half : 2 * group + half;
+    const uint32_t tm_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::kSCol + 128 * group + 64 * half;
     // where this CTA's partial of the A unit at the walk goes: slot 0 unless an earlier run began it
     int slot = w.b == 0 ? 0 : static_cast<int>(blockIdx.x) - run_of(f0 - w.b, total, P);
-    auto out_index = [&](const Walk& x, int i) {
-      const long long u = (static_cast<long long>(x.kvh) * a.units[PASS - 1] + x.t) * MT + i;
-      return (u * a.n_part[PASS - 1] + 4 * slot + part) * 128 + row;
+    auto out_index = [&](const Walk& x) {
+      const long long u = (static_cast<long long>(x.kvh) * a.units[PASS - 1] + x.t) * MT + tile;
+      return (u * a.n_part[PASS - 1] + parts_of_run(MT) * slot + part) * 128 + row;
     };
     bool ok = true;
     int at = -1;    // ordinal of the current A unit in this CTA
     int first = 0;  // its first B tile
     int epoch = 0;
-    // per A tile of the unit.  Row pass: reference and sum of the row, its last visible key.  Column pass: the
-    // key's sum, its score factor, the first row that sees it.
-    float m[MT], l[MT], cst[MT];
-    int bound[MT];
+    // Row pass: reference and sum of the row, its last visible key.  Column pass: the key's sum, its score
+    // factor, the first row that sees it.
+    float m = -INFINITY, l = 0.f, cst = 0.f;
+    int bound = 0;
     for (int f = 0; f < n_tiles; ++f) {
       if (f == 0 || w.b == 0) {
         ++at;
@@ -368,118 +373,113 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
           if (!ok) break;
         }
         first = b_first<PASS>(a, w.t);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int r = L::kRows * w.t + 128 * i + row;
-          cst[i] = PASS == 2 ? consts[(at % kConstBufs) * L::kRows + 128 * i + row] : 0.f;
-          m[i] = -INFINITY;
-          l[i] = 0.f;
-          bound[i] = PASS == 1 ? (r < a.n_rows ? a.history_len + r / a.group : -1) : max(0, r - a.history_len) * a.group;
-        }
+        const int r = L::kRows * w.t + 128 * tile + row;
+        if (PASS == 2) cst = consts[(at % kConstBufs) * L::kRows + 128 * tile + row];
+        m = -INFINITY;
+        l = 0.f;
+        bound = PASS == 1 ? (r < a.n_rows ? a.history_len + r / a.group : -1) : max(0, r - a.history_len) * a.group;
       }
-      const int pb = resident ? first + w.b : f % kParBufs;
-      ok = wait_warp(L::parFull + pb, resident ? epoch : f / kParBufs);
-      if (!ok) break;
-      const float4* p0 = reinterpret_cast<const float4*>(par + (pb * 2 + 0) * 128 + c0);
-      const float4* p1 = reinterpret_cast<const float4*>(par + (pb * 2 + 1) * 128 + c0);
-      const uint32_t exist = PASS == 1 ? valid[pb * 4 + part] : 0u;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int g = MT * f + i, sg = g & 1;
-        ok = wait_warp(L::sFull + sg, g >> 1);
+      if (MT == 2 || (f & 1) == group) {
+        const int pb = resident ? first + w.b : f % kParBufs;
+        ok = wait_warp(L::parFull + pb, resident ? epoch : f / kParBufs) && wait_warp(L::sFull + group, MT == 2 ? f : f >> 1);
         if (!ok) break;
         tc::fence_after_sync();
-        uint32_t sv[32];
-        tc::ld_32x32b_x32(tm_s + 128 * sg, sv);
-        // columns of the chunk that count, as bits
-        uint32_t vis;
-        if (PASS == 1) {
-          const int n = bound[i] - 128 * w.b + 1 - c0;
-          vis = (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u) & exist;
-        } else {
-          const int r0 = 128 * (first + w.b) + c0, lo = bound[i] - r0, hi = a.n_rows - r0;
-          vis = (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1u)) &
-                (hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u);
-        }
-        const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
-        tc::wait_ld();
-        tc::fence_before_sync();
-        arrive_warp(L::sFree + sg);  // this warp's part of the score tile is in registers
-        if (PASS == 1) {
-          // sum of 2^(s - ref) over the chunk, s = S * (k_scale c2)
-          auto sum_from = [&](float ref) {
-            const f2 nm2 = mk2(-ref, -ref);
-            f2 sa = mk2(0.f, 0.f), sb = mk2(0.f, 0.f);
 #pragma unroll
-            for (int n = 0; n < 32; n += 4) {
-              const float4 k4 = p0[n >> 2];
-              const f2 xa = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), mk2(k4.x, k4.y), nm2);
-              const f2 xb = fma2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), mk2(k4.z, k4.w), nm2);
-              sa = add2(sa, mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))));
-              sb = add2(sb, mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb))));
-            }
-            return (lo2(sa) + lo2(sb)) + (hi2(sa) + hi2(sb));
-          };
-          float s = 0.f;
-          bool plain = !masked && !__any_sync(0xffffffffu, m[i] == -INFINITY);
-          if (plain) {
-            s = sum_from(m[i]);
-            plain = !__any_sync(0xffffffffu, !(s < kSumLimit));  // true for NaN
-          }
-          if (!plain) {  // masks, a first chunk, or a score far above the reference: scores, maximum, sum
-            const float* k1 = par + (pb * 2 + 0) * 128 + c0;
-            float cm = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < 32; ++n) {
-              const float y = ((vis >> n) & 1u) ? __uint_as_float(sv[n]) * k1[n] : -INFINITY;
-              sv[n] = __float_as_uint(y);
-              cm = fmaxf(cm, y);
-            }
-            // a first chunk, or more than 2^32 above the reference: the reference moves up
-            if (m[i] == -INFINITY || cm > m[i] + 32.f) {
-              if (m[i] != -INFINITY) l[i] *= fast_exp2(m[i] - cm);
-              m[i] = cm;
-            }
-            const float ref = m[i] == -INFINITY ? 0.f : m[i];
-            s = 0.f;
-#pragma unroll
-            for (int n = 0; n < 32; ++n) s += fast_exp2(__uint_as_float(sv[n]) - ref);
-          }
-          l[i] += s;
-        } else {
-          const f2 c2 = mk2(cst[i], cst[i]);
-          float tile_sum = 0.f;
-          if (!masked) {
-            f2 sa = mk2(0.f, 0.f), sb = mk2(0.f, 0.f);
-#pragma unroll
-            for (int n = 0; n < 32; n += 4) {
-              const float4 nm = p0[n >> 2], il = p1[n >> 2];
-              const f2 xa = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), c2, mk2(nm.x, nm.y));
-              const f2 xb = fma2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), c2, mk2(nm.z, nm.w));
-              sa = fma2(mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))), mk2(il.x, il.y), sa);
-              sb = fma2(mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb))), mk2(il.z, il.w), sb);
-            }
-            tile_sum = (lo2(sa) + lo2(sb)) + (hi2(sa) + hi2(sb));
+        for (int c = 0; c < 2; ++c) {
+          const int c0 = 64 * half + 32 * c;
+          const float4* p0 = reinterpret_cast<const float4*>(par + (pb * 2 + 0) * 128 + c0);
+          const float4* p1 = reinterpret_cast<const float4*>(par + (pb * 2 + 1) * 128 + c0);
+          uint32_t sv[32];
+          tc::ld_32x32b_x32(tm_s + 32 * c, sv);
+          // columns of the chunk that count, as bits
+          const uint32_t exist = PASS == 1 ? valid[pb * 4 + (c0 >> 5)] : 0u;
+          uint32_t vis;
+          if (PASS == 1) {
+            const int n = bound - 128 * w.b + 1 - c0;
+            vis = (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u) & exist;
           } else {
-            const float* nm = par + (pb * 2 + 0) * 128 + c0;
-            const float* il = par + (pb * 2 + 1) * 128 + c0;
-#pragma unroll
-            for (int n = 0; n < 32; ++n) {
-              const float p = fast_exp2(fmaf(__uint_as_float(sv[n]), cst[i], nm[n])) * il[n];
-              tile_sum += ((vis >> n) & 1u) ? p : 0.f;  // a row that does not see the key adds nothing, NaN neither
-            }
+            const int r0 = 128 * (first + w.b) + c0, lo = bound - r0, hi = a.n_rows - r0;
+            vis = (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1u)) &
+                  (hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u);
           }
-          l[i] += tile_sum;
-        }
-      }
-      if (!ok) break;
-      if (!resident) arrive_warp(L::parFree + pb);
-      if (w.b + 1 == w.n || f + 1 == n_tiles) {  // the A unit, or this CTA's part of it, is done
+          const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
+          tc::wait_ld();
+          if (c == 1) {
+            tc::fence_before_sync();
+            arrive_warp(L::sFree + group);  // this warp's part of the score tile is in registers
+          }
+          if (PASS == 1) {
+            // sum of 2^(s - ref) over the chunk, s = S * (k_scale c2)
+            auto sum_from = [&](float ref) {
+              const f2 nm2 = mk2(-ref, -ref);
+              f2 sa = mk2(0.f, 0.f), sb = mk2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          if (PASS == 1) a.row_part[out_index(w, i)] = make_float2(m[i], l[i]);
-          else a.col_part[out_index(w, i)] = l[i];
+              for (int n = 0; n < 32; n += 4) {
+                const float4 k4 = p0[n >> 2];
+                const f2 xa = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), mk2(k4.x, k4.y), nm2);
+                const f2 xb = fma2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), mk2(k4.z, k4.w), nm2);
+                sa = add2(sa, mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))));
+                sb = add2(sb, mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb))));
+              }
+              return (lo2(sa) + lo2(sb)) + (hi2(sa) + hi2(sb));
+            };
+            float s = 0.f;
+            bool plain = !masked && !__any_sync(0xffffffffu, m == -INFINITY);
+            if (plain) {
+              s = sum_from(m);
+              plain = !__any_sync(0xffffffffu, !(s < kSumLimit));  // true for NaN
+            }
+            if (!plain) {  // masks, a first chunk, or a score far above the reference: scores, maximum, sum
+              const float* k1 = par + (pb * 2 + 0) * 128 + c0;
+              float cm = -INFINITY;
+#pragma unroll
+              for (int n = 0; n < 32; ++n) {
+                const float y = ((vis >> n) & 1u) ? __uint_as_float(sv[n]) * k1[n] : -INFINITY;
+                sv[n] = __float_as_uint(y);
+                cm = fmaxf(cm, y);
+              }
+              // a first chunk, or more than 2^32 above the reference: the reference moves up
+              if (m == -INFINITY || cm > m + 32.f) {
+                if (m != -INFINITY) l *= fast_exp2(m - cm);
+                m = cm;
+              }
+              const float ref = m == -INFINITY ? 0.f : m;
+              s = 0.f;
+#pragma unroll
+              for (int n = 0; n < 32; ++n) s += fast_exp2(__uint_as_float(sv[n]) - ref);
+            }
+            l += s;
+          } else {
+            const f2 c2 = mk2(cst, cst);
+            float tile_sum = 0.f;
+            if (!masked) {
+              f2 sa = mk2(0.f, 0.f), sb = mk2(0.f, 0.f);
+#pragma unroll
+              for (int n = 0; n < 32; n += 4) {
+                const float4 nm = p0[n >> 2], il = p1[n >> 2];
+                const f2 xa = fma2(mk2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])), c2, mk2(nm.x, nm.y));
+                const f2 xb = fma2(mk2(__uint_as_float(sv[n + 2]), __uint_as_float(sv[n + 3])), c2, mk2(nm.z, nm.w));
+                sa = fma2(mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))), mk2(il.x, il.y), sa);
+                sb = fma2(mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb))), mk2(il.z, il.w), sb);
+              }
+              tile_sum = (lo2(sa) + lo2(sb)) + (hi2(sa) + hi2(sb));
+            } else {
+              const float* nm = par + (pb * 2 + 0) * 128 + c0;
+              const float* il = par + (pb * 2 + 1) * 128 + c0;
+#pragma unroll
+              for (int n = 0; n < 32; ++n) {
+                const float p = fast_exp2(fmaf(__uint_as_float(sv[n]), cst, nm[n])) * il[n];
+                tile_sum += ((vis >> n) & 1u) ? p : 0.f;  // a row that does not see the key adds nothing, NaN neither
+              }
+            }
+            l += tile_sum;
+          }
         }
+        if (!resident) arrive_warp(L::parFree + pb);
+      }
+      if (w.b + 1 == w.n || f + 1 == n_tiles) {  // the A unit, or this CTA's part of it, is done
+        if (PASS == 1) a.row_part[out_index(w)] = make_float2(m, l);
+        else a.col_part[out_index(w)] = l;
         slot = 0;
       }
       const int kvh = w.kvh;
@@ -501,10 +501,8 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
         slot = x.b == 0 ? 0 : static_cast<int>(blockIdx.x) - run_of(f - x.b, total, P);
         const long long end = min(f1, f + (x.n - x.b));
         if (x.kvh > w.kvh || (x.kvh == w.kvh && x.t >= w.t)) {
-          for (int i = 0; i < MT; ++i) {
-            if (PASS == 1) a.row_part[out_index(x, i)] = make_float2(0.f, -1.f);
-            else a.col_part[out_index(x, i)] = 0.f;
-          }
+          if (PASS == 1) a.row_part[out_index(x)] = make_float2(0.f, -1.f);
+          else a.col_part[out_index(x)] = 0.f;
         }
         f = end;
       }
@@ -862,7 +860,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeights
   const int t = static_cast<int>(blockIdx.x) * kRows / 128, n_all = static_cast<int>(blockIdx.x) * kRows + 32 * group + lane;
   const int mt = a.a_rows[0] / 128;
   grid_dep_trigger();
-  const int parts = 4 * segments_of<1>(a, kvh, t / mt);  // four column quarters a run
+  const int parts = parts_of_run(mt) * segments_of<1>(a, kvh, t / mt);
   grid_dep_wait();
   const int tile = n_all / 128, n = n_all % 128;  // a CTA's rows are of one A unit
   if (tile >= a.row_tiles) return;
@@ -903,7 +901,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeights
 __global__ void __launch_bounds__(128) chunk_acc_kernel(ChunkWeightsArgs a) {
   const int t = blockIdx.x, kvh = blockIdx.y, n = threadIdx.x;
   const int mt = a.a_rows[1] / 128;
-  const int parts = 4 * segments_of<2>(a, kvh, t / mt);
+  const int parts = parts_of_run(mt) * segments_of<2>(a, kvh, t / mt);
   grid_dep_wait();
   const int key = 128 * t + n;
   if (key >= a.n_keys) return;
@@ -949,7 +947,7 @@ ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads,
     // an A unit of n pairs lies in at most ceil(n / floor(total / runs)) + 1 runs, and in no more than there are
     const long long shortest = total / p.runs[i];
     const long long seg = std::min<long long>(p.runs[i], (most[i] + shortest - 1) / shortest + 1);
-    p.n_part[i] = static_cast<int>(4 * seg);
+    p.n_part[i] = parts_of_run(p.a_rows[i] / 128) * static_cast<int>(seg);
     part[i] = static_cast<long long>(n_kv_heads) * p.units[i] * p.a_rows[i] * p.n_part[i];
   }
   auto round = [](long long x) { return (x + 255) / 256 * 256; };
