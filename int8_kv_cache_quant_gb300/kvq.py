@@ -567,7 +567,8 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
     workspace, wbytes = _ws(workspace, need, cache.k.device)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_decode_step_accum_int8kv(
-        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, _p(block_table), n_blocks, _p(ctx_lens), int(max_ctx), float(softmax_scale), _hp(out), _p(acc), stride, _p(slot_pos),
+        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, _p(block_table), n_blocks, _p(ctx_lens),
+        int(max_ctx), float(softmax_scale), _hp(out), _p(acc), stride, _p(slot_pos),
         _p(pos) if slot_pos is not None else None, _p(workspace), wbytes, ctypes.byref(o), _stream(stream)))
     return ret
 
@@ -615,7 +616,8 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     B, H = int(ctx_lens.shape[0]), cache.n_kv_heads
     if (acc_out is None) != (slot_pos_out is None):
         raise ValueError("%s: acc_out and slot_pos_out go together" % fn)
-    if acc_out is None:
+    in_place = acc_out is None
+    if in_place:
         acc_out, slot_pos_out = acc, slot_pos
     if new_lens is None:
         new_lens = torch.empty_like(ctx_lens)
@@ -625,8 +627,10 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
     stride, slots = _row_stride(fn, "acc", acc, torch.float32, B, H, dev)
     pstride, pslots = _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H, dev)
-    ostride, oslots = _row_stride(fn, "acc_out", acc_out, torch.float32, B, H, dev)
-    qstride, qslots = _row_stride(fn, "slot_pos_out", slot_pos_out, torch.int32, B, H, dev)
+    ostride, oslots, qstride, qslots = stride, slots, pstride, pslots
+    if not in_place:
+        ostride, oslots = _row_stride(fn, "acc_out", acc_out, torch.float32, B, H, dev)
+        qstride, qslots = _row_stride(fn, "slot_pos_out", slot_pos_out, torch.int32, B, H, dev)
     if pstride != stride or qstride != ostride:
         raise ValueError("%s: slot_pos must be laid out like acc, slot_pos_out like acc_out" % fn)
     if min(slots, pslots) < max_ctx or min(oslots, qslots) < min(keep, max_ctx):
