@@ -22,8 +22,8 @@
 // * evict_move_kernel: a CTA per (page below the budget, KV head, sequence) fills that page's holes.
 //   The cache stores V as [dim][16 slots], so a token's V is one byte of every 16: a whole page's
 //   rows are rebuilt in registers and stored as 16-byte words.
-// When at most kFewMoves tokens can move (a serving batch that evicts one token a step), the select
-// kernel's warps move the codes too, and the second launch falls away.
+// When few tokens can move (a serving batch that evicts a token a step, or some hundreds every now and
+// then), the select kernel's warps move the codes too (FEW), and the second launch falls away.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -46,7 +46,13 @@ constexpr int kMaxCluster = 8;
 // Order keys a CTA keeps in shared memory (64 KB); slots of its range past them are read again.
 constexpr int kKeyCap = 16384;
 constexpr int kPosRegs = 8;  // positions a thread keeps in registers between their maximum and the keys
-constexpr int kFewMoves = 16;
+// Tokens of a (sequence, KV head) that the select kernel moves itself at most, for a batch of fewer units than
+// SMs and for a larger one.  A warp's move of a token costs little but its sectors; the page kernel
+// reads and writes every page below the budget, but uses all SMs and whole words.  Measured (select kernel |
+// page kernel, us): 8 sequences x 8 heads of 1024 tokens, 64 moves 10.9 | 17.9, 256 20.5 | 22.3, 512
+// 27.7 | 22.0; 1 x 4 of 4096: 256 18.9 | 17.7, 512 25.7 | 18.8; 64 x 8 of 2048: 512 124 | 216, 1024 176 | 223,
+// 2048 possible and 1550 made on average 411 | 269.
+constexpr int kFewMoves = 256, kFewMovesLarge = 1024;
 constexpr int kBatch = 4;  // slots a thread has in flight
 constexpr int kCands = 256;  // keys that are compared with each other
 // What the move kernel finds for a slot below the budget: the physical slot (page * 16 + slot) that
@@ -62,6 +68,7 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+template <bool FEW>
 struct SelShared {
   uint32_t own[kDigits][256];    // this CTA's histograms
   uint32_t total[kDigits][256];  // the cluster's
@@ -71,7 +78,8 @@ struct SelShared {
   int n_cand, cand_base, thr_slot;
   uint32_t n_cands, thr_key;
   unsigned long long own_cand[kCands], cand[kCands];  // this CTA's, the cluster's: the keys that the last selection is among, with ~slot below
-  int n_few, few_src[kFewMoves], few_dst[kFewMoves];  // FEW: this CTA's moves
+  int n_few;
+  int2 few[FEW ? kFewMovesLarge : 1];  // FEW: this CTA's moves, from and to
 };
 static_assert(2 * (kKeyCap / 32) <= kDigits * 256, "a CTA's kept bits and ranks fit in place of its histograms");
 
@@ -136,12 +144,12 @@ __device__ __forceinline__ void move_token(const EvictArgs& a, const int32_t* bt
 
 // FEW: at most kFewMoves tokens can move; the codes are moved here.
 template <bool FEW>
-__global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), n_cta = static_cast<int>(cluster.num_blocks());
   const int kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ SelShared sh;
+  __shared__ SelShared<FEW> sh;
   extern __shared__ __align__(16) uint32_t keys[];  // [min(range, kKeyCap)]
   auto barrier = [&] {  // of the cluster
     if (n_cta > 1) cluster.sync();
@@ -488,9 +496,7 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
       }
       if (FEW) {
         if (s[i] != t) {
-          const int n = atomicAdd(&sh.n_few, 1);
-          sh.few_src[n] = s[i];
-          sh.few_dst[n] = t;
+          sh.few[atomicAdd(&sh.n_few, 1)] = make_int2(s[i], t);
         }
       } else {
         int32_t m = kStays;
@@ -505,7 +511,7 @@ __global__ void __launch_bounds__(kSelThreads, FEW ? 1 : 2) evict_select_kernel(
   }
   if (FEW) {  // the codes, a warp a token; no two moves touch the same slot
     __syncthreads();
-    for (int i = warp; i < sh.n_few; i += kSelWarps) move_token(a, bt, kvh, sh.few_src[i], sh.few_dst[i], lane);
+    for (int i = warp; i < sh.n_few; i += kSelWarps) move_token(a, bt, kvh, sh.few[i].x, sh.few[i].y, lane);
   }
 }
 
@@ -590,12 +596,10 @@ cudaError_t launch_evict(const EvictArgs& a, int n_sms, cudaStream_t stream) {
   const int c = select_cluster(a, n_sms);
   const int range = ((a.max_ctx + c - 1) / c + 31) / 32 * 32;
   const size_t smem = static_cast<size_t>(std::min(range, kKeyCap)) * 4;
-  // Few moves in the select kernel's warps, each a few hundred bytes in dozens of small pieces; a page at
-  // a time in a kernel of their own when there are more.
-  const bool few = a.max_moves <= kFewMoves;
+  const bool few = a.max_moves <= (static_cast<long long>(a.batch) * a.n_kv_heads < n_sms ? kFewMoves : kFewMovesLarge);
   auto kern = few ? evict_select_kernel<true> : evict_select_kernel<false>;
   cudaError_t e;
-  if (smem > 32 * 1024 &&
+  if (smem > 16 * 1024 &&
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4)) != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
