@@ -392,8 +392,8 @@ int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t
                                   size_t workspace_bytes, void* stream);
 
 /* Workspace (bytes) of kvq_cache_evict: per (sequence, KV head) the moves of the largest possible
- * eviction (min(keep, max_ctx - keep) of them) and 4 bytes for every slot below the budget.  0 if an
- * argument is not positive. */
+ * eviction (min(keep, max_ctx - keep) of them), 4 bytes for every slot below the budget and, where max_ctx is
+ * past 16384, 8 bytes for every 32 slots.  0 if an argument is not positive. */
 size_t kvq_evict_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max_ctx, int32_t keep);
 
 /*

@@ -29,8 +29,8 @@
 // together get out of L2; with two A tiles it is half of that.  With few row tiles the column pass keeps
 // all of them in shared memory instead.  An A unit that two CTAs share leaves one partial each, and the
 // partials are added in the order of the line: the same result every time.  Roles of a CTA's warps:
-//   warps 0-15   softmax: thread = tensor-memory lane 32 (w % 4) + lane, columns 32 (w / 4) .. of every
-//                128 x 128 score tile; four warps a scheduler hide each other's latencies
+//   warps 0-15   softmax: thread = tensor-memory lane 32 (w % 4) + lane, two groups of eight warps with a
+//                score tile each (the other group's is multiplied meanwhile), 64 of its columns a warp
 //   warps 16-19  A loaders (128 threads): an A tile from shared memory to tensor memory; in the WIDEN column
 //                pass, where they widen it, two groups (warps 16-23) take every second unit
 //   WIDEN row pass: warps 20-27 B producers, two groups of 128 threads that take every second tile
@@ -42,8 +42,17 @@
 // that share a ring announce themselves on barriers of their own.
 // Tensor memory: A tiles (head_dim / 2 columns each) | two score tiles, filled in turn.
 //
-// What bounds it: at head_dim 256 the tensor core (1024 cycles a 128 x 128 tile at 4096 multiply-adds a
-// cycle and SM; its 16384 exponentials take 512 at 32 a cycle), at head_dim 128 both alike.
+// What bounds it.  Long chunks at head_dim 256: the tensor core (a 128 x 128 tile is 1024 cycles at 4096
+// multiply-adds a cycle and SM, its 16384 exponentials 512 at 32 a cycle).  2048 queries after 30720 x 24 heads:
+// 1100 us, the two products at 1.46 PFLOP/s, 76 % of what the library's bf16 product reaches; with a quarter of
+// the multiplications 810 us, with a quarter of them and no exponentials 690 us.  Else the way of a score tile
+// through tensor memory, registers and barriers, some 1500 cycles whatever the head_dim, and the five
+// launches: a prompt of 2048 at head_dim 128 takes 77 us (row pass 35, column pass 32), 64 queries over 32768
+// keys 56 us (22 and 22, of which 5 each are the pages out of memory).
+// Measured both ways, us by row tiles of 128 after 16384 keys (head_dim 256, 4 KV heads | 128, 8 KV heads):
+//   keys widened by every CTA | once:      4: 50 | 56, 6: 63 | 68, 8: 80 | 82, 12: 104 | 105, 16: 130 | 128, 32: 233 | 217
+//                                          4: 60 | 63, 6: 82 | 81, 8: 101 | 96, 12: 140 | 126, 32: 344 | 287
+//   one A tile a unit | two (row pass):    2: 41 | 39, 4: 59 | 50, 6: 72 | 63 and 2: 47 | 41, 4: 74 | 60, 6: 100 | 82
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -850,7 +859,9 @@ __device__ int segments_of(const ChunkWeightsArgs& a, int kvh, int t) {
 // takes a row; WARPS warps share a row's parts (a row cut over a whole GPU has dozens) and a CTA of 8 warps
 // has 8 / WARPS times 32 rows.
 constexpr int kRowWarps = 8;
-constexpr int kFewParts = 16;  // parts a row, up to which a warp takes them all
+// Parts of a row up to which a warp takes them all.  2048 row tiles of a few parts each: 5.7 us against 10.2 with
+// eight warps a row; 8 row tiles of 76 parts: 6.6 us with eight warps, one would read them one after another.
+constexpr int kFewParts = 16;
 
 template <int WARPS>
 __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeightsArgs a) {
@@ -924,7 +935,7 @@ ChunkWeightsPlan chunk_weights_plan(int n_tokens, int n_q_heads, int n_kv_heads,
   // Two A tiles a unit share each B tile; one A tile a unit is loaded ahead of its use.  The row pass has
   // many B tiles a unit, so it takes two wherever there are two; the column pass does when the rows are
   // many enough to outweigh the loads.
-  p.a_rows[0] = p.row_tiles > 1 ? 256 : 128;
+  p.a_rows[0] = p.row_tiles > 1 ? 256 : 128;  // measured at the top of this file
   p.widen_once = p.row_tiles >= 8;
   p.a_rows[1] = p.widen_once ? 256 : 128;
   long long most[2] = {0, 0};

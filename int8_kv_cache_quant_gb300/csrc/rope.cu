@@ -15,6 +15,8 @@
 // Bound: bytes, each row once in and once out.  A thread owns one column of a token (kVec pairs, two
 // 16-byte words of a row; the dims that are not rotated are columns without arithmetic), computes its
 // cos and sin once and applies them to several heads, with the loads of four heads in flight.
+// 2048 tokens x (24 + 4) heads of 256, 64 dims rotated (29 MB in, 29 MB out): 11.9 us, 4.9 TB/s, most of the outputs staying in L2; one
+// token 1.8 us, a launch.
 #include <cuda_bf16.h>
 
 #include "kvq_dev.cuh"
@@ -183,7 +185,9 @@ static cudaError_t launch_rope_v(RopeArgs a, int n_sms, cudaStream_t stream) {
   const int rest = (a.head_dim - a.rotary_dim) / V;
   a.columns = a.rotary_dim / (2 * V) + (rest + 1) / 2;
   // Heads per thread: as many (up to 8) as leave a thousand threads for every SM.  More of them share
-  // one evaluation of cos and sin; fewer spread a short call over the GPU.
+  // one evaluation of cos and sin; fewer spread a short call over the GPU.  Always
+  // one | always 8, us: one token 1.9 | 3.0, 64 x (32 + 8) heads of 128 2.1 | 3.4, 2048 x (24 + 4) of 256 19.0 |
+  // 12.3; at most 2 or 16: 13.5 and 12.0 for the last.
   int per = 8;
   while (per > 1 && static_cast<long long>(a.n_tokens) * ((H + per - 1) / per) * a.columns < 1024LL * n_sms) per /= 2;
   a.head_groups = (H + per - 1) / per;

@@ -385,8 +385,8 @@ def kvq_attn_decode_int8kv_noalloc(cache, q, block_table, ctx_lens, max_ctx, sof
 
 def kvq_debug_fault_inject(mode, wait_budget_cycles=0):
     """Test entry point of the failure path (see kvq.h): mode 0 none, 1 a decode stage-1 copy left
-    un-issued, 2 a prefill piece left un-issued; every bounded wait gives up after
-    wait_budget_cycles (<= 0: the default)."""
+    un-issued, 2 a prefill piece left un-issued, 3 a sparse chunk left un-issued, 4 a key tile of the chunk
+    weights not announced; every bounded wait gives up after wait_budget_cycles (<= 0: the default)."""
     _check("kvq_debug_fault_inject", lib().kvq_debug_fault_inject(int(mode), int(wait_budget_cycles)))
 
 
