@@ -342,7 +342,7 @@ size_t kvq_step_accum_workspace_bytes(int32_t batch, int32_t n_new, int32_t n_q_
  *   slot_pos  : device int32 [batch][n_kv_heads][acc_stride], or NULL (only with k_new)
  *   pos       : device int32 [batch], or NULL; given exactly when slot_pos is
  *   workspace : device, >= kvq_step_accum_workspace_bytes(...), 16-byte aligned
- *   max_ctx   : > 0
+ *   max_ctx   : > 0, at most 2^30 (KVQ_ERR_UNSUPPORTED past it)
  *   other arguments as kvq_decode_step_int8kv; opts->force_route 1 is KVQ_ERR_UNSUPPORTED (the call
  *   always takes the split route, with one split for a short context)
  * A key whose page is outside the pool is skipped (KVQ_DEV_BAD_BLOCK) and gets no weight; when a
@@ -384,7 +384,8 @@ size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, in
  * A key on a page outside the pool is skipped (KVQ_DEV_BAD_BLOCK) and gets no weight.  If a bounded wait
  * runs out (KVQ_DEV_TIMEOUT), the rows and keys it leaves unfinished add nothing.  A row whose scores are
  * not finite gives the keys it sees the weights of its formula, NaN among them.
- * KVQ_ERR_UNSUPPORTED when n_tokens * (n_q_heads / n_kv_heads) or history_len + n_tokens reaches 2^30.
+ * KVQ_ERR_UNSUPPORTED when the rows n_tokens * (n_q_heads / n_kv_heads) or the keys history_len + n_tokens reach
+ * 2^30, or the 128 x 128 score tiles of all KV heads 2^35.
  */
 int kvq_attn_chunk_weights_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
                                   int32_t history_len, const int32_t* block_table_row, int32_t n_blocks_row,
@@ -416,7 +417,7 @@ size_t kvq_evict_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max_
  *                            other arrays, which receive entries 0 .. new_lens[b] - 1
  *   keep > 0, n_sink >= 0, n_recent >= 0, n_sink + n_recent <= keep
  *   new_lens               : device int32 [batch], not ctx_lens itself
- *   max_ctx                : host bound of ctx_lens; a longer ctx (or one past what the block-table row
+ *   max_ctx                : host bound of ctx_lens, at most 2^30 (KVQ_ERR_UNSUPPORTED past it); a longer ctx (or one past what the block-table row
  *                            maps) is clamped to it and sets KVQ_DEV_BAD_POS
  *   workspace              : device, >= kvq_evict_workspace_bytes(...), 16-byte aligned
  * A move whose source or destination page is outside the pool leaves the destination's codes and

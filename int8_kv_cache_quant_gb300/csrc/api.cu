@@ -433,6 +433,7 @@ int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, cons
                         max_ctx, out);
   if (st != KVQ_OK) return st;
   if (!acc || max_ctx <= 0 || acc_stride < max_ctx) return KVQ_ERR_INVALID_ARG;
+  if (max_ctx > 1 << 30) return KVQ_ERR_UNSUPPORTED;  // slots are counted in 32 bits, a block of them ahead
   if ((slot_pos == nullptr) != (pos == nullptr) || (slot_pos && !k_new)) return KVQ_ERR_INVALID_ARG;
   if (!aligned4(acc) || !aligned4(slot_pos) || !aligned4(pos)) return KVQ_ERR_MISALIGNED;
   if (opts && opts->force_route == 1) return KVQ_ERR_UNSUPPORTED;
@@ -471,8 +472,10 @@ static bool chunk_weights_sizes_ok(int32_t n_tokens, int32_t n_q_heads, int32_t 
   if (n_tokens <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || history_len < 0 || n_q_heads % n_kv_heads != 0) return false;
   // rows of a KV head and keys are counted in 32 bits, with room for a tile more
   const long long limit = 1LL << 30;
-  return static_cast<long long>(n_tokens) * (n_q_heads / n_kv_heads) < limit &&
-         static_cast<long long>(history_len) + n_tokens < limit;
+  const long long rows = static_cast<long long>(n_tokens) * (n_q_heads / n_kv_heads), keys = static_cast<long long>(history_len) + n_tokens;
+  if (rows >= limit || keys >= limit) return false;
+  // and so are a CTA's score tiles
+  return (rows + 127) / 128 * ((keys + 127) / 128) < (1LL << 35) / n_kv_heads;
 }
 
 size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,
@@ -567,6 +570,7 @@ int kvq_cache_evict(const kvq_cache* cache, int32_t batch, const int32_t* block_
     return KVQ_ERR_INVALID_ARG;
   if (new_lens == ctx_lens) return KVQ_ERR_INVALID_ARG;
   if (batch > 65535 || cache->n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;  // grid y and z
+  if (max_ctx > 1 << 30) return KVQ_ERR_UNSUPPORTED;  // slots are counted in 32 bits, a block of them ahead
   if (!aligned4(block_table) || !aligned4(ctx_lens) || !aligned4(acc) || !aligned4(slot_pos) || !aligned4(acc_out) ||
       !aligned4(slot_pos_out) || !aligned4(new_lens))
     return KVQ_ERR_MISALIGNED;

@@ -39,6 +39,7 @@ def opts(split=0, force=0):
     (INVALID, dict(hq=23)), (INVALID, dict(batch=0)), (INVALID, dict(opts=opts(split=24))),
     (INVALID, dict(opts=opts(force=3))), (UNSUPPORTED, dict(opts=opts(force=1))), (UNSUPPORTED, dict(hq=4 * 17)),
     (UNSUPPORTED, dict(n_new=9)), (UNSUPPORTED, dict(batch=65536)), (UNSUPPORTED, dict(c=cache(d=192))),
+    (UNSUPPORTED, dict(max_ctx=(1 << 30) + 1, stride=1 << 31)),
     (UNSUPPORTED, dict(c=cache(block=32))), (MISALIGNED, dict(q=A + 2)), (MISALIGNED, dict(acc=A + 2)),
     (MISALIGNED, dict(ws=A + 8)), (MISALIGNED, dict(c=cache(kp=A + 4))), (WORKSPACE, dict(ws=None)),
     (WORKSPACE, dict(wb=1000, opts=opts(split=64)))])
@@ -66,6 +67,7 @@ def weights(L, c=None, q=A, n=10, hq=24, hist=20, bt=A, nb=8, scale=0.1, acc=A, 
     (INVALID, dict(hq=26)), (INVALID, dict(hist=-1)), (INVALID, dict(nb=0)), (INVALID, dict(nb=1)), (INVALID, dict(stride=29)),
     (INVALID, dict(scale=0.0)), (INVALID, dict(scale=-0.1)), (INVALID, dict(scale=float("nan"))), (INVALID, dict(scale=float("inf"))),
     (UNSUPPORTED, dict(n=1 << 28, hist=0, nb=1 << 24, stride=1 << 28)), (UNSUPPORTED, dict(hist=(1 << 30) - 10, nb=1 << 27, stride=1 << 31)),
+    (UNSUPPORTED, dict(n=1 << 22, hist=1 << 29, nb=1 << 26, stride=1 << 31)),  # a CTA's tiles are counted in 32 bits
     (UNSUPPORTED, dict(c=cache(hkv=65536), hq=65536)), (UNSUPPORTED, dict(c=cache(d=64))), (MISALIGNED, dict(q=A + 8)),
     (MISALIGNED, dict(acc=A + 1)), (MISALIGNED, dict(ws=A + 8)), (WORKSPACE, dict(ws=None))])
 def test_chunk_weights_refusals(L, status, kw):
@@ -73,7 +75,7 @@ def test_chunk_weights_refusals(L, status, kw):
 
 
 def test_chunk_weights_workspace():
-    # 10 queries x 6 heads: one row tile and one key tile per KV head, up to two runs of four column quarters
+    # 10 queries x 6 heads: one row tile and one key tile per KV head, up to two runs of four parts
     # each; the row statistics; the queries in bf16
     rows = 4 * 128
     assert k.kvq_chunk_weights_workspace_bytes(10, 24, 4, 20, 256) == rows * 8 * 8 + 2 * rows * 4 + rows * 256 * 2 + rows * 8 * 4
@@ -101,6 +103,7 @@ def evict(L, c=None, batch=2, bt=A, mb=8, ctx=A, max_ctx=100, keep=64, sink=0, r
     (INVALID, dict(ao=A, po=A + 1024, ostride=64)),                 # in place with other rows
     (INVALID, dict(nl=A)),                                          # the lengths in place
     (UNSUPPORTED, dict(batch=65536)), (UNSUPPORTED, dict(c=cache(hkv=65536))), (UNSUPPORTED, dict(c=cache(d=64))),
+    (UNSUPPORTED, dict(max_ctx=(1 << 30) + 1, stride=1 << 31)),
     (MISALIGNED, dict(acc=A + 1)), (MISALIGNED, dict(nl=A + 2)), (MISALIGNED, dict(ws=A + 4)),
     (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(wb=15))])
 def test_evict_refusals(L, status, kw):

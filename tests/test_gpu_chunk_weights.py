@@ -26,8 +26,9 @@ def check(pool, row, hist, q, acc0, acc, scale):
         rows = q[:, h * G:(h + 1) * G].reshape(T * G, D).astype(np.float64)
         p, _, rel, _ = R.weights(k[h], v[h], ok, rows, hist + 1 + np.arange(T).repeat(G), scale)
         ref = acc0[h, :n] + p.sum(0)
-        # beside the weights' own errors (R.weights): a tile's 32 columns a thread are summed in pairs, then the
-        # tiles, the parts (two halves a run) and acc: 32 + tiles + 64 roundings at most
+        # beside the weights' own errors (R.weights): 32 columns are summed in four chains (10 roundings), then two
+        # such sums a tile, the parts (at most four a run) and acc: 10 + 2 tiles + parts + 1 roundings, within
+        # 96 + tiles for the cases' 19 tiles and the few runs that share a key tile
         tol = (rel[:, None] * p).sum(0) + (96 + -(-T * G // 128)) * 2.0 ** -24 * np.abs(ref) + 1e-30
         bad = np.abs(acc[h, :n] - ref) > tol
         assert not bad.any(), (h, np.argwhere(bad)[:4].ravel(), np.abs(acc[h, :n] - ref).max())
