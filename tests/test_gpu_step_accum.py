@@ -59,13 +59,25 @@ CASES = [  # lens, hkv, G, d, n_new, split
 @pytest.mark.parametrize("write", [True, False])
 @pytest.mark.parametrize("lens,hkv,G,d,n_new,split", CASES)
 def test_step(kvq, lens, hkv, G, d, n_new, split, write):
+    run_step(kvq, lens, hkv, G, d, n_new, split, write)
+
+
+@pytest.mark.parametrize("lens,hkv,G,d,n_new,split,extra", [
+    ([300] * 22 + [1, 17], 4, 6, 256, 1, 0, 0), ([90] * 40 + [33], 2, 8, 128, 1, 16, 0),  # a merging warp a row
+    ([165000], 1, 1, 128, 1, 16, 0),                                            # 10313 splits
+    ([1030, 555], 3, 2, 128, 2, 0, 1), ([1030, 555], 3, 2, 256, 1, 0, 2), ([4097], 2, 1, 128, 1, 0, 3)])  # odd rows of acc
+def test_step_in_its_other_launches(kvq, lens, hkv, G, d, n_new, split, extra):
+    run_step(kvq, lens, hkv, G, d, n_new, split, True, extra)
+
+
+def run_step(kvq, lens, hkv, G, d, n_new, split, write, extra=0):
     import torch
     rng = np.random.default_rng(lens[0] * 31 + hkv * 7 + G + d + n_new)
     B = len(lens)
     table, nb = table_of(rng, lens)
     pool = R.Pool.random(rng, nb, hkv, d)
     cache = pool.to_gpu(kvq)
-    max_ctx, slots = max(lens), table.shape[1] * 16
+    max_ctx, slots = max(lens), table.shape[1] * 16 + extra
     q, qt = bf(rng, B, n_new, hkv * G, d)
     kn, vn = bf(rng, B, n_new, hkv, d)[1], bf(rng, B, n_new, hkv, d)[1]
     acc0 = np.exp(rng.standard_normal((B, hkv, slots))).astype(np.float32)
