@@ -201,6 +201,34 @@ def test_same_bits_on_another_stream_and_in_a_graph(kvq):
     assert kvq.kvq_device_status() == 0
 
 
+def test_two_streams_at_once(kvq):
+    """Calls of different shapes on two streams, each with its own workspace: the bits of calls one by one."""
+    import torch
+    rng = np.random.default_rng(17)
+    hkv, G, d = 2, 4, 256
+    table, nb = table_of(rng, [1300])
+    cache, bt = R.Pool.random(rng, nb, hkv, d).to_gpu(kvq), dev(table[0])
+    shapes = [(20, 900), (300, 1000), (1, 1200), (64, 0)]
+    qs = [bf(rng, T, hkv * G, d)[1] for T, _ in shapes]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    size = max(kvq.kvq_chunk_weights_workspace_bytes(T, hkv * G, hkv, h, d) for T, h in shapes)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    want = torch.zeros((4, hkv, 1301), device="cuda")
+    got = torch.zeros((2, 4, hkv, 1301), device="cuda")
+    for i, (T, h) in enumerate(shapes):
+        for _ in range(3):
+            kvq.kvq_attn_chunk_weights_int8kv(cache, qs[i], h, bt, 0.07, want[i], workspace=ws[2])
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, (T, h) in enumerate(shapes):
+            for s in range(2):
+                j = (i + s) % 4
+                kvq.kvq_attn_chunk_weights_int8kv(cache, qs[j], shapes[j][1], bt, 0.07, got[s, j], workspace=ws[s], stream=streams[s])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], want)
+    assert kvq.kvq_device_status() == 0
+
+
 def test_refused_tensors(kvq):
     import torch
     c = kvq.KVCache(8, 2, 128)
