@@ -472,12 +472,13 @@ def kvq_attn_sparse_int8kv(cache, q, cell_offsets, cells, block_table_row, softm
 
 
 def _need(fn, name, t, dtype, shape, dev):
-    """t is a contiguous tensor of this type and shape on the current CUDA device, number dev."""
+    """Pointer of t, a contiguous tensor of this type and shape on the current CUDA device, number dev."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: %s must be a contiguous %s tensor of shape %s (got %s %s)"
                          % (fn, name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
     if t.get_device() != dev:
         _elsewhere(fn, name, t)
+    return t.data_ptr()
 
 
 def _elsewhere(fn, name, t):
@@ -499,8 +500,8 @@ def _ws(workspace, need, device):
 
 
 def _row_stride(fn, name, t, dtype, B, H, dev):
-    """(elements from one (sequence, KV head) row of a [B][H][slots] tensor to the next, slots): rows
-    contiguous and evenly spaced (a view of wider rows will do)."""
+    """(elements from one (sequence, KV head) row of a [B][H][slots] tensor to the next, slots, pointer): rows
+    contiguous and evenly spaced (a view of wider rows will do), on the current device."""
     shape, st = t.shape, t.stride()
     if t.dtype is not dtype or len(shape) != 3 or shape[0] != B or shape[1] != H or (st[2] != 1 and shape[2] > 1):
         raise ValueError("%s: %s must be a %s tensor [%d][%d][slots] with contiguous rows" % (fn, name, dtype, B, H))
@@ -510,7 +511,7 @@ def _row_stride(fn, name, t, dtype, B, H, dev):
         raise ValueError("%s: the rows of %s must be evenly spaced" % (fn, name))
     if t.get_device() != dev:
         _elsewhere(fn, name, t)
-    return stride, slots
+    return stride, slots, t.data_ptr()
 
 
 def kvq_step_accum_workspace_bytes(batch, n_new, n_q_heads, max_ctx, head_dim, split_rows=0):
@@ -547,19 +548,20 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
                 _elsewhere(fn, name, t)
     if D != cache.head_dim:
         raise ValueError("%s: q has head_dim %d, the cache %d" % (fn, D, cache.head_dim))
-    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
+    ctx_p = _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
     n_blocks = block_table.shape[-1]
-    _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
-    stride, slots = _row_stride(fn, "acc", acc, torch.float32, B, H, dev)
+    table_p = _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
+    stride, slots, acc_p = _row_stride(fn, "acc", acc, torch.float32, B, H, dev)
+    slot_pos_p = pos_p = None
     if slots < max_ctx:
         raise ValueError("%s: acc has %d slots, max_ctx is %d" % (fn, slots, max_ctx))
     if slot_pos is not None:
-        pstride, slots = _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H, dev)
+        pstride, slots, slot_pos_p = _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H, dev)
         if pstride != stride or slots < max_ctx:
             raise ValueError("%s: slot_pos must be shaped and laid out like acc" % fn)
         if pos is None:
             raise ValueError("%s: slot_pos needs pos" % fn)
-        _need(fn, "pos", pos, torch.int32, (B,), dev)
+        pos_p = _need(fn, "pos", pos, torch.int32, (B,), dev)
     o = _decode_opts(split_rows, 0, 0, stage1_events, launches)
     need = 0
     if workspace is None:
@@ -567,9 +569,9 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
     workspace, wbytes = _ws(workspace, need, cache.k.device)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_decode_step_accum_int8kv(
-        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, _p(block_table), n_blocks, _p(ctx_lens),
-        int(max_ctx), float(softmax_scale), _hp(out), _p(acc), stride, _p(slot_pos),
-        _p(pos) if slot_pos is not None else None, _p(workspace), wbytes, ctypes.byref(o), _stream(stream)))
+        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx),
+        float(softmax_scale), _hp(out), acc_p, stride, slot_pos_p, pos_p, _p(workspace), wbytes, ctypes.byref(o),
+        _stream(stream)))
     return ret
 
 
@@ -589,7 +591,7 @@ def kvq_attn_chunk_weights_int8kv(cache, q, history_len, block_table_row, softma
     _need(fn, "block_table_row", block_table_row, torch.int32, (n_blocks,), dev)
     if acc.dim() != 2 or acc.shape[1] < history_len + T:
         raise ValueError("%s: acc must be [%d][>= %d]" % (fn, cache.n_kv_heads, history_len + T))
-    stride, _ = _row_stride(fn, "acc", acc[None], torch.float32, 1, cache.n_kv_heads, dev)
+    stride, _, _ = _row_stride(fn, "acc", acc[None], torch.float32, 1, cache.n_kv_heads, dev)
     need = 0
     if workspace is None:
         need = kvq_chunk_weights_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), D)
@@ -622,15 +624,15 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     if new_lens is None:
         new_lens = torch.empty_like(ctx_lens)
     dev, n_blocks = _current_device(), block_table.shape[-1]
-    _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
-    _need(fn, "new_lens", new_lens, torch.int32, (B,), dev)
-    _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
-    stride, slots = _row_stride(fn, "acc", acc, torch.float32, B, H, dev)
-    pstride, pslots = _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H, dev)
-    ostride, oslots, qstride, qslots = stride, slots, pstride, pslots
+    ctx_p = _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
+    new_p = _need(fn, "new_lens", new_lens, torch.int32, (B,), dev)
+    table_p = _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
+    stride, slots, acc_p = _row_stride(fn, "acc", acc, torch.float32, B, H, dev)
+    pstride, pslots, pos_p = _row_stride(fn, "slot_pos", slot_pos, torch.int32, B, H, dev)
+    ostride, oslots, acc_out_p, qstride, qslots, pos_out_p = stride, slots, acc_p, pstride, pslots, pos_p
     if not in_place:
-        ostride, oslots = _row_stride(fn, "acc_out", acc_out, torch.float32, B, H, dev)
-        qstride, qslots = _row_stride(fn, "slot_pos_out", slot_pos_out, torch.int32, B, H, dev)
+        ostride, oslots, acc_out_p = _row_stride(fn, "acc_out", acc_out, torch.float32, B, H, dev)
+        qstride, qslots, pos_out_p = _row_stride(fn, "slot_pos_out", slot_pos_out, torch.int32, B, H, dev)
     if pstride != stride or qstride != ostride:
         raise ValueError("%s: slot_pos must be laid out like acc, slot_pos_out like acc_out" % fn)
     if min(slots, pslots) < max_ctx or min(oslots, qslots) < min(keep, max_ctx):
@@ -639,9 +641,8 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     workspace, wbytes = _ws(workspace, need, cache.k.device)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_cache_evict(
-        ctypes.byref(c), B, _p(block_table), n_blocks, _p(ctx_lens), int(max_ctx), int(keep), int(n_sink),
-        int(n_recent), _p(acc), _p(slot_pos), stride, _p(acc_out), _p(slot_pos_out), ostride, _p(new_lens),
-        _p(workspace), wbytes, _stream(stream)))
+        ctypes.byref(c), B, table_p, n_blocks, ctx_p, int(max_ctx), int(keep), int(n_sink), int(n_recent), acc_p, pos_p,
+        stride, acc_out_p, pos_out_p, ostride, new_p, _p(workspace), wbytes, _stream(stream)))
     return acc_out, slot_pos_out, new_lens
 
 
@@ -680,42 +681,46 @@ def kvq_rope_bf16(q, k, pos, phases, layout=ROPE_HALF, rotary_offset=0, attn_fac
         raise ValueError("%s: q and k are both None" % fn)
     T, _, D = ref.shape
     dev = _current_device()
+    q_p = qo_p = k_p = ko_p = None
+    hq = qs = qos = hk = ks = kos = 0
     if q is not None:
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        hq, qs = _heads(fn, "q", q, T, D, dev)
-        ho, qos = _heads(fn, "q_out", q_out, T, D, dev)
+        hq, qs, q_p = _heads(fn, "q", q, T, D, dev)
+        ho, qos, qo_p = _heads(fn, "q_out", q_out, T, D, dev)
         if ho != hq:
             raise ValueError("%s: q_out has %d heads, q %d" % (fn, ho, hq))
-    else:
-        q_out, hq, qs, qos = None, 0, 0, 0
     if k is not None:
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-        hk, ks = _heads(fn, "k", k, T, D, dev)
-        ho, kos = _heads(fn, "k_out", k_out, T, D, dev)
+        hk, ks, k_p = _heads(fn, "k", k, T, D, dev)
+        ho, kos, ko_p = _heads(fn, "k_out", k_out, T, D, dev)
         if ho != hk:
             raise ValueError("%s: k_out has %d heads, k %d" % (fn, ho, hk))
-    else:
-        k_out, hk, ks, kos = None, 0, 0, 0
     n = phases.numel()
-    _need(fn, "pos", pos, torch.int32, (T,), dev)
-    _need(fn, "phases", phases, torch.int64, (n,), dev)
-    _check(fn, lib().kvq_rope_bf16(_p(q), _p(q_out), qs, qos, hq, _p(k), _p(k_out), ks, kos, hk, D, T, _p(pos),
-                                   _p(phases), 2 * n, int(rotary_offset), int(layout), float(attn_factor),
-                                   _stream(stream)))
-    return q_out, k_out
+    pos_p = _need(fn, "pos", pos, torch.int32, (T,), dev)
+    phases_p = _need(fn, "phases", phases, torch.int64, (n,), dev)
+    _check(fn, lib().kvq_rope_bf16(q_p, qo_p, qs, qos, hq, k_p, ko_p, ks, kos, hk, D, T, pos_p, phases_p, 2 * n,
+                                   int(rotary_offset), int(layout), float(attn_factor), _stream(stream)))
+    return (q_out if q is not None else None), (k_out if k is not None else None)
 
 
 def _heads(fn, name, t, T, D, dev):
-    """(heads, token stride) of bf16 rows [T][heads][D], heads and dims contiguous, tokens any stride apart."""
-    shape, st = t.shape, t.stride()
-    if (t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[0] != T or shape[2] != D
-            or (st[2] != 1 and D > 1) or (st[1] != D and shape[1] > 1)):
-        raise ValueError("%s: %s must be bf16 [%d][heads][%d] with contiguous heads" % (fn, name, T, D))
+    """(heads, token stride, pointer) of bf16 rows [T][heads][D] on the current device: heads and dims contiguous,
+    tokens any stride apart."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[0] != T or shape[2] != D:
+        _not_heads(fn, name, T, D)
+    H, (st, sh, sd) = shape[1], t.stride()
+    if (sh != D and H > 1) or (sd != 1 and D > 1):
+        _not_heads(fn, name, T, D)
     if t.get_device() != dev:
         _elsewhere(fn, name, t)
-    return shape[1], st[0]
+    return H, st, t.data_ptr()
+
+
+def _not_heads(fn, name, T, D):
+    raise ValueError("%s: %s must be bf16 [%d][heads][%d] with contiguous heads" % (fn, name, T, D))
 
 
 def kvq_debug_prefill_q_codes(q, stream=None):
