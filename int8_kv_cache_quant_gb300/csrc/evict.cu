@@ -26,10 +26,10 @@
 // When few tokens can move (a serving batch that evicts a token a step, or some hundreds every now and
 // then), the select kernel's warps move the codes too (FEW), and the second launch falls away.
 //
-// Bound.  One sequence: the chain of barriers and dependent loads (32768 to 4096 in 4 heads: 32 us, the select
+// Bound.  One sequence: the chain of barriers and dependent loads (32768 to 4096 in 4 heads: 30 us, the select
 // kernel 19 on 32 SMs; 1025 to 1024 in 8 x 8: 6.6 us).  A large batch: select about half its issue slots, move the
 // sectors of the layout, in which a token's V is a byte of every 16: 64 x 8 of up to 16384 to 2048 moves 1.12 GB
-// of sectors for 0.41 GB of tokens, 206 us at 5.45 TB/s, select 71 us.
+// of sectors for 0.41 GB of tokens, about 175 us at 6.4 TB/s, select 71 us.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -56,10 +56,10 @@ constexpr int kPosRegs = 8;  // positions a thread keeps in registers between th
 // Tokens of a (sequence, KV head) that the select kernel moves itself at most, for a batch of fewer units than
 // SMs and for a larger one.  A warp's move of a token costs little but its sectors; the page kernel
 // reads and writes every page below the budget, but uses all SMs and whole words.  Measured (select kernel |
-// page kernel, us): 8 sequences x 8 heads of 1024 tokens, 64 moves 10.9 | 17.9, 256 20.5 | 22.3, 512
-// 27.7 | 22.0; 1 x 4 of 4096: 256 18.9 | 17.7, 512 25.7 | 18.8; 64 x 8 of 2048: 512 124 | 216, 1024 176 | 223,
-// 2048 possible and 1550 made on average 411 | 269.
-constexpr int kFewMoves = 256, kFewMovesLarge = 1024;
+// page kernel, us): 8 sequences x 8 heads of 1024 tokens, 64 moves 10.9 | 13.8, 128 15.7 | 16.7, 256 20.4 | 17.2; 1 x 4 of
+// 4096: 64 12.7 | 13.7, 128 14.6 | 14.4, 256 18.9 | 15.6; 64 x 8 of 2048: 16 25 | 57, 256 87 | 126, 512 125 | 140,
+// 1024 176 | 149.
+constexpr int kFewMoves = 128, kFewMovesLarge = 512;
 constexpr int kBatch = 4;  // slots a thread has in flight
 constexpr int kCands = 256;  // keys that are compared with each other
 // What the move kernel finds for a slot below the budget: the physical slot (page * 16 + slot) that
@@ -522,9 +522,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
   }
 }
 
-// The moves into one page below the budget.
+// The moves into one page below the budget: every load before the first store, and eight CTAs of 256 threads an
+// SM (sixteen of 128).  64 x 8 of up to 16384: 244 us the call, 273 without the bound on registers, 260 with K's stores
+// before V's words.
 template <int D>
-__global__ void __launch_bounds__(D) evict_move_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(D, 2048 / D) evict_move_kernel(EvictArgs a) {
   const int p = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   __shared__ int32_t from[KVQ_BLOCK_SIZE];  // by destination slot: physical slot, or negative
   __shared__ int any;
@@ -559,12 +561,12 @@ __global__ void __launch_bounds__(D) evict_move_kernel(EvictArgs a) {
   // K: a token's chunk of 16 dims is one 16-byte word; thread = (chunk tid / 16, slot tid % 16)
   const int slot = tid % KVQ_BLOCK_SIZE, ch = tid / KVQ_BLOCK_SIZE;
   const int f = from[slot];
+  uint4 kc = make_uint4(0, 0, 0, 0);
+  float sc = 0.f;
   if (f >= 0) {
     const long long ph = ph_of(f);
-    *reinterpret_cast<uint4*>(a.k + ((dph * (D / 16) + ch) * KVQ_BLOCK_SIZE + slot) * 16) =
-        *reinterpret_cast<const uint4*>(a.k + ((ph * (D / 16) + ch) * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE) * 16);
-    if (ch == 0) a.k_scale[dph * KVQ_BLOCK_SIZE + slot] = a.k_scale[ph * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE];
-    if (ch == 1) a.v_scale[dph * KVQ_BLOCK_SIZE + slot] = a.v_scale[ph * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE];
+    kc = *reinterpret_cast<const uint4*>(a.k + ((ph * (D / 16) + ch) * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE) * 16);
+    if (ch < 2) sc = (ch ? a.v_scale : a.k_scale)[ph * KVQ_BLOCK_SIZE + f % KVQ_BLOCK_SIZE];
   }
   uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -575,6 +577,10 @@ __global__ void __launch_bounds__(D) evict_move_kernel(EvictArgs a) {
     }
   }
   *row = make_uint4(word[0], word[1], word[2], word[3]);
+  if (f >= 0) {
+    *reinterpret_cast<uint4*>(a.k + ((dph * (D / 16) + ch) * KVQ_BLOCK_SIZE + slot) * 16) = kc;
+    if (ch < 2) (ch ? a.v_scale : a.k_scale)[dph * KVQ_BLOCK_SIZE + slot] = sc;
+  }
 }
 
 // CTAs of a select cluster: as many (1, 2, 4 or 8) as keep at least 1024 slots each and all clusters

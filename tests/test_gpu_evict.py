@@ -116,8 +116,9 @@ def test_long_contexts_past_the_keys_in_shared_memory(kvq):
 
 
 def test_many_moves_in_a_large_batch(kvq):
-    """160 units: up to 1024 moves each without the page kernel."""
+    """160 units: up to 512 moves each without the page kernel."""
     rng = np.random.default_rng(5)
+    assert run(kvq, rng, [1400, 5, 901] + [1300] * 77, 2, 128, 900, 4, 100, "spread", in_place=True) == 0
     assert run(kvq, rng, [1700, 5, 901] + [1300] * 77, 2, 128, 900, 4, 100, "spread", in_place=False) == 0
 
 
@@ -136,7 +137,7 @@ def test_lengths_past_the_bound_and_bad_pages(kvq):
     table, nb = table_of(rng, [320, 320])
     table[0, 1], table[0, 10], table[1, 19] = -1, nb, 1 << 30
     assert run(kvq, rng, [320, 320], 2, 256, 160, 0, 8, "spread", in_place=True, table=(table, nb)) == DEV_BAD_BLOCK
-    # the same where whole pages are filled (more than 256 moves)
+    # the same where whole pages are filled (more than 128 moves)
     table, nb = table_of(rng, [700, 699])
     table[0, 1], table[0, 30], table[1, 40] = -1, nb, 1 << 30
     assert run(kvq, rng, [700, 699], 2, 128, 300, 0, 8, "spread", in_place=True, table=(table, nb)) == DEV_BAD_BLOCK
