@@ -33,7 +33,7 @@
 //                score tile each (the other group's is multiplied meanwhile), 64 of its columns a warp
 //   warps 16-19  A loaders (128 threads): an A tile from shared memory to tensor memory; in the WIDEN column
 //                pass, where they widen it, two groups (warps 16-23) take every second unit
-//   WIDEN row pass: warps 20-27 B producers, two groups of 128 threads that take every second tile
+//   WIDEN row pass: warps 20-27 B producers, thread = key, two groups with half of the dims each
 //   the last warps: MMA issue, tile copies, page copies (WIDEN)
 // Shared memory: a ring of tiles | WIDEN: a ring of pages.  A tiles take their turn before the first B tile of
 // their unit in the ring of tiles, or (WIDEN row pass) as halves in the ring of pages; the WIDEN column
@@ -120,7 +120,7 @@ struct Cw {
   static_assert(kAlloc <= 227 * 1024, "shared memory");
   static_assert(kPages <= 4 && kLasts <= 20, "page bits, last copies");
   static_assert(!kProduce || kTileBytes / 2 <= kPageBytes, "half an A tile fits in a page slot");
-  static_assert(!WIDEN || (kStages % 2 == 0 && kPages % 2 == 0 && kParBufs % 2 == 0), "a slot belongs to one group");
+  static_assert(!WIDEN || (kStages % 2 == 0 && kPages % 2 == 0 && kParBufs % 2 == 0), "a column pass slot belongs to one loader group");
   // barriers: tiles, score tiles, column parameters, A units, key constants, pages
   static constexpr int full = 0, empty = full + kStages, sFull = empty + kStages, sFree = sFull + 2, parFull = sFree + 2,
                        parFree = parFull + kParBufs, aFull = parFree + kParBufs, aFree = aFull + 2, constFull = aFree + 2,
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
   if (tid == 0) {
     // a lane of each warp arrives for its warp: a thread's arrival costs as much as a warp's
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&bars[L::full + s], L::kProduce ? 4 : 1);
+      mbar_init(&bars[L::full + s], L::kProduce ? 8 : 1);
       mbar_init(&bars[L::empty + s], 4);
     }
     for (int s = 0; s < 2; ++s) {
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
     for (int s = 0; s < kConstBufs; ++s) mbar_init(&bars[L::constFull + s], 4);
     for (int s = 0; s < L::kPages; ++s) {
       mbar_init(&bars[L::pageFull + s], 1);
-      mbar_init(&bars[L::pageFree + s], 4);
+      mbar_init(&bars[L::pageFree + s], L::kProduce ? 8 : 4);
     }
     mbar_init(&bars[L::drain], 1);
     for (int s = 0; s < L::kASets * L::kAParts; ++s) mbar_init(&bars[L::aTile + s], 1);
@@ -524,21 +524,18 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
     uint32_t phases = 0;  // per page slot: parity of its next key tile
     for (int f = 0; f < n_tiles; ++f) {
       if (f == 0 || w.b == 0) ++at;
-      if ((f & 1) != group) {  // the other group's; its stage, page slot and parameter buffer too
-        step<1>(a, w);
-        continue;
-      }
       const int pb = f % kParBufs, s = f % ST, x = L::page_entry(f, at), ps = x % L::kPages;
       ok = wait_warp(L::pageFull + ps, phases >> ps);
       phases ^= 1u << ps;
-      if (ok && f >= kParBufs) ok = wait_warp(L::parFree + pb, f / kParBufs - 1);
+      if (ok && group == 0 && f >= kParBufs) ok = wait_warp(L::parFree + pb, f / kParBufs - 1);
       if (ok && f >= ST) ok = wait_warp(L::empty + s, f / ST - 1);
       if (!ok) break;
       const uint8_t* page = sm + L::offPages + ps * L::kPageBytes;
       const uint8_t* src = page + (n >> 4) * (D * KVQ_BLOCK_SIZE) + (n & 15) * 16;
       uint8_t* tile = sm + s * L::kTileBytes;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
+      for (int j = 0; j < D / 32; ++j) {  // this group's half of the dims
+        const int i = group * (D / 32) + j;
         uint32_t h[8];
         widen16_bf16(*reinterpret_cast<const uint4*>(src + i * 256), h);
         uint8_t* piece = tile + (i >> 2) * kPieceBytes;
@@ -550,10 +547,12 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
       tc::fence_proxy_async_smem();  // each writer's stores come before the tensor core's reads
       // test-only fault injection: CTA 0's first tile is never announced
       if (!(a.fault == 4 && blockIdx.x == 0 && f == 0)) arrive_warp(L::full + s);
-      par[(pb * 2 + 0) * 128 + n] = real ? ks * a.c2 : 0.f;
-      const uint32_t bits = __ballot_sync(0xffffffffu, real);
-      if (lane == 0) valid[pb * 4 + (n >> 5)] = bits;
-      arrive_warp(L::parFull + pb);
+      if (group == 0) {
+        par[(pb * 2 + 0) * 128 + n] = real ? ks * a.c2 : 0.f;
+        const uint32_t bits = __ballot_sync(0xffffffffu, real);
+        if (lane == 0) valid[pb * 4 + (n >> 5)] = bits;
+        arrive_warp(L::parFull + pb);
+      }
       arrive_warp(L::pageFree + ps);
       step<1>(a, w);
     }
@@ -739,6 +738,7 @@ __global__ void __launch_bounds__(Cw<D, PASS, MT, WIDEN>::kThreads, 1) chunk_wei
           if (PASS == 2 && WIDEN) cst = reinterpret_cast<const float*>(src + 8 * D * KVQ_BLOCK_SIZE)[n] * a.c2;
           if (PASS == 2) consts[(at % kConstBufs) * L::kRows + 128 * i + n] = cst;
           arrive_warp(L::kARing ? L::empty + s : L::pageFree + s);
+          if (L::kProduce && lane == 0) mbar_arrive(&bars[L::pageFree + s]);  // a key tile has eight readers
         }
       }
       tc::wait_st();  // also when a wait ran out: nothing is on its way to tensor memory when it is given back
