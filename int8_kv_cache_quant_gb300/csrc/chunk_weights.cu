@@ -48,7 +48,7 @@
 // the multiplications 810 us, with a quarter of them and no exponentials 690 us.  Else the way of a score tile
 // through tensor memory, registers and barriers, some 1500 cycles whatever the head_dim, and the five
 // launches: a prompt of 2048 at head_dim 128 takes 77 us (row pass 35, column pass 32), 64 queries over 32768
-// keys 56 us (22 and 22, of which 5 each are the pages out of memory).
+// keys 54 us (20 and 22, of which 5 each are the pages out of memory).
 // Measured both ways, us by row tiles of 128 after 16384 keys (head_dim 256, 4 KV heads | 128, 8 KV heads):
 //   keys widened by every CTA | once:      4: 50 | 56, 6: 63 | 68, 8: 80 | 82, 12: 104 | 105, 16: 130 | 128, 32: 233 | 217
 //                                          4: 60 | 63, 6: 82 | 81, 8: 101 | 96, 12: 140 | 126, 32: 344 | 287

@@ -41,6 +41,7 @@ CASES = [  # tokens, history, hkv, G, d
     (100, 413, 2, 4, 128), (333, 47, 1, 5, 256), (513, 0, 2, 2, 128), (64, 1999, 8, 4, 128), (40, 3000, 1, 12, 256),
     (5, 700, 3, 20, 128), (777, 600, 1, 3, 256),
     (1, 40000, 3, 1, 128), (1, 30000, 2, 1, 256), (129, 20000, 1, 1, 256), (30, 2500, 3, 8, 256), (100, 1500, 2, 5, 128),
+    (3, 5, 300, 2, 128), (150, 90, 200, 1, 256), (260, 10, 170, 1, 128),  # more KV heads than SMs
     (120, 900, 2, 6, 128), (110, 900, 2, 6, 256), (150, 900, 2, 6, 128), (150, 5000, 3, 6, 256)]
 
 

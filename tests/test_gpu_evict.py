@@ -97,6 +97,7 @@ CASES = [  # lens, hkv, d, keep, sink, recent
     ([1], 1, 128, 1, 0, 0), ([2], 1, 256, 1, 0, 1), ([17], 3, 128, 16, 0, 0), ([33, 0, 16, 5], 2, 256, 16, 1, 4),
     ([100, 64, 65, 1], 2, 128, 64, 4, 60), ([257, 300], 2, 256, 250, 4, 32), ([1025] * 3, 4, 128, 1024, 4, 64),
     ([1500, 700, 31], 5, 128, 333, 0, 50), ([2049], 1, 256, 77, 2, 0), ([4100], 2, 128, 2050, 4, 100),
+    ([70, 300], 300, 128, 64, 2, 8),
     ([9000], 1, 256, 1000, 4, 128), ([9000, 8193], 2, 128, 4097, 0, 999), ([12345], 1, 128, 12344, 0, 1)]
 
 

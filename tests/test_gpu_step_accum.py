@@ -286,3 +286,35 @@ def test_the_serving_loop(kvq):
                     assert len(have) == lens[b] and {0, 1} <= have
                     assert set(range(max(0, step - recent + 1), step + 1)) <= have
     assert kvq.kvq_device_status() == 0
+
+
+def test_pages_past_two_gigabytes(kvq):
+    """The same calls on pages at the end of a pool whose K passes 2^31 bytes: the bits of a small pool."""
+    import torch
+    rng = np.random.default_rng(43)
+    hkv, G, d, T, hist, keep = 4, 6, 256, 300, 900, 500
+    n = hist + T
+    table, nb = table_of(rng, [n + 1])
+    small = R.Pool.random(rng, nb, hkv, d).to_gpu(kvq)
+    far = (1 << 31) // (hkv * d * 16) + 100 - nb
+    big = kvq.KVCache.wrap(*(torch.empty((far + nb,) + t.shape[1:], dtype=t.dtype, device="cuda")
+                             for t in (small.k, small.v, small.k_scale, small.v_scale)))
+    for t, u in zip((big.k, big.v, big.k_scale, big.v_scale), (small.k, small.v, small.k_scale, small.v_scale)):
+        t[far:] = u
+    q, k, v = (bf(rng, T, h, d)[1] for h in (hkv * G, hkv, hkv))
+    slots = table.shape[1] * 16
+    res = []
+    for cache, first in ((small, 0), (big, far)):
+        bt = dev((table + first).astype(np.int32))
+        acc = torch.zeros((1, hkv, slots), device="cuda")
+        sp = torch.arange(slots, dtype=torch.int32, device="cuda").repeat(1, hkv, 1)
+        for rows in (1, 20, T):  # one row tile, a few, and keys widened once
+            kvq.kvq_attn_chunk_weights_int8kv(cache, q[:rows], hist, bt[0], 0.05, acc[0])
+        out = kvq.kvq_decode_step_accum_int8kv(cache, k[:1], v[:1], q[:1], bt, dev(np.array([n + 1], np.int32)), n + 1, 0.05, acc,
+                                               slot_pos=sp, pos=dev(np.array([n], np.int32)))
+        for budget in (n - 20, keep):  # moves in the select kernel, and page by page
+            length = dev(np.array([n + 1 if budget != keep else n - 20], np.int32))
+            kvq.kvq_cache_evict(cache, bt, length, n + 1, budget, acc, sp, n_sink=4, n_recent=32)
+        res.append([t.cpu() for t in (out, acc, sp)] + [t[first:].cpu() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)])
+    assert kvq.kvq_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*res))
