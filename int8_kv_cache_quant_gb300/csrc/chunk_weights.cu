@@ -982,7 +982,8 @@ template <int D, int PASS, int MT, bool WIDEN>
 static cudaError_t launch_pass(const ChunkWeightsArgs& a, cudaStream_t stream) {
   using L = Cw<D, PASS, MT, WIDEN>;
   auto kern = chunk_weights_kernel<D, PASS, MT, WIDEN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kAlloc, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(a.runs[PASS - 1]), dim3(L::kThreads), L::kAlloc, stream, a);
 }

@@ -678,7 +678,8 @@ static cudaError_t launch_stage1(const DecodeArgs& a, dim3 grid, cudaStream_t st
   constexpr int DEPTH = 24 / NTEAM;
   using L = DecodeSmem<D, NT, NTEAM, DEPTH>;
   auto kern = decode_stage1_kernel<D, NT, NTEAM, DEPTH, SPLIT, MROW, WRITE, SCORES>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kTotal, done);
   if (e != cudaSuccess) return e;
   if (a.ev_begin && (e = cudaEventRecord(a.ev_begin, stream)) != cudaSuccess) return e;
   if ((e = launch_pdl(kern, grid, dim3(L::kWarps * 32), L::kTotal, stream, a)) != cudaSuccess) return e;

@@ -612,9 +612,8 @@ cudaError_t launch_evict(const EvictArgs& a, int n_sms, cudaStream_t stream) {
   const bool few = a.max_moves <= (static_cast<long long>(a.batch) * a.n_kv_heads < n_sms ? kFewMoves : kFewMovesLarge);
   auto kern = few ? evict_select_kernel<true> : evict_select_kernel<false>;
   cudaError_t e;
-  if (smem > 16 * 1024 &&
-      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4)) != cudaSuccess)
-    return e;
+  static std::atomic<uint64_t> done[2];
+  if ((e = allow_smem(reinterpret_cast<const void*>(kern), kKeyCap * 4, done[few])) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c, a.n_kv_heads, a.batch);
   cfg.blockDim = dim3(kSelThreads);

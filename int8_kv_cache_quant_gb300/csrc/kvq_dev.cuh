@@ -3,6 +3,7 @@
 // helpers, exact int8 -> fp16 widening, and the device status word.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -178,6 +179,19 @@ inline cudaError_t launch_pdl(void (*kernel)(Arg), dim3 grid, dim3 block, size_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory, always the same for a kernel: asked for once a device (`done`,
+// the kernel's own, has a bit for each), since asking costs the host as much as a launch.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 __device__ __forceinline__ float fast_log2(float x) {
