@@ -149,7 +149,7 @@ __device__ __forceinline__ void move_token(const EvictArgs& a, const int32_t* bt
 
 }  // namespace
 
-// FEW: at most kFewMoves tokens can move; the codes are moved here.
+// FEW: few tokens can move (kFewMovesLarge at most); the codes are moved here.
 template <bool FEW>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a) {
   cg::cluster_group cluster = cg::this_cluster();

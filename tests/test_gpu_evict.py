@@ -116,6 +116,13 @@ def test_long_contexts_past_the_keys_in_shared_memory(kvq):
     assert run(kvq, rng, [17001] + [16400] * 2 + [3] * 157, 1, 256, 16390, 4, 300, "zeros", in_place=True) == 0
 
 
+@pytest.mark.parametrize("kind,keep", [("spread", 5000), ("zeros", 70001), ("odd", 139990)])
+def test_clusters_whose_ranges_pass_shared_memory(kvq, kind, keep):
+    """140001 slots on eight CTAs: 17504 each."""
+    rng = np.random.default_rng(6)
+    assert run(kvq, rng, [140001], 1, 128, keep, 4, 300, kind, in_place=kind != "odd") == 0
+
+
 def test_many_moves_in_a_large_batch(kvq):
     """160 units: up to 512 moves each without the page kernel."""
     rng = np.random.default_rng(5)
