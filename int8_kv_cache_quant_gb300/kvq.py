@@ -3,6 +3,10 @@
 Every function here has the name of the C entry point it calls.  torch supplies device
 memory and the current stream; all arithmetic runs in libkvq's CUDA kernels.  There is no
 CPU fallback: if libkvq.so is missing or the call fails, an exception is raised.
+
+A call runs on the current stream, or on `stream` where one is given.  What it allocates (a workspace, a result
+that was not passed in) belongs to that stream; tensors that are passed in are ordered before and after the call
+by the caller, as with torch's own operators.
 """
 import ctypes
 import os
@@ -173,9 +177,29 @@ def _host_ok(fn, *tensors):
                              "address space (e.g. tensor.pin_memory())")
 
 
-def _new_out(shape, q):
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one).  The allocator hands a block that one stream has
+    freed to that stream's next tensor at once, so a block that the call's kernels use has to be the call's stream's."""
+    if stream is None or stream.cuda_stream == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream):
+    """_empty, for what the caller gets and will read on the current stream (after waiting for the call): the block
+    is not given away before that stream's work on it is done."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None and t.is_cuda and stream.cuda_stream != _stream(None):
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _new_out(shape, q, stream):
     # a host q (zero-copy) gets its result in page-locked host memory too
-    return torch.empty(shape, dtype=torch.float32, device=q.device, pin_memory=q.device.type == "cpu")
+    if q.device.type == "cpu":
+        return torch.empty(shape, dtype=torch.float32, pin_memory=True)
+    return _result(shape, torch.float32, q.device, stream)
 
 
 class KVCache:
@@ -248,11 +272,11 @@ def kvq_rope_quant_write(cache, q, k_new, v_new, seq_idx, pos, block_table, cos_
     if q is not None:
         dev = q.device
         if q_codes is None:
-            q_codes = torch.empty((T, Hq, D), dtype=torch.int8, device=dev)
+            q_codes = _result((T, Hq, D), torch.int8, dev, stream)
         if q_scales is None:
-            q_scales = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+            q_scales = _result((T, Hq), torch.float32, dev, stream)
         if q_rot is None:
-            q_rot = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+            q_rot = _result((T, Hq, D), torch.bfloat16, dev, stream)
     c = cache.struct()
     _check("kvq_rope_quant_write", lib().kvq_rope_quant_write(
         ctypes.byref(c), _p(q) if q is not None else None, Hq, _p(k_new), _p(v_new), T, _p(seq_idx), _p(pos),
@@ -298,12 +322,12 @@ def kvq_attn_decode_int8kv(cache, q, block_table, ctx_lens, max_ctx, softmax_sca
     pair of torch.cuda.Event recorded around the stage-1 kernel (profiling)."""
     B, Hq, D = q.shape
     if out is None:
-        out = _new_out((B, Hq, D), q)
+        out = _new_out((B, Hq, D), q, stream)
     _host_ok("kvq_attn_decode_int8kv", q, out)
     o = _decode_opts(split_rows, route_threshold, force_route, stage1_events)
     need = int(lib().kvq_decode_workspace_bytes(B, Hq, max(1, int(max_ctx)), D, ctypes.byref(o)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.k.device)
+        workspace = _empty(need, torch.uint8, cache.k.device, stream)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     c = cache.struct()
     _check("kvq_attn_decode_int8kv", lib().kvq_attn_decode_int8kv(
@@ -320,12 +344,12 @@ def kvq_attn_verify_int8kv(cache, q, block_table, ctx_lens, max_ctx, softmax_sca
     keys t < ctx_lens[b] - nq + 1 + i.  Returns out fp32 [B][nq][Hq][D]."""
     B, nq, Hq, D = q.shape
     if out is None:
-        out = _new_out((B, nq, Hq, D), q)
+        out = _new_out((B, nq, Hq, D), q, stream)
     _host_ok("kvq_attn_verify_int8kv", q, out)
     o = _decode_opts(split_rows, route_threshold, force_route, stage1_events)
     need = int(lib().kvq_verify_workspace_bytes(B, nq, Hq, max(1, int(max_ctx)), D, ctypes.byref(o)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.k.device)
+        workspace = _empty(need, torch.uint8, cache.k.device, stream)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     c = cache.struct()
     _check("kvq_attn_verify_int8kv", lib().kvq_attn_verify_int8kv(
@@ -347,7 +371,7 @@ def kvq_decode_step_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, max_ct
         q, k_new, v_new = q[:, None], k_new[:, None], v_new[:, None]
     B, nq, Hq, D = q.shape
     if out is None:
-        out = _new_out((B, nq, Hq, D), q)
+        out = _new_out((B, nq, Hq, D), q, stream)
         ret = out[:, 0] if squeeze else out
     else:
         ret = out  # the caller's buffer, in the caller's shape ([B][Hq][D] for the one-token step)
@@ -355,7 +379,7 @@ def kvq_decode_step_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, max_ct
     o = _decode_opts(split_rows, route_threshold, force_route, stage1_events, launches)
     need = int(lib().kvq_verify_workspace_bytes(B, nq, Hq, max(1, int(max_ctx)), D, ctypes.byref(o)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.k.device)
+        workspace = _empty(need, torch.uint8, cache.k.device, stream)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     c = cache.struct()
     _check("kvq_decode_step_int8kv", lib().kvq_decode_step_int8kv(
@@ -404,10 +428,9 @@ def kvq_attn_prefill_first_bf16(cache, q, k_new, v_new, block_table_row, softmax
     written into the cache as int8); returns the high-precision causal attention, fp32 [T][Hq][D]."""
     T, Hq, D = q.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float32, device=q.device)
+        out = _result((T, Hq, D), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = torch.empty(kvq_prefill_first_workspace_bytes(T, Hq, cache.n_kv_heads, D), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(kvq_prefill_first_workspace_bytes(T, Hq, cache.n_kv_heads, D), torch.uint8, q.device, stream)
     c = cache.struct()
     _check("kvq_attn_prefill_first_bf16", lib().kvq_attn_prefill_first_bf16(
         ctypes.byref(c), _p(q), _p(k_new), _p(v_new), T, Hq, _p(block_table_row), int(block_table_row.numel()),
@@ -420,10 +443,10 @@ def kvq_attn_prefill_int8(cache, q, history_len, block_table_row, softmax_scale,
     """q: bf16 [T][Hq][D]; block_table_row int32 [n]; returns out fp32 [T][Hq][D]."""
     T, Hq, D = q.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float32, device=q.device)
+        out = _result((T, Hq, D), torch.float32, q.device, stream)
     need = kvq_prefill_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), D)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     c = cache.struct()
     _check("kvq_attn_prefill_int8", lib().kvq_attn_prefill_int8(
@@ -438,10 +461,10 @@ def kvq_attn_prefill_int8_qcodes(cache, q_codes, q_scales, history_len, block_ta
     """q_codes int8 [T][Hq][D], q_scales fp32 [T][Hq] (from kvq_rope_quant_write); returns fp32 [T][Hq][D]."""
     T, Hq, D = q_codes.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float32, device=q_codes.device)
+        out = _result((T, Hq, D), torch.float32, q_codes.device, stream)
     need = kvq_prefill_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), D)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_codes.device)
+        workspace = _empty(need, torch.uint8, q_codes.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     c = cache.struct()
     _check("kvq_attn_prefill_int8_qcodes", lib().kvq_attn_prefill_int8_qcodes(
@@ -459,11 +482,10 @@ def kvq_attn_sparse_int8kv(cache, q, cell_offsets, cells, block_table_row, softm
     """q: bf16 [N][Hq][D]; cell_offsets int32 [N+1]; cells int32; returns fp32 [N][Hq][D]."""
     N, Hq, D = q.shape
     if out is None:
-        out = torch.empty((N, Hq, D), dtype=torch.float32, device=q.device)
+        out = _result((N, Hq, D), torch.float32, q.device, stream)
     nb = int(block_table_row.numel())
     if workspace is None:
-        workspace = torch.empty(kvq_sparse_workspace_bytes(nb, cache.n_kv_heads, D), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(kvq_sparse_workspace_bytes(nb, cache.n_kv_heads, D), torch.uint8, q.device, stream)
     c = cache.struct()
     _check("kvq_attn_sparse_int8kv", lib().kvq_attn_sparse_int8kv(
         ctypes.byref(c), _p(q), N, Hq, _p(cell_offsets), _p(cells), _p(block_table_row),
@@ -492,10 +514,10 @@ def _cache_struct(fn, cache, dev):
     return cache.struct()
 
 
-def _ws(workspace, need, device):
+def _ws(workspace, need, device, stream):
     """(workspace tensor, its bytes): the caller's, or one of `need` bytes on the device."""
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        workspace = _empty(max(need, 16), torch.uint8, device, stream)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -533,7 +555,7 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
         q = q[:, None]
     B, nq, Hq, D = q.shape
     if out is None:
-        out = _new_out((B, nq, Hq, D), q)
+        out = _new_out((B, nq, Hq, D), q, stream)
         ret = out[:, 0] if squeeze else out
     else:
         ret = out
@@ -566,7 +588,7 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
     need = 0
     if workspace is None:
         need = int(lib().kvq_step_accum_workspace_bytes(B, nq, Hq, int(max_ctx), D, ctypes.byref(o)))
-    workspace, wbytes = _ws(workspace, need, cache.k.device)
+    workspace, wbytes = _ws(workspace, need, cache.k.device, stream)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_decode_step_accum_int8kv(
         ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx),
@@ -595,7 +617,7 @@ def kvq_attn_chunk_weights_int8kv(cache, q, history_len, block_table_row, softma
     need = 0
     if workspace is None:
         need = kvq_chunk_weights_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), D)
-    workspace, wbytes = _ws(workspace, need, q.device)
+    workspace, wbytes = _ws(workspace, need, q.device, stream)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_attn_chunk_weights_int8kv(
         ctypes.byref(c), _p(q), T, Hq, int(history_len), _p(block_table_row), n_blocks,
@@ -622,7 +644,7 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     if in_place:
         acc_out, slot_pos_out = acc, slot_pos
     if new_lens is None:
-        new_lens = torch.empty_like(ctx_lens)
+        new_lens = _result(ctx_lens.shape, torch.int32, ctx_lens.device, stream)
     dev, n_blocks = _current_device(), block_table.shape[-1]
     ctx_p = _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
     new_p = _need(fn, "new_lens", new_lens, torch.int32, (B,), dev)
@@ -638,7 +660,7 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     if min(slots, pslots) < max_ctx or min(oslots, qslots) < min(keep, max_ctx):
         raise ValueError("%s: acc and slot_pos need max_ctx slots, the outputs min(keep, max_ctx)" % fn)
     need = kvq_evict_workspace_bytes(B, H, int(max_ctx), int(keep)) if workspace is None else 0
-    workspace, wbytes = _ws(workspace, need, cache.k.device)
+    workspace, wbytes = _ws(workspace, need, cache.k.device, stream)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_cache_evict(
         ctypes.byref(c), B, table_p, n_blocks, ctx_p, int(max_ctx), int(keep), int(n_sink), int(n_recent), acc_p, pos_p,
@@ -685,14 +707,14 @@ def kvq_rope_bf16(q, k, pos, phases, layout=ROPE_HALF, rotary_offset=0, attn_fac
     hq = qs = qos = hk = ks = kos = 0
     if q is not None:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out = _result(q.shape, torch.bfloat16, q.device, stream)
         hq, qs, q_p = _heads(fn, "q", q, T, D, dev)
         ho, qos, qo_p = _heads(fn, "q_out", q_out, T, D, dev)
         if ho != hq:
             raise ValueError("%s: q_out has %d heads, q %d" % (fn, ho, hq))
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+            k_out = _result(k.shape, torch.bfloat16, k.device, stream)
         hk, ks, k_p = _heads(fn, "k", k, T, D, dev)
         ho, kos, ko_p = _heads(fn, "k_out", k_out, T, D, dev)
         if ho != hk:
@@ -726,8 +748,8 @@ def _not_heads(fn, name, T, D):
 def kvq_debug_prefill_q_codes(q, stream=None):
     """Q quantisation step alone: returns (int8 codes [T][Hq][D], fp32 scales [T][Hq])."""
     T, Hq, D = q.shape
-    codes = torch.empty((T, Hq, D), dtype=torch.int8, device=q.device)
-    scales = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    codes = _result((T, Hq, D), torch.int8, q.device, stream)
+    scales = _result((T, Hq), torch.float32, q.device, stream)
     _check("kvq_debug_prefill_q_codes", lib().kvq_debug_prefill_q_codes(
         _p(q), T, Hq, D, _p(codes), _p(scales), _stream(stream)))
     return codes, scales
@@ -740,12 +762,12 @@ def kvq_debug_prefill_qk_int32(cache, q_codes, q_scales, history_len, block_tabl
     k0..k0+nk-1, out fp32 [T][Hq][D]).  split_tiles: -1 the call's own key-range split, 0 none,
     r > 0 a forced tail of r key tiles."""
     T, Hq, D = q_codes.shape
-    s = torch.empty((128, nk), dtype=torch.int32, device=q_codes.device)
+    s = _result((128, nk), torch.int32, q_codes.device, stream)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float32, device=q_codes.device)
+        out = _result((T, Hq, D), torch.float32, q_codes.device, stream)
     need = kvq_prefill_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), D)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_codes.device)
+        workspace = _empty(need, torch.uint8, q_codes.device, stream)
     c = cache.struct()
     _check("kvq_debug_prefill_qk_int32", lib().kvq_debug_prefill_qk_int32(
         ctypes.byref(c), _p(q_codes), _p(q_scales), T, Hq, int(history_len), _p(block_table_row),
