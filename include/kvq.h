@@ -347,7 +347,8 @@ size_t kvq_step_accum_workspace_bytes(int32_t batch, int32_t n_new, int32_t n_q_
  *   always takes the split route, with one split for a short context)
  * A key whose page is outside the pool is skipped (KVQ_DEV_BAD_BLOCK) and gets no weight; when a
  * sequence's new tokens are not written (KVQ_DEV_BAD_POS) no entry is set.  A row whose scores are
- * not finite gives its keys the weights of its formula, NaN among them.
+ * not finite gives the keys it sees the weights of its formula, NaN among them; a row that scores -infinity
+ * alone gives nothing, like one with no key.
  */
 int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
                                  int32_t batch, int32_t n_new, int32_t n_q_heads, const int32_t* block_table,
@@ -383,7 +384,8 @@ size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, in
  *                    history_len, head_dim), 16-byte aligned; its contents on entry do not matter
  * A key on a page outside the pool is skipped (KVQ_DEV_BAD_BLOCK) and gets no weight.  If a bounded wait
  * runs out (KVQ_DEV_TIMEOUT), the rows and keys it leaves unfinished add nothing.  A row whose scores are
- * not finite gives the keys it sees the weights of its formula, NaN among them.
+ * not finite gives the keys it sees the weights of its formula, NaN among them; a row that scores -infinity
+ * alone gives nothing, like one with no key.
  * KVQ_ERR_UNSUPPORTED when the rows n_tokens * (n_q_heads / n_kv_heads) or the keys history_len + n_tokens reach
  * 2^30, or the 128 x 128 score tiles of all KV heads 2^35.
  */

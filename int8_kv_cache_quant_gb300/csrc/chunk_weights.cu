@@ -876,14 +876,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeights
   const int tile = n_all / 128, n = n_all % 128;  // a CTA's rows are of one A unit
   if (tile >= a.row_tiles) return;
   const float2* p = a.row_part + (static_cast<long long>(kvh) * a.units[0] * mt + tile) * a.n_part[0] * 128 + n;
-  // (m, l) of several (m, l): the largest m, the sums moved onto it; a sum below zero marks a dropped part
+  // (m, l) of several (m, l): the largest m, the sums moved onto it; a sum below zero marks a dropped part.  A part
+  // without a maximum has the sum 0 (no key) or NaN (every score is), which stays NaN through the products.
   float m = -INFINITY, l = 0.f;
   auto merge = [&](const float2& v) {
+    const float x = fmaxf(m, v.x);
     if (v.y < 0.f || l < 0.f) {
       l = -1.f;
-    } else if (v.x != -INFINITY) {
-      const float x = fmaxf(m, v.x);
-      l = (m == -INFINITY ? 0.f : l * fast_exp2(m - x)) + v.y * fast_exp2(v.x - x);
+    } else if (x == -INFINITY) {
+      l += v.y;
+    } else {
+      l = l * fast_exp2(m - x) + v.y * fast_exp2(v.x - x);
       m = x;
     }
   };

@@ -62,8 +62,12 @@ __device__ __forceinline__ void accum_block(const StepAccumArgs& sa, int chunk, 
     const float4* st = reinterpret_cast<const float4*>(a.part_stats) + orow * a.n_split;
     float m = -INFINITY, l = 0.f;
     auto join = [&](float om, float ol) {
+      // without a maximum a sum is 0 (no key) or NaN (every score is): it stays NaN through the products below
       const float top = fmaxf(m, om);
-      if (top == -INFINITY) return;
+      if (top == -INFINITY) {
+        l += ol;
+        return;
+      }
       l = l * fast_exp2(m - top) + ol * fast_exp2(om - top);
       m = top;
     };
@@ -72,7 +76,7 @@ __device__ __forceinline__ void accum_block(const StepAccumArgs& sa, int chunk, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = s0 + i * kRowLanes < n ? st[s0 + i * kRowLanes] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) join(v[i].x, v[i].x == -INFINITY ? 0.f : v[i].z);
+      for (int i = 0; i < 4; ++i) join(v[i].x, v[i].w);
     }
 #pragma unroll
     for (int off = kRowLanes / 2; off > 0; off >>= 1) {

@@ -635,16 +635,20 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
       Ms = fmaxf(Ms, mstat[(q2 * L::kRows + hh) * 4 + 0]);
       Mz = fmaxf(Mz, mstat[(q2 * L::kRows + hh) * 4 + 1]);
     }
-    float lsum_all = 0.f;
+    float lsum_all = 0.f, no_max = 0.f;
     for (int q2 = 0; q2 < NTEAM; ++q2) {
       const float* stt = mstat + (q2 * L::kRows + hh) * 4;
       if (Ms != -INFINITY && stt[0] != -INFINITY) lsum_all += stt[2] * fast_exp2(stt[0] - Ms);
+      else if (SCORES) no_max += stt[2];
       mw[hh * NTEAM + q2] = (Mz != -INFINITY && stt[1] != -INFINITY) ? fast_exp2(stt[1] - Mz) : 0.f;
     }
     mfin[hh * 4 + 0] = Ms;
     mfin[hh * 4 + 1] = Mz;
     mfin[hh * 4 + 2] = lsum_all;
-    mfin[hh * 4 + 3] = (lsum_all > 0.f && Mz != -INFINITY) ? fast_exp2(Mz - Ms) / lsum_all : 0.f;
+    // SCORES: the sum that the weights divide by.  A team without a maximum had no key (its sum is 0) or nothing but
+    // NaN (fmaxf drops those, the sum does not), and then NaN is the row's sum.
+    if (SCORES) mfin[hh * 4 + 3] = lsum_all + no_max;
+    else mfin[hh * 4 + 3] = (lsum_all > 0.f && Mz != -INFINITY) ? fast_exp2(Mz - Ms) / lsum_all : 0.f;
   }
   __syncthreads();
   for (int idx = threadIdx.x; idx < R * D; idx += blockDim.x) {
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
         a.part_stats[pu * 4 + 0] = mfin[hh * 4 + 0];
         a.part_stats[pu * 4 + 1] = mfin[hh * 4 + 1];
         a.part_stats[pu * 4 + 2] = mfin[hh * 4 + 2];
-        a.part_stats[pu * 4 + 3] = 0.f;
+        a.part_stats[pu * 4 + 3] = SCORES ? mfin[hh * 4 + 3] : 0.f;
       }
     } else {
       a.out[orow * D + d] = o * mfin[hh * 4 + 3];

@@ -64,7 +64,7 @@ struct DecodeArgs {
   const void* v_new;
   float* out;          // fp32 [B][nq][Hq][D]
   float* part_acc;     // fp32 [B][nq][Hq][n_split][D]  (split route)
-  float* part_stats;   // fp32 [B][nq][Hq][n_split][4]  (split route: m_s, m_z, l, unused)
+  float* part_stats;   // fp32 [B][nq][Hq][n_split][4]  (split route: m_s, m_z, l, with scores: l with NaN kept)
   int split_rows;      // keys per split (split route); ignored by the single route
   int n_split;         // splits per sequence in the grid (split route)
   unsigned int* status;
