@@ -106,6 +106,22 @@ __device__ __forceinline__ void accum_block(const StepAccumArgs& sa, int chunk, 
         ahead[i] = __ldcg(reinterpret_cast<const float4*>(sc + static_cast<long long>(r0 + kRowsAhead + i) * a.scores_stride));
     }
   }
+  if (w[0] != w[0]) {
+    // A row that is not finite has made every sum NaN.  Again, row by row: it gives NaN to the keys it sees and nothing
+    // to the others, where 0 * NaN is neither.  (A branch in the loop above cost 6 of 40 us at 24 rows.)
+    const int page = a.block_table[static_cast<long long>(b) * a.max_blocks_per_seq + t / KVQ_BLOCK_SIZE];
+    w[0] = w[1] = w[2] = w[3] = 0.f;
+    for (int r = 0; r < R; ++r) {
+      const float il = row_il[r];
+      if (il == il) {
+        add(__ldcg(reinterpret_cast<const float4*>(sc + r * a.scores_stride)), r);
+      } else if (page >= 0 && page < a.num_blocks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t + i <= ctx - nq + r / G) w[i] = il;
+      }
+    }
+  }
   if (whole) {
     *reinterpret_cast<float4*>(sa.acc + at) = make_float4(old.x + w[0], old.y + w[1], old.z + w[2], old.w + w[3]);
     return;

@@ -104,3 +104,32 @@ def test_chunk_with_keys_of_nan(kvq, T, hist, keys, G, d):
     assert np.isnan(a[1, :n]).all() and (a[1, n:] == 1).all()  # the last query sees every key
     one = R.Pool(*(x[:, :1] for x in (pool.k, pool.v, pool.ks, pool.vs)))
     check_chunk(one, table[0], hist, q[:, :G], acc0[:1], a[:1], 0.07)
+
+
+@pytest.mark.parametrize("G,d,bad", [(1, 128, np.nan), (3, 256, np.nan), (2, 128, np.inf)])
+def test_step_rows_that_are_not_finite_reach_only_the_keys_they_see(kvq, G, d, bad):
+    """The first two of four query rows are not finite: the last two tokens, and the keys of a page that is not in the
+    pool, are not theirs."""
+    import torch
+    from int8_kv_cache_quant_gb300.kvq import DEV_BAD_BLOCK
+    rng = np.random.default_rng(G)
+    ctx, hkv, nq = 99, 2, 4
+    table, nb = table_of(rng, [ctx])
+    table[0, 2] = nb + 1
+    pool = R.Pool.random(rng, nb, hkv, d)
+    q, qt = bf(rng, 1, nq, hkv * G, d)
+    qt[0, :2, :, 5] = float(bad)
+    acc = dev(np.ones((1, hkv, 112), np.float32))
+    kvq.kvq_decode_step_accum_int8kv(pool.to_gpu(kvq), None, None, qt, dev(table), dev(np.array([ctx], np.int32)), ctx, 0.06, acc,
+                                     split_rows=32)
+    assert kvq.kvq_device_status() == DEV_BAD_BLOCK
+    a = acc.cpu().numpy()[0]
+    seen = np.arange(112) < ctx - 2
+    seen[32:48] = False
+    assert np.isnan(a[:, seen]).all() and (a[:, 32:48] == 1).all() and (a[:, ctx:] == 1).all()
+    kf, vf, ok = pool.rows(table[0], ctx)
+    for h in range(hkv):
+        rows = q[0, 2:, h * G:(h + 1) * G].reshape(2 * G, d).astype(np.float64)
+        p, _, rel, _ = R.weights(kf[h], vf[h], ok, rows, np.repeat([ctx - 1, ctx], G), 0.06)
+        ref = 1.0 + p[:, ctx - 2:].sum(0)
+        assert (np.abs(a[h, ctx - 2:ctx] - ref) <= (rel[:, None] * p[:, ctx - 2:]).sum(0) + (nq * G + 1) * 2.0 ** -24 * ref).all()
