@@ -905,9 +905,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeights
     if (warp != 0) return;
     for (int i = 1; i < WARPS; ++i) merge(part_s[i][lane]);
   }
-  // a row with no key (or without its sum) gives no weight
+  // A row with no key gives no weight; nor does one without its sum, whatever its scores: 2^(s - inf) is 0, while 2^s
+  // may be infinite.
   const long long r = (static_cast<long long>(kvh) * a.row_tiles + tile) * 128 + n;
-  a.row_nm[r] = m == -INFINITY ? 0.f : -m;
+  a.row_nm[r] = l < 0.f ? -INFINITY : m == -INFINITY ? 0.f : -m;
   a.row_il[r] = l < 0.f || l == 0.f ? 0.f : __fdiv_rn(1.0f, l);
 }
 

@@ -133,3 +133,33 @@ def test_step_rows_that_are_not_finite_reach_only_the_keys_they_see(kvq, G, d, b
         p, _, rel, _ = R.weights(kf[h], vf[h], ok, rows, np.repeat([ctx - 1, ctx], G), 0.06)
         ref = 1.0 + p[:, ctx - 2:].sum(0)
         assert (np.abs(a[h, ctx - 2:ctx] - ref) <= (rel[:, None] * p[:, ctx - 2:]).sum(0) + (nq * G + 1) * 2.0 ** -24 * ref).all()
+
+
+@pytest.mark.parametrize("T,hist", [(1000, 3000), (300, 4000)])  # keys widened once, and by each CTA
+def test_rows_that_a_timeout_left_out_give_nothing_whatever_their_scores(kvq, T, hist):
+    """Scores far past 2^128, whose exponential is infinite: the rows that the first run of the row pass did not finish
+    (host-injected) give 0, not infinity times 0."""
+    import torch
+    from int8_kv_cache_quant_gb300.kvq import DEV_TIMEOUT
+    rng = np.random.default_rng(T)
+    hkv, G, d, scale = 1, 2, 128, 20.0
+    table, nb = table_of(rng, [hist + T])
+    pool = R.Pool.random(rng, nb, hkv, d)
+    q, qt = bf(rng, T, G, d)
+    acc = torch.zeros((1, hist + T), device="cuda")
+    cache, bt = pool.to_gpu(kvq), dev(table[0])
+    try:
+        kvq.kvq_debug_fault_inject(4, 20_000_000)
+        kvq.kvq_attn_chunk_weights_int8kv(cache, qt, hist, bt, scale, acc)
+        assert kvq.kvq_device_status() == DEV_TIMEOUT
+    finally:
+        kvq.kvq_debug_fault_inject(0, 0)
+    a = acc.double().cpu().numpy()
+    # whole row tiles are gone, each other row gives 1 up to the relative error of a weight (as R.weights bounds it)
+    k = pool.rows(table[0], hist + T)[0][0]
+    amp = (np.abs(q.reshape(T * G, d)) @ np.abs(k).T).max() * scale * 1.4427
+    rel = 4 * np.log(2) * amp * (d / 16 + 5) * 2.0 ** -23 + 4 * 2.0 ** -22 + (hist + T) * 2.0 ** -24
+    assert amp > 1000 and rel < 0.1
+    assert np.isfinite(a).all() and (a >= 0).all()
+    kept = [T * G - x for x in range(128, T * G, 128)]
+    assert min(abs(a.sum() - n) - n * rel for n in kept) <= 0, a.sum()
