@@ -61,8 +61,6 @@ kvq_decode_opts decode_defaults(const kvq_decode_opts* o) {
   return r;
 }
 
-constexpr int kMaxSplits = 16384;
-
 // Test-only fault injection (kvq_debug_fault_inject): the mode and the wait budget that the
 // kernels launched from now on receive.
 std::atomic<int> g_fault_mode{0};
@@ -270,7 +268,7 @@ int decode_plan(const kvq_cache* cache, int32_t batch, int32_t nq, int32_t n_q_h
   plan->bytes = 0;
   if (split) {
     const long long n_split = (static_cast<long long>(mc) + o.split_rows - 1) / o.split_rows;
-    if (n_split > kMaxSplits) return KVQ_ERR_UNSUPPORTED;
+    if (n_split > kvq::kMaxSplits) return KVQ_ERR_UNSUPPORTED;
     plan->n_split = static_cast<int>(n_split);
     plan->bytes = decode_workspace_bytes(batch * nq, n_q_heads, mc, cache->head_dim, o.split_rows);
   }
@@ -458,6 +456,7 @@ int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, cons
   a.acc_stride = acc_stride;
   a.slot_pos = slot_pos;
   a.pos = pos;
+  if (!kvq::step_accum_grid_ok(a.d)) return KVQ_ERR_UNSUPPORTED;
   int launched = 0;
   const int rc = cuda_status(kvq::launch_step_accum(a, static_cast<cudaStream_t>(stream), &launched));
   if (o.launches) *o.launches = launched;
@@ -931,7 +930,7 @@ int kvq_debug_stream_floor(const kvq_cache* cache, int32_t batch, const int32_t*
     split_rows = kvq_decode_auto_split_rows(batch, cache->n_kv_heads, cache->head_dim, max_ctx, sms);
   }
   const long long n_split = (static_cast<long long>(max_ctx) + split_rows - 1) / split_rows;
-  if (n_split > kMaxSplits) return KVQ_ERR_UNSUPPORTED;
+  if (n_split > kvq::kMaxSplits) return KVQ_ERR_UNSUPPORTED;
   kvq::DecodeArgs a{};
   a.k = cache->k;
   a.v = cache->v;

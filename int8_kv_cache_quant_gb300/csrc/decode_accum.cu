@@ -15,6 +15,7 @@
 // 5.3 TB/s of K and V, the tail 31); few sequences are latency and the row arithmetic of stage 1 (1 x 1024: 8.5 us; 4
 // new tokens after 32763, 24 rows a KV head: 40 us, stage 1 36, tail 10 alone and part of it behind stage 1).
 // One launch for merge and weights: 11.8 -> 8.5 us at 1 x 1024 against a launch each.
+#include <atomic>
 #include <cstdint>
 
 #include "decode_merge.cuh"
@@ -160,23 +161,38 @@ __global__ void __launch_bounds__(kAccumThreads, D == 256 && WARPS ? 2 : 3) step
   accum_block(sa, x % sa.key_blocks, unit % sa.d.n_kv_heads, unit / sa.d.n_kv_heads);
 }
 
-template <int D>
-static cudaError_t launch_tail(StepAccumArgs a, cudaStream_t stream) {
-  const DecodeArgs& d = a.d;
+// CTAs of the tail: those that merge, those of keys per (sequence, KV head), all.
+struct TailGrid {
+  bool warps;
+  long long merge, keys, all;
+};
+static TailGrid tail_grid(const DecodeArgs& d) {
   const long long rows = static_cast<long long>(d.batch) * d.nq * d.n_q_heads, units = static_cast<long long>(d.batch) * d.n_kv_heads;
-  const bool warps = decode_merge_by_warps(d);
-  const long long mb = warps ? (rows + 7) / 8 : rows * (D / kMergeCols);
-  a.key_blocks = (d.max_ctx + kAccumKeys - 1) / kAccumKeys;
-  if (mb + units * a.key_blocks > INT32_MAX) return cudaErrorInvalidValue;
-  a.merge_blocks = static_cast<int>(mb);
-  const dim3 grid(static_cast<unsigned>(mb + units * a.key_blocks));
-  if (warps) return launch_pdl(step_tail_kernel<D, true>, grid, dim3(kAccumThreads), 0, stream, a);
-  const size_t smem = static_cast<size_t>(d.n_split) * sizeof(float);
-  if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(step_tail_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(step_tail_kernel<D, false>, grid, dim3(kAccumThreads), smem, stream, a);
+  TailGrid g;
+  g.warps = decode_merge_by_warps(d);
+  g.merge = g.warps ? (rows + 7) / 8 : rows * (d.head_dim / kMergeCols);
+  g.keys = (static_cast<long long>(d.max_ctx) + kAccumKeys - 1) / kAccumKeys;
+  g.all = g.merge + units * g.keys;
+  return g;
+}
+
+bool step_accum_grid_ok(const DecodeArgs& d) { return tail_grid(d).all <= INT32_MAX; }
+
+// Stage 1 writes the new tokens, so whatever can be refused is asked for before it.
+template <int D>
+static cudaError_t prepare_tail(const DecodeArgs& d, const TailGrid& g) {
+  static std::atomic<uint64_t> done{0};
+  if (g.warps || d.n_split * sizeof(float) <= 40 * 1024) return cudaSuccess;
+  return allow_smem(reinterpret_cast<const void*>(step_tail_kernel<D, false>), kMaxSplits * sizeof(float), done);
+}
+
+template <int D>
+static cudaError_t launch_tail(StepAccumArgs a, const TailGrid& g, cudaStream_t stream) {
+  a.merge_blocks = static_cast<int>(g.merge);
+  a.key_blocks = static_cast<int>(g.keys);
+  const dim3 grid(static_cast<unsigned>(g.all));
+  return g.warps ? launch_pdl(step_tail_kernel<D, true>, grid, dim3(kAccumThreads), 0, stream, a)
+                 : launch_pdl(step_tail_kernel<D, false>, grid, dim3(kAccumThreads), a.d.n_split * sizeof(float), stream, a);
 }
 
 template <int D>
@@ -199,11 +215,13 @@ static cudaError_t launch_stage1_scores(const DecodeArgs& a, dim3 grid, cudaStre
 
 cudaError_t launch_step_accum(const StepAccumArgs& a, cudaStream_t stream, int* launched) {
   *launched = 2;
-  const dim3 grid(a.d.n_split, a.d.n_kv_heads, a.d.batch);
-  const cudaError_t e = a.d.head_dim == 256 ? launch_stage1_scores<256>(a.d, grid, stream)
-                                            : launch_stage1_scores<128>(a.d, grid, stream);
+  const TailGrid g = tail_grid(a.d);
+  cudaError_t e = a.d.head_dim == 256 ? prepare_tail<256>(a.d, g) : prepare_tail<128>(a.d, g);
   if (e != cudaSuccess) return e;
-  return a.d.head_dim == 256 ? launch_tail<256>(a, stream) : launch_tail<128>(a, stream);
+  const dim3 grid(a.d.n_split, a.d.n_kv_heads, a.d.batch);
+  e = a.d.head_dim == 256 ? launch_stage1_scores<256>(a.d, grid, stream) : launch_stage1_scores<128>(a.d, grid, stream);
+  if (e != cudaSuccess) return e;
+  return a.d.head_dim == 256 ? launch_tail<256>(a, g, stream) : launch_tail<128>(a, g, stream);
 }
 
 }  // namespace kvq

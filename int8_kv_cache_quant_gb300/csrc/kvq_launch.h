@@ -83,6 +83,7 @@ enum class DecodeRoute { kSingle = 1, kSplit = 2 };
 // Test-only fault injection and wait budget of the kernels launched next (kvq_debug_fault_inject).
 int debug_fault_mode();
 long long debug_wait_budget();
+constexpr int kMaxSplits = 16384;  // decode_plan makes no more: a merging CTA has a weight for each in shared memory
 size_t decode_workspace_bytes(int batch, int n_q_heads, int max_ctx, int head_dim, int split_rows);
 // The route, split size and workspace bytes a decode call with these (checked) arguments takes:
 // the automatic split size of this GPU when opts->split_rows is 0.  A kvq_status.
@@ -107,6 +108,8 @@ struct StepAccumArgs {
   const int32_t* pos;  // int32 [B]: position of each sequence's first new token
   int merge_blocks, key_blocks;  // set by launch_step_accum: CTAs that merge, CTAs of keys per (sequence, KV head)
 };
+// The tail's CTAs can be counted (the grid's x).
+bool step_accum_grid_ok(const DecodeArgs& d);
 cudaError_t launch_step_accum(const StepAccumArgs& a, cudaStream_t stream, int* launched);
 
 // Attention weights of a chunk of queries, summed per key.  [0]: the row pass, [1]: the column pass.
