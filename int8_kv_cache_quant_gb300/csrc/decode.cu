@@ -171,32 +171,24 @@ static cudaError_t launch_stage1_rows(const DecodeArgs& a, dim3 grid, cudaStream
   }
 }
 
+// Past kMergeSmem bytes of splits' weights the merge has to ask for its shared memory (48 KB less its own arrays are
+// free); it does so before stage 1, which may write the cache.
+template <int D>
+static cudaError_t prepare_merge(const DecodeArgs& a) {
+  static std::atomic<uint64_t> done{0};
+  if (decode_merge_by_warps(a) || a.n_split * sizeof(float) <= kMergeSmem) return cudaSuccess;
+  return allow_smem(reinterpret_cast<const void*>(decode_merge_kernel<D>), kMaxSplits * sizeof(float), done);
+}
+
+template <int D>
 static cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream) {
-  cudaError_t e;
   const long long units = static_cast<long long>(a.batch) * a.nq * a.n_q_heads;
+  cudaError_t e;
   if (decode_merge_by_warps(a)) {
-    const dim3 gw(static_cast<unsigned>((units + 7) / 8));
-    e = a.head_dim == 256 ? launch_pdl(decode_merge_warp_kernel<256>, gw, dim3(256), 0, stream, a)
-                          : launch_pdl(decode_merge_warp_kernel<128>, gw, dim3(256), 0, stream, a);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
-  }
-  const size_t wbytes = static_cast<size_t>(a.n_split) * sizeof(float);
-  dim3 g2(a.n_q_heads, a.batch * a.nq, a.head_dim / kMergeCols);
-  if (a.head_dim == 256) {
-    if (wbytes > 48 * 1024) {
-      e = cudaFuncSetAttribute(decode_merge_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(wbytes));
-      if (e != cudaSuccess) return e;
-    }
-    e = launch_pdl(decode_merge_kernel<256>, g2, dim3(kMergeThreads), wbytes, stream, a);
+    e = launch_pdl(decode_merge_warp_kernel<D>, dim3(static_cast<unsigned>((units + 7) / 8)), dim3(256), 0, stream, a);
   } else {
-    if (wbytes > 48 * 1024) {
-      e = cudaFuncSetAttribute(decode_merge_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(wbytes));
-      if (e != cudaSuccess) return e;
-    }
-    e = launch_pdl(decode_merge_kernel<128>, g2, dim3(kMergeThreads), wbytes, stream, a);
+    const dim3 g2(a.n_q_heads, a.batch * a.nq, D / kMergeCols);
+    e = launch_pdl(decode_merge_kernel<D>, g2, dim3(kMergeThreads), a.n_split * sizeof(float), stream, a);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -210,13 +202,11 @@ cudaError_t launch_decode(const DecodeArgs& a, DecodeRoute route, cudaStream_t s
     return launch_stage1_rows<128, false>(a, grid, stream);
   }
   dim3 grid(a.n_split, a.n_kv_heads, a.batch);
-  cudaError_t e;
-  if (a.head_dim == 256)
-    e = launch_stage1_rows<256, true>(a, grid, stream);
-  else
-    e = launch_stage1_rows<128, true>(a, grid, stream);
+  cudaError_t e = a.head_dim == 256 ? prepare_merge<256>(a) : prepare_merge<128>(a);
   if (e != cudaSuccess) return e;
-  return launch_decode_merge(a, stream);
+  e = a.head_dim == 256 ? launch_stage1_rows<256, true>(a, grid, stream) : launch_stage1_rows<128, true>(a, grid, stream);
+  if (e != cudaSuccess) return e;
+  return a.head_dim == 256 ? launch_decode_merge<256>(a, stream) : launch_decode_merge<128>(a, stream);
 }
 
 }  // namespace kvq

@@ -182,7 +182,7 @@ bool step_accum_grid_ok(const DecodeArgs& d) { return tail_grid(d).all <= INT32_
 template <int D>
 static cudaError_t prepare_tail(const DecodeArgs& d, const TailGrid& g) {
   static std::atomic<uint64_t> done{0};
-  if (g.warps || d.n_split * sizeof(float) <= 40 * 1024) return cudaSuccess;
+  if (g.warps || d.n_split * sizeof(float) <= kMergeSmem) return cudaSuccess;
   return allow_smem(reinterpret_cast<const void*>(step_tail_kernel<D, false>), kMaxSplits * sizeof(float), done);
 }
 

@@ -17,6 +17,7 @@ namespace kvq {
 // dims; each thread keeps 8 independent loads in flight.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeCols = 64;
+constexpr size_t kMergeSmem = 40 * 1024;  // of splits' weights: with the merge's own arrays below the 48 KB of any kernel
 
 // wts: [n_split] weights of the partial accumulators (shared memory).
 template <int D>

@@ -71,3 +71,28 @@ def test_steps_of_many_splits_from_two_host_threads():
         # 1500 calls 8 a[0] + 1500 a[8] = 1500.  1500 additions are each within half a step of a sum below 256 (2^-17),
         # and a weight's relative error is that of its score (below 8 in log2 units) and a few exponentials: 1e-5
         assert abs(8 * a[0] + 1500 * a[8] - 1500) < 8 * 1500 * 2.0 ** -17 + 1500 * 1e-5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n_split", [10240, 10241, 11200, 11800, 12288, 12289, 16384])
+def test_a_decode_step_of_many_splits(n_split, d):
+    """Whatever the bound of the lengths: the result of the call with the smallest bound, to the bit (a short context's
+    splits are the same)."""
+    import torch
+    rng = np.random.default_rng(n_split)
+    n, hkv, G = 100, 1, 4
+    bits = lambda *shape: torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(torch.bfloat16).cuda()  # noqa: E731
+    q, k_new, v_new, kf, vf = bits(1, G, d), bits(1, hkv, d), bits(1, hkv, d), bits(n - 1, hkv, d), bits(n - 1, hkv, d)
+    ctx = torch.tensor([n], dtype=torch.int32, device="cuda")
+    res = []
+    for slots in (112, 16 * n_split):
+        cache = k.KVCache(7, hkv, d)
+        table = torch.full((1, slots // 16), -1, dtype=torch.int32, device="cuda")
+        table[0, :7] = torch.arange(7)
+        k.kvq_quant_write(cache, kf, vf, torch.zeros(n - 1, dtype=torch.int32, device="cuda"),
+                          torch.arange(n - 1, dtype=torch.int32, device="cuda"), table)
+        out = k.kvq_decode_step_int8kv(cache, k_new, v_new, q, table, ctx, slots, 0.1, split_rows=16, force_route=2)
+        res.append((out, k.kvq_attn_decode_int8kv(cache, q, table, ctx, slots, 0.1, split_rows=16, force_route=2), cache.k, cache.v))
+    assert k.kvq_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*res))
