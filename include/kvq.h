@@ -187,7 +187,8 @@ size_t kvq_decode_workspace_bytes(int32_t batch, int32_t n_q_heads, int32_t max_
  * one split: on a GPU that one CTA per (sequence, KV head) does not fill, splitting even a
  * 1024-key context is faster ([DOT4]'s table switches at 2048 keys for a smaller GPU).
  *   q          : device bf16 [batch][n_q_heads][head_dim]
- *   block_table: device int32 [batch][max_blocks_per_seq]
+ *   block_table: device int32 [batch][max_blocks_per_seq]; a row maps fewer than 2^31 keys (max_blocks_per_seq < 2^27)
+ *                in every decode, verify and step call, else KVQ_ERR_UNSUPPORTED
  *   ctx_lens   : device int32 [batch], each in [0, max_ctx]; ctx 0 gives zeros; a ctx above
  *                max_ctx (or above what the sequence's block-table row maps) is clamped to it on
  *                both routes and sets KVQ_DEV_BAD_POS
