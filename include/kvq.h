@@ -152,7 +152,9 @@ int kvq_rope_quant_write(const kvq_cache* cache, const void* q, int32_t n_q_head
 /* Options of kvq_attn_decode_int8kv (pass NULL for the defaults). */
 typedef struct kvq_decode_opts {
   int32_t split_rows;      /* keys per split in the split route, a multiple of 16; 0 -> sized to
-                            * the GPU by kvq_decode_auto_split_rows */
+                            * the GPU by kvq_decode_auto_split_rows.  The split route takes at most 16384
+                            * splits of max_ctx (KVQ_ERR_UNSUPPORTED past them): any max_ctx up to 2^25 with
+                            * 0, 16384 * split_rows otherwise */
   int32_t route_threshold; /* > 0: max_ctx <= threshold -> single-CTA route ([DOT4] route table
                             * uses 2048); 0 -> automatic: the split route whenever the split size
                             * leaves more than one split of max_ctx, else the single-CTA route */
@@ -343,7 +345,8 @@ size_t kvq_step_accum_workspace_bytes(int32_t batch, int32_t n_new, int32_t n_q_
  *   slot_pos  : device int32 [batch][n_kv_heads][acc_stride], or NULL (only with k_new)
  *   pos       : device int32 [batch], or NULL; given exactly when slot_pos is
  *   workspace : device, >= kvq_step_accum_workspace_bytes(...), 16-byte aligned
- *   max_ctx   : > 0, at most 2^30 (KVQ_ERR_UNSUPPORTED past it)
+ *   max_ctx   : > 0, at most 2^30 and at most 16384 splits (KVQ_ERR_UNSUPPORTED past either): 2^25 with the
+ *               automatic split, 2^30 from split_rows = 65536 on
  *   other arguments as kvq_decode_step_int8kv; opts->force_route 1 is KVQ_ERR_UNSUPPORTED (the call
  *   always takes the split route, with one split for a short context)
  * A key whose page is outside the pool is skipped (KVQ_DEV_BAD_BLOCK) and gets no weight; when a
