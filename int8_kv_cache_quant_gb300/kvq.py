@@ -39,6 +39,15 @@ class _Cache(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class _Int32:
+    """An int32 argument of the calls that answer a size, checked as it is converted."""
+
+    @classmethod
+    def from_param(cls, v):
+        _fit("kvq", v)
+        return ctypes.c_int32(int(v))
+
+
 class _DecodeOpts(ctypes.Structure):
     _fields_ = [("split_rows", ctypes.c_int32), ("route_threshold", ctypes.c_int32),
                 ("force_route", ctypes.c_int32), ("stage1_event_begin", ctypes.c_void_p),
@@ -76,45 +85,45 @@ def lib():
         L.kvq_attn_prefill_int8_qcodes.argtypes = [cp, vp, vp, i32, i32, i32, vp, i32, f32, vp, vp, sz, vp]
         L.kvq_decode_workspace_bytes.restype = sz
         L.kvq_decode_auto_split_rows.restype = i32
-        L.kvq_decode_auto_split_rows.argtypes = [i32, i32, i32, i32, i32]
+        L.kvq_decode_auto_split_rows.argtypes = [_Int32, _Int32, _Int32, _Int32, _Int32]
         L.kvq_prefill_split_tiles.restype = i32
         L.kvq_device_accessible.restype = i32
         L.kvq_device_accessible.argtypes = [ctypes.c_void_p]
-        L.kvq_prefill_split_tiles.argtypes = [i32, i32, i32, i32]
-        L.kvq_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(_DecodeOpts)]
+        L.kvq_prefill_split_tiles.argtypes = [_Int32, _Int32, _Int32, _Int32]
+        L.kvq_decode_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32, ctypes.POINTER(_DecodeOpts)]
         L.kvq_attn_decode_int8kv.argtypes = [cp, vp, i32, i32, vp, i32, vp, i32, f32, vp, vp, sz,
                                              ctypes.POINTER(_DecodeOpts), vp]
         L.kvq_attn_decode_int8kv_noalloc.argtypes = [cp, vp, i32, i32, vp, i32, vp, i32, f32, vp,
                                                      ctypes.POINTER(_DecodeOpts), vp]
         L.kvq_verify_workspace_bytes.restype = sz
-        L.kvq_verify_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(_DecodeOpts)]
+        L.kvq_verify_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32, _Int32, ctypes.POINTER(_DecodeOpts)]
         L.kvq_attn_verify_int8kv.argtypes = [cp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, vp, sz,
                                              ctypes.POINTER(_DecodeOpts), vp]
         L.kvq_decode_step_int8kv.argtypes = [cp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, vp, sz,
                                              ctypes.POINTER(_DecodeOpts), vp]
         i64 = ctypes.c_int64
         L.kvq_step_accum_workspace_bytes.restype = sz
-        L.kvq_step_accum_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(_DecodeOpts)]
+        L.kvq_step_accum_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32, _Int32, ctypes.POINTER(_DecodeOpts)]
         L.kvq_decode_step_accum_int8kv.argtypes = [cp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, vp, i64,
                                                    vp, vp, vp, sz, ctypes.POINTER(_DecodeOpts), vp]
         L.kvq_chunk_weights_workspace_bytes.restype = sz
-        L.kvq_chunk_weights_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.kvq_chunk_weights_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32, _Int32]
         L.kvq_attn_chunk_weights_int8kv.argtypes = [cp, vp, i32, i32, i32, vp, i32, f32, vp, i64, vp, sz, vp]
         L.kvq_evict_workspace_bytes.restype = sz
-        L.kvq_evict_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.kvq_evict_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32]
         L.kvq_cache_evict.argtypes = [cp, i32, vp, i32, vp, i32, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp, vp, sz, vp]
         L.kvq_rope_phases.argtypes = [i32, ctypes.c_double, ctypes.POINTER(_RopeScaling),
                                       ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_float)]
         L.kvq_rope_bf16.argtypes = [vp, vp, i64, i64, i32, vp, vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, i32, f32, vp]
         L.kvq_prefill_first_workspace_bytes.restype = sz
-        L.kvq_prefill_first_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.kvq_prefill_first_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32]
         L.kvq_attn_prefill_first_bf16.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, f32, vp, vp, sz, vp]
         L.kvq_prefill_workspace_bytes.restype = sz
-        L.kvq_prefill_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.kvq_prefill_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32, _Int32]
         L.kvq_attn_prefill_int8.argtypes = [cp, vp, i32, i32, i32, vp, i32, f32, vp, vp, sz, vp]
         L.kvq_attn_sparse_int8kv.argtypes = [cp, vp, i32, i32, vp, vp, vp, i32, f32, vp, vp, sz, vp]
         L.kvq_sparse_workspace_bytes.restype = sz
-        L.kvq_sparse_workspace_bytes.argtypes = [i32, i32, i32]
+        L.kvq_sparse_workspace_bytes.argtypes = [_Int32, _Int32, _Int32]
         L.kvq_debug_prefill_q_codes.argtypes = [vp, i32, i32, i32, vp, vp, vp]
         L.kvq_debug_fault_inject.argtypes = [i32, ctypes.c_int64]
         L.kvq_debug_stream_floor.argtypes = [cp, i32, vp, i32, vp, i32, i32, vp]
@@ -155,6 +164,13 @@ def _hp(t):
         raise ValueError("a host tensor must be page-locked memory mapped into the device's address space "
                          "(e.g. tensor.pin_memory())")
     return t.data_ptr()
+
+
+def _fit(fn, *values):
+    """Refuses whole numbers that ctypes would cut to their low 32 bits: a budget of 2^32 + 1 would evict all but one."""
+    for v in values:
+        if (int(v) + 0x80000000) >> 32:
+            raise ValueError("%s: %d does not fit in 32 bits" % (fn, v))
 
 
 def _check(fn, status):
@@ -265,6 +281,7 @@ def kvq_rope_quant_write(cache, q, k_new, v_new, seq_idx, pos, block_table, cos_
     rule on Q, K and V; K/V into the cache.  q: bf16 [T][Hq][D] or None.  Returns
     (q_codes int8 [T][Hq][D], q_scales fp32 [T][Hq], q_rot bf16 [T][Hq][D]), allocated when not
     given (None when q is None)."""
+    _fit("kvq_rope_quant_write", rotary_dim)
     bt = block_table if block_table.dim() == 2 else block_table.view(1, -1)
     T = int(seq_idx.numel())
     Hq = int(q.shape[1]) if q is not None else 0
@@ -287,6 +304,7 @@ def kvq_rope_quant_write(cache, q, k_new, v_new, seq_idx, pos, block_table, cos_
 
 
 def _decode_opts(split_rows, route_threshold, force_route, events=None, launches=None):
+    _fit("split_rows, route_threshold, force_route", split_rows, route_threshold, force_route)
     ev0 = ev1 = None
     if events is not None:
         ev0, ev1 = (ctypes.c_void_p(e.cuda_event) for e in events)
@@ -320,6 +338,7 @@ def kvq_attn_decode_int8kv(cache, q, block_table, ctx_lens, max_ctx, softmax_sca
     """q: bf16 [B][Hq][D]; block_table int32 [B][M]; ctx_lens int32 [B] (device);
     max_ctx: host bound of ctx_lens.  Returns out fp32 [B][Hq][D].  stage1_events: optional
     pair of torch.cuda.Event recorded around the stage-1 kernel (profiling)."""
+    _fit("kvq_attn_decode_int8kv", max_ctx)
     B, Hq, D = q.shape
     if out is None:
         out = _new_out((B, Hq, D), q, stream)
@@ -342,6 +361,7 @@ def kvq_attn_verify_int8kv(cache, q, block_table, ctx_lens, max_ctx, softmax_sca
                            stream=None, stage1_events=None):
     """q: bf16 [B][nq][Hq][D], the nq newest tokens of each sequence; row i of sequence b sees
     keys t < ctx_lens[b] - nq + 1 + i.  Returns out fp32 [B][nq][Hq][D]."""
+    _fit("kvq_attn_verify_int8kv", max_ctx)
     B, nq, Hq, D = q.shape
     if out is None:
         out = _new_out((B, nq, Hq, D), q, stream)
@@ -366,6 +386,7 @@ def kvq_decode_step_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, max_ct
     [B][nq][Hkv][D], positions ctx_lens[b] - nq + j) into the cache, then attend with their
     query rows q bf16 [B][nq][Hq][D].  A 3-D q ([B][Hq][D]) with 3-D k_new / v_new
     ([B][Hkv][D]) is the one-token step.  Returns out fp32 shaped like q."""
+    _fit("kvq_decode_step_int8kv", max_ctx)
     squeeze = q.dim() == 3
     if squeeze:
         q, k_new, v_new = q[:, None], k_new[:, None], v_new[:, None]
@@ -397,6 +418,7 @@ def kvq_attn_decode_int8kv_noalloc(cache, q, block_table, ctx_lens, max_ctx, sof
     """kvq_attn_decode_int8kv without a workspace argument, for callers that cannot allocate:
     the split-K partials live in a fixed scratch array inside the library.  `out` (fp32
     [B][Hq][D]) must be provided by the caller; nothing is allocated here."""
+    _fit("kvq_attn_decode_int8kv_noalloc", max_ctx)
     B, Hq, D = q.shape
     _host_ok("kvq_attn_decode_int8kv_noalloc", q, out)
     o = _decode_opts(split_rows, route_threshold, force_route)
@@ -411,6 +433,7 @@ def kvq_debug_fault_inject(mode, wait_budget_cycles=0):
     """Test entry point of the failure path (see kvq.h): mode 0 none, 1 a decode stage-1 copy left
     un-issued, 2 a prefill piece left un-issued, 3 a sparse chunk left un-issued, 4 a key tile of the chunk
     weights not announced; every bounded wait gives up after wait_budget_cycles (<= 0: the default)."""
+    _fit("kvq_debug_fault_inject", mode)
     _check("kvq_debug_fault_inject", lib().kvq_debug_fault_inject(int(mode), int(wait_budget_cycles)))
 
 
@@ -441,6 +464,7 @@ def kvq_attn_prefill_first_bf16(cache, q, k_new, v_new, block_table_row, softmax
 def kvq_attn_prefill_int8(cache, q, history_len, block_table_row, softmax_scale, out=None,
                           workspace=None, stream=None):
     """q: bf16 [T][Hq][D]; block_table_row int32 [n]; returns out fp32 [T][Hq][D]."""
+    _fit("kvq_attn_prefill_int8", history_len)
     T, Hq, D = q.shape
     if out is None:
         out = _result((T, Hq, D), torch.float32, q.device, stream)
@@ -459,6 +483,7 @@ def kvq_attn_prefill_int8(cache, q, history_len, block_table_row, softmax_scale,
 def kvq_attn_prefill_int8_qcodes(cache, q_codes, q_scales, history_len, block_table_row, softmax_scale,
                                  out=None, workspace=None, stream=None):
     """q_codes int8 [T][Hq][D], q_scales fp32 [T][Hq] (from kvq_rope_quant_write); returns fp32 [T][Hq][D]."""
+    _fit("kvq_attn_prefill_int8_qcodes", history_len)
     T, Hq, D = q_codes.shape
     if out is None:
         out = _result((T, Hq, D), torch.float32, q_codes.device, stream)
@@ -549,6 +574,7 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
     over the query heads of its KV head; the new tokens' entries start from zero.  slot_pos (int32,
     shaped like acc) receives the new tokens' positions pos[b] + j (pos: int32 [B]).  Returns out
     fp32 shaped like q."""
+    _fit("kvq_decode_step_accum_int8kv", max_ctx)
     fn = "kvq_decode_step_accum_int8kv"
     squeeze = q.dim() == 3
     if squeeze:
@@ -606,6 +632,7 @@ def kvq_attn_chunk_weights_int8kv(cache, q, history_len, block_table_row, softma
     """Adds to acc (fp32 [Hkv][>= history_len + T]) the attention weights that the causal queries q (bf16
     [T][Hq][D], at slots history_len ..) give to every key of the sequence, summed over the queries and
     over the query heads of each KV head.  block_table_row int32 [n].  Returns acc."""
+    _fit("kvq_attn_chunk_weights_int8kv", history_len)
     fn = "kvq_attn_chunk_weights_int8kv"
     T, Hq, D = q.shape
     dev, n_blocks = _current_device(), block_table_row.numel()
@@ -636,6 +663,7 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     budget move into the slots given up below it.  acc fp32 / slot_pos int32 [B][Hkv][>= max_ctx];
     acc_out / slot_pos_out: None for in place, or tensors [B][Hkv][>= min(keep, max_ctx)].  Returns
     (acc_out, slot_pos_out, new_lens int32 [B])."""
+    _fit("kvq_cache_evict", max_ctx, keep, n_sink, n_recent)
     fn = "kvq_cache_evict"
     B, H = int(ctx_lens.shape[0]), cache.n_kv_heads
     if (acc_out is None) != (slot_pos_out is None):
@@ -673,6 +701,7 @@ def kvq_rope_phases(rotary_dim, base=10000.0, scaling="none", factor=1.0, origin
     """The plan of kvq_rope_bf16: (phases, attn_factor), phases int64 [rotary_dim / 2] (the bits of the
     64-bit fractions of a turn per position).  scaling: "none", "linear", "ntk", "yarn", "bands" or
     "divisors"."""
+    _fit("kvq_rope_phases", rotary_dim)
     if scaling not in _ROPE_SCALINGS:
         raise ValueError("kvq_rope_phases: unknown scaling %r" % (scaling,))
     n = max(int(rotary_dim), 0) // 2
@@ -697,6 +726,7 @@ def kvq_rope_bf16(q, k, pos, phases, layout=ROPE_HALF, rotary_offset=0, attn_fac
     views of a packed projection (token stride free, heads and dims contiguous).  q_out / k_out:
     None for new tensors, or tensors like the inputs, the inputs themselves among them.  Returns
     (q_out, k_out)."""
+    _fit("kvq_rope_bf16", rotary_offset, layout)
     fn = "kvq_rope_bf16"
     ref = q if q is not None else k
     if ref is None:
@@ -761,6 +791,7 @@ def kvq_debug_prefill_qk_int32(cache, q_codes, q_scales, history_len, block_tabl
     of one unit: returns (S int32 [128][nk] for query rows q0..q0+127 of q_head and keys
     k0..k0+nk-1, out fp32 [T][Hq][D]).  split_tiles: -1 the call's own key-range split, 0 none,
     r > 0 a forced tail of r key tiles."""
+    _fit("kvq_debug_prefill_qk_int32", history_len, split_tiles, q_head, q0, k0, nk)
     T, Hq, D = q_codes.shape
     s = _result((128, nk), torch.int32, q_codes.device, stream)
     if out is None:
@@ -778,6 +809,7 @@ def kvq_debug_prefill_qk_int32(cache, q_codes, q_scales, history_len, block_tabl
 
 def kvq_debug_stream_floor(cache, block_table, ctx_lens, max_ctx, split_rows=0, stream=None):
     """The K/V stream of decode stage 1 alone (same grid, rings and copies, no arithmetic)."""
+    _fit("kvq_debug_stream_floor", max_ctx, split_rows)
     c = cache.struct()
     _check("kvq_debug_stream_floor", lib().kvq_debug_stream_floor(
         ctypes.byref(c), int(block_table.shape[0]), _p(block_table), int(block_table.shape[1]), _p(ctx_lens),
