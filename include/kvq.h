@@ -469,6 +469,7 @@ typedef struct kvq_rope_scaling {
  * fraction, phases[j] = round(frac(inv[j] / 2 pi) * 2^64), and the factor on cos and sin
  * (attn_factor, may be NULL).  Host only; the caller copies phases to the device once.
  *   scaling: NULL for none
+ * KVQ_ERR_INVALID_ARG, with phases left as they are, when a frequency is not a finite number.
  */
 int kvq_rope_phases(int32_t rotary_dim, double base, const kvq_rope_scaling* scaling, uint64_t* phases,
                     float* attn_factor);

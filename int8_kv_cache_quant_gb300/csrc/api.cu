@@ -644,7 +644,7 @@ int kvq_rope_phases(int32_t rotary_dim, double base, const kvq_rope_scaling* sca
   } else if (z.kind == KVQ_ROPE_DIVISORS) {
     if (!z.divisors) return KVQ_ERR_INVALID_ARG;
   }
-  for (int32_t j = 0; j < rotary_dim / 2; ++j) {
+  auto frequency = [&](int32_t j) {
     double inv = std::pow(base, -2.0 * j / r);
     if (z.kind == KVQ_ROPE_LINEAR) {
       inv /= z.factor;
@@ -656,10 +656,15 @@ int kvq_rope_phases(int32_t rotary_dim, double base, const kvq_rope_scaling* sca
       const double mix = std::min(1.0, std::max(0.0, (turns - z.low) / (z.high - z.low)));
       inv = inv / z.factor * (1.0 - mix) + inv * mix;
     } else if (z.kind == KVQ_ROPE_DIVISORS) {
-      if (!(z.divisors[j] > 0.0)) return KVQ_ERR_INVALID_ARG;
       inv /= z.divisors[j];
     }
-    double turns = inv / kTwoPi;
+    return inv;
+  };
+  // every frequency before the first phase is written: one past what a double holds has no fraction of a turn
+  for (int32_t j = 0; j < rotary_dim / 2; ++j)
+    if ((z.kind == KVQ_ROPE_DIVISORS && !(z.divisors[j] > 0.0)) || !std::isfinite(frequency(j))) return KVQ_ERR_INVALID_ARG;
+  for (int32_t j = 0; j < rotary_dim / 2; ++j) {
+    double turns = frequency(j) / kTwoPi;
     turns -= std::floor(turns);
     const double scaled = std::nearbyint(std::ldexp(turns, 64));
     phases[j] = scaled >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(scaled);
