@@ -244,6 +244,8 @@ class KVCache:
         for name, t, dtype, shape in want:
             if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError("KVCache.wrap: %s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
+            if t.device != k.device:  # the calls look at k's device alone
+                raise ValueError("KVCache.wrap: %s is on %s, k on %s" % (name, t.device, k.device))
         c = cls.__new__(cls)
         c.num_blocks, c.n_kv_heads, c.head_dim = int(nb), int(hkv), int(chunks) * 16
         c.k, c.v, c.k_scale, c.v_scale = k, v, k_scale, v_scale

@@ -74,3 +74,14 @@ def test_numbers_past_32_bits_are_refused(name, args):
 def test_sizes_asked_for_past_32_bits_are_refused(call):
     with pytest.raises((ValueError, ctypes.ArgumentError), match="32 bits"):
         call()
+
+
+@pytest.mark.parametrize("which", [1, 2, 3])
+def test_wrapped_tensors_of_different_devices_are_refused(which):
+    import torch
+    t = [torch.zeros((3, 2, 8, 16, 16), dtype=torch.int8), torch.zeros((3, 2, 128, 16), dtype=torch.int8), torch.zeros((3, 2, 16)),
+         torch.zeros((3, 2, 16))]
+    assert k.KVCache.wrap(*t).head_dim == 128
+    t[which] = t[which].to("meta")
+    with pytest.raises(ValueError, match="meta"):
+        k.KVCache.wrap(*t)
