@@ -480,8 +480,9 @@ int kvq_rope_phases(int32_t rotary_dim, double base, const kvq_rope_scaling* sca
  * pair (x, y) of frequency j of every head of token i, with turns = frac(pos[i] * phases[j] / 2^64):
  *   x' = x c - y s, y' = y c + x s, c = attn_factor cos(2 pi turns), s = attn_factor sin(2 pi turns)
  * in fp32, rounded once to bf16.  Dims outside [rotary_offset, rotary_offset + rotary_dim) are
- * copied.  The turns are exact for every position, negative ones too: -pos undoes a rotation, and is
- * the rotation's gradient.
+ * copied.  The product with the position is exact for every int32 position, negative ones too: -pos undoes a
+ * rotation, and is the rotation's gradient.  (The phases of kvq_rope_phases are rounded in double precision:
+ * an angle is within 1.1e-6 rad of its frequency's at position 2^31, and proportionally nearer before.)
  *   q, k      : device bf16 rows of n_q_heads (n_kv_heads) heads of head_dim, a token's row q_stride
  *               (k_stride) elements after the one before: a view of a packed projection is taken as
  *               it is.  n_q_heads or n_kv_heads may be 0 (its pointers are not used)

@@ -35,3 +35,20 @@ def test_a_frequency_that_is_no_number_is_refused_and_nothing_is_written(kw):
 def test_frequencies_at_the_ends_of_a_double_are_taken(kw):
     st, out, af = plan(**kw)
     assert st == 0 and not (out == 7).any() and af == 1.0
+
+
+@pytest.mark.parametrize("base,r", [(500.0, 6), (1e4, 64), (1e4, 256), (1e6, 128), (1e7, 1024)])
+def test_angles_of_far_positions_against_the_frequencies(base, r):
+    """At position 2^31, against 50 digits.  The plan rounds in double precision: the exponent 2j / r (2^-53 relative,
+    which moves base^-x by at most x ln(base) base^-x <= 1/e of that), the power (an ulp, 2^-52 relative), 2 pi and the
+    division by it (2^-53 each), all on a frequency of at most 1; then half of 2^-64 turns.  That is 4.4 times 2^-53 in
+    the angle per position."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 50
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    st, out, _ = plan(r, base)
+    assert st == 0
+    for j in range(r // 2):
+        turns = Decimal(base) ** (Decimal(-2 * j) / Decimal(r)) / two_pi
+        err = abs(Decimal(int(out[j])) / 2 ** 64 - turns % 1) * two_pi * 2 ** 31
+        assert err <= Decimal(4.4 * 2.0 ** -22 + 2.0 ** -31), (j, err)
