@@ -25,6 +25,9 @@
  *     step needs no separate host-device copies.  kvq_device_accessible() tells such a
  *     pointer from pageable host memory, which a kernel cannot read: the library cannot
  *     detect that case on the device, so a caller that may hold either checks first.
+ *   - A workspace belongs to one call at a time: calls that may run at the same time (on two streams, or in
+ *     two graphs that are replayed so) need one each.  The eviction's holds slots and pages that it reads back
+ *     as addresses, so one that another call overwrites can send it outside the cache.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *   - bf16 tensors are passed as raw 16-bit patterns (const void*).
  *   - Outputs of the attention calls are fp32 (a bf16 output would add up to 2^-9
@@ -376,7 +379,8 @@ size_t kvq_chunk_weights_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, in
  * t <= history_len + i, its own among them), added up per key:
  *   acc[kvh][t] += sum over the queries i and the query heads h of KV head kvh of p[i][h][t],
  *   p[i][h][:] = softmax over the visible t of softmax_scale * q[i][h] . k^[t].
- * Scores from the bf16 queries and the int8 codes exactly as in decode (q is not quantised); statistics
+ * Scores from the bf16 queries and the int8 codes as in decode (q is not quantised; nor is it scaled by a power
+ * of two as there, so that a row whose sum of |q code| passes fp32's range, elements near 1e34, is infinite); statistics
  * and sums in fp32, in a fixed order: the same call gives the same bits.  For all of a prompt's
  * queries call it chunk by chunk; for an observation window, with the prompt's last queries only.
  *   q              : device bf16 [n_tokens][n_q_heads][head_dim]

@@ -47,11 +47,12 @@
 // 1100 us, the two products at 1.46 PFLOP/s, 76 % of what the library's bf16 product reaches; with a quarter of
 // the multiplications 810 us, with a quarter of them and no exponentials 690 us.  Else the way of a score tile
 // through tensor memory, registers and barriers, some 1500 cycles whatever the head_dim, and the five
-// launches: a prompt of 2048 at head_dim 128 takes 77 us (row pass 35, column pass 32), 64 queries over 32768
+// launches: a prompt of 2047 at head_dim 128 takes 77 us (row pass 35, column pass 32), 32 queries over 32768
 // keys 54 us (20 and 22, of which 5 each are the pages out of memory).
 // Measured both ways, us by row tiles of 128 after 16384 keys (head_dim 256, 4 KV heads | 128, 8 KV heads):
 //   keys widened by every CTA | once:      4: 50 | 56, 6: 63 | 68, 8: 80 | 82, 12: 104 | 105, 16: 130 | 128, 32: 233 | 217
 //                                          4: 60 | 63, 6: 82 | 81, 8: 101 | 96, 12: 140 | 126, 32: 344 | 287
+//   (One rule from eight row tiles on: at head_dim 256 it costs 1 to 2 % up to 15.)
 //   one A tile a unit | two (row pass):    2: 41 | 39, 4: 59 | 50, 6: 72 | 63 and 2: 47 | 41, 4: 74 | 60, 6: 100 | 82
 #include <algorithm>
 

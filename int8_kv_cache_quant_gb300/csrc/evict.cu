@@ -27,7 +27,8 @@
 // then), the select kernel's warps move the codes too (FEW), and the second launch falls away.
 //
 // Bound.  One sequence: the chain of barriers and dependent loads (32768 to 4096 in 4 heads: 30 us, the select
-// kernel 19 on 32 SMs; 1025 to 1024 in 8 x 8: 6.6 us).  A large batch: select about half its issue slots, move the
+// kernel 19 on 32 SMs; 1025 to 1024 in 8 x 8: 6.6 us with a max_ctx of at most 1152, 12.5 from 2048 on, where the
+// host's bound leaves room for many moves).  A large batch: select about half its issue slots, move the
 // sectors of the layout, in which a token's V is a byte of every 16: 64 x 8 of up to 16384 to 2048 moves 1.12 GB
 // of sectors for 0.41 GB of tokens, about 175 us at 6.4 TB/s, select 71 us.
 #include <algorithm>
