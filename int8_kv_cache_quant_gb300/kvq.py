@@ -198,6 +198,8 @@ def _empty(shape, dtype, device, stream):
     freed to that stream's next tensor at once, so a block that the call's kernels use has to be the call's stream's."""
     if stream is None or stream.cuda_stream == _stream(None):
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # another library's, known by its handle
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
@@ -306,7 +308,8 @@ def kvq_rope_quant_write(cache, q, k_new, v_new, seq_idx, pos, block_table, cos_
 
 
 def _decode_opts(split_rows, route_threshold, force_route, events=None, launches=None):
-    _fit("split_rows, route_threshold, force_route", split_rows, route_threshold, force_route)
+    if split_rows or route_threshold or force_route:
+        _fit("split_rows, route_threshold, force_route", split_rows, route_threshold, force_route)
     ev0 = ev1 = None
     if events is not None:
         ev0, ev1 = (ctypes.c_void_p(e.cuda_event) for e in events)

@@ -99,3 +99,21 @@ def test_memory_of_a_call_on_another_stream(kvq, monkeypatch, name):
     flat = lambda r: [t for t in (r if isinstance(r, tuple) else (r,))]  # noqa: E731
     for a, b in zip(flat(want) + here.state(), flat(got) + there.state()):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_a_stream_known_by_its_handle(kvq):
+    """An object of another library that has a cuda_stream, and nothing else of torch's streams."""
+    import torch
+
+    class Handle:
+        pass
+
+    s, h = torch.cuda.Stream(), Handle()
+    h.cuda_stream = s.cuda_stream
+    here, there = Side(kvq), Side(kvq)
+    want = CALLS["evict"](kvq, here)
+    torch.cuda.synchronize()
+    got = CALLS["evict"](kvq, there, stream=h)
+    torch.cuda.synchronize()
+    assert kvq.kvq_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(list(want) + here.state(), list(got) + there.state()))

@@ -25,6 +25,7 @@ def current(monkeypatch):
 
     monkeypatch.setattr(k.kvq, "_stream", lambda s: entered[-1] if s is None else s.cuda_stream)
     monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
     return entered
 
 
