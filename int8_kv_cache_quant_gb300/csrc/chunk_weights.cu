@@ -878,18 +878,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeights
   if (tile >= a.row_tiles) return;
   const float2* p = a.row_part + (static_cast<long long>(kvh) * a.units[0] * mt + tile) * a.n_part[0] * 128 + n;
   // (m, l) of several (m, l): the largest m, the sums moved onto it; a sum below zero marks a dropped part.  A part
-  // without a maximum has the sum 0 (no key) or NaN (every score is), which stays NaN through the products.
+  // without a maximum has the sum 0 (no key) or NaN (every score is), and 2^-inf times it is the same.
   float m = -INFINITY, l = 0.f;
+  bool dropped = false;
   auto merge = [&](const float2& v) {
-    const float x = fmaxf(m, v.x);
-    if (v.y < 0.f || l < 0.f) {
-      l = -1.f;
-    } else if (x == -INFINITY) {
-      l += v.y;
-    } else {
-      l = l * fast_exp2(m - x) + v.y * fast_exp2(v.x - x);
-      m = x;
-    }
+    const float x = fmaxf(m, v.x), ref = x == -INFINITY ? 0.f : x;
+    l = fmaf(v.y, fast_exp2(v.x - ref), l * fast_exp2(m - ref));
+    m = x;
+    dropped = dropped || v.y < 0.f;
   };
   for (int i0 = warp; i0 < parts; i0 += 8 * WARPS) {
     float2 v[8];
@@ -901,11 +897,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(ChunkWeights
   }
   if (WARPS > 1) {
     static_assert(WARPS == 1 || WARPS == kRowWarps, "a block barrier joins one group");
-    part_s[warp][lane] = make_float2(m, l);
+    part_s[warp][lane] = make_float2(m, dropped ? -1.f : l);
     __syncthreads();
     if (warp != 0) return;
     for (int i = 1; i < WARPS; ++i) merge(part_s[i][lane]);
   }
+  if (dropped) l = -1.f;
   // A row with no key gives no weight; nor does one without its sum, whatever its scores: 2^(s - inf) is 0, while 2^s
   // may be infinite.
   const long long r = (static_cast<long long>(kvh) * a.row_tiles + tile) * 128 + n;

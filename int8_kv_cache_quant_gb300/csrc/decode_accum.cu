@@ -63,13 +63,9 @@ __device__ __forceinline__ void accum_block(const StepAccumArgs& sa, int chunk, 
     const float4* st = reinterpret_cast<const float4*>(a.part_stats) + orow * a.n_split;
     float m = -INFINITY, l = 0.f;
     auto join = [&](float om, float ol) {
-      // without a maximum a sum is 0 (no key) or NaN (every score is): it stays NaN through the products below
-      const float top = fmaxf(m, om);
-      if (top == -INFINITY) {
-        l += ol;
-        return;
-      }
-      l = l * fast_exp2(m - top) + ol * fast_exp2(om - top);
+      // without a maximum a sum is 0 (no key) or NaN (every score is), and 2^-inf times it is the same
+      const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.f : top;
+      l = l * fast_exp2(m - ref) + ol * fast_exp2(om - ref);
       m = top;
     };
     for (int s0 = tid % kRowLanes; s0 < n; s0 += 4 * kRowLanes) {
