@@ -502,6 +502,70 @@ int kvq_rope_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_st
                   int32_t head_dim, int32_t n_tokens, const int32_t* pos, const uint64_t* phases, int32_t rotary_dim,
                   int32_t rotary_offset, int32_t layout, float attn_factor, void* stream);
 
+/* Order of the frequencies of several axes: one axis after the other, or axes taking turns (0, 1, 2, 0, 1, 2, ..),
+ * those whose section is used up left out. */
+#define KVQ_ROPE_CHUNKED 0
+#define KVQ_ROPE_TURNS 1
+/* Their ladder: frequency j of the rotated part base^(-2j / rotary_dim) whatever its axis, or the i-th frequency of an
+ * axis base^(-i / sections[axis]). */
+#define KVQ_ROPE_SHARED 0
+#define KVQ_ROPE_PER_AXIS 1
+
+/*
+ * kvq_rope_axes_phases — the plan of kvq_rope_axes_bf16 and kvq_rope_append_int8kv: positions with several axes (time,
+ * height and width of a patch; a text token has the same number on all of them).  rotary_dim is twice the sum of the
+ * sections; frequency j rotates by the position on axis axis_of[j].
+ *   n_axes      : 1 .. 4
+ *   sections    : host [n_axes], frequencies of each axis, 0 or more; rotary_dim at most 1024
+ *   scaling     : as in kvq_rope_phases, of each ladder; NULL for none.  DIVISORS only with KVQ_ROPE_SHARED
+ *   phases      : host [rotary_dim / 2], receives turns per position * 2^64; the caller copies it to the device once
+ *   axis_of     : host [rotary_dim / 2], receives the axes; stays on the host
+ *   attn_factor : receives the factor on cos and sin, or NULL
+ * Host only.  Nothing is written on an error.
+ */
+int kvq_rope_axes_phases(int32_t n_axes, const int32_t* sections, int32_t order, int32_t ladder, double base,
+                         const kvq_rope_scaling* scaling, uint64_t* phases, uint8_t* axis_of, float* attn_factor);
+
+/*
+ * kvq_rope_axes_bf16 — kvq_rope_bf16 with positions on n_axes axes: the pair of frequency j of token i rotates by
+ * pos[axis_of[j]][i].  With one axis and inverse 0 it gives the bits of kvq_rope_bf16.
+ *   pos     : device int32 [n_axes][pos_stride], pos_stride >= n_tokens (not used with one axis)
+ *   axis_of : host [rotary_dim / 2], each below n_axes; read before the call returns
+ *   inverse : 1 turns the other way (sin negated, the factor kept): the gradient of the rotation
+ *   other arguments as kvq_rope_bf16.
+ */
+int kvq_rope_axes_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                       const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_kv_heads,
+                       int32_t head_dim, int32_t n_tokens, const int32_t* pos, int64_t pos_stride, int32_t n_axes,
+                       const uint64_t* phases, const uint8_t* axis_of, int32_t rotary_dim, int32_t rotary_offset,
+                       int32_t layout, float attn_factor, int32_t inverse, void* stream);
+
+/*
+ * kvq_rope_append_int8kv — new tokens into the cache in one call, by positions that need not be slots (kvq_rope_quant_write
+ * takes positions that are, and a table): q rotated to bf16, k rotated, k and v quantised by the kvq_quant_write rule and
+ * written to slot[i] of sequence seq_idx[i].  Exactly, so that the codes are determined: cos and sin are the fp32
+ * numbers nearest to attn_factor cos(2 pi turns) and attn_factor sin(2 pi turns) (one in some 2^19 is the neighbour),
+ * and each pair becomes x' = RN(RN(x c) - RN(y s)), y' = RN(RN(y c) + RN(x s)) in fp32; q rounds those to bf16, k's
+ * codes come from them unrounded.
+ *   q, q_out     : device bf16 rows, a token's q_stride (q_out_stride) elements after the one before; q itself as q_out
+ *                  (in place), or rows that do not overlap the inputs.  n_q_heads 0: no queries
+ *   k_new, v_new : device bf16 rows of the cache's heads, k_stride and v_stride elements apart (views of a packed projection)
+ *   seq_idx, slot: device int32 [n_tokens].  slot -1 marks a padding token: nothing of it is written, its row of
+ *                  q_out neither.  Tokens must target distinct slots
+ *   block_table  : device int32 [num_seqs][max_blocks_per_seq]
+ *   pos, phases, axis_of, attn_factor : as kvq_rope_axes_bf16 (attn_factor finite)
+ *   rotary_dim   : a multiple of 16, rotary_offset of 8 (KVQ_ERR_UNSUPPORTED otherwise)
+ * Rows start on 16-byte boundaries: pointers 16-byte aligned, strides multiples of 8 (KVQ_ERR_MISALIGNED).
+ * A token whose seq_idx, slot or page is out of range writes no K/V and sets KVQ_DEV_BAD_SEQ / KVQ_DEV_BAD_POS /
+ * KVQ_DEV_BAD_BLOCK; its q is rotated all the same.
+ */
+int kvq_rope_append_int8kv(const kvq_cache* cache, const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride,
+                           int32_t n_q_heads, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                           int32_t n_tokens, const int32_t* seq_idx, const int32_t* slot, const int32_t* block_table,
+                           int32_t num_seqs, int32_t max_blocks_per_seq, const int32_t* pos, int64_t pos_stride,
+                           int32_t n_axes, const uint64_t* phases, const uint8_t* axis_of, int32_t rotary_dim,
+                           int32_t rotary_offset, int32_t layout, float attn_factor, void* stream);
+
 /* Workspace (bytes) of kvq_attn_prefill_int8 for a chunk of n_tokens queries after
  * history_len keys: the int8 Q codes and their fp32 scales, and the K/V codes of every
  * (KV head, 128-key tile) of the history_len + n_tokens keys widened once to fp16 in the

@@ -673,17 +673,24 @@ int kvq_rope_phases(int32_t rotary_dim, double base, const kvq_rope_scaling* sca
   return KVQ_OK;
 }
 
-int kvq_rope_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
-                  const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_kv_heads,
-                  int32_t head_dim, int32_t n_tokens, const int32_t* pos, const uint64_t* phases, int32_t rotary_dim,
-                  int32_t rotary_offset, int32_t layout, float attn_factor, void* stream) {
+}  // extern "C"
+
+// What the calls that rotate rows check of them, and their arguments but for the positions.
+static int rope_rows(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                     const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_kv_heads,
+                     int32_t head_dim, int32_t n_tokens, const int32_t* pos, const uint64_t* phases, int32_t rotary_dim,
+                     int32_t rotary_offset, int32_t layout, float attn_factor, kvq::RopeArgs* args, bool* nothing) {
+  *nothing = false;
   if (n_tokens < 0 || n_q_heads < 0 || n_kv_heads < 0 || head_dim <= 0) return KVQ_ERR_INVALID_ARG;
   if (layout != KVQ_ROPE_HALF && layout != KVQ_ROPE_INTERLEAVED) return KVQ_ERR_UNSUPPORTED;
   if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_offset < 0 ||
       static_cast<long long>(rotary_offset) + rotary_dim > head_dim)
     return KVQ_ERR_INVALID_ARG;
   if (head_dim > 1024 || static_cast<long long>(n_q_heads) + n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
-  if (n_tokens == 0 || n_q_heads + n_kv_heads == 0) return KVQ_OK;
+  if (n_tokens == 0 || n_q_heads + n_kv_heads == 0) {
+    *nothing = true;
+    return KVQ_OK;
+  }
   if (!pos || !phases) return KVQ_ERR_INVALID_ARG;
   if (n_q_heads && (!q || !q_out)) return KVQ_ERR_INVALID_ARG;
   if (n_kv_heads && (!k || !k_out)) return KVQ_ERR_INVALID_ARG;
@@ -699,9 +706,7 @@ int kvq_rope_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_st
   auto odd = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) != 0; };
   if (odd(q) || odd(q_out) || odd(k) || odd(k_out) || !aligned4(pos) || reinterpret_cast<uintptr_t>(phases) % 8 != 0)
     return KVQ_ERR_MISALIGNED;
-  const int sms = device_sm_count();
-  if (sms <= 0) return KVQ_ERR_CUDA;
-  kvq::RopeArgs a{};
+  kvq::RopeArgs& a = *args;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
   a.q_out = static_cast<uint16_t*>(q_out);
@@ -720,7 +725,169 @@ int kvq_rope_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_st
   a.rotary_offset = rotary_offset;
   a.interleaved = layout == KVQ_ROPE_INTERLEAVED;
   a.attn_factor = attn_factor;
+  return KVQ_OK;
+}
+
+// Positions on several axes; axis_of (host) names the axis of each of the n frequencies.
+static int rope_axes(const int32_t* pos, int64_t pos_stride, int32_t n_axes, const uint8_t* axis_of, int32_t n,
+                     int32_t n_tokens, kvq::RopeAxes* ax) {
+  if (n_axes < 1 || n_axes > kvq::kMaxAxes) return KVQ_ERR_UNSUPPORTED;
+  if (!axis_of || (n_axes > 1 && pos_stride < n_tokens)) return KVQ_ERR_INVALID_ARG;
+  ax->pos = pos;
+  ax->pos_stride = n_axes > 1 ? pos_stride : 0;
+  ax->n = n_axes;
+  for (int32_t j = 0; j < n; ++j) {
+    if (axis_of[j] >= n_axes) return KVQ_ERR_INVALID_ARG;
+    ax->map[j / 16] |= static_cast<uint32_t>(axis_of[j]) << (2 * (j % 16));
+  }
+  return KVQ_OK;
+}
+
+extern "C" {
+
+int kvq_rope_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                  const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_kv_heads,
+                  int32_t head_dim, int32_t n_tokens, const int32_t* pos, const uint64_t* phases, int32_t rotary_dim,
+                  int32_t rotary_offset, int32_t layout, float attn_factor, void* stream) {
+  kvq::RopeArgs a{};
+  bool nothing;
+  const int st = rope_rows(q, q_out, q_stride, q_out_stride, n_q_heads, k, k_out, k_stride, k_out_stride, n_kv_heads,
+                           head_dim, n_tokens, pos, phases, rotary_dim, rotary_offset, layout, attn_factor, &a, &nothing);
+  if (st != KVQ_OK || nothing) return st;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
   return cuda_status(kvq::launch_rope(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int kvq_rope_axes_bf16(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                       const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_kv_heads,
+                       int32_t head_dim, int32_t n_tokens, const int32_t* pos, int64_t pos_stride, int32_t n_axes,
+                       const uint64_t* phases, const uint8_t* axis_of, int32_t rotary_dim, int32_t rotary_offset,
+                       int32_t layout, float attn_factor, int32_t inverse, void* stream) {
+  kvq::RopeAxesArgs a{};
+  bool nothing;
+  int st = rope_rows(q, q_out, q_stride, q_out_stride, n_q_heads, k, k_out, k_stride, k_out_stride, n_kv_heads, head_dim,
+                     n_tokens, pos, phases, rotary_dim, rotary_offset, layout, attn_factor, &a, &nothing);
+  if (st != KVQ_OK || nothing) return st;
+  st = rope_axes(pos, pos_stride, n_axes, axis_of, rotary_dim / 2, n_tokens, &a.axes);
+  if (st != KVQ_OK) return st;
+  a.sin_factor = inverse ? -attn_factor : attn_factor;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  return cuda_status(kvq::launch_rope_axes(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int kvq_rope_axes_phases(int32_t n_axes, const int32_t* sections, int32_t order, int32_t ladder, double base,
+                         const kvq_rope_scaling* scaling, uint64_t* phases, uint8_t* axis_of, float* attn_factor) {
+  if (n_axes < 1 || n_axes > kvq::kMaxAxes) return KVQ_ERR_UNSUPPORTED;
+  if (order != KVQ_ROPE_CHUNKED && order != KVQ_ROPE_TURNS) return KVQ_ERR_UNSUPPORTED;
+  if (ladder != KVQ_ROPE_SHARED && ladder != KVQ_ROPE_PER_AXIS) return KVQ_ERR_UNSUPPORTED;
+  if (!sections || !phases || !axis_of) return KVQ_ERR_INVALID_ARG;
+  int32_t n = 0;
+  for (int32_t i = 0; i < n_axes; ++i) {
+    if (sections[i] < 0 || sections[i] > kvq::kMaxRotaryDim / 2) return KVQ_ERR_INVALID_ARG;
+    n += sections[i];
+  }
+  if (n < 1 || n > kvq::kMaxRotaryDim / 2) return KVQ_ERR_INVALID_ARG;
+  // the axis of each frequency, and its place in its axis's own ladder
+  uint8_t axis[kvq::kMaxRotaryDim / 2];
+  int32_t place[kvq::kMaxRotaryDim / 2], used[kvq::kMaxAxes] = {};
+  for (int32_t j = 0, turn = 0; j < n; ++j) {
+    while (used[turn] == sections[turn]) turn = (turn + 1) % n_axes;
+    axis[j] = static_cast<uint8_t>(turn);
+    place[j] = used[turn]++;
+    if (order == KVQ_ROPE_TURNS) turn = (turn + 1) % n_axes;
+  }
+  uint64_t made[kvq::kMaxRotaryDim / 2];
+  float factor = 1.0f;
+  if (ladder == KVQ_ROPE_SHARED) {
+    const int st = kvq_rope_phases(2 * n, base, scaling, made, &factor);
+    if (st != KVQ_OK) return st;
+  } else {
+    if (scaling && scaling->kind == KVQ_ROPE_DIVISORS) return KVQ_ERR_UNSUPPORTED;
+    uint64_t own[kvq::kMaxRotaryDim / 2];
+    for (int32_t i = 0; i < n_axes; ++i) {
+      if (sections[i] == 0) continue;
+      const int st = kvq_rope_phases(2 * sections[i], base, scaling, own, &factor);
+      if (st != KVQ_OK) return st;
+      for (int32_t j = 0; j < n; ++j)
+        if (axis[j] == i) made[j] = own[place[j]];
+    }
+  }
+  for (int32_t j = 0; j < n; ++j) {
+    phases[j] = made[j];
+    axis_of[j] = axis[j];
+  }
+  if (attn_factor) *attn_factor = factor;
+  return KVQ_OK;
+}
+
+int kvq_rope_append_int8kv(const kvq_cache* cache, const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride,
+                           int32_t n_q_heads, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                           int32_t n_tokens, const int32_t* seq_idx, const int32_t* slot, const int32_t* block_table,
+                           int32_t num_seqs, int32_t max_blocks_per_seq, const int32_t* pos, int64_t pos_stride,
+                           int32_t n_axes, const uint64_t* phases, const uint8_t* axis_of, int32_t rotary_dim,
+                           int32_t rotary_offset, int32_t layout, float attn_factor, void* stream) {
+  int st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  const int D = cache->head_dim, H = cache->n_kv_heads;
+  if (n_tokens < 0 || n_q_heads < 0 || num_seqs <= 0 || max_blocks_per_seq <= 0) return KVQ_ERR_INVALID_ARG;
+  if (layout != KVQ_ROPE_HALF && layout != KVQ_ROPE_INTERLEAVED) return KVQ_ERR_UNSUPPORTED;
+  if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_offset < 0 ||
+      static_cast<long long>(rotary_offset) + rotary_dim > D)
+    return KVQ_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0 || rotary_offset % 8 != 0) return KVQ_ERR_UNSUPPORTED;  // whole 16-byte words of pairs
+  if (static_cast<long long>(n_q_heads) + H > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (!decode_row_ok(max_blocks_per_seq)) return KVQ_ERR_UNSUPPORTED;
+  if (!std::isfinite(attn_factor)) return KVQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return KVQ_OK;
+  if (!k_new || !v_new || !seq_idx || !slot || !block_table || !pos || !phases) return KVQ_ERR_INVALID_ARG;
+  if (n_q_heads && (!q || !q_out)) return KVQ_ERR_INVALID_ARG;
+  const long long qd = static_cast<long long>(n_q_heads) * D, kd = static_cast<long long>(H) * D;
+  if (n_tokens > 1) {
+    if (k_stride < kd || v_stride < kd || (n_q_heads && (q_stride < qd || q_out_stride < qd))) return KVQ_ERR_INVALID_ARG;
+    if (n_q_heads && q == q_out && q_stride != q_out_stride) return KVQ_ERR_INVALID_ARG;  // in place means the same rows
+    if (k_stride % 8 != 0 || v_stride % 8 != 0 || (n_q_heads && (q_stride % 8 != 0 || q_out_stride % 8 != 0)))
+      return KVQ_ERR_MISALIGNED;
+  }
+  if (!aligned16(k_new) || !aligned16(v_new) || (n_q_heads && (!aligned16(q) || !aligned16(q_out)))) return KVQ_ERR_MISALIGNED;
+  if (!aligned4(seq_idx) || !aligned4(slot) || !aligned4(block_table) || !aligned4(pos) ||
+      reinterpret_cast<uintptr_t>(phases) % 8 != 0)
+    return KVQ_ERR_MISALIGNED;
+  kvq::RopeAppendArgs a{};
+  st = rope_axes(pos, pos_stride, n_axes, axis_of, rotary_dim / 2, n_tokens, &a.axes);
+  if (st != KVQ_OK) return st;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.num_blocks = cache->num_blocks;
+  a.n_kv_heads = H;
+  a.head_dim = D;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.q_stride = n_tokens > 1 ? q_stride : qd;
+  a.q_out_stride = n_tokens > 1 ? q_out_stride : qd;
+  a.k_stride = n_tokens > 1 ? k_stride : kd;
+  a.v_stride = n_tokens > 1 ? v_stride : kd;
+  a.n_q_heads = n_q_heads;
+  a.n_tokens = n_tokens;
+  a.seq_idx = seq_idx;
+  a.slot = slot;
+  a.block_table = block_table;
+  a.num_seqs = num_seqs;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.phases = reinterpret_cast<const unsigned long long*>(phases);
+  a.rotary_dim = rotary_dim;
+  a.rotary_offset = rotary_offset;
+  a.interleaved = layout == KVQ_ROPE_INTERLEAVED;
+  a.attn_factor = attn_factor;
+  a.status = status_ptr();
+  return cuda_status(kvq::launch_rope_append(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kvq_prefill_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,

@@ -204,6 +204,47 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t stream);
 
+// Positions on several axes, and the axis of each frequency: two bits each.
+constexpr int kMaxAxes = 4;
+constexpr int kMaxRotaryDim = 1024;
+struct RopeAxes {
+  const int32_t* pos;    // [n][pos_stride]
+  long long pos_stride;
+  int n;
+  uint32_t map[kMaxRotaryDim / 2 / 16];
+};
+struct RopeAxesArgs : RopeArgs {  // pos is not used
+  RopeAxes axes;
+  float sin_factor;  // attn_factor, negative for the inverse
+};
+cudaError_t launch_rope_axes(const RopeAxesArgs& a, int n_sms, cudaStream_t stream);
+
+// Rotation, quantisation and append of new tokens.
+struct RopeAppendArgs {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks, n_kv_heads, head_dim;
+  const uint16_t* q;      // bf16 rows, a token's q_stride elements after the one before
+  uint16_t* q_out;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  long long q_stride, q_out_stride, k_stride, v_stride;
+  int n_q_heads, n_tokens;
+  const int32_t* seq_idx;
+  const int32_t* slot;
+  const int32_t* block_table;
+  int num_seqs, max_blocks_per_seq;
+  const unsigned long long* phases;  // [rotary_dim / 2]
+  int rotary_dim, rotary_offset, interleaved;
+  float attn_factor;
+  RopeAxes axes;
+  unsigned int* status;
+  int q_heads_per_block, q_blocks;  // set by launch_rope_append
+};
+cudaError_t launch_rope_append(const RopeAppendArgs& a, int n_sms, cudaStream_t stream);
+
 struct SparseArgs {
   const int8_t* k;
   const int8_t* v;

@@ -95,6 +95,52 @@ __device__ __forceinline__ float quant_rule_warp_packed(const float (&x)[P], uin
   return scale;
 }
 
+// The same rule where a row is held by LANES neighbouring lanes (a power of two) and the warp by several rows, all of
+// its lanes taking part: no row's zeros and no row's ties change another's way through.
+template <int P, int LANES>
+__device__ __forceinline__ float quant_rule_rows_packed(const float (&x)[P], uint32_t (&packed)[P / 4]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  const float scale = __fdiv_rn(amax, 127.0f);
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+  constexpr float kNearHalf = 0.49993896484375f;  // 1/2 - 2^-14
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+  if (amax == 0.0f) r = 0.0f;  // zeros give zeros
+  bool exact_needed = false;
+#pragma unroll
+  for (int w = 0; w < P / 4; ++w) {
+    uint32_t sb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float y = __fmul_rn(x[4 * w + j], r);
+      const float sr = __fadd_rn(y, kRound);
+      exact_needed |= !(fabsf(__fsub_rn(y, __fsub_rn(sr, kRound))) <= kNearHalf);
+      sb[j] = __float_as_uint(sr);
+    }
+    packed[w] = __byte_perm(__byte_perm(sb[0], sb[1], 0x0040u), __byte_perm(sb[2], sb[3], 0x0040u), 0x5410u);
+  }
+  if (exact_needed && amax != 0.0f) {  // (a row of zeros and NaN has codes 0, as in the rule above)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float y = __fmul_rn(x[i], r);
+      if (!(fabsf(__fsub_rn(y, __fsub_rn(__fadd_rn(y, kRound), kRound))) <= kNearHalf)) {
+        const float ce = fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -127.0f), 127.0f);
+        const uint32_t sh = 8u * (i % 4);
+        packed[i / 4] = (packed[i / 4] & ~(0xFFu << sh)) | ((static_cast<uint32_t>(static_cast<int>(ce)) & 0xFFu) << sh);
+      }
+    }
+  }
+  if (amax == 0.0f) {
+#pragma unroll
+    for (int w = 0; w < P / 4; ++w) packed[w] = 0u;
+  }
+  return scale;
+}
+
 // K codes of one token into its slot: [page][head][d/16][slot][16].  Lane l's dims l*P .. l*P+P-1
 // lie in chunk (l*P)/16 at byte (l*P)%16 of the 16-byte row.  ph = page * n_kv_heads + head.
 template <int D>

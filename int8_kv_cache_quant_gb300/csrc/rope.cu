@@ -18,10 +18,15 @@
 // cos and sin once and applies them to several heads, with the loads of four heads in flight.
 // 2048 tokens x (24 + 4) heads of 256, 64 dims rotated (29 MB in, 29 MB out): 11.9 us, 4.9 TB/s, most of the outputs staying in L2; one
 // token 1.8 us, a launch.
-#include <cuda_bf16.h>
+//
+// With several axes (kvq_rope_axes_bf16: time, height and width of a patch) a frequency takes the position of its own
+// axis: a thread loads a token's positions (four at most) and picks one for each of its pairs by two bits of the
+// call's arguments, so that the map costs no load.  The inverse has the sine's sign turned.
+#include <type_traits>
 
 #include "kvq_dev.cuh"
 #include "kvq_launch.h"
+#include "rope_dev.cuh"
 
 namespace kvq {
 
@@ -51,33 +56,6 @@ __device__ __forceinline__ void cos_sin_turns(int32_t t, float& c, float& s) {
   if (q & 2u) s = -s;
 }
 
-template <int V>
-struct Word;  // V bf16 values as one load or store
-template <>
-struct Word<8> { using T = uint4; };
-template <>
-struct Word<4> { using T = uint2; };
-template <>
-struct Word<2> { using T = uint32_t; };
-template <>
-struct Word<1> { using T = uint16_t; };
-
-template <int V>
-__device__ __forceinline__ void unpack(const typename Word<V>::T& w, float (&x)[V]) {
-  const uint16_t* h = reinterpret_cast<const uint16_t*>(&w);
-#pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = bf16_bits_to_float(h[i]);
-}
-
-template <int V>
-__device__ __forceinline__ typename Word<V>::T pack(const float (&x)[V]) {
-  typename Word<V>::T w;
-  uint16_t* h = reinterpret_cast<uint16_t*>(&w);
-#pragma unroll
-  for (int i = 0; i < V; ++i) h[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
-  return w;
-}
-
 constexpr int kRopeThreads = 128;
 constexpr int kInFlight = 4;  // heads whose loads a thread issues before it works on the first
 
@@ -85,8 +63,9 @@ constexpr int kInFlight = 4;  // heads whose loads a thread issues before it wor
 
 // Thread (token, head group hg, column): heads hg, hg + head_groups, ... of the token.
 // INTER: the pair of frequency j is dims (2j, 2j + 1) of the rotated part; else (j, j + r/2).
-template <int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
+template <int V, bool INTER, class Args>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ Args a) {
+  constexpr bool AXES = std::is_same<Args, RopeAxesArgs>::value;
   using W = typename Word<V>::T;
   const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
   grid_dep_wait();
@@ -111,13 +90,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   }
   float c[V], s[V];
   if (rotated) {
-    const unsigned long long p = static_cast<unsigned long long>(static_cast<long long>(a.pos[tok]));
+    if constexpr (AXES) {
+      int32_t p[kMaxAxes];
+      load_axes(a.axes, tok, p);
+      const uint32_t map = a.axes.map[(col * V) / 16] >> (2 * (col * V % 16));
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const unsigned long long ph = p * __ldg(a.phases + col * V + i);
-      cos_sin_turns(static_cast<int32_t>((ph + 0x80000000ull) >> 32), c[i], s[i]);
-      c[i] *= a.attn_factor;
-      s[i] *= a.attn_factor;
+      for (int i = 0; i < V; ++i) {
+        const unsigned long long ph = position_bits(axis_position(p, map, i)) * __ldg(a.phases + col * V + i);
+        cos_sin_turns(static_cast<int32_t>((ph + 0x80000000ull) >> 32), c[i], s[i]);
+        c[i] *= a.attn_factor;
+        s[i] *= a.sin_factor;
+      }
+    } else {
+      const unsigned long long p = position_bits(a.pos[tok]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const unsigned long long ph = p * __ldg(a.phases + col * V + i);
+        cos_sin_turns(static_cast<int32_t>((ph + 0x80000000ull) >> 32), c[i], s[i]);
+        c[i] *= a.attn_factor;
+        s[i] *= a.attn_factor;
+      }
     }
   }
   const int H = a.n_q_heads + a.n_kv_heads;
@@ -180,8 +172,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   }
 }
 
-template <int V>
-static cudaError_t launch_rope_v(RopeArgs a, int n_sms, cudaStream_t stream) {
+template <int V, class Args>
+static cudaError_t launch_rope_v(Args a, int n_sms, cudaStream_t stream) {
   const int H = a.n_q_heads + a.n_kv_heads;
   const int rest = (a.head_dim - a.rotary_dim) / V;
   a.columns = a.rotary_dim / (2 * V) + (rest + 1) / 2;
@@ -196,11 +188,12 @@ static cudaError_t launch_rope_v(RopeArgs a, int n_sms, cudaStream_t stream) {
   const long long blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks));
-  return a.interleaved ? launch_pdl(rope_kernel<V, true>, grid, dim3(kRopeThreads), 0, stream, a)
-                       : launch_pdl(rope_kernel<V, false>, grid, dim3(kRopeThreads), 0, stream, a);
+  return a.interleaved ? launch_pdl(rope_kernel<V, true, Args>, grid, dim3(kRopeThreads), 0, stream, a)
+                       : launch_pdl(rope_kernel<V, false, Args>, grid, dim3(kRopeThreads), 0, stream, a);
 }
 
-cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t stream) {
+template <class Args>
+static cudaError_t launch_rope_any(const Args& a, int n_sms, cudaStream_t stream) {
   // the widest word that every row, the rotated part and both its halves are whole numbers of
   long long bits = a.rotary_dim / 2 | a.rotary_offset | a.head_dim | 8;
   if (a.n_q_heads) bits |= a.q_stride | a.q_out_stride | static_cast<long long>(reinterpret_cast<uintptr_t>(a.q) / 2) |
@@ -214,5 +207,8 @@ cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t stream) {
     default: return launch_rope_v<1>(a, n_sms, stream);
   }
 }
+
+cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t stream) { return launch_rope_any(a, n_sms, stream); }
+cudaError_t launch_rope_axes(const RopeAxesArgs& a, int n_sms, cudaStream_t stream) { return launch_rope_any(a, n_sms, stream); }
 
 }  // namespace kvq

@@ -60,6 +60,7 @@ class _RopeScaling(ctypes.Structure):
 
 
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+_ROPE_ORDERS, _ROPE_LADDERS = {"chunked": 0, "turns": 1}, {"shared": 0, "per_axis": 1}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4, "divisors": 5}
 
 _lib = None
@@ -115,6 +116,12 @@ def lib():
         L.kvq_rope_phases.argtypes = [i32, ctypes.c_double, ctypes.POINTER(_RopeScaling),
                                       ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_float)]
         L.kvq_rope_bf16.argtypes = [vp, vp, i64, i64, i32, vp, vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, i32, f32, vp]
+        L.kvq_rope_axes_phases.argtypes = [i32, ctypes.POINTER(i32), i32, i32, ctypes.c_double, ctypes.POINTER(_RopeScaling),
+                                           ctypes.POINTER(ctypes.c_uint64), vp, ctypes.POINTER(ctypes.c_float)]
+        L.kvq_rope_axes_bf16.argtypes = [vp, vp, i64, i64, i32, vp, vp, i64, i64, i32, i32, i32, vp, i64, i32, vp, vp, i32,
+                                         i32, i32, f32, i32, vp]
+        L.kvq_rope_append_int8kv.argtypes = [cp, vp, vp, i64, i64, i32, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, vp, i64,
+                                             i32, vp, vp, i32, i32, i32, f32, vp]
         L.kvq_prefill_first_workspace_bytes.restype = sz
         L.kvq_prefill_first_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32]
         L.kvq_attn_prefill_first_bf16.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, f32, vp, vp, sz, vp]
@@ -701,22 +708,29 @@ def kvq_cache_evict(cache, block_table, ctx_lens, max_ctx, keep, acc, slot_pos, 
     return acc_out, slot_pos_out, new_lens
 
 
+def _rope_scaling(fn, n, scaling, factor, original_len, low, high, divisors):
+    """The C struct of a scaling of n frequencies."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError("%s: unknown scaling %r" % (fn, scaling))
+    div = None
+    if divisors is not None:
+        if len(divisors) != n:
+            raise ValueError("%s: %d divisors for %d frequencies" % (fn, len(divisors), n))
+        div = (ctypes.c_double * n)(*[float(x) for x in divisors])
+    z = _RopeScaling(_ROPE_SCALINGS[scaling], float(factor), float(original_len), float(low), float(high),
+                     ctypes.cast(div, ctypes.POINTER(ctypes.c_double)) if div is not None else None)
+    z.keep = div  # the struct holds its address alone
+    return z
+
+
 def kvq_rope_phases(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=32.0,
                     divisors=None, device="cuda"):
     """The plan of kvq_rope_bf16: (phases, attn_factor), phases int64 [rotary_dim / 2] (the bits of the
     64-bit fractions of a turn per position).  scaling: "none", "linear", "ntk", "yarn", "bands" or
     "divisors"."""
     _fit("kvq_rope_phases", rotary_dim)
-    if scaling not in _ROPE_SCALINGS:
-        raise ValueError("kvq_rope_phases: unknown scaling %r" % (scaling,))
     n = max(int(rotary_dim), 0) // 2
-    div = None
-    if divisors is not None:
-        if len(divisors) != n:
-            raise ValueError("kvq_rope_phases: %d divisors for %d frequencies" % (len(divisors), n))
-        div = (ctypes.c_double * n)(*[float(x) for x in divisors])
-    z = _RopeScaling(_ROPE_SCALINGS[scaling], float(factor), float(original_len), float(low), float(high),
-                     ctypes.cast(div, ctypes.POINTER(ctypes.c_double)) if div is not None else None)
+    z = _rope_scaling("kvq_rope_phases", n, scaling, factor, original_len, low, high, divisors)
     host = torch.empty(n, dtype=torch.int64)
     af = ctypes.c_float(1.0)
     _check("kvq_rope_phases", lib().kvq_rope_phases(
@@ -760,6 +774,127 @@ def kvq_rope_bf16(q, k, pos, phases, layout=ROPE_HALF, rotary_offset=0, attn_fac
     _check(fn, lib().kvq_rope_bf16(q_p, qo_p, qs, qos, hq, k_p, ko_p, ks, kos, hk, D, T, pos_p, phases_p, 2 * n,
                                    int(rotary_offset), int(layout), float(attn_factor), _stream(stream)))
     return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+class RopeAxes:
+    """A plan of kvq_rope_axes_bf16 and kvq_rope_append_int8kv: phases (int64 [rotary_dim / 2] on the device, the bits of
+    the 64-bit fractions of a turn per position), the axis of each frequency, and the factor on cos and sin."""
+
+    __slots__ = ("phases", "axis_of", "attn_factor", "n_axes", "rotary_dim")
+
+    def __init__(self, phases, axis_of, attn_factor=1.0):
+        self.phases, self.axis_of, self.attn_factor = phases, bytes(axis_of), float(attn_factor)
+        self.n_axes, self.rotary_dim = max(self.axis_of, default=0) + 1, 2 * len(self.axis_of)
+        if phases.dtype is not torch.int64 or tuple(phases.shape) != (len(self.axis_of),) or not phases.is_contiguous():
+            raise ValueError("RopeAxes: phases must be a contiguous int64 tensor [%d]" % len(self.axis_of))
+        if self.n_axes > 4:
+            raise ValueError("RopeAxes: %d axes, at most 4" % self.n_axes)
+
+
+def kvq_rope_axes_phases(sections, base=10000.0, order="chunked", ladder="shared", scaling="none", factor=1.0,
+                         original_len=0.0, low=1.0, high=32.0, divisors=None, device="cuda"):
+    """A RopeAxes plan: sections[a] frequencies for axis a, "chunked" (one axis after the other) or in "turns"; one "shared"
+    ladder of frequencies, or a ladder "per_axis".  Scalings as in kvq_rope_phases."""
+    fn = "kvq_rope_axes_phases"
+    if order not in _ROPE_ORDERS or ladder not in _ROPE_LADDERS:
+        raise ValueError("%s: unknown order or ladder (%r, %r)" % (fn, order, ladder))
+    _fit(fn, *sections)
+    sections = [int(n) for n in sections]
+    n = max(sum(sections), 0)
+    z = _rope_scaling(fn, n, scaling, factor, original_len, low, high, divisors)
+    host, axis_of, af = torch.empty(n, dtype=torch.int64), ctypes.create_string_buffer(max(n, 1)), ctypes.c_float(1.0)
+    _check(fn, lib().kvq_rope_axes_phases(
+        len(sections), (ctypes.c_int32 * max(len(sections), 1))(*sections), _ROPE_ORDERS[order], _ROPE_LADDERS[ladder],
+        float(base), ctypes.byref(z), ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_uint64)), axis_of, ctypes.byref(af)))
+    return RopeAxes(host.to(device), axis_of.raw[:n], af.value)
+
+
+def _axes(fn, pos, plan, T, dev):
+    """(pointer, stride, axes) of pos int32 [axes][T] (or [T] with one axis); the plan's phases are on the device."""
+    n = plan.n_axes
+    shape = pos.shape
+    if len(shape) == 1:
+        shape = (1,) + tuple(shape)
+    if pos.dtype is not torch.int32 or len(shape) != 2 or shape[0] < n or shape[1] != T or (T > 1 and pos.stride(-1) != 1):
+        raise ValueError("%s: pos must be int32 [%d][%d] with contiguous rows (got %s %s)" % (fn, n, T, pos.dtype, tuple(pos.shape)))
+    stride = pos.stride(0) if n > 1 else T
+    if pos.get_device() != dev:
+        _elsewhere(fn, "pos", pos)
+    if plan.phases.get_device() != dev:
+        _elsewhere(fn, "the plan", plan.phases)
+    if stride < T:
+        raise ValueError("%s: the rows of pos overlap" % fn)
+    return pos.data_ptr(), stride, n
+
+
+def kvq_rope_axes_bf16(q, k, pos, plan, layout=ROPE_HALF, rotary_offset=0, inverse=False, q_out=None, k_out=None, stream=None):
+    """kvq_rope_bf16 with positions on several axes: pos int32 [axes][T] ([T] with one axis), plan a RopeAxes.  inverse turns
+    the other way: the gradient of the rotation.  Returns (q_out, k_out)."""
+    fn = "kvq_rope_axes_bf16"
+    _fit(fn, rotary_offset, layout)
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("%s: q and k are both None" % fn)
+    T, _, D = ref.shape
+    dev = _current_device()
+    q_p = qo_p = k_p = ko_p = None
+    hq = qs = qos = hk = ks = kos = 0
+    if q is not None:
+        if q_out is None:
+            q_out = _result(q.shape, torch.bfloat16, q.device, stream)
+        hq, qs, q_p = _heads(fn, "q", q, T, D, dev)
+        ho, qos, qo_p = _heads(fn, "q_out", q_out, T, D, dev)
+        if ho != hq:
+            raise ValueError("%s: q_out has %d heads, q %d" % (fn, ho, hq))
+    if k is not None:
+        if k_out is None:
+            k_out = _result(k.shape, torch.bfloat16, k.device, stream)
+        hk, ks, k_p = _heads(fn, "k", k, T, D, dev)
+        ho, kos, ko_p = _heads(fn, "k_out", k_out, T, D, dev)
+        if ho != hk:
+            raise ValueError("%s: k_out has %d heads, k %d" % (fn, ho, hk))
+    pos_p, pos_stride, n_axes = _axes(fn, pos, plan, T, dev)
+    _check(fn, lib().kvq_rope_axes_bf16(q_p, qo_p, qs, qos, hq, k_p, ko_p, ks, kos, hk, D, T, pos_p, pos_stride, n_axes,
+                                        plan.phases.data_ptr(), plan.axis_of, plan.rotary_dim, int(rotary_offset), int(layout),
+                                        plan.attn_factor, 1 if inverse else 0, _stream(stream)))
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+def kvq_rope_append_int8kv(cache, q, k_new, v_new, pos, plan, seq_idx, slot, block_table, layout=ROPE_HALF, rotary_offset=0,
+                           q_out=None, stream=None):
+    """New tokens into the cache: q bf16 [T][Hq][D] (or None) rotated by pos (int32 [axes][T]) and plan into q_out, k_new
+    rotated and k_new, v_new bf16 [T][Hkv][D] quantised into slot[i] of sequence seq_idx[i] (int32 [T]; slot -1: a padding
+    token, nothing of it is written).  Rows may be views of a packed projection.  block_table int32 [S][M].  Returns q_out."""
+    fn = "kvq_rope_append_int8kv"
+    _fit(fn, rotary_offset, layout)
+    T, H, D = k_new.shape
+    dev = _current_device()
+    if H != cache.n_kv_heads or D != cache.head_dim:
+        raise ValueError("%s: k_new has %d heads of %d, the cache %d of %d" % (fn, H, D, cache.n_kv_heads, cache.head_dim))
+    _, ks, k_p = _heads(fn, "k_new", k_new, T, D, dev)
+    hv, vs, v_p = _heads(fn, "v_new", v_new, T, D, dev)
+    if hv != H:
+        raise ValueError("%s: v_new has %d heads, the cache %d" % (fn, hv, H))
+    q_p = qo_p = None
+    hq = qs = qos = 0
+    if q is not None:
+        if q_out is None:
+            q_out = _result(q.shape, torch.bfloat16, q.device, stream)
+        hq, qs, q_p = _heads(fn, "q", q, T, D, dev)
+        ho, qos, qo_p = _heads(fn, "q_out", q_out, T, D, dev)
+        if ho != hq:
+            raise ValueError("%s: q_out has %d heads, q %d" % (fn, ho, hq))
+    pos_p, pos_stride, n_axes = _axes(fn, pos, plan, T, dev)
+    seq_p = _need(fn, "seq_idx", seq_idx, torch.int32, (T,), dev)
+    slot_p = _need(fn, "slot", slot, torch.int32, (T,), dev)
+    n_seqs, n_blocks = block_table.shape
+    table_p = _need(fn, "block_table", block_table, torch.int32, (n_seqs, n_blocks), dev)
+    c = _cache_struct(fn, cache, dev)
+    _check(fn, lib().kvq_rope_append_int8kv(
+        ctypes.byref(c), q_p, qo_p, qs, qos, hq, k_p, ks, v_p, vs, T, seq_p, slot_p, table_p, n_seqs, n_blocks, pos_p, pos_stride,
+        n_axes, plan.phases.data_ptr(), plan.axis_of, plan.rotary_dim, int(rotary_offset), int(layout), plan.attn_factor,
+        _stream(stream)))
+    return q_out if q is not None else None
 
 
 def _heads(fn, name, t, T, D, dev):

@@ -1,0 +1,122 @@
+"""Refusals and host arithmetic of the operators around windowed attention: no GPU, nothing is launched."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import forget_ref as R
+import int8_kv_cache_quant_gb300 as k
+import window_ref as WR
+
+A = 256  # an aligned address that is never used
+INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 1, 2, 3, 4
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def L():
+    return k.lib()
+
+
+def cache(d=256, hkv=4, block=16, kp=A):
+    return k.kvq._Cache(kp, A, A, A, 8, block, hkv, d)
+
+
+MAP = bytes([0, 1, 2] * 42 + [0, 0])
+
+
+def axes(L, q=A, qo=A, qs=24 * 256, qos=24 * 256, hq=24, kk=A, ko=A, ks=1024, kos=1024, hk=4, d=256, T=10, pos=A, ps=10, n=3, ph=A,
+         axis_of=MAP, r=256, off=0, layout=0, f=1.0, inv=0):
+    return L.kvq_rope_axes_bf16(q, qo, qs, qos, hq, kk, ko, ks, kos, hk, d, T, pos, ps, n, ph, axis_of, r, off, layout, f, inv, None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(q=None)), (INVALID, dict(qo=None)), (INVALID, dict(kk=None)), (INVALID, dict(pos=None)), (INVALID, dict(ph=None)),
+    (INVALID, dict(axis_of=None)), (INVALID, dict(axis_of=b"\3" * 128)), (INVALID, dict(ps=9)), (INVALID, dict(T=-1)),
+    (INVALID, dict(r=255)), (INVALID, dict(r=0)), (INVALID, dict(off=2)), (INVALID, dict(qs=24 * 256 - 1)), (INVALID, dict(qos=24 * 256 + 8)),
+    (UNSUPPORTED, dict(n=0)), (UNSUPPORTED, dict(n=5)), (UNSUPPORTED, dict(layout=2)), (UNSUPPORTED, dict(d=1025)),
+    (MISALIGNED, dict(q=A + 1)), (MISALIGNED, dict(pos=A + 2)), (MISALIGNED, dict(ph=A + 4)), (0, dict(T=0)), (0, dict(hq=0, hk=0))])
+def test_axes_refusals(L, status, kw):
+    assert axes(L, **kw) == status
+
+
+def append(L, c=None, q=A, qo=A, qs=6144, qos=6144, hq=24, kk=A, ks=1024, v=A, vs=1024, T=10, seq=A, slot=A, bt=A, ns=2, mb=8, pos=A,
+           ps=10, n=3, ph=A, axis_of=MAP, r=256, off=0, layout=0, f=1.0):
+    return L.kvq_rope_append_int8kv(ctypes.byref(c or cache()), q, qo, qs, qos, hq, kk, ks, v, vs, T, seq, slot, bt, ns, mb, pos, ps, n,
+                                    ph, axis_of, r, off, layout, f, None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(q=None)), (INVALID, dict(qo=None)), (INVALID, dict(kk=None)), (INVALID, dict(v=None)), (INVALID, dict(seq=None)),
+    (INVALID, dict(slot=None)), (INVALID, dict(bt=None)), (INVALID, dict(pos=None)), (INVALID, dict(ph=None)), (INVALID, dict(axis_of=None)),
+    (INVALID, dict(axis_of=b"\3" * 128)), (INVALID, dict(ps=9)), (INVALID, dict(T=-1)), (INVALID, dict(hq=-1)), (INVALID, dict(ns=0)),
+    (INVALID, dict(mb=0)), (INVALID, dict(r=258)), (INVALID, dict(off=8)), (INVALID, dict(ks=1016)), (INVALID, dict(vs=1016)),
+    (INVALID, dict(qos=6152)), (INVALID, dict(f=NAN)), (INVALID, dict(f=INF)), (UNSUPPORTED, dict(r=24, axis_of=MAP)),
+    (UNSUPPORTED, dict(r=128, off=4)), (UNSUPPORTED, dict(n=0)), (UNSUPPORTED, dict(n=5)), (UNSUPPORTED, dict(layout=2)),
+    (UNSUPPORTED, dict(c=cache(d=64))), (UNSUPPORTED, dict(c=cache(block=32))), (UNSUPPORTED, dict(mb=1 << 27)),
+    (UNSUPPORTED, dict(hq=65536)), (MISALIGNED, dict(q=A + 8)), (MISALIGNED, dict(kk=A + 8)), (MISALIGNED, dict(v=A + 2)),
+    (MISALIGNED, dict(ks=1028)), (MISALIGNED, dict(qo=2 * A, qos=6146)), (MISALIGNED, dict(slot=A + 2)), (MISALIGNED, dict(ph=A + 4)),
+    (MISALIGNED, dict(c=cache(kp=A + 4))), (0, dict(T=0))])
+def test_append_refusals(L, status, kw):
+    assert append(L, **kw) == status
+
+
+@pytest.mark.parametrize("order", ["chunked", "turns"])
+@pytest.mark.parametrize("sections", [[64], [24, 20, 20], [16, 24, 24], [1, 5], [0, 3, 0, 4], [7, 0, 0]])
+@pytest.mark.parametrize("kind,kw", [("none", {}), ("linear", dict(factor=4.0)), ("yarn", dict(factor=8.0, original_len=4096.0)),
+                                     ("bands", dict(factor=8.0, original_len=8192.0, low=1.0, high=4.0))])
+def test_axes_phases(L, order, sections, kind, kw):
+    plan = k.kvq_rope_axes_phases(sections, 1.0e6, order, "shared", kind, device="cpu", **kw)
+    axis_of = WR.sections_to_axes(sections, order)
+    assert list(plan.axis_of) == axis_of and plan.rotary_dim == 2 * sum(sections) and plan.n_axes == max(axis_of) + 1
+    phases, factor = k.kvq_rope_phases(2 * sum(sections), 1.0e6, kind, device="cpu", **kw)
+    assert np.array_equal(plan.phases.numpy(), phases.numpy()) and plan.attn_factor == factor
+    own = k.kvq_rope_axes_phases(sections, 1.0e6, order, "per_axis", kind, device="cpu", **kw)
+    ref_kw = {("length" if n == "original_len" else n): v for n, v in kw.items()}
+    for a, n in enumerate(sections):
+        if n:
+            inv, factor = R.inv_freq(2 * n, 1.0e6, kind, **ref_kw)
+            turns = inv / (2 * np.pi)
+            got = own.phases.numpy().view(np.uint64)[np.array(axis_of) == a].astype(np.float64) / 2.0 ** 64
+            # fp64 powers and quotients, and half a step of 2^-64 turns
+            np.testing.assert_allclose(got, turns - np.floor(turns), rtol=16 * 2.0 ** -53, atol=2.0 ** -65)
+            assert own.attn_factor == np.float32(factor)
+
+
+def test_axes_phases_refusals(L):
+    for bad in (dict(sections=[]), dict(sections=[1] * 5), dict(sections=[0, 0]), dict(sections=[-1, 4]), dict(sections=[513]),
+                dict(sections=[300, 300]), dict(sections=[4], base=0.0), dict(sections=[4], scaling="yarn", factor=2.0),
+                dict(sections=[2, 2], ladder="per_axis", scaling="divisors", divisors=[1.0] * 4)):
+        with pytest.raises(k.KvqError):
+            k.kvq_rope_axes_phases(device="cpu", **bad)
+    for bad in (dict(sections=[4], order="mixed"), dict(sections=[4], ladder="own"), dict(sections=[4], scaling="other"),
+                dict(sections=[2, 2], scaling="divisors", divisors=[1.0]), dict(sections=[2 ** 32 + 4])):
+        with pytest.raises(ValueError):
+            k.kvq_rope_axes_phases(device="cpu", **bad)
+    plan = k.kvq_rope_axes_phases([2, 2], scaling="divisors", divisors=[1.0, 2.0, 4.0, 8.0], device="cpu")
+    assert plan.phases.numel() == 4
+    # nothing is written on an error: the second axis has one frequency, for which the ntk scaling has no base
+    ph, ax = (ctypes.c_uint64 * 4)(7, 7, 7, 7), (ctypes.c_uint8 * 4)(7, 7, 7, 7)
+    z = k.kvq._RopeScaling(2, 2.0, 0.0, 1.0, 32.0, None)
+    assert L.kvq_rope_axes_phases(2, (ctypes.c_int32 * 2)(3, 1), 0, 1, 1.0e4, ctypes.byref(z), ph, ax, None) == INVALID
+    assert list(ph) == [7] * 4 and list(ax) == [7] * 4
+
+
+def test_plan_checks():
+    import torch
+    for phases, axis_of in ((torch.zeros(4), [0] * 4), (torch.zeros(4, dtype=torch.int64), [0] * 5),
+                            (torch.zeros(4, dtype=torch.int64), [0, 1, 2, 4])):
+        with pytest.raises(ValueError):
+            k.RopeAxes(phases, axis_of)
+
+
+def test_host_tensors_are_refused(monkeypatch):
+    """No host pointer reaches a kernel."""
+    import torch
+    monkeypatch.setattr(k.kvq, "_current_device", lambda: 0)
+    plan = k.kvq_rope_axes_phases([64], device="cpu")
+    x, pos = torch.zeros((2, 4, 128), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        k.kvq_rope_axes_bf16(x, None, pos, plan, q_out=x)
+    with pytest.raises(ValueError):
+        k.kvq_rope_append_int8kv(k.KVCache(2, 4, 128, device="cpu"), None, x, x, pos, plan, pos, pos, pos.view(1, 2))

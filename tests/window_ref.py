@@ -1,0 +1,76 @@
+"""Plain references (numpy) of the operators around windowed attention: rotary positions with several axes and the
+append with rotation.  They read the documented layouts and share no code with the library."""
+import numpy as np
+
+PAGE = 16
+
+
+def sections_to_axes(sections, order):
+    """The axis of each frequency."""
+    if order == "chunked":
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = list(sections), []
+    while sum(left):
+        for a in range(len(left)):
+            if left[a]:
+                out.append(a)
+                left[a] -= 1
+    return out
+
+
+def turns(pos, phases, axis_of):
+    """Turns [T][r/2] as signed 64-bit fractions: the product with the position modulo 2^64."""
+    p = np.asarray(pos, np.int64)[np.array(list(axis_of))].T.astype(np.uint64)
+    with np.errstate(over="ignore"):
+        return (p * np.asarray(phases, np.uint64)).astype(np.int64)
+
+
+def angles(pos, phases, axis_of):
+    return turns(pos, phases, axis_of).astype(np.float64) * (2 * np.pi / 2.0 ** 64)
+
+
+def cos_sin_f32(t, factor):
+    """factor cos and factor sin of the turns to the nearest fp32, through the longest float there is."""
+    a = t.astype(np.longdouble) * (2 * np.longdouble("3.14159265358979323846264338327950288") / np.longdouble(2.0) ** 64)
+    f = np.longdouble(np.float32(factor))
+    return (np.cos(a) * f).astype(np.float32), (np.sin(a) * f).astype(np.float32)
+
+
+def rotate_f32(x, c, s, off, inter):
+    """x [T][H][D] fp32 rotated with the header's roundings."""
+    y = x.copy()
+    half = c.shape[1]
+    i = np.arange(half)
+    ia, ib = (off + 2 * i, off + 2 * i + 1) if inter else (off + i, off + half + i)
+    c, s = c[:, None], s[:, None]
+    a, b = x[..., ia], x[..., ib]
+    y[..., ia] = a * c - b * s
+    y[..., ib] = b * c + a * s
+    return y
+
+
+def quantise(x):
+    """The rule on fp32 rows: (codes, scales)."""
+    amax = np.abs(x).max(-1).astype(np.float32)
+    scale = (amax / np.float32(127.0)).astype(np.float32)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        q = (x / scale[..., None]).astype(np.float32)
+    code = np.clip(np.rint(np.where(amax[..., None] > 0, q, 0.0)), -127, 127).astype(np.int8)
+    return code, scale
+
+
+def append(pool, k, v, seq, slot, table):
+    """Rows k, v [T][Hkv][D] fp32 into a forget_ref.Pool's pages; which tokens were written."""
+    (kc, ks), (vc, vs) = quantise(k), quantise(v)
+    done = []
+    for i in range(len(seq)):
+        ok = 0 <= seq[i] < table.shape[0] and 0 <= slot[i] < PAGE * table.shape[1]
+        page = int(table[seq[i], slot[i] // PAGE]) if ok else -1
+        ok = ok and 0 <= page < pool.nb
+        done.append(ok)
+        if ok:
+            at = slot[i] % PAGE
+            pool.k[page, :, :, at] = kc[i].reshape(pool.hkv, pool.d // 16, 16)
+            pool.v[page, :, :, at] = vc[i]
+            pool.ks[page, :, at], pool.vs[page, :, at] = ks[i], vs[i]
+    return np.array(done)
