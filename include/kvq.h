@@ -316,6 +316,31 @@ int kvq_decode_step_int8kv(const kvq_cache* cache, const void* k_new, const void
                            float softmax_scale, float* out, void* workspace, size_t workspace_bytes,
                            const kvq_decode_opts* opts, void* stream);
 
+/* Workspace (bytes) of kvq_decode_step_window_int8kv: kvq_verify_workspace_bytes of the keys the call can read of a
+ * sequence, min(max_ctx, whole pages of n_sink keys and of window + n_new - 1 keys).  0 when the call takes the
+ * single-CTA route or an argument is not positive (n_sink may be 0). */
+size_t kvq_step_window_workspace_bytes(int32_t batch, int32_t n_new, int32_t n_q_heads, int32_t n_kv_heads,
+                                       int32_t max_ctx, int32_t window, int32_t n_sink, int32_t head_dim,
+                                       const kvq_decode_opts* opts);
+
+/*
+ * kvq_decode_step_window_int8kv — kvq_decode_step_int8kv (with k_new = v_new = NULL: kvq_attn_verify_int8kv) with a
+ * sliding window and first tokens that stay visible: the row at position p (row i of sequence b: p = ctx_lens[b] - n_new + i)
+ * sees the keys t <= p with t > p - window or t < n_sink.  Positions are slots of the sequence.
+ *   window : > 0; as many keys as max_ctx or more is no window
+ *   n_sink : >= 0 first keys that every row sees (up to itself)
+ *   workspace : >= kvq_step_window_workspace_bytes(...), 16-byte aligned
+ *   other arguments as kvq_decode_step_int8kv; opts->route_threshold and the automatic split go by the keys the call
+ *   can read of a sequence (above), not by max_ctx.
+ * Pages that no row sees are not read, nor are their block-table entries: they can have gone back to the pool.  The
+ * time goes by the window.
+ */
+int kvq_decode_step_window_int8kv(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
+                                  int32_t batch, int32_t n_new, int32_t n_q_heads, const int32_t* block_table,
+                                  int32_t max_blocks_per_seq, const int32_t* ctx_lens, int32_t max_ctx,
+                                  float softmax_scale, int32_t window, int32_t n_sink, float* out, void* workspace,
+                                  size_t workspace_bytes, const kvq_decode_opts* opts, void* stream);
+
 /*
  * A cache that forgets.  A sequence may hold fewer tokens than it has seen: kvq_cache_evict keeps,
  * per (sequence, KV head), the tokens that the queries have attended to most, and the next tokens are

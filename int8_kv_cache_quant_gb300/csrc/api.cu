@@ -468,6 +468,54 @@ int kvq_decode_step_accum_int8kv(const kvq_cache* cache, const void* k_new, cons
   return rc;
 }
 
+// The most keys that a windowed step counts of a sequence (window_map): whole pages of the first keys, and of the rows'
+// windows, which may begin at the end of a page.
+static int32_t window_keys(int32_t max_ctx, int32_t n_new, int32_t window, int32_t n_sink) {
+  const long long pages = (static_cast<long long>(n_sink) + KVQ_BLOCK_SIZE - 1) / KVQ_BLOCK_SIZE +
+                          (static_cast<long long>(window) + n_new - 1 + 2 * (KVQ_BLOCK_SIZE - 1)) / KVQ_BLOCK_SIZE;
+  return static_cast<int32_t>(std::min<long long>(std::max(max_ctx, 1), pages * KVQ_BLOCK_SIZE));
+}
+
+size_t kvq_step_window_workspace_bytes(int32_t batch, int32_t n_new, int32_t n_q_heads, int32_t n_kv_heads,
+                                       int32_t max_ctx, int32_t window, int32_t n_sink, int32_t head_dim,
+                                       const kvq_decode_opts* opts) {
+  if (n_kv_heads <= 0 || max_ctx <= 0 || window <= 0 || n_sink < 0) return 0;
+  return kvq_verify_workspace_bytes(batch, n_new, n_q_heads, window_keys(max_ctx, n_new, window, n_sink), head_dim, opts);
+}
+
+int kvq_decode_step_window_int8kv(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
+                                  int32_t batch, int32_t n_new, int32_t n_q_heads, const int32_t* block_table,
+                                  int32_t max_blocks_per_seq, const int32_t* ctx_lens, int32_t max_ctx,
+                                  float softmax_scale, int32_t window, int32_t n_sink, float* out, void* workspace,
+                                  size_t workspace_bytes, const kvq_decode_opts* opts, void* stream) {
+  int st = check_decode(cache, k_new, v_new, q, batch, n_new, n_q_heads, block_table, max_blocks_per_seq, ctx_lens,
+                        max_ctx, out);
+  if (st != KVQ_OK) return st;
+  if (window <= 0 || n_sink < 0) return KVQ_ERR_INVALID_ARG;
+  const int mc = max_ctx > 0 ? max_ctx : 1;
+  const int32_t keys = window_keys(mc, n_new, window, n_sink);
+  const kvq_decode_opts o = decode_defaults(opts);
+  if (o.split_rows % KVQ_BLOCK_SIZE != 0 || o.force_route < 0 || o.force_route > 2) return KVQ_ERR_INVALID_ARG;
+  if (decode_split_route(o, keys) && !workspace) return KVQ_ERR_WORKSPACE;
+  kvq::DecodePlan plan;
+  st = kvq::decode_plan(cache, batch, n_new, n_q_heads, keys, opts, &plan);
+  if (st != KVQ_OK) return st;
+  if (plan.split) {
+    if (!workspace || workspace_bytes < plan.bytes) return KVQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
+  }
+  kvq::DecodeArgs a = decode_args(cache, k_new, v_new, q, batch, n_new, n_q_heads, block_table, max_blocks_per_seq,
+                                  ctx_lens, mc, softmax_scale, out, o, plan);
+  if (plan.split) place_partials(&a, workspace);
+  a.window = std::min(window, mc);
+  a.n_sink = std::min(n_sink, mc);
+  int launched = 0;
+  const int rc = cuda_status(kvq::launch_step_window(a, plan.split ? kvq::DecodeRoute::kSplit : kvq::DecodeRoute::kSingle,
+                                                     static_cast<cudaStream_t>(stream), &launched));
+  if (o.launches) *o.launches = launched;
+  return rc;
+}
+
 // Largest number of CTAs a pass of the chunk weights runs: more than any GPU the library is built for has
 // SMs, so that the workspace size does not depend on the GPU.
 constexpr int kChunkWeightsMaxRuns = 160;

@@ -134,17 +134,6 @@ cudaError_t launch_stream_floor(const DecodeArgs& a, cudaStream_t stream) {
   return launch_pdl(decode_stream_kernel<128>, grid, dim3(256), L::kTotal, stream, a);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(DecodeArgs a) {
-  extern __shared__ float wts[];
-  decode_merge_block<D>(a, blockIdx.x, blockIdx.y, blockIdx.z, wts);
-}
-
-template <int D>
-__global__ void __launch_bounds__(256) decode_merge_warp_kernel(DecodeArgs a) {
-  decode_merge_warps<D>(a, blockIdx.x);
-}
-
 size_t decode_workspace_bytes(int batch, int n_q_heads, int max_ctx, int head_dim, int split_rows) {
   const long long n_split = (static_cast<long long>(max_ctx) + split_rows - 1) / split_rows;
   const long long units = static_cast<long long>(batch) * n_q_heads * n_split;
@@ -169,29 +158,6 @@ static cudaError_t launch_stage1_rows(const DecodeArgs& a, dim3 grid, cudaStream
     case 6: return launch_stage1<D, 6, SPLIT>(a, grid, stream);
     default: return cudaErrorInvalidValue;
   }
-}
-
-// Past kMergeSmem bytes of splits' weights the merge has to ask for its shared memory (48 KB less its own arrays are
-// free); it does so before stage 1, which may write the cache.
-template <int D>
-static cudaError_t prepare_merge(const DecodeArgs& a) {
-  static std::atomic<uint64_t> done{0};
-  if (decode_merge_by_warps(a) || a.n_split * sizeof(float) <= kMergeSmem) return cudaSuccess;
-  return allow_smem(reinterpret_cast<const void*>(decode_merge_kernel<D>), kMaxSplits * sizeof(float), done);
-}
-
-template <int D>
-static cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream) {
-  const long long units = static_cast<long long>(a.batch) * a.nq * a.n_q_heads;
-  cudaError_t e;
-  if (decode_merge_by_warps(a)) {
-    e = launch_pdl(decode_merge_warp_kernel<D>, dim3(static_cast<unsigned>((units + 7) / 8)), dim3(256), 0, stream, a);
-  } else {
-    const dim3 g2(a.n_q_heads, a.batch * a.nq, D / kMergeCols);
-    e = launch_pdl(decode_merge_kernel<D>, g2, dim3(kMergeThreads), a.n_split * sizeof(float), stream, a);
-  }
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, DecodeRoute route, cudaStream_t stream, int* launched) {

@@ -19,8 +19,17 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeCols = 64;
 constexpr size_t kMergeSmem = 40 * 1024;  // of splits' weights: with the merge's own arrays below the 48 KB of any kernel
 
+// Live splits of sequence b: those that begin below its (virtual, with a window) length.
+template <bool WIN>
+__device__ __forceinline__ int live_splits(const DecodeArgs& a, int b) {
+  int ctx = a.ctx_lens[b];
+  ctx = max(0, min(ctx, min(a.max_blocks_per_seq * KVQ_BLOCK_SIZE, a.max_ctx)));
+  if constexpr (WIN) ctx -= window_map(ctx, a.nq, a.window, a.n_sink).skipped * KVQ_BLOCK_SIZE;
+  return min(a.n_split, (ctx + a.split_rows - 1) / a.split_rows);
+}
+
 // wts: [n_split] weights of the partial accumulators (shared memory).
-template <int D>
+template <int D, bool WIN = false>
 __device__ __forceinline__ void decode_merge_block(const DecodeArgs& a, int h, int row, int col_block, float* wts) {
   constexpr int TPG = kMergeCols / 4;           // threads per split group (4 dims each)
   constexpr int NG = kMergeThreads / TPG;       // split groups
@@ -44,9 +53,7 @@ __device__ __forceinline__ void decode_merge_block(const DecodeArgs& a, int h, i
     if (grp + u * NG < a.n_split) v[u] = acc[static_cast<long long>(grp + u * NG) * (D / 4)];
   float4 st0 = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
   if (tid < a.n_split) st0 = reinterpret_cast<const float4*>(stats)[tid];
-  int ctx = a.ctx_lens[b];
-  ctx = max(0, min(ctx, min(a.max_blocks_per_seq * KVQ_BLOCK_SIZE, a.max_ctx)));
-  const int n = min(a.n_split, (ctx + a.split_rows - 1) / a.split_rows);
+  const int n = live_splits<WIN>(a, b);
 
   float Ms = tid < n ? st0.x : -INFINITY, Mz = tid < n ? st0.y : -INFINITY;
   for (int s = tid + kMergeThreads; s < n; s += kMergeThreads) {
@@ -144,7 +151,7 @@ __device__ __forceinline__ void decode_merge_block(const DecodeArgs& a, int h, i
 // 64-dim block) CTAs of decode_merge_block would take several.  The same rule as that kernel.
 constexpr int kMergeWarpMaxSplits = 32;
 
-template <int D>
+template <int D, bool WIN = false>
 __device__ __forceinline__ void decode_merge_warps(const DecodeArgs& a, int block) {
   constexpr int PER = D / 32;  // dims per lane
   const int lane = threadIdx.x & 31;
@@ -153,9 +160,7 @@ __device__ __forceinline__ void decode_merge_warps(const DecodeArgs& a, int bloc
   grid_dep_wait();  // the partials come from stage 1
   if (unit >= static_cast<long long>(a.batch) * a.nq * Hq) return;  // warp-uniform
   const int row = static_cast<int>(unit / Hq), b = row / a.nq;
-  int ctx = a.ctx_lens[b];
-  ctx = max(0, min(ctx, min(a.max_blocks_per_seq * KVQ_BLOCK_SIZE, a.max_ctx)));
-  const int n = min(a.n_split, (ctx + a.split_rows - 1) / a.split_rows);
+  const int n = live_splits<WIN>(a, b);
   const long long pu0 = unit * a.n_split;
   float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
   if (lane < n) st = reinterpret_cast<const float4*>(a.part_stats)[pu0 + lane];
@@ -203,6 +208,40 @@ __device__ __forceinline__ void decode_merge_warps(const DecodeArgs& a, int bloc
 // Many (query row, head) units and few splits: a warp a unit.
 inline bool decode_merge_by_warps(const DecodeArgs& a) {
   return a.n_split <= kMergeWarpMaxSplits && static_cast<long long>(a.batch) * a.nq * a.n_q_heads >= 512;
+}
+
+template <int D, bool WIN>
+__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(DecodeArgs a) {
+  extern __shared__ float wts[];
+  decode_merge_block<D, WIN>(a, blockIdx.x, blockIdx.y, blockIdx.z, wts);
+}
+
+template <int D, bool WIN>
+__global__ void __launch_bounds__(256) decode_merge_warp_kernel(DecodeArgs a) {
+  decode_merge_warps<D, WIN>(a, blockIdx.x);
+}
+
+// Past kMergeSmem bytes of splits' weights the merge has to ask for its shared memory (48 KB less its own arrays are
+// free); it does so before stage 1, which may write the cache.
+template <int D, bool WIN = false>
+static cudaError_t prepare_merge(const DecodeArgs& a) {
+  static std::atomic<uint64_t> done{0};
+  if (decode_merge_by_warps(a) || a.n_split * sizeof(float) <= kMergeSmem) return cudaSuccess;
+  return allow_smem(reinterpret_cast<const void*>(decode_merge_kernel<D, WIN>), kMaxSplits * sizeof(float), done);
+}
+
+template <int D, bool WIN = false>
+static cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream) {
+  const long long units = static_cast<long long>(a.batch) * a.nq * a.n_q_heads;
+  cudaError_t e;
+  if (decode_merge_by_warps(a)) {
+    e = launch_pdl(decode_merge_warp_kernel<D, WIN>, dim3(static_cast<unsigned>((units + 7) / 8)), dim3(256), 0, stream, a);
+  } else {
+    const dim3 g2(a.n_q_heads, a.batch * a.nq, D / kMergeCols);
+    e = launch_pdl(decode_merge_kernel<D, WIN>, g2, dim3(kMergeThreads), a.n_split * sizeof(float), stream, a);
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 }  // namespace kvq

@@ -93,7 +93,10 @@ __device__ __forceinline__ void write_new_tokens(const DecodeArgs& a, int b, int
 // fused step's write of the new tokens is compiled in (and runs when a.k_new is set).  SCORES: every
 // score also goes to a.scores (log2 units, -inf for a key the row does not see), for the pass that
 // turns them into weights once the row's maximum and sum are known; a dropped range leaves -inf.
-template <int D, int NT, int NTEAM, int DEPTH, bool SPLIT, bool MROW, bool WRITE, bool SCORES>
+// WIN: a sliding window and first keys that stay visible.  Pages that no row sees are not read: the range, its
+// splits and every position below are virtual, counted without them (window_map), and only the look-ups in the
+// block table put them back.
+template <int D, int NT, int NTEAM, int DEPTH, bool SPLIT, bool MROW, bool WRITE, bool SCORES, bool WIN = false>
 __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8) ? 2 : 1)
     decode_stage1_kernel(DecodeArgs a) {
   using L = DecodeSmem<D, NT, NTEAM, DEPTH>;
@@ -122,8 +125,9 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
   const int32_t* bt = a.block_table + static_cast<long long>(b) * a.max_blocks_per_seq + t_begin / KVQ_BLOCK_SIZE;
   // The team's first 32 page ids are read together with ctx (not after it): entries past the
   // sequence's pages are read but not used; the row bound keeps every read inside the table.
+  // (With a window the entries to read depend on ctx.)
   int pg = -1;
-  {
+  if constexpr (!WIN) {
     const int first = t_begin / KVQ_BLOCK_SIZE + p + lane * NTEAM;
     if (nt == 0 && first < a.max_blocks_per_seq) pg = __ldg(bt + p + lane * NTEAM);
   }
@@ -164,6 +168,16 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
     ctx = min(ctx, cap);
   }
   if (ctx < 0) ctx = 0;
+  WindowMap wm{};
+  if constexpr (WIN) {
+    wm = window_map(ctx, nq, a.window, a.n_sink);
+    ctx -= wm.skipped * KVQ_BLOCK_SIZE;
+  }
+  // entry i of the block-table row, counted from this CTA's first page
+  auto page_at = [&](int i) {
+    if constexpr (WIN) return __ldg(bt + i + (t_begin / KVQ_BLOCK_SIZE + i >= wm.sink_pages ? wm.skipped : 0));
+    else return __ldg(bt + i);
+  };
   const int t_end = SPLIT ? min(ctx, t_begin + a.split_rows) : ctx;
   const int n_pages = (t_end > t_begin) ? (t_end - t_begin + KVQ_BLOCK_SIZE - 1) / KVQ_BLOCK_SIZE : 0;
   // One new token (plain decode, single-warp teams, head_dim 256): the owning warp requests the
@@ -244,6 +258,9 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
   // page ids of this team (read by its issuing warp, nt = 0), a window of 32 in its lanes
   // (lane i <-> page k = wb + i)
   int wb = 0;
+  if constexpr (WIN) {
+    if (nt == 0 && lane < npp) pg = page_at(p + lane * NTEAM);
+  }
   if (lane >= npp) pg = -1;
   int n_issued = 0;  // pages of the team whose copies the issuing warp has issued
   // test-only fault injection: the first team of CTA 0 leaves its second page un-issued (no copy
@@ -253,7 +270,7 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
   auto issue = [&](int k) {
     while (k >= wb + 32) {
       wb += 32;
-      pg = (wb + lane < npp) ? __ldg(bt + p + (wb + lane) * NTEAM) : -1;
+      pg = (wb + lane < npp) ? page_at(p + (wb + lane) * NTEAM) : -1;
     }
     const int page = __shfl_sync(0xffffffffu, pg, k - wb);
     ++n_issued;
@@ -292,7 +309,7 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
       for (int pr = (lo_all - t_begin) / KVQ_BLOCK_SIZE; pr < n_pages; ++pr) {
         if (pr % NTEAM != p || ((pr / NTEAM) < DEPTH) != first_batch) continue;
         const int tp = t_begin + pr * KVQ_BLOCK_SIZE;
-        const int page = __ldg(bt + pr);
+        const int page = page_at(pr);
         const int lo = max(tp, first_new), hi = min(tp + KVQ_BLOCK_SIZE, t_end);
         const int w0 = first_batch ? 0 : nt, step = first_batch ? 1 : NT;
         if (page >= 0 && page < a.num_blocks && lo + w0 < hi)
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
       w_sk = quant_rule_warp_packed(xk, kpk);
       w_sv = quant_rule_warp_packed(xv, vpk);
       // the page: from the issuing window (page k <-> lane k) when it holds it
-      const int page = (k_w < 32) ? __shfl_sync(0xffffffffu, pg, k_w) : __ldg(bt + pr_w);
+      const int page = (k_w < 32) ? __shfl_sync(0xffffffffu, pg, k_w) : page_at(pr_w);
       w_ok = page >= 0 && page < a.num_blocks;
       if (w_ok) {
         const long long ph = static_cast<long long>(page) * a.n_kv_heads + kvh;
@@ -402,6 +419,12 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
       const int r = nt * 8 + 2 * c + i;
       if (r < R) lim[i] = min(t_end, ctx - nq + 1 + r / G);
     }
+  }
+  // WIN: the first key of the rows' windows
+  int low[2] = {ctx - a.window, ctx - a.window};
+  if constexpr (WIN && MROW) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) low[i] = ctx - nq + 1 + min(nt * 8 + 2 * c + i, R - 1) / G - a.window;
   }
 
   // per-lane ldmatrix offsets: K rows are tokens (in row_token order), Q^T rows are heads,
@@ -479,8 +502,10 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float cqi = i ? cq1 : cq0;
-      const float s0 = (v0 && (!MROW || t0 < lim[i])) ? S[i] * sk0 * cqi : -INFINITY;
-      const float s1 = (v1 && (!MROW || t1 < lim[i])) ? S[2 + i] * sk1 * cqi : -INFINITY;
+      const bool see0 = v0 && (!MROW || t0 < lim[i]) && (!WIN || t0 >= low[i] || t0 < a.n_sink);
+      const bool see1 = v1 && (!MROW || t1 < lim[i]) && (!WIN || t1 >= low[i] || t1 < a.n_sink);
+      const float s0 = see0 ? S[i] * sk0 * cqi : -INFINITY;
+      const float s1 = see1 ? S[2 + i] * sk1 * cqi : -INFINITY;
       if constexpr (SCORES) {
         const int row = nt * 8 + 2 * c + i;
         if (row < R) {
@@ -489,7 +514,8 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
           if (t1 < t_end) sc[t1] = s1;
         }
       }
-      const float z0 = s0 + lv0, z1 = s1 + lv1;
+      // (a key behind the window may have any scale)
+      const float z0 = WIN && !see0 ? -INFINITY : s0 + lv0, z1 = WIN && !see1 ? -INFINITY : s1 + lv1;
       float tms = fmaxf(s0, s1), tmz = fmaxf(z0, z1);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
@@ -674,14 +700,14 @@ __global__ void __launch_bounds__(NT * NTEAM * 32, (D == 128 && NT * NTEAM == 8)
   }
 }
 
-template <int D, int NT, bool SPLIT, bool MROW = true, bool WRITE = true, bool SCORES = false>
+template <int D, int NT, bool SPLIT, bool MROW = true, bool WRITE = true, bool SCORES = false, bool WIN = false>
 static cudaError_t launch_stage1(const DecodeArgs& a, dim3 grid, cudaStream_t stream) {
   // One n-tile: 8 single-warp teams x 3 stages.  More rows: up to 16 warps in as many teams
   // as fit (pages in flight per SM), each ring 24 / NTEAM deep.
   constexpr int NTEAM = NT == 1 ? 8 : 16 / NT;
   constexpr int DEPTH = 24 / NTEAM;
   using L = DecodeSmem<D, NT, NTEAM, DEPTH>;
-  auto kern = decode_stage1_kernel<D, NT, NTEAM, DEPTH, SPLIT, MROW, WRITE, SCORES>;
+  auto kern = decode_stage1_kernel<D, NT, NTEAM, DEPTH, SPLIT, MROW, WRITE, SCORES, WIN>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kTotal, done);
   if (e != cudaSuccess) return e;

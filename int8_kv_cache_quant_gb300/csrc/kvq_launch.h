@@ -78,7 +78,23 @@ struct DecodeArgs {
   // units, fp32 [B][Hkv][G * nq][scores_stride]
   float* scores;
   long long scores_stride;
+  // windowed step only: a row at position p sees keys t <= p with t > p - window or t < n_sink; both at most max_ctx
+  int window, n_sink;
 };
+// Pages that a windowed step does not read: of a sequence of ctx keys whose first of nq rows is at ctx - nq, those
+// behind the pages of the first n_sink keys and before the first row's window.  The others are counted without them
+// (a virtual length ctx - 16 * skipped, virtual pages): page v is page v of the block-table row below `sink_pages`, else
+// page v + skipped.
+struct WindowMap {
+  int sink_pages, skipped;
+};
+__host__ __device__ inline WindowMap window_map(int ctx, int nq, int window, int n_sink) {
+  WindowMap m;
+  m.sink_pages = n_sink / KVQ_BLOCK_SIZE + (n_sink % KVQ_BLOCK_SIZE != 0);
+  const int low = ctx - nq - window + 1;  // the first key of the first row's window
+  m.skipped = low > 0 && low / KVQ_BLOCK_SIZE > m.sink_pages ? low / KVQ_BLOCK_SIZE - m.sink_pages : 0;
+  return m;
+}
 enum class DecodeRoute { kSingle = 1, kSplit = 2 };
 // Test-only fault injection and wait budget of the kernels launched next (kvq_debug_fault_inject).
 int debug_fault_mode();
@@ -95,6 +111,7 @@ struct DecodePlan {
 int decode_plan(const kvq_cache* cache, int32_t batch, int32_t nq, int32_t n_q_heads, int32_t max_ctx,
                 const kvq_decode_opts* opts, DecodePlan* plan);
 cudaError_t launch_decode(const DecodeArgs& a, DecodeRoute route, cudaStream_t stream, int* launched);
+cudaError_t launch_step_window(const DecodeArgs& a, DecodeRoute route, cudaStream_t stream, int* launched);
 // the stage-1 kernel's K/V stream alone, split route geometry (kvq_debug_stream_floor)
 cudaError_t launch_stream_floor(const DecodeArgs& a, cudaStream_t stream);
 

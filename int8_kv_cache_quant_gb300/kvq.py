@@ -107,6 +107,10 @@ def lib():
         L.kvq_step_accum_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32, _Int32, ctypes.POINTER(_DecodeOpts)]
         L.kvq_decode_step_accum_int8kv.argtypes = [cp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, vp, i64,
                                                    vp, vp, vp, sz, ctypes.POINTER(_DecodeOpts), vp]
+        L.kvq_step_window_workspace_bytes.restype = sz
+        L.kvq_step_window_workspace_bytes.argtypes = [_Int32] * 8 + [ctypes.POINTER(_DecodeOpts)]
+        L.kvq_decode_step_window_int8kv.argtypes = [cp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, i32, i32, vp, vp, sz,
+                                                    ctypes.POINTER(_DecodeOpts), vp]
         L.kvq_chunk_weights_workspace_bytes.restype = sz
         L.kvq_chunk_weights_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32, _Int32]
         L.kvq_attn_chunk_weights_int8kv.argtypes = [cp, vp, i32, i32, i32, vp, i32, f32, vp, i64, vp, sz, vp]
@@ -633,6 +637,69 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
         float(softmax_scale), _hp(out), acc_p, stride, slot_pos_p, pos_p, _p(workspace), wbytes, ctypes.byref(o),
         _stream(stream)))
     return ret
+
+
+def kvq_step_window_workspace_bytes(batch, n_new, n_q_heads, n_kv_heads, max_ctx, window, n_sink, head_dim, split_rows=0,
+                                    force_route=0):
+    o = _decode_opts(split_rows, 0, force_route)
+    return int(lib().kvq_step_window_workspace_bytes(batch, n_new, n_q_heads, n_kv_heads, max_ctx, window, n_sink, head_dim,
+                                                     ctypes.byref(o)))
+
+
+def kvq_decode_step_window_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, max_ctx, softmax_scale, window, n_sink=0,
+                                  out=None, workspace=None, split_rows=0, force_route=0, stream=None, stage1_events=None,
+                                  launches=None):
+    """kvq_decode_step_int8kv (k_new = v_new = None: kvq_attn_verify_int8kv) with a sliding window: the row at position p
+    sees keys t <= p with t > p - window or t < n_sink.  Returns out fp32 shaped like q."""
+    fn = "kvq_decode_step_window_int8kv"
+    _fit(fn, max_ctx, window, n_sink)
+    squeeze = q.dim() == 3
+    if squeeze:
+        q = q[:, None]
+    B, nq, Hq, D = q.shape
+    if out is None:
+        out = _new_out((B, nq, Hq, D), q, stream)
+        ret = out[:, 0] if squeeze else out
+    else:
+        ret = out
+    H, dev = cache.n_kv_heads, _current_device()
+    q_p = _step_rows(fn, "q", q, torch.bfloat16, B * nq * Hq * D, dev)
+    out_p = _step_rows(fn, "out", out, torch.float32, B * nq * Hq * D, dev)
+    k_p = v_p = None
+    if k_new is not None or v_new is not None:
+        if k_new is None or v_new is None:
+            raise ValueError("%s: k_new and v_new go together" % fn)
+        k_p = _step_rows(fn, "k_new", k_new, torch.bfloat16, B * nq * H * D, dev)
+        v_p = _step_rows(fn, "v_new", v_new, torch.bfloat16, B * nq * H * D, dev)
+    if D != cache.head_dim:
+        raise ValueError("%s: q has head_dim %d, the cache %d" % (fn, D, cache.head_dim))
+    ctx_p = _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
+    n_blocks = block_table.shape[-1]
+    table_p = _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
+    o = _decode_opts(split_rows, 0, force_route, stage1_events, launches)
+    ws_p, wbytes = None, 0
+    if workspace is None:
+        need = int(lib().kvq_step_window_workspace_bytes(B, nq, Hq, H, int(max_ctx), int(window), int(n_sink), D, ctypes.byref(o)))
+        if need:
+            workspace = _empty(need, torch.uint8, cache.k.device, stream)
+    if workspace is not None:
+        ws_p, wbytes = _p(workspace), workspace.numel() * workspace.element_size()
+    c = _cache_struct(fn, cache, dev)
+    _check(fn, lib().kvq_decode_step_window_int8kv(
+        ctypes.byref(c), k_p, v_p, q_p, B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx), float(softmax_scale), int(window),
+        int(n_sink), out_p, ws_p, wbytes, ctypes.byref(o), _stream(stream)))
+    return ret
+
+
+def _step_rows(fn, name, t, dtype, n, dev):
+    """Pointer of n contiguous elements on the current device, or in mapped page-locked host memory (zero-copy)."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: %s must be a contiguous %s tensor of %d elements" % (fn, name, dtype, n))
+    if t.get_device() != dev:
+        if t.is_cuda:
+            _elsewhere(fn, name, t)
+        return _hp(t)
+    return t.data_ptr()
 
 
 def kvq_chunk_weights_workspace_bytes(n_tokens, n_q_heads, n_kv_heads, history_len, head_dim):

@@ -22,6 +22,44 @@ def cache(d=256, hkv=4, block=16, kp=A):
     return k.kvq._Cache(kp, A, A, A, 8, block, hkv, d)
 
 
+def step(L, c=None, k_new=A, v_new=A, q=A, batch=1, n_new=1, hq=24, bt=A, mb=8, ctx=A, max_ctx=100, w=50, sink=4, out=A, ws=A,
+         wb=1 << 30, opts=None):
+    return L.kvq_decode_step_window_int8kv(ctypes.byref(c or cache()), k_new, v_new, q, batch, n_new, hq, bt, mb, ctx, max_ctx, 0.1, w,
+                                           sink, out, ws, wb, ctypes.byref(opts) if opts else None, None)
+
+
+def opts(split=0, force=0):
+    return k.kvq._decode_opts(split, 0, force)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(w=0)), (INVALID, dict(w=-1)), (INVALID, dict(sink=-1)), (INVALID, dict(q=None)), (INVALID, dict(out=None)),
+    (INVALID, dict(ctx=None)), (INVALID, dict(bt=None)), (INVALID, dict(k_new=None)), (INVALID, dict(v_new=None)), (INVALID, dict(hq=23)),
+    (INVALID, dict(batch=0)), (INVALID, dict(n_new=0)), (INVALID, dict(max_ctx=-1)), (INVALID, dict(opts=opts(split=24))),
+    (INVALID, dict(opts=opts(force=3))), (UNSUPPORTED, dict(hq=4 * 17)), (UNSUPPORTED, dict(n_new=9)), (UNSUPPORTED, dict(batch=65536)),
+    (UNSUPPORTED, dict(c=cache(d=192))), (UNSUPPORTED, dict(mb=1 << 27)), (UNSUPPORTED, dict(max_ctx=1 << 30, w=1 << 30, opts=opts(16, 2))),
+    (MISALIGNED, dict(q=A + 2)), (MISALIGNED, dict(k_new=A + 8)), (MISALIGNED, dict(out=A + 4)), (MISALIGNED, dict(ctx=A + 1)),
+    (MISALIGNED, dict(ws=A + 8, opts=opts(16, 2))), (WORKSPACE, dict(ws=None, opts=opts(16, 2))),
+    (WORKSPACE, dict(wb=1000, opts=opts(16, 2)))])
+def test_step_refusals(L, status, kw):
+    assert step(L, **kw) == status
+
+
+def test_step_workspace(L):
+    # the keys that count: pages of the first tokens, and of a window that may begin at the end of a page
+    need = lambda *a, **kw: k.kvq_step_window_workspace_bytes(*a, **kw)  # noqa: E731
+    full = lambda keys: k.kvq_verify_workspace_bytes(2, 3, 8, keys, 128, split_rows=64)  # noqa: E731
+    assert need(2, 3, 8, 2, 100000, 1000, 5, 128, split_rows=64) == full(16 + 16 * ((1000 + 2 + 30) // 16))
+    assert need(2, 3, 8, 2, 500, 1000, 5, 128, split_rows=64) == full(500)
+    assert need(2, 3, 8, 2, 1 << 30, 2 ** 31 - 1, 2 ** 31 - 1, 128, split_rows=65536) == k.kvq_verify_workspace_bytes(
+        2, 3, 8, 1 << 30, 128, split_rows=65536)
+    assert need(2, 3, 8, 2, 500, 0, 5, 128) == 0 and need(2, 3, 8, 2, 500, 5, -1, 128) == 0
+    assert need(1, 1, 24, 4, 100000, 30, 0, 256) == 0  # one split: the single-CTA route
+    n = need(2, 3, 8, 2, 100000, 1000, 5, 128, split_rows=64)
+    kw = dict(c=cache(d=128, hkv=2), batch=2, n_new=3, hq=8, max_ctx=100000, mb=6250, w=1000, sink=5, opts=opts(split=64))
+    assert step(L, wb=n - 1, **kw) == WORKSPACE
+
+
 MAP = bytes([0, 1, 2] * 42 + [0, 0])
 
 

@@ -74,3 +74,28 @@ def append(pool, k, v, seq, slot, table):
             pool.v[page, :, :, at] = vc[i]
             pool.ks[page, :, at], pool.vs[page, :, at] = ks[i], vs[i]
     return np.array(done)
+
+
+def attend(k, v, ok, q, pos, window, sink, scale):
+    """Attention of rows q [R][D] at positions pos [R] over keys k, v [n][D] (0 .. n-1, ok: on a page of the pool), 64 bits:
+    out [R][D], the bound of the relative error of a weight (as forget_ref.weights derives it) and mag = sum p |v|."""
+    n, D = k.shape
+    t, p = np.arange(n)[None], np.asarray(pos, np.int64)[:, None]
+    seen = (t <= p) & ((t > p - window) | (t < sink)) & ok[None]
+    s = np.where(seen, (q @ k.T) * scale, -np.inf)
+    m = s.max(1, keepdims=True, initial=-np.inf)
+    w = np.where(seen, np.exp(s - np.where(np.isfinite(m), m, 0.0)), 0.0)
+    l = w.sum(1, keepdims=True)
+    w = w / np.where(l > 0, l, 1.0)
+    amp = (np.abs(q) @ np.abs(k).T * scale * 1.4427 * seen).max(1, initial=0.0)
+    rel = 4 * np.log(2) * amp * (D / 16 + 5) * 2.0 ** -23 + 4 * 2.0 ** -22 + seen.sum(1) * 2.0 ** -24
+    return w @ v, rel, w @ np.abs(v)
+
+
+def unread_pages(table, lens, n_new, window, sink, fill):
+    """The block tables with every entry that no row sees replaced by `fill`."""
+    t = table.copy()
+    for b, n in enumerate(lens):
+        low = max(0, int(n) - n_new - window + 1) // PAGE
+        t[b, -(-sink // PAGE):low] = fill
+    return t
