@@ -660,6 +660,46 @@ int kvq_attn_prefill_int8_qcodes(const kvq_cache* cache, const int8_t* q_codes, 
                                  float softmax_scale, float* out, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* Type of an attention output. */
+#define KVQ_OUT_FP32 0
+#define KVQ_OUT_BF16 1
+
+/* Workspace (bytes) of kvq_attn_prefill_window_int8kv: the 128-key tiles that any query sees, their K codes widened to bf16
+ * and their V codes to fp16 in the attention kernel's operand layout (4 * head_dim bytes a key and KV head) with three
+ * factors a key, and two parts (128 rows of head_dim + 2 floats) for each of up to 160 CTAs.  It does not depend on the
+ * GPU.  0 if an argument is not positive (history_len and n_sink may be 0), n_q_heads is no multiple of n_kv_heads,
+ * head_dim is not 128 / 256, or the sizes are past what the call takes. */
+size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,
+                                          int32_t window, int32_t n_sink, int32_t head_dim);
+
+/*
+ * kvq_attn_prefill_window_int8kv — a chunk of n_tokens queries of one sequence with a sliding window and first tokens that
+ * stay visible, from the int8 cache: query i sits at slot p = history_len + i and sees the keys t <= p with
+ * t > p - window or t < n_sink.
+ *   out[i][h] = sum_t softmax_t(s) * v^[t],  s[t] = softmax_scale * q[i][h] . k^[t]
+ * over those keys.  Scores from the bf16 queries and the int8 codes as in decode (q is not quantised; a row whose
+ * sum of |q code| passes fp32's range, elements near 1e34, is infinite), statistics and sums in fp32 in a fixed order (the
+ * same call gives the same bits); the softmax weights, times the V scales, go into the second product as fp16 (2^-11
+ * relative), and the output is rounded once: bf16, or fp32, which then shows the weights' rounding.  V scales below 2^-100
+ * count as 2^-100.  The chunk's own K/V must already be in the cache (kvq_rope_append_int8kv, kvq_quant_write); history_len
+ * may be 0.
+ *   q              : device bf16 [n_tokens][n_q_heads][head_dim]
+ *   block_table_row: device int32 [n_blocks_row], covering history_len + n_tokens keys; entries of pages that no query
+ *                    sees are not read
+ *   softmax_scale  : finite and > 0
+ *   window         : > 0;  n_sink : >= 0
+ *   out            : device [n_tokens][n_q_heads][head_dim] of out_type, KVQ_OUT_BF16 or KVQ_OUT_FP32
+ *   workspace      : device, >= kvq_prefill_window_workspace_bytes(...), 16-byte aligned; its contents on entry do not matter
+ * A key on a page outside the pool is skipped (KVQ_DEV_BAD_BLOCK); a row that sees no key, or scores -infinity alone, gives
+ * zeros.  If a bounded wait runs out (KVQ_DEV_TIMEOUT), the rows concerned are not written.
+ * KVQ_ERR_UNSUPPORTED when the rows n_tokens * (n_q_heads / n_kv_heads) or the keys reach 2^30, or the pairs of 128-row and
+ * 128-key tiles of all KV heads 2^35.
+ */
+int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
+                                   int32_t history_len, const int32_t* block_table_row, int32_t n_blocks_row,
+                                   float softmax_scale, int32_t window, int32_t n_sink, void* out, int32_t out_type,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace (bytes) of kvq_attn_sparse_int8kv: one gather record per (logical page, KV head,
  * slot) of the sequence, 2 * head_dim + 16 bytes each (the token's K codes, V codes, both
  * scales and a page-valid word).  0 if an argument is not positive or head_dim is not 128 / 256. */
@@ -771,11 +811,12 @@ int kvq_debug_stream_floor(const kvq_cache* cache, int32_t batch, const int32_t*
  * does not issue the copy of its second page, with mode 2 the producer of prefill attention CTA 0
  * does not issue its fourth piece, with mode 3 the sparse CTA of (query 0, KV head 0) does not
  * issue the copies of its second chunk, with mode 4 the first CTA of the chunk weights' row pass does not
- * announce its first key tile (mode 0: no injection).  No copy is left in flight:
+ * announce its first key tile, with mode 5 the first CTA of the windowed prefill does not issue its fourth piece
+ * (mode 0: no injection).  No copy is left in flight:
  * the consumer's wait runs out, the kernel sets KVQ_DEV_TIMEOUT, waits (bounded) for the copies it
  * did issue, drops that CTA's result (decode single route: zero output rows; split route: an empty
  * partial that the merge skips; prefill: the unit's output rows are not written; sparse: the
- * query's rows are zeros; chunk weights: the rows concerned give no weight) and returns; the device stays usable.  Process-wide, host only; kvq_debug_fault_inject(0, 0) restores the defaults.
+ * query's rows are zeros; chunk weights: the rows concerned give no weight; windowed prefill: the rows concerned are not written) and returns; the device stays usable.  Process-wide, host only; kvq_debug_fault_inject(0, 0) restores the defaults.
  * KVQ_ERR_INVALID_ARG for an unknown mode.
  */
 int kvq_debug_fault_inject(int32_t mode, int64_t wait_budget_cycles);

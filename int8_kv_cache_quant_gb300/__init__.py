@@ -10,6 +10,7 @@ from .kvq import (KVCache, KvqError, ROPE_HALF, ROPE_INTERLEAVED, kvq_attn_decod
                   kvq_attn_chunk_weights_int8kv, kvq_cache_evict, kvq_chunk_weights_workspace_bytes,
                   kvq_debug_stream_floor, kvq_decode_step_accum_int8kv, kvq_evict_workspace_bytes,
                   kvq_decode_step_window_int8kv, kvq_step_window_workspace_bytes,
+                  kvq_attn_prefill_window_int8kv, kvq_prefill_window_workspace_bytes,
                   kvq_rope_bf16, kvq_rope_phases, RopeAxes, kvq_rope_append_int8kv, kvq_rope_axes_bf16, kvq_rope_axes_phases, kvq_step_accum_workspace_bytes,
                   kvq_debug_prefill_qk_int32,
                   kvq_decode_auto_split_rows, kvq_decode_step_int8kv, kvq_decode_workspace_bytes, kvq_device_status,

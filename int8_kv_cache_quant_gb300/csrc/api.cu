@@ -94,7 +94,7 @@ const char* kvq_status_string(int s) {
 }
 
 int kvq_debug_fault_inject(int32_t mode, int64_t wait_budget_cycles) {
-  if (mode < 0 || mode > 4) return KVQ_ERR_INVALID_ARG;
+  if (mode < 0 || mode > 5) return KVQ_ERR_INVALID_ARG;
   g_wait_budget.store(wait_budget_cycles > 0 ? static_cast<long long>(wait_budget_cycles) : kvq::kWaitBudgetCycles);
   g_fault_mode.store(mode);
   return KVQ_OK;
@@ -1029,6 +1029,92 @@ int kvq_attn_prefill_int8(const kvq_cache* cache, const void* q, int32_t n_token
   e = kvq::launch_prefill(a, s);
   if (e != cudaSuccess) return e == cudaErrorNotSupported ? KVQ_ERR_UNSUPPORTED : KVQ_ERR_CUDA;
   return KVQ_OK;
+}
+
+// Rows, keys and tile pairs are counted in 32 bits, a tile of them ahead.
+static bool prefill_window_sizes_ok(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len) {
+  constexpr long long kMost = 1LL << 30;
+  const long long rows = static_cast<long long>(n_tokens) * (n_q_heads / n_kv_heads), keys = static_cast<long long>(history_len) + n_tokens;
+  if (rows >= kMost || keys >= kMost) return false;
+  return ((rows + 127) / 128) * ((keys + 127) / 128 + 1) * n_kv_heads < 1LL << 35;
+}
+
+// The plan of checked sizes on a GPU of n_sms SMs (any number gives the same workspace).
+static kvq::PrefillWindowPlan prefill_window_plan_of(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads,
+                                                     int32_t history_len, int32_t window, int32_t n_sink, int32_t head_dim,
+                                                     int n_sms) {
+  constexpr int32_t kMost = 1 << 30;  // more keys than there are
+  return kvq::prefill_window_plan(n_tokens, n_q_heads, n_kv_heads, history_len, std::min(window, kMost),
+                                  std::min(n_sink, kMost), head_dim, n_sms);
+}
+
+size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len,
+                                          int32_t window, int32_t n_sink, int32_t head_dim) {
+  if (n_tokens <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || history_len < 0 || window <= 0 || n_sink < 0) return 0;
+  if (n_q_heads % n_kv_heads != 0 || (head_dim != 128 && head_dim != 256)) return 0;
+  if (!prefill_window_sizes_ok(n_tokens, n_q_heads, n_kv_heads, history_len)) return 0;
+  return static_cast<size_t>(
+      prefill_window_plan_of(n_tokens, n_q_heads, n_kv_heads, history_len, window, n_sink, head_dim, 1).bytes);
+}
+
+int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
+                                   int32_t history_len, const int32_t* block_table_row, int32_t n_blocks_row,
+                                   float softmax_scale, int32_t window, int32_t n_sink, void* out, int32_t out_type,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!q || !block_table_row || !out) return KVQ_ERR_INVALID_ARG;
+  if (n_tokens <= 0 || n_q_heads <= 0 || history_len < 0 || n_blocks_row <= 0) return KVQ_ERR_INVALID_ARG;
+  if (window <= 0 || n_sink < 0) return KVQ_ERR_INVALID_ARG;
+  if (out_type != KVQ_OUT_FP32 && out_type != KVQ_OUT_BF16) return KVQ_ERR_UNSUPPORTED;
+  const int H = cache->n_kv_heads, D = cache->head_dim;
+  if (n_q_heads % H != 0) return KVQ_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(history_len) + n_tokens > static_cast<long long>(n_blocks_row) * KVQ_BLOCK_SIZE)
+    return KVQ_ERR_INVALID_ARG;
+  if (H > 65535 || !prefill_window_sizes_ok(n_tokens, n_q_heads, H, history_len)) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(block_table_row)) return KVQ_ERR_MISALIGNED;
+  if (!workspace) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
+  const kvq::PrefillWindowPlan size = prefill_window_plan_of(n_tokens, n_q_heads, H, history_len, window, n_sink, D, 1);
+  if (workspace_bytes < static_cast<size_t>(size.bytes)) return KVQ_ERR_WORKSPACE;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  const kvq::PrefillWindowPlan p = prefill_window_plan_of(n_tokens, n_q_heads, H, history_len, window, n_sink, D, sms);
+  kvq::PrefillWindowArgs a{};
+  a.k = cache->k;
+  a.v = cache->v;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.num_blocks = cache->num_blocks;
+  a.n_kv_heads = H;
+  a.q = q;
+  a.n_q_heads = n_q_heads;
+  a.group = n_q_heads / H;
+  a.history_len = history_len;
+  a.n_rows = n_tokens * a.group;
+  a.n_keys = history_len + n_tokens;
+  a.window = std::min(window, 1 << 30);
+  a.n_sink = std::min(n_sink, 1 << 30);
+  a.block_table_row = block_table_row;
+  a.c2 = softmax_scale * 1.44269504088896341f;
+  a.out = out;
+  a.out_bf16 = out_type == KVQ_OUT_BF16;
+  a.row_tiles = p.row_tiles;
+  a.first_tile = p.first_tile;
+  a.sink_tiles = p.sink_tiles;
+  a.key_tiles = p.key_tiles;
+  a.line = p.line;
+  char* ws = static_cast<char*>(workspace);
+  a.k_tiles = reinterpret_cast<uint8_t*>(ws);
+  a.v_tiles = reinterpret_cast<uint8_t*>(ws + p.off_v);
+  a.par = reinterpret_cast<float*>(ws + p.off_par);
+  a.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
+  a.part = reinterpret_cast<float4*>(ws + p.off_part);
+  a.status = status_ptr();
+  a.wait_budget = kvq::debug_wait_budget();
+  a.fault = kvq::debug_fault_mode();
+  return cuda_status(kvq::launch_prefill_window(a, D, p.runs, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kvq_prefill_first_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads,

@@ -56,8 +56,6 @@
 //   one A tile a unit | two (row pass):    2: 41 | 39, 4: 59 | 50, 6: 72 | 63 and 2: 47 | 41, 4: 74 | 60, 6: 100 | 82
 #include <algorithm>
 
-#include <cuda_bf16.h>
-
 #include "kvq_dev.cuh"
 #include "kvq_launch.h"
 #include "tcgen05.cuh"
@@ -200,21 +198,6 @@ __device__ __forceinline__ void step(const ChunkWeightsArgs& a, Walk& w) {
     ++w.kvh;
   }
   w.n = b_count<PASS>(a, w.t);
-}
-
-// 16 int8 codes -> eight words of two bf16 each.  With 0x43 above it, the low seven bits of a code are
-// the bf16 number 128 + (code & 127), and its sign bit alone is 128 or 256: their difference is
-// the code, exactly.
-__device__ __forceinline__ void widen16_bf16(const uint4& raw, uint32_t* out) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t v = __byte_perm(w[i >> 1], 0x43434343u, (i & 1) ? kSelB23 : kSelB01);
-    const uint32_t lo = v & 0xFF7FFF7Fu, hi = v & 0xFF80FF80u;
-    const __nv_bfloat162 d =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
-    out[i] = *reinterpret_cast<const uint32_t*>(&d);
-  }
 }
 
 // The page of key t: its (page * n_kv_heads + kvh), or -1 (past the context, or outside the pool).

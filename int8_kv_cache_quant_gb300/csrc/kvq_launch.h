@@ -169,6 +169,44 @@ struct ChunkWeightsArgs {
 };
 cudaError_t launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream);
 
+// A chunk of prompt queries with a sliding window and first keys that stay visible.
+struct PrefillWindowPlan {
+  int row_tiles;         // 128 (query, head) rows of a KV head
+  int first_tile;        // the first 128-key tile of any query's window
+  int sink_tiles;        // tiles of first keys before it that are kept as well
+  int key_tiles;         // tiles of a KV head in the workspace: sink_tiles, then first_tile on
+  long long line;        // (row tile, key tile) pairs of one KV head
+  int runs;              // CTAs, each with an equal run of all KV heads' pairs
+  long long off_v, off_par, off_ml, off_part, bytes;
+};
+PrefillWindowPlan prefill_window_plan(int n_tokens, int n_q_heads, int n_kv_heads, int history_len, int window,
+                                      int n_sink, int head_dim, int n_sms);
+struct PrefillWindowArgs {
+  const int8_t* k;
+  const int8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  int num_blocks, n_kv_heads;
+  const void* q;  // bf16 [T][Hq][D]
+  int n_q_heads, group, history_len, n_rows, n_keys;  // n_rows = T * group
+  int window, n_sink;
+  const int32_t* block_table_row;
+  float c2;       // softmax_scale * log2(e)
+  void* out;      // [T][Hq][D], bf16 or fp32
+  int out_bf16;
+  int row_tiles, first_tile, sink_tiles, key_tiles;
+  long long line;
+  uint8_t* k_tiles;   // workspace [Hkv][key_tiles][D / 64 pieces of 16 KB]: codes in bf16, tile order
+  uint8_t* v_tiles;   // workspace, likewise in fp16
+  float* par;         // workspace [Hkv][key_tiles][3][128]: score factor, log2 of the V scale, its inverse
+  float2* part_ml;    // workspace [runs][2][128]: (reference, sum) of a unit's part, sum < 0: dropped
+  float4* part;       // workspace [runs][2][D / 4][128]: its numerator
+  unsigned int* status;
+  long long wait_budget;
+  int fault;
+};
+cudaError_t launch_prefill_window(const PrefillWindowArgs& a, int head_dim, int runs, cudaStream_t stream);
+
 // Eviction by accumulated weight.
 struct EvictArgs {
   int8_t* k;

@@ -3,6 +3,8 @@
 // row scales, and bounded waits that give up together.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "kvq_dev.cuh"
 #include "tcgen05.cuh"
 
@@ -71,6 +73,21 @@ __device__ __forceinline__ void widen16(const int4 raw, uint4& c0, uint4& c1) {
   i8x4_to_h2x2(static_cast<uint32_t>(raw.w), kSelB01, kSelB23, lo, hi);
   c1.z = lo;
   c1.w = hi;
+}
+
+// 16 int8 codes -> eight words of two bf16 each.  With 0x43 above it, the low seven bits of a code are
+// the bf16 number 128 + (code & 127), and its sign bit alone is 128 or 256: their difference is
+// the code, exactly.
+__device__ __forceinline__ void widen16_bf16(const uint4& raw, uint32_t* out) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t v = __byte_perm(w[i >> 1], 0x43434343u, (i & 1) ? kSelB23 : kSelB01);
+    const uint32_t lo = v & 0xFF7FFF7Fu, hi = v & 0xFF80FF80u;
+    const __nv_bfloat162 d =
+        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
+    out[i] = *reinterpret_cast<const uint32_t*>(&d);
+  }
 }
 
 __device__ __forceinline__ void sts128(uint8_t* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }

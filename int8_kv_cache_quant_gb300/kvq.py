@@ -126,6 +126,9 @@ def lib():
                                          i32, i32, f32, i32, vp]
         L.kvq_rope_append_int8kv.argtypes = [cp, vp, vp, i64, i64, i32, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, vp, i64,
                                              i32, vp, vp, i32, i32, i32, f32, vp]
+        L.kvq_prefill_window_workspace_bytes.restype = sz
+        L.kvq_prefill_window_workspace_bytes.argtypes = [_Int32] * 7
+        L.kvq_attn_prefill_window_int8kv.argtypes = [cp, vp, i32, i32, i32, vp, i32, f32, i32, i32, vp, i32, vp, sz, vp]
         L.kvq_prefill_first_workspace_bytes.restype = sz
         L.kvq_prefill_first_workspace_bytes.argtypes = [_Int32, _Int32, _Int32, _Int32]
         L.kvq_attn_prefill_first_bf16.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, f32, vp, vp, sz, vp]
@@ -448,7 +451,7 @@ def kvq_attn_decode_int8kv_noalloc(cache, q, block_table, ctx_lens, max_ctx, sof
 def kvq_debug_fault_inject(mode, wait_budget_cycles=0):
     """Test entry point of the failure path (see kvq.h): mode 0 none, 1 a decode stage-1 copy left
     un-issued, 2 a prefill piece left un-issued, 3 a sparse chunk left un-issued, 4 a key tile of the chunk
-    weights not announced; every bounded wait gives up after wait_budget_cycles (<= 0: the default)."""
+    weights not announced, 5 a piece of the windowed prefill left un-issued; every bounded wait gives up after wait_budget_cycles (<= 0: the default)."""
     _fit("kvq_debug_fault_inject", mode)
     _check("kvq_debug_fault_inject", lib().kvq_debug_fault_inject(int(mode), int(wait_budget_cycles)))
 
@@ -511,6 +514,40 @@ def kvq_attn_prefill_int8_qcodes(cache, q_codes, q_scales, history_len, block_ta
     _check("kvq_attn_prefill_int8_qcodes", lib().kvq_attn_prefill_int8_qcodes(
         ctypes.byref(c), _p(q_codes), _p(q_scales), T, Hq, int(history_len), _p(block_table_row),
         int(block_table_row.numel()), float(softmax_scale), _p(out), _p(workspace), wbytes, _stream(stream)))
+    return out
+
+
+def kvq_prefill_window_workspace_bytes(n_tokens, n_q_heads, n_kv_heads, history_len, window, n_sink, head_dim):
+    return int(lib().kvq_prefill_window_workspace_bytes(n_tokens, n_q_heads, n_kv_heads, history_len, window, n_sink, head_dim))
+
+
+_OUT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def kvq_attn_prefill_window_int8kv(cache, q, history_len, block_table_row, softmax_scale, window, n_sink=0, out=None,
+                                   out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """A chunk of prompt queries with a sliding window: q bf16 [T][Hq][D] at slots history_len .. sees keys t <= its slot p with
+    t > p - window or t < n_sink.  block_table_row int32 [n].  Returns out [T][Hq][D], bf16 or fp32 (out's type, or out_dtype)."""
+    fn = "kvq_attn_prefill_window_int8kv"
+    _fit(fn, history_len, window, n_sink)
+    T, Hq, D = q.shape
+    dev, n_blocks = _current_device(), block_table_row.numel()
+    q_p = _need(fn, "q", q, torch.bfloat16, (T, Hq, cache.head_dim), dev)
+    table_p = _need(fn, "block_table_row", block_table_row, torch.int32, (n_blocks,), dev)
+    kind = out_dtype if out is None else out.dtype
+    if kind not in _OUT_TYPES:
+        raise ValueError("%s: the output is bf16 or fp32 (got %s)" % (fn, kind))
+    if out is None:
+        out = _result((T, Hq, D), kind, q.device, stream)
+    out_p = _need(fn, "out", out, kind, (T, Hq, D), dev)
+    need = 0
+    if workspace is None:
+        need = kvq_prefill_window_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), int(window), int(n_sink), D)
+    workspace, wbytes = _ws(workspace, need, q.device, stream)
+    c = _cache_struct(fn, cache, dev)
+    _check(fn, lib().kvq_attn_prefill_window_int8kv(
+        ctypes.byref(c), q_p, T, Hq, int(history_len), table_p, n_blocks, float(softmax_scale), int(window), int(n_sink), out_p,
+        _OUT_TYPES[kind], _p(workspace), wbytes, _stream(stream)))
     return out
 
 

@@ -60,6 +60,55 @@ def test_step_workspace(L):
     assert step(L, wb=n - 1, **kw) == WORKSPACE
 
 
+def prompt(L, c=None, q=A, n=10, hq=24, hist=20, bt=A, nb=8, scale=0.1, w=50, sink=4, out=A, kind=1, ws=A, wb=1 << 40):
+    return L.kvq_attn_prefill_window_int8kv(ctypes.byref(c or cache()), q, n, hq, hist, bt, nb, scale, w, sink, out, kind, ws, wb, None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(q=None)), (INVALID, dict(bt=None)), (INVALID, dict(out=None)), (INVALID, dict(n=0)), (INVALID, dict(hq=0)),
+    (INVALID, dict(hq=26)), (INVALID, dict(hist=-1)), (INVALID, dict(nb=0)), (INVALID, dict(nb=1)), (INVALID, dict(w=0)),
+    (INVALID, dict(w=-5)), (INVALID, dict(sink=-1)), (INVALID, dict(scale=0.0)), (INVALID, dict(scale=-0.1)), (INVALID, dict(scale=NAN)),
+    (INVALID, dict(scale=INF)), (UNSUPPORTED, dict(kind=2)), (UNSUPPORTED, dict(kind=-1)),
+    (UNSUPPORTED, dict(n=1 << 28, hist=0, nb=1 << 24)), (UNSUPPORTED, dict(hist=(1 << 30) - 10, nb=1 << 27)),
+    (UNSUPPORTED, dict(n=1 << 25, hist=1 << 29, nb=1 << 26)), (UNSUPPORTED, dict(c=cache(hkv=65536), hq=65536)),
+    (UNSUPPORTED, dict(c=cache(d=64))), (MISALIGNED, dict(q=A + 8)), (MISALIGNED, dict(out=A + 8)), (MISALIGNED, dict(bt=A + 2)),
+    (MISALIGNED, dict(ws=A + 8)), (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(wb=1000))])
+def test_prompt_refusals(L, status, kw):
+    assert prompt(L, **kw) == status
+
+
+def prompt_tiles(T, hq, hkv, hist, window, sink):
+    """(pairs of 128-row and 128-key tiles of a KV head that share a visible key, key tiles of them), by their definition."""
+    G = hq // hkv
+    pairs, tiles = 0, set()
+    for r0 in range(0, T * G, 128):
+        i0, i1 = r0 // G, min(r0 + 127, T * G - 1) // G
+        # the tiles from the first query's window to the last query, and those of the first tokens
+        mine = set(range(max(0, hist + i0 - window + 1) // 128, (hist + i1) // 128 + 1)) | set(range(min(-(-sink // 128), (hist + i1) // 128 + 1)))
+        pairs += len(mine)
+        tiles |= mine
+    return pairs, len(tiles)
+
+
+@pytest.mark.parametrize("T,hq,hkv,hist,window,sink,d", [
+    (10, 24, 4, 20, 50, 4, 256), (1, 1, 1, 0, 1, 0, 128), (2048, 24, 4, 30720, 4096, 4, 256), (500, 6, 2, 1111, 129, 300, 128),
+    (300, 8, 8, 5000, 77, 20000, 128), (33, 24, 4, 5000, 2 ** 31 - 1, 2 ** 31 - 1, 256)])
+def test_prompt_workspace(L, T, hq, hkv, hist, window, sink, d):
+    pairs, tiles = prompt_tiles(T, hq, hkv, hist, window, sink)
+    runs = min(160, pairs * hkv)
+    want = hkv * tiles * (4 * 128 * d + 1536) + runs * 2 * 128 * (d + 2) * 4
+    assert k.kvq_prefill_window_workspace_bytes(T, hq, hkv, hist, window, sink, d) == want
+    kw = dict(c=cache(d=d, hkv=hkv), n=T, hq=hq, hist=hist, nb=-(-(hist + T) // 16), w=window, sink=sink)
+    assert prompt(L, wb=want - 1, **kw) == WORKSPACE
+
+
+def test_prompt_workspace_of_nothing(L):
+    need = k.kvq_prefill_window_workspace_bytes
+    assert need(0, 24, 4, 20, 50, 4, 256) == need(10, 23, 4, 20, 50, 4, 256) == need(10, 24, 4, -1, 50, 4, 256) == 0
+    assert need(10, 24, 4, 20, 0, 4, 256) == need(10, 24, 4, 20, 50, -1, 256) == need(10, 24, 4, 20, 50, 4, 192) == 0
+    assert need(1 << 28, 24, 4, 0, 50, 4, 256) == 0
+
+
 MAP = bytes([0, 1, 2] * 42 + [0, 0])
 
 

@@ -99,3 +99,40 @@ def unread_pages(table, lens, n_new, window, sink, fill):
         low = max(0, int(n) - n_new - window + 1) // PAGE
         t[b, -(-sink // PAGE):low] = fill
     return t
+
+
+def prompt(pool, table_row, q, history, window, sink, scale):
+    """Windowed attention of the queries q [T][Hq][D] (fp64 of bf16), 64 bits: out [T][Hq][D], and what an fp32 result of the
+    tensor-core kernel may be off.
+
+    A weight is 2^(z - r), z = S kf + lv with S the exact products' fp32 sum (16 a step, at most a step of 2^-23 of the
+    partial sums each), kf = k_scale c two roundings, lv = log2 v_scale two steps, z and z - r one rounding each: with A
+    the largest c sum |q k| and B the largest |z|, |dz| <= A (D / 16 + 5) 2^-23 + 4 B 2^-24; twice that times ln 2 for the weight
+    and its sum, two exponentials of 2^-22, the additions of the sum (n 2^-24), quotient and inverse scale.  In the
+    numerator it is rounded to fp16, half a step: 2^-11 relative, or 2^-25 absolute where the largest weight of the row
+    is at least 1: 2^-25 max(p v_scale) sum |code| in the output."""
+    T, Hq, D = q.shape
+    n = history + T
+    k, v, ok = pool.rows(table_row, n)
+    G = Hq // pool.hkv
+    page, at = np.where(ok, np.asarray(table_row)[np.arange(n) // PAGE], 0), np.arange(n) % PAGE
+    out, tol = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    t, p = np.arange(n)[None], (history + np.arange(T))[:, None]
+    seen = (t <= p) & ((t > p - window) | (t < sink)) & ok[None]
+    for h in range(Hq):
+        kh, vh = k[h // G], v[h // G]
+        vs = pool.vs[page, h // G, at].astype(np.float64)
+        code = np.abs(vh) / np.where(vs > 0, vs, 1.0)[:, None]
+        s = np.where(seen, (q[:, h] @ kh.T) * scale, -np.inf)
+        m = s.max(1, keepdims=True, initial=-np.inf)
+        w = np.where(seen, np.exp(s - np.where(np.isfinite(m), m, 0.0)), 0.0)
+        l = w.sum(1, keepdims=True)
+        w = w / np.where(l > 0, l, 1.0)
+        a = (np.abs(q[:, h]) @ np.abs(kh).T * scale * 1.4427 * seen).max(1, initial=0.0)
+        b = a + np.abs(np.log2(np.maximum(vs, 2.0 ** -100))).max()
+        dz = a * (D / 16 + 5) * 2.0 ** -23 + 4 * b * 2.0 ** -24
+        rel = 2 * np.log(2) * dz + 4 * 2.0 ** -22 + 2 * seen.sum(1) * 2.0 ** -24
+        out[:, h] = w @ vh
+        tol[:, h] = (rel[:, None] + 2.0 ** -11) * (w @ np.abs(vh)) + \
+            2.0 ** -25 * (w * vs).max(1, initial=0.0)[:, None] * (seen @ code) + 1e-30
+    return out, tol
