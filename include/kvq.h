@@ -692,8 +692,8 @@ size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, i
  *   workspace      : device, >= kvq_prefill_window_workspace_bytes(...), 16-byte aligned; its contents on entry do not matter
  * A key on a page outside the pool is skipped (KVQ_DEV_BAD_BLOCK); a row that sees no key, or scores -infinity alone, gives
  * zeros.  If a bounded wait runs out (KVQ_DEV_TIMEOUT), the rows concerned are not written.
- * KVQ_ERR_UNSUPPORTED when the rows n_tokens * (n_q_heads / n_kv_heads) or the keys reach 2^30, or the pairs of 128-row and
- * 128-key tiles of all KV heads 2^35.
+ * KVQ_ERR_UNSUPPORTED when the GQA group exceeds 1024, the rows n_tokens * (n_q_heads / n_kv_heads) or the keys reach 2^30, or
+ * the pairs of 128-row and 128-key tiles of all KV heads 2^35.
  */
 int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
                                    int32_t history_len, const int32_t* block_table_row, int32_t n_blocks_row,

@@ -1072,7 +1072,7 @@ int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_
   if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
   if (static_cast<long long>(history_len) + n_tokens > static_cast<long long>(n_blocks_row) * KVQ_BLOCK_SIZE)
     return KVQ_ERR_INVALID_ARG;
-  if (H > 65535 || !prefill_window_sizes_ok(n_tokens, n_q_heads, H, history_len)) return KVQ_ERR_UNSUPPORTED;
+  if (H > 65535 || n_q_heads / H > 1024 || !prefill_window_sizes_ok(n_tokens, n_q_heads, H, history_len)) return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out) || !aligned4(block_table_row)) return KVQ_ERR_MISALIGNED;
   if (!workspace) return KVQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
@@ -1092,6 +1092,7 @@ int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_
   a.n_q_heads = n_q_heads;
   a.group = n_q_heads / H;
   a.history_len = history_len;
+  a.group_inv = a.group == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + a.group - 1) / a.group);
   a.n_rows = n_tokens * a.group;
   a.n_keys = history_len + n_tokens;
   a.window = std::min(window, 1 << 30);

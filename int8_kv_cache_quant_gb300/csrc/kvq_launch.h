@@ -189,6 +189,7 @@ struct PrefillWindowArgs {
   int num_blocks, n_kv_heads;
   const void* q;  // bf16 [T][Hq][D]
   int n_q_heads, group, history_len, n_rows, n_keys;  // n_rows = T * group
+  uint32_t group_inv;  // ceil(2^32 / group), 0 for 1
   int window, n_sink;
   const int32_t* block_table_row;
   float c2;       // softmax_scale * log2(e)
@@ -200,7 +201,7 @@ struct PrefillWindowArgs {
   uint8_t* v_tiles;   // workspace, likewise in fp16
   float* par;         // workspace [Hkv][key_tiles][3][128]: score factor, log2 of the V scale, its inverse
   float2* part_ml;    // workspace [runs][2][128]: (reference, sum) of a unit's part, sum < 0: dropped
-  float4* part;       // workspace [runs][2][D / 4][128]: its numerator
+  float4* part;       // workspace [runs][2][128 * D / 4]: its numerator, as the softmax threads hold it
   unsigned int* status;
   long long wait_budget;
   int fault;

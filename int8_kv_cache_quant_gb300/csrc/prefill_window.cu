@@ -22,12 +22,17 @@
 // the order of the line, so that the same call gives the same bits; one that lies within a run is written at once.
 //
 // A CTA's warps:
-//   warps 0-7  softmax: thread = (row, half of the tile's keys); lanes 32 (w % 4) .. of tensor memory
+//   warps 0-7  softmax: rows 32 (w % 4) .. of the tile (the lanes of tensor memory that the warp can reach), half of its keys
 //   warp 8     MMA issue and tensor-memory allocation
 //   warp 9     tile copies: a ring of 16 KB pieces in the order the MMAs take them, and the keys' factors
-// Tensor memory: S (128 columns) | P, two buffers of 64 | O (head_dim) | at head_dim 128 also Q (64).  S is one
-// buffer: its threads hold it in registers and free it before they work on it, so that the next Q K^T runs meanwhile.
-// P in tensor memory leaves the shared memory to the K/V tiles (and at head_dim 256 to Q).
+// Tensor memory: S (128 columns) | P, two buffers of 64 | O (head_dim).  S is one buffer: its threads hold it in
+// registers and free it before they work on it, so that the next Q K^T runs meanwhile.  P in tensor memory leaves the
+// shared memory to Q and the K/V tiles.
+// A softmax thread holds four rows x 16 keys of its warp's 32 x 64 (tcgen05.ld.16x256b), not one row x 64: with a row a
+// thread every thread needs all keys' factors, 512 bytes a load of the 128 that shared memory gives a cycle, 1500 cycles
+// a tile; so it is a quarter of that, for two shuffles a row in the maximum.
+// The next row tile's queries are on their way while the last tile of this one is worked on, and the products go on
+// through the change: the next Q K^T runs while the output is written.
 #include <algorithm>
 
 #include "kvq_dev.cuh"
@@ -39,8 +44,8 @@ namespace kvq {
 
 namespace {
 
-constexpr int kWSoftWarps = 8, kWSoftThreads = 32 * kWSoftWarps, kWMmaWarp = kWSoftWarps;
-constexpr int kWThreads = kWSoftThreads + 64;
+constexpr int kWSoftWarps = 16, kWMmaWarp = kWSoftWarps, kWCopyWarp = kWMmaWarp + 1, kWQWarp = kWCopyWarp + 1, kWQWarps = 2;
+constexpr int kWThreads = 32 * (kWQWarp + kWQWarps);
 constexpr int kWParBufs = 4;
 constexpr float kWLazy = 8.0f;  // a tile may exceed its row's reference by 2^8
 // V scales below this count as this: their codes' share of an output, at most 127 * 2^-100, is lost in any other
@@ -48,35 +53,68 @@ constexpr float kWMinScale = 7.8886091e-31f;  // 2^-100
 
 template <int D>
 struct Pw {
-  static constexpr bool kQTmem = D == 128;
   static constexpr int kSlots = D == 256 ? 8 : 10;           // pieces in the ring
-  static constexpr int kStageBytes = 128 * D * 2;            // the output tile in bf16; at head_dim 256 Q's place
-  static constexpr int offRing = kStageBytes;
-  static constexpr int offPar = offRing + kSlots * kPieceBytes;  // [buf][3][128] fp32
-  static constexpr int offRed = offPar + kWParBufs * 3 * 128 * 4;  // [2][part][128] fp32
-  static constexpr int offBar = offRed + 2 * 2 * 128 * 4;
-  // barriers
+  static constexpr int kQBytes = 128 * D * 2;                // Q in pieces of 16 KB
+  static constexpr int offRing = kQBytes;
+  static constexpr int offPar = offRing + kSlots * kPieceBytes;    // [buf][3][128] fp32
+  static constexpr int offRef = offPar + kWParBufs * 3 * 128 * 4;  // [128] the rows' references
+  static constexpr int offRed = offRef + 128 * 4;            // [maximum, sum][group][half of the keys][128] a row's two warps
+  static constexpr int offSum = offRed + 2 * 2 * 2 * 128 * 4;    // [2][sum, sum, reference][128] what a unit's other group leaves
+  static constexpr int kStageStride = 80;                    // of 32 bf16 columns: no bank conflicts
+  static constexpr int offStage = offSum + 2 * 3 * 128 * 4;  // [warp of a group][32 rows]
+  static constexpr int offBar = offStage + 8 * 32 * kStageStride;
+  // barriers; those of two are by a tile's parity, so that each has one group on one side
   static constexpr int full = 0, empty = full + kSlots, parFull = empty + kSlots, parFree = parFull + kWParBufs,
-                       sFull = parFree + kWParBufs, sFree = sFull + 1, pFull = sFree + 1, pvDone = pFull + 2,
-                       qFull = pvDone + 2, oFree = qFull + 1, drain = oFree + 1, kNumBars = drain + 1;
+                       sFull = parFree + kWParBufs, pFull = sFull + 2, pvDone = pFull + 2, decided = pvDone + 2,
+                       sumReady = decided + 8, qFull = sumReady + 8, qFree = qFull + 1, oFree = qFree + 1,
+                       drain = oFree + 1, kNumBars = drain + 1;
   static constexpr int offFlag = offBar + kNumBars * 8;      // abort flag, TMEM base
   static constexpr int kAlloc = offFlag + 16 + 1024;
-  static constexpr uint32_t kPCol = 128, kOCol = 256, kQCol = kOCol + 128, kTmemCols = 512;
+  // Tensor memory: two score tiles, O, and at head_dim 128 two P tiles.  At head_dim 256 a P tile takes its score tile's place.
+  static constexpr bool kOverlay = D == 256;
+  static constexpr uint32_t kOCol = 256, kTmemCols = 512;
+  static constexpr uint32_t kPHalf = kOverlay ? 64 : 32;  // columns from a P tile's first half of the keys to its second
+  __device__ static uint32_t p_col(int b) { return kOverlay ? 128 * b : 384 + 64 * b; }
+  static_assert(offBar % 8 == 0 && offStage % 16 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
-// A barrier of COUNT threads that gives them all the OR of `pred`: they take the same way.
-template <int COUNT>
-__device__ __forceinline__ bool bar_or(int id, bool pred) {
+// A barrier of two warps that gives them the OR of `pred`: they take the same way.
+__device__ __forceinline__ bool pair_or(int id, bool pred) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 64, q;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(r)
-      : "r"(pred ? 1u : 0u), "r"(id), "n"(COUNT)
+      : "r"(pred ? 1u : 0u), "r"(id)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 5, %0;" ::"n"(kWSoftThreads) : "memory"); }
+
+// 16 bytes to shared memory without passing through registers; zeros where `real` is false.
+__device__ __forceinline__ void cp_async16(uint8_t* dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// wait_or_abort in few instructions, since a dozen copies of it stand in the loops: the CTA's end reports the timeout.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long budget) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort_flag || clock64() - t0 > budget) {
+      *abort_flag = 1;
+      return false;
+    }
+  return true;
+}
+
+// x / d for x and d below 2^15, with inv = ceil(2^32 / d), or 0 for d = 1.
+__device__ __forceinline__ int small_div(int x, uint32_t inv) {
+  return inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), inv)) : x;
+}
+
+// Row of a quadrant that register pair j of a thread's fragment belongs to (tcgen05.cuh, two loads of 16 lanes).
+__device__ __forceinline__ int frag_row(int lane, int j) { return (j >> 1) * 16 + (j & 1) * 8 + (lane >> 2); }
 
 }  // namespace
 
@@ -93,6 +131,13 @@ __host__ __device__ inline RowTileKeys row_tile_keys(int t, int n_rows, int grou
   r.sink = sink < r.low ? sink : r.low;
   r.n = r.sink + p_hi / 128 - r.low + 1;
   return r;
+}
+
+// Whether a row tile's x-th scores, two tiles ahead, are made before the values at hand: not where they wait for those (P in
+// their place) or for new queries.
+template <int D>
+__device__ __forceinline__ bool scores_first(int x) {
+  return !Pw<D>::kOverlay && x != 0;
 }
 
 // Place on the line: KV head, row tile, key tile x of its n.
@@ -221,7 +266,8 @@ __global__ void __launch_bounds__(256) window_tiles_kernel(const __grid_constant
       float vs = a.v_scale[at];
       if (vs < kWMinScale) vs = kWMinScale;
       lv = log2f(vs);
-      iv = 1.0f / vs;
+      // (finite: 0 times it is 0 for the rows that do not see the key; the others have its infinity or NaN from lv)
+      iv = vs < INFINITY ? 1.0f / vs : 0.0f;
     }
     float* par = a.par + u * 384;
     par[tid] = kf;
@@ -234,13 +280,14 @@ __global__ void __launch_bounds__(256) window_tiles_kernel(const __grid_constant
 template <int D>
 __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __grid_constant__ PrefillWindowArgs a) {
   using L = Pw<D>;
-  constexpr int NP = D / 64, OC = D / 2;  // pieces of a K or V tile; O columns of a softmax thread
+  constexpr int NP = D / 64;  // pieces of a K or V tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
-  uint8_t* stage = sm;
   uint8_t* ring = sm + L::offRing;
   float* par = reinterpret_cast<float*>(sm + L::offPar);
+  float* refs = reinterpret_cast<float*>(sm + L::offRef);
   float* red = reinterpret_cast<float*>(sm + L::offRed);
+  float* sums = reinterpret_cast<float*>(sm + L::offSum);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::offBar);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::offFlag);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::offFlag + 4);
@@ -258,16 +305,20 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     }
     for (int s = 0; s < kWParBufs; ++s) {
       mbar_init(&bars[L::parFull + s], 1);
-      mbar_init(&bars[L::parFree + s], kWSoftWarps);
+      mbar_init(&bars[L::parFree + s], 8);
     }
-    mbar_init(&bars[L::sFull], 1);
-    mbar_init(&bars[L::sFree], kWSoftWarps);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars[L::pFull + s], kWSoftWarps);
+      mbar_init(&bars[L::sFull + s], 1);
+      mbar_init(&bars[L::pFull + s], 8);
       mbar_init(&bars[L::pvDone + s], 1);
     }
-    mbar_init(&bars[L::qFull], kWSoftWarps);
-    mbar_init(&bars[L::oFree], kWSoftWarps);
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&bars[L::decided + s], 2);
+      mbar_init(&bars[L::sumReady + s], 2);
+    }
+    mbar_init(&bars[L::qFull], kWQWarps);
+    mbar_init(&bars[L::qFree], 1);
+    mbar_init(&bars[L::oFree], 8);
     mbar_init(&bars[L::drain], 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -276,264 +327,340 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  grid_dep_wait();  // the tiles come from the kernel before
-  grid_dep_trigger();
 
   if (warp < kWSoftWarps) {
     // ================================================================ softmax warps
-    const int row = (warp & 3) * 32 + lane, part = warp >> 2, gbar = 1 + (warp & 3);
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tm_o = tmem + lane_base + L::kOCol + part * OC;
-    const uint32_t tm_p = tmem + lane_base + L::kPCol + part * 32;
+    // Two groups of eight warps take turns at the tiles; of a group a warp has the rows 32 quad .. and half of the keys.
+    const int quad = warp & 3, part = (warp >> 2) & 1, group = warp >> 3, c = lane & 3, pair_id = 1 + 4 * group + quad;
+    const uint32_t lanes0 = static_cast<uint32_t>(quad * 32) << 16, lanes1 = lanes0 + (16u << 16);
     bool failed = false;
-    float2* ml = a.part_ml + static_cast<long long>(run) * 256;
-    if (part == 0) {  // until they are written: dropped
-      ml[row] = make_float2(-INFINITY, -1.0f);
-      ml[128 + row] = make_float2(-INFINITY, -1.0f);
-    }
-    int f = 0;
-    while (f < n_tiles) {
-      // ---- a unit: the key tiles of row tile w.t that belong to this run
-      const bool first_of_run = f == 0, from_start = w.x == 0;
-      const int n_unit = min(w.keys.n - w.x, n_tiles - f);
-      const bool to_end = w.x + n_unit == w.keys.n;
-      const int r = 128 * w.t + row, qi = r / a.group;
-      const int pos = a.history_len + qi;
-      const int last_row = a.n_rows - 128 * w.t;  // rows of this tile: row < last_row
-      // ---- Q
-      if constexpr (L::kQTmem) {
-        uint32_t qw[32];  // this thread's 64 dims
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q) +
-            (static_cast<long long>(qi) * a.n_q_heads + w.kvh * a.group + (r - qi * a.group)) * D + part * 64);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = row < last_row ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          qw[4 * i] = v.x;
-          qw[4 * i + 1] = v.y;
-          qw[4 * i + 2] = v.z;
-          qw[4 * i + 3] = v.w;
-        }
-        tc::st_32x32b_x32(tmem + lane_base + L::kQCol + part * 32, qw);
-        tc::wait_st();
-      } else {
-        // a warp takes 16 rows, a row at a time: lane = 16-byte chunk
-        uint4 v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int n = warp * 16 + i, rr = 128 * w.t + n, q2 = rr / a.group;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (n < last_row)
-            v[i] = __ldg(reinterpret_cast<const uint4*>(
-                             static_cast<const uint16_t*>(a.q) +
-                             (static_cast<long long>(q2) * a.n_q_heads + w.kvh * a.group + (rr - q2 * a.group)) * D) + lane);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          sts128(stage + (lane >> 3) * kPieceBytes + tc::sw128_off(warp * 16 + i, lane & 7), v[i]);
-        tc::fence_proxy_async_smem();
-      }
-      tc::fence_before_sync();
+    auto await = [&](int bar, uint32_t parity) {
+      failed |= !wait_on(&bars[bar], parity, abort_flag, a.wait_budget);
+    };
+    auto arrive = [&](int bar) {  // for the warp
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::qFull]);
-
-      float ref = -INFINITY, l = 0.0f;
-      for (int j = 0; j < n_unit; ++j, ++f) {
-        const int b = f & 1, pb = f % kWParBufs;
-        const int k0 = 128 * w.tile();
-        failed |= !wait_or_abort(&bars[L::sFull], f & 1, a.status, abort_flag, a.wait_budget);
-        tc::fence_after_sync();
-        uint32_t s0[32], s1[32];
-        tc::ld_32x32b_x32(tmem + lane_base + 64 * part, s0);
-        tc::ld_32x32b_x32(tmem + lane_base + 64 * part + 32, s1);
-        failed |= !wait_or_abort(&bars[L::parFull + pb], (f / kWParBufs) & 1, a.status, abort_flag, a.wait_budget);
-        tc::wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::sFree]);
-        const float4* kf = reinterpret_cast<const float4*>(par + pb * 384 + 64 * part);
-        const float4* lv = kf + 32;
-        const float4* iv = kf + 64;
-        f2 z[32];
-        float m0 = -INFINITY, m1 = -INFINITY;
+      if (lane == 0) mbar_arrive(&bars[bar]);
+    };
+    auto pick = [&](const float (&x)[4]) { return c < 2 ? (c == 0 ? x[0] : x[1]) : (c == 2 ? x[2] : x[3]); };  // x[c]
+    grid_dep_wait();  // the tiles come from the kernel before
+    grid_dep_trigger();
+    float2* ml = a.part_ml + static_cast<long long>(run) * 256;
+    if (warp < 4) {  // until they are written: dropped
+      ml[quad * 32 + lane] = make_float2(-INFINITY, -1.0f);
+      ml[128 + quad * 32 + lane] = make_float2(-INFINITY, -1.0f);
+    }
+    int f_unit = 0, left_sums = 0;
+    while (f_unit < n_tiles) {
+      // ---- a unit: the key tiles of row tile w.t that belong to this run.  The thread has four rows, frag_row(lane, j).
+      const int n_unit = min(w.keys.n - w.x, n_tiles - f_unit);
+      const bool whole_unit = w.x == 0 && n_unit == w.keys.n;
+      const bool ends_it = ((f_unit + n_unit - 1) & 1) == group;  // this group has the unit's last tile, and writes its result
+      const int r0 = 128 * w.t + quad * 32, q0 = r0 / a.group, g0 = r0 - q0 * a.group;  // the warp's first row: query, head
+      auto query = [&](int row) { return q0 + small_div(g0 + row, a.group_inv); };       // of the warp's row
+      float ref[4];
+      f2 l[4];
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const float4 k4 = kf[n], l4 = lv[n];
-          const uint32_t* s = n < 8 ? s0 + 4 * n : s1 + 4 * (n - 8);
-          z[2 * n] = fma2(mk2(__uint_as_float(s[0]), __uint_as_float(s[1])), mk2(k4.x, k4.y), mk2(l4.x, l4.y));
-          z[2 * n + 1] = fma2(mk2(__uint_as_float(s[2]), __uint_as_float(s[3])), mk2(k4.z, k4.w), mk2(l4.z, l4.w));
-          m0 = fmax3(m0, lo2(z[2 * n]), hi2(z[2 * n]));
-          m1 = fmax3(m1, lo2(z[2 * n + 1]), hi2(z[2 * n + 1]));
-        }
-        // keys of this thread's half that the row sees: n < hi, and n >= lo or n < sk
-        const int kk = k0 + 64 * part, hi = pos + 1 - kk, lo = pos - a.window + 1 - kk, sk = a.n_sink - kk;
-        const bool whole = hi >= 64 && (lo <= 0 || sk >= 64);
-        if (!whole) {
-          m0 = m1 = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            const bool v0 = 2 * n < hi && (2 * n >= lo || 2 * n < sk);
-            const bool v1 = 2 * n + 1 < hi && (2 * n + 1 >= lo || 2 * n + 1 < sk);
-            z[n] = mk2(v0 ? lo2(z[n]) : -INFINITY, v1 ? hi2(z[n]) : -INFINITY);
-            m0 = fmax3(m0, lo2(z[n]), hi2(z[n]));
-          }
-        }
-        red[(b * 2 + part) * 128 + row] = fmaxf(m0, m1);
-        if (bar_or<64>(gbar, failed)) break;  // both halves of these rows leave together
-        const float m = fmaxf(red[b * 256 + row], red[b * 256 + 128 + row]);
-        float scale = 1.0f;
-        if (j == 0) {
-          ref = m;
-        } else if (m > ref + kWLazy) {
-          scale = ref == -INFINITY ? 0.0f : fast_exp2(ref - m);
-          l *= scale;
-          ref = m;
-        }
-        const float nr = ref == -INFINITY ? 0.0f : -ref;
-        const f2 nr2 = mk2(nr, nr);
-        uint32_t p[32];
-        f2 la = mk2(0.f, 0.f), lb = mk2(0.f, 0.f);
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const float4 i4 = iv[n];
-          const f2 xa = add2(z[2 * n], nr2), xb = add2(z[2 * n + 1], nr2);
-          const f2 wa = mk2(fast_exp2(lo2(xa)), fast_exp2(hi2(xa))), wb = mk2(fast_exp2(lo2(xb)), fast_exp2(hi2(xb)));
-          p[2 * n] = pack_half2(lo2(wa), hi2(wa));
-          p[2 * n + 1] = pack_half2(lo2(wb), hi2(wb));
-          f2 ia = mk2(i4.x, i4.y), ib = mk2(i4.z, i4.w);
-          if (!whole) {  // a hidden key may have any scale
-            ia = mk2(lo2(wa) == 0.f ? 0.f : i4.x, hi2(wa) == 0.f ? 0.f : i4.y);
-            ib = mk2(lo2(wb) == 0.f ? 0.f : i4.z, hi2(wb) == 0.f ? 0.f : i4.w);
-          }
-          la = fma2(wa, ia, la);
-          lb = fma2(wb, ib, lb);
-        }
-        const f2 ls = add2(la, lb);
-        l += lo2(ls) + hi2(ls);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::parFree + pb]);
-        // this buffer of P was read by the product of tile f - 2
-        if (f >= 2) failed |= !wait_or_abort(&bars[L::pvDone + b], ((f >> 1) - 1) & 1, a.status, abort_flag, a.wait_budget);
-        if (__any_sync(0xffffffffu, scale != 1.0f)) {
-          // O holds the products up to tile f - 1 (of this unit: j > 0)
-          failed |= !wait_or_abort(&bars[L::pvDone + (b ^ 1)], ((f - 1) >> 1) & 1, a.status, abort_flag, a.wait_budget);
-          tc::fence_after_sync();
-          const f2 sc2 = mk2(scale, scale);
-#pragma unroll 1
-          for (int c = 0; c < OC / 32; ++c) {
-            uint32_t o[32];
-            tc::ld_32x32b_x32(tm_o + 32 * c, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const f2 x = mul2(mk2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), sc2);
-              o[e] = __float_as_uint(lo2(x));
-              o[e + 1] = __float_as_uint(hi2(x));
-            }
-            tc::st_32x32b_x32(tm_o + 32 * c, o);
-          }
-        }
-        tc::fence_after_sync();
-        tc::st_32x32b_x32(tm_p + b * 64, p);
-        tc::wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::pFull + b]);
-        if (j + 1 < n_unit) window_step(a, w);
+      for (int j = 0; j < 4; ++j) {
+        ref[j] = -INFINITY;
+        l[j] = mk2(0.f, 0.f);
       }
-      if (!failed)
-        failed = !wait_or_abort(&bars[L::pvDone + ((f - 1) & 1)], ((f - 1) >> 1) & 1, a.status, abort_flag, a.wait_budget);
-      tc::fence_after_sync();
-      red[part * 128 + row] = l;
-      if (bar_or<kWSoftThreads>(5, failed)) break;  // all softmax warps leave together
-      l = red[row] + red[128 + row];
-      if (from_start && to_end) {
-        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        const int h = w.kvh * a.group + (r - qi * a.group);
-        if (a.out_bf16) {
-          // through shared memory, 16-byte chunk c of a row at c ^ (row % 8); Q's place is free, the unit's products done
+      for (int u = (f_unit & 1) == group ? 0 : 1; u < n_unit; u += 2) {
+        const int f = f_unit + u, pb = f % kWParBufs, x = w.x + u;
+        const int kk = 128 * (x < w.keys.sink ? x : x - w.keys.sink + w.keys.low) + 64 * part;  // the warp's first key
+        const uint32_t tm_s = tmem + 128 * group + 64 * part;
+        const float2* kf = reinterpret_cast<const float2*>(par + pb * 384 + 64 * part) + c;
+        await(L::parFull + pb, (f / kWParBufs) & 1);
+        await(L::sFull + group, (f >> 1) & 1);
+        tc::fence_after_sync();
+        // The scores pass through registers 32 keys at a time, and twice: first they become z, with a row's maximum, and go
+        // back.  Loops of few instructions, and many warps at them: a tile unrolled in registers came out of the
+        // instruction caches at a third of the speed.
+        float m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < OC / 32; ++c) {
-            uint32_t o[32];
-            tc::ld_32x32b_x32(tm_o + 32 * c, o);
-            tc::wait_ld();
+        for (int k = 0; k < 2; ++k) {
+          uint32_t y[32];
+          tc::ld_16x256b_x4(tm_s + lanes0 + 32 * k, y);
+          tc::ld_16x256b_x4(tm_s + lanes1 + 32 * k, y + 16);
+          tc::wait_ld();
+          // z of the four rows' keys 8 i + 2 c (and the one after it)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t hw[4];
+          for (int i = 0; i < 4; ++i) {
+            const float2 k2 = kf[16 * k + 4 * i], l2 = kf[64 + 16 * k + 4 * i];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * y]) * inv,
-                                                               __uint_as_float(o[8 * e + 2 * y + 1]) * inv);
-                hw[y] = *reinterpret_cast<const uint32_t*>(&x);
+            for (int j = 0; j < 4; ++j) {
+              uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
+              const f2 z = fma2(mk2(__uint_as_float(s[0]), __uint_as_float(s[1])), mk2(k2.x, k2.y), mk2(l2.x, l2.y));
+              s[0] = __float_as_uint(lo2(z));
+              s[1] = __float_as_uint(hi2(z));
+            }
+          }
+          // hidden keys: a row at position p sees n < hi, and n >= lo or n < sk, counted from the first of these keys
+          const int k0 = kk + 32 * k, sk = a.n_sink - k0, hi0 = a.history_len + q0 + 1 - k0;
+          if (hi0 < 32 || (a.history_len + query(31) + 1 - a.window > k0 && sk < 32)) {  // the same in the warp
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int hi = a.history_len + query(frag_row(lane, j)) + 1 - k0 - 2 * c, lo = hi - a.window, first = min(sk - 2 * c, hi);
+              const unsigned span = static_cast<unsigned>(min(hi, 32)) - static_cast<unsigned>(min(lo, 32));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int n = 8 * (e >> 1) + (e & 1);
+                uint32_t& s = y[(j >> 1) * 16 + 4 * (e >> 1) + 2 * (j & 1) + (e & 1)];
+                if (static_cast<unsigned>(n - min(lo, 32)) >= span && n >= first) s = 0xff800000u;  // -infinity
               }
-              const int chunk = part * (OC / 8) + 4 * c + e;
-              sts128(stage + row * (2 * D) + ((chunk ^ (row & 7)) << 4), make_uint4(hw[0], hw[1], hw[2], hw[3]));
             }
           }
-          tc::fence_before_sync();
-          soft_bar();
-          if (lane == 0) mbar_arrive(&bars[L::oFree]);
-          constexpr int PER = 256 / D;  // rows a warp copies at a time (D / 8 chunks each)
 #pragma unroll
-          for (int i = 0; i < 16 / PER; ++i) {
-            const int n = warp * 16 + i * PER + lane / (D / 8), chunk = lane % (D / 8);
-            if (n < last_row) {
-              const int rr = 128 * w.t + n, q2 = rr / a.group;
-              reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                       (static_cast<long long>(q2) * a.n_q_heads + w.kvh * a.group + (rr - q2 * a.group)) * D)[chunk] =
-                  *reinterpret_cast<const uint4*>(stage + n * (2 * D) + ((chunk ^ (n & 7)) << 4));
-            }
-          }
-          soft_bar();  // the stage is read before the next unit's Q takes its place
-        } else {
-          float* dst = static_cast<float*>(a.out) + (static_cast<long long>(qi) * a.n_q_heads + h) * D + part * OC;
-#pragma unroll 1
-          for (int c = 0; c < OC / 32; ++c) {
-            uint32_t o[32];
-            tc::ld_32x32b_x32(tm_o + 32 * c, o);
-            tc::wait_ld();
-            if (row < last_row) {
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(dst + 32 * c + e) =
-                    make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
+              m[j] = fmax3(m[j], __uint_as_float(s[0]), __uint_as_float(s[1]));
             }
-          }
-          tc::fence_before_sync();
-          soft_bar();
-          if (lane == 0) mbar_arrive(&bars[L::oFree]);
+          tc::st_16x256b_x4(tm_s + lanes0 + 32 * k, y);
+          tc::st_16x256b_x4(tm_s + lanes1 + 32 * k, y + 16);
         }
-      } else {
-        // a part: the numerator four columns of all rows at a time
-        const int slot = 2 * run + (first_of_run ? 0 : 1);
-        float4* dst = a.part + (static_cast<long long>(slot) * (D / 4) + part * (OC / 4)) * 128 + row;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 1));
+          m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 2));
+        }
+        float* mine = red + (2 * group + part) * 128 + quad * 32;
+        const float* others = red + (2 * group + (part ^ 1)) * 128 + quad * 32;
+        mine[frag_row(lane, c)] = pick(m);
+        tc::wait_st();
+        if (pair_or(pair_id, failed)) {
+          failed = true;
+          break;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], others[frag_row(lane, j)]);
+        // The rows' references, decided tile by tile: the other group's warp with these rows has decided for the tile before.
+        if (f > 0) await(L::decided + 4 * (group ^ 1) + quad, ((f - 1) >> 1) & 1);
+        bool moved = false;
+        if (u == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ref[j] = m[j];
+          if (part == 0) refs[quad * 32 + frag_row(lane, c)] = pick(ref);
+          arrive(L::decided + 4 * group + quad);
+        } else {
+          float now[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            now[j] = refs[quad * 32 + frag_row(lane, j)];
+            moved |= now[j] != ref[j] || m[j] > now[j] + kWLazy;
+          }
+          if (!__any_sync(0xffffffffu, moved)) {
+            arrive(L::decided + 4 * group + quad);
+          } else {
+            // the other group has moved a reference, or this tile does
+            float scale[4];
+            moved = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              // (from -infinity there is nothing in l, but NaN, which stays)
+              const float s = ref[j] == now[j] || ref[j] == -INFINITY ? 1.0f : fast_exp2(ref[j] - now[j]);
+              ref[j] = now[j];
+              scale[j] = 1.0f;
+              if (m[j] > now[j] + kWLazy) {
+                scale[j] = now[j] == -INFINITY ? 0.0f : fast_exp2(now[j] - m[j]);
+                ref[j] = m[j];
+                moved = true;
+              }
+              l[j] = mul2(l[j], mk2(s * scale[j], s * scale[j]));
+            }
+            pair_or(pair_id, false);  // both have read the references
+            if (part == 0) refs[quad * 32 + frag_row(lane, c)] = pick(ref);
+            arrive(L::decided + 4 * group + quad);
+            if (__any_sync(0xffffffffu, moved)) {
+              // O holds the products up to tile f - 1 (of this unit: u > 0); half of its columns
+              await(L::pvDone + (group ^ 1), ((f - 1) >> 1) & 1);
+              tc::fence_after_sync();
 #pragma unroll 1
-        for (int c = 0; c < OC / 32; ++c) {
-          uint32_t o[32];
-          tc::ld_32x32b_x32(tm_o + 32 * c, o);
+              for (int o = 0; o < D / 32; ++o) {  // 16 lanes, 32 columns
+                const uint32_t at = tmem + (o & 1 ? lanes1 : lanes0) + L::kOCol + part * (D / 2) + 32 * (o >> 1);
+                const float sa = o & 1 ? scale[2] : scale[0], sb = o & 1 ? scale[3] : scale[1];
+                uint32_t y[16];
+                tc::ld_16x256b_x4(at, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * (e & 2 ? sb : sa));
+                tc::st_16x256b_x4(at, y);
+              }
+            }
+          }
+        }
+        if (!L::kOverlay && f >= 2) {  // this group's P was read by the product of tile f - 2
+          await(L::pvDone + group, ((f >> 1) - 1) & 1);
+          tc::fence_after_sync();
+        }
+        const uint32_t tm_p = tmem + L::p_col(group) + L::kPHalf * part;  // head_dim 256: where scores were that have been taken
+        float nr[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) nr[j] = ref[j] == -INFINITY ? 0.0f : -ref[j];
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          uint32_t y[32], p0[8], p1[8];
+          tc::ld_16x256b_x4(tm_s + lanes0 + 32 * k, y);
+          tc::ld_16x256b_x4(tm_s + lanes1 + 32 * k, y + 16);
           tc::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[(8 * c + e) * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          for (int i = 0; i < 4; ++i) {
+            const float2 i2 = kf[128 + 16 * k + 4 * i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
+              const f2 v = add2(mk2(__uint_as_float(s[0]), __uint_as_float(s[1])), mk2(nr[j], nr[j]));
+              const float w0 = fast_exp2(lo2(v)), w1 = fast_exp2(hi2(v));
+              l[j] = fma2(mk2(w0, w1), mk2(i2.x, i2.y), l[j]);
+              (j < 2 ? p0 : p1)[2 * i + (j & 1)] = pack_half2(w0, w1);
+            }
+          }
+          tc::st_16x128b_x4(tm_p + lanes0 + 16 * k, p0);
+          tc::st_16x128b_x4(tm_p + lanes1 + 16 * k, p1);
         }
-        if (part == 0) ml[(slot & 1) * 128 + row] = make_float2(ref, l);
+        arrive(L::parFree + pb);
+        tc::wait_st();
         tc::fence_before_sync();
-        soft_bar();
-        if (lane == 0) mbar_arrive(&bars[L::oFree]);
+        arrive(L::pFull + group);
       }
+      if (pair_or(pair_id, failed)) break;
+      // ---- the unit's sums: this warp's
+      float sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[j] = lo2(l[j]) + hi2(l[j]);
+        sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+        sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+      }
+      float* left = sums + (left_sums & 1) * 384 + quad * 32;
+      if (!ends_it) {
+        if (n_unit > 1) {
+          // left for the group that has the last tile, which may still have the sums before these to take: two places, two
+          // barriers (the ones before those it took before it decided for its tile of the row tile between)
+          left[128 * part + frag_row(lane, c)] = pick(sum);
+          if (part == 0) left[256 + frag_row(lane, c)] = pick(ref);
+          arrive(L::sumReady + 4 * (left_sums & 1) + quad);
+        }
+      } else {
+        // ---- its result: O once its last product is there, with all sums
+        const int f = f_unit + n_unit - 1;
+        await(L::pvDone + group, (f >> 1) & 1);
+        if (n_unit > 1) await(L::sumReady + 4 * (left_sums & 1) + quad, (left_sums >> 1) & 1);
+        tc::fence_after_sync();
+        float* mine = red + (4 + 2 * group + part) * 128 + quad * 32;
+        const float* others = red + (4 + 2 * group + (part ^ 1)) * 128 + quad * 32;
+        mine[frag_row(lane, c)] = pick(sum);
+        if (pair_or(pair_id, failed)) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[j] += others[frag_row(lane, j)];
+          if (n_unit > 1) {
+            const float at = left[256 + frag_row(lane, j)];
+            sum[j] += (left[frag_row(lane, j)] + left[128 + frag_row(lane, j)]) *
+                      (at == -INFINITY || at == ref[j] ? 1.0f : fast_exp2(at - ref[j]));
+          }
+        }
+        auto load_o = [&](int o, uint32_t* y) {  // 32 columns of the four rows
+          const uint32_t at = tmem + L::kOCol + part * (D / 2) + 32 * o;
+          tc::ld_16x256b_x4(at + lanes0, y);
+          tc::ld_16x256b_x4(at + lanes1, y + 16);
+          tc::wait_ld();
+        };
+        auto row_at = [&](int row) {  // where the warp's row stands in the output
+          const int q = query(row), h = w.kvh * a.group + (r0 + row - q * a.group);
+          return (static_cast<long long>(q) * a.n_q_heads + h) * D;
+        };
+        if (whole_unit) {
+          float inv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) inv[j] = sum[j] > 0.0f || sum[j] != sum[j] ? 1.0f / sum[j] : 0.0f;
+          if (a.out_bf16) {
+            // a warp's 32 rows x 32 columns through shared memory, then 64 bytes of a row at a time
+            uint8_t* tile = sm + L::offStage + (warp & 7) * 32 * L::kStageStride;
+            uint16_t* dst[4];
+            bool real[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              real[i] = r0 + 8 * i + (lane >> 2) < a.n_rows;
+              dst[i] = static_cast<uint16_t*>(a.out) + row_at(8 * i + (lane >> 2)) + part * (D / 2) + 8 * c;
+            }
+#pragma unroll 1
+            for (int o = 0; o < D / 64; ++o) {
+              uint32_t y[32];
+              load_o(o, y);
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {  // pair e: row e / 8, then i, then row
+                const int j = (e >> 3) * 2 + (e & 1), i = (e >> 1) & 3;
+                *reinterpret_cast<__nv_bfloat162*>(tile + frag_row(lane, j) * L::kStageStride + 16 * i + 4 * c) =
+                    __floats2bfloat162_rn(__uint_as_float(y[2 * e]) * inv[j], __uint_as_float(y[2 * e + 1]) * inv[j]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (real[i])
+                  *reinterpret_cast<uint4*>(dst[i] + 32 * o) =
+                      *reinterpret_cast<const uint4*>(tile + (8 * i + (lane >> 2)) * L::kStageStride + 16 * c);
+            }
+          } else {
+            float* dst[4];
+            bool real[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              real[j] = r0 + frag_row(lane, j) < a.n_rows;
+              dst[j] = static_cast<float*>(a.out) + row_at(frag_row(lane, j)) + part * (D / 2) + 2 * c;
+            }
+#pragma unroll 1
+            for (int o = 0; o < D / 64; ++o) {
+              uint32_t y[32];
+              load_o(o, y);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int j = (e >> 3) * 2 + (e & 1), i = (e >> 1) & 3;
+                if (real[j])
+                  *reinterpret_cast<float2*>(dst[j] + 32 * o + 8 * i) =
+                      make_float2(__uint_as_float(y[2 * e]) * inv[j], __uint_as_float(y[2 * e + 1]) * inv[j]);
+              }
+            }
+          }
+        } else {
+          // a part: the numerator as the threads hold it
+          const int slot = 2 * run + (f_unit == 0 ? 0 : 1);
+          float4* dst = a.part + ((static_cast<long long>(slot) * 4 + quad) * 2 + part) * (D / 64 * 8 * 32) + lane;
+#pragma unroll 1
+          for (int o = 0; o < D / 64; ++o) {
+            uint32_t y[32];
+            load_o(o, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[(8 * o + e) * 32] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]),
+                                                  __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
+          }
+          if (part == 0) ml[(slot & 1) * 128 + quad * 32 + frag_row(lane, c)] = make_float2(pick(ref), pick(sum));
+        }
+      }
+      if (ends_it) {  // O is read, the stage too: the next unit's first product may write O
+        tc::fence_before_sync();
+        arrive(L::oFree);
+      }
+      if (n_unit > 1) ++left_sums;
+      f_unit += n_unit;
+      w.x += n_unit - 1;
       window_step(a, w);
     }
   } else if (warp == kWMmaWarp) {
     // ================================================================ MMA issue
-    const uint64_t qd0 = tc::sdesc_sw128(smem_u32(stage)), rd0 = tc::sdesc_sw128(smem_u32(ring));
+    grid_dep_wait();
+    grid_dep_trigger();
+    const uint64_t qd0 = tc::sdesc_sw128(smem_u32(sm)), rd0 = tc::sdesc_sw128(smem_u32(ring));
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(128, 128), idesc_pv = tc::idesc_f16_f32(128, D);
-    int slot = 0, unit = 0;
+    int slot = 0;
     uint32_t ph = 0;
     bool ok = true;
     auto await = [&](int bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, a.status, abort_flag, a.wait_budget));
+      ok = __all_sync(0xffffffffu, wait_on(&bars[bar], parity, abort_flag, a.wait_budget));
       return ok;
     };
     auto next_slot = [&]() {
@@ -542,9 +669,18 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         ph ^= 1u;
       }
     };
-    auto scores = [&](int f, bool first) {  // S = Q K_f^T
-      if (first && !await(L::qFull, unit & 1)) return;
-      if (f >= 1 && !await(L::sFree, (f - 1) & 1)) return;
+    // S = Q K_f^T, in tile f's score tile: free once the P of tile f - 2 has been made (the caller has waited for it) or, where P
+    // lies in it, multiplied
+    WindowWalk ws = w;  // of the scores
+    int fs = 0, s_unit = -1;
+    auto scores = [&]() {
+      const int b = fs & 1;
+      if (fs == 0 || ws.x == 0) {
+        ++s_unit;
+        if (!await(L::qFull, s_unit & 1)) return;
+      }
+      if (L::kOverlay && fs >= 2 && !await(L::pvDone + b, ((fs >> 1) - 1) & 1)) return;
+      const bool last = ws.x + 1 == ws.keys.n;  // of its row tile: Q's place is free then
       for (int qa = 0; qa < NP; ++qa) {
         if (!await(L::full + slot, ph)) return;
         if (elect_one()) {
@@ -552,23 +688,25 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           const uint64_t kd = rd0 + static_cast<uint64_t>((slot * kPieceBytes) >> 4);
           const uint64_t qd = qd0 + static_cast<uint64_t>((qa * kPieceBytes) >> 4);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            if constexpr (L::kQTmem)
-              tc::mma_f16_ts(tmem, tmem + L::kQCol + 32 * qa + 8 * s, kd + 2 * s, idesc_qk, (qa | s) ? 1u : 0u);
-            else
-              tc::mma_f16_ss(tmem, qd + 2 * s, kd + 2 * s, idesc_qk, (qa | s) ? 1u : 0u);
-          }
+          for (int s = 0; s < 4; ++s) tc::mma_f16_ss(tmem + 128 * b, qd + 2 * s, kd + 2 * s, idesc_qk, (qa | s) ? 1u : 0u);
           tc::commit(&bars[L::empty + slot]);
-          if (qa == NP - 1) tc::commit(&bars[L::sFull]);
+          if (qa == NP - 1) {
+            tc::commit(&bars[L::sFull + b]);
+            if (last) tc::commit(&bars[L::qFree]);
+          }
         }
         __syncwarp();
         next_slot();
       }
+      ++fs;
+      window_step(a, ws);
     };
-    auto values = [&](int f, bool first, int of_unit) {  // O (+)= P_f V_f
+    int v_unit = -1;
+    auto values = [&](int f) {  // O (+)= P_f V_f
       const int b = f & 1;
-      if (!await(L::pFull + b, (f >> 1) & 1)) return;
-      if (first && of_unit > 0 && !await(L::oFree, (of_unit - 1) & 1)) return;
+      const bool first = f == 0 || w.x == 0;
+      if (first) ++v_unit;
+      if (first && v_unit > 0 && !await(L::oFree, (v_unit - 1) & 1)) return;  // the row tile before has been read
       for (int kh = 0; kh < 2; ++kh) {
         const int s0 = slot;
         for (int dh = 0; dh < D / 128; ++dh) {
@@ -580,7 +718,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           const uint64_t vd = rd0 + static_cast<uint64_t>((s0 * kPieceBytes) >> 4);
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            tc::mma_f16_ts(tmem + L::kOCol, tmem + L::kPCol + 64 * b + 32 * kh + 8 * s, vd + 2 * s, idesc_pv,
+            tc::mma_f16_ts(tmem + L::kOCol, tmem + L::p_col(b) + L::kPHalf * kh + 8 * s, vd + 2 * s, idesc_pv,
                            (first && kh == 0 && s == 0) ? 0u : 1u);
 #pragma unroll
           for (int dh = 0; dh < D / 128; ++dh) tc::commit(&bars[L::empty + s0 + dh]);
@@ -588,39 +726,36 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         }
         __syncwarp();
       }
-    };
-    // Q K^T runs a tile ahead of P V within a unit; at a unit's end P V comes first (the next Q waits for it)
-    bool was_first = false;
-    for (int f = 0; ok && f < n_tiles; ++f) {
-      const bool first = f == 0 || w.x == 0;
-      if (first && f > 0) {
-        values(f - 1, was_first, unit);
-        if (!ok) break;
-        ++unit;
-      }
-      scores(f, first);
-      if (!ok) break;
-      if (!first) values(f - 1, was_first, unit);
-      was_first = first;
       window_step(a, w);
+    };
+    // The scores run two tiles ahead of the values: beside tile f's weights, tile f + 1 is with the other group.
+    scores();
+    if (ok && n_tiles > 1) scores();
+    for (int f = 0; ok && f < n_tiles; ++f) {
+      if (!await(L::pFull + (f & 1), (f >> 1) & 1)) break;
+      const bool early = scores_first<D>(ws.x);
+      if (early && fs < n_tiles) scores();
+      if (ok) values(f);
+      if (ok && !early && fs < n_tiles) scores();
     }
-    if (ok) values(n_tiles - 1, was_first, unit);
     // every MMA this warp issued has completed before the CTA releases tensor memory
     if (elect_one()) {
       tc::commit(&bars[L::drain]);
       mbar_wait(&bars[L::drain], 0, a.status, a.wait_budget);
     }
     __syncwarp();
-  } else {
+  } else if (warp == kWCopyWarp) {
     // ================================================================ tile copies
-    int slot = 0, fills = 0, par_fills = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    const bool skip_one = a.fault == 5 && blockIdx.x == 0;  // test-only: the fourth piece is never copied
     if (lane == 0) {
+      grid_dep_wait();
+      grid_dep_trigger();
+      int slot = 0, fills = 0, par_fills = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      const bool skip_one = a.fault == 5 && blockIdx.x == 0;  // test-only: the fourth piece is never copied
       auto push = [&](const uint8_t* src) {
         for (int i = 0; i < NP; ++i) {
-          if (fills >= L::kSlots && !wait_or_abort(&bars[L::empty + slot], ph ^ 1u, a.status, abort_flag, a.wait_budget)) {
+          if (fills >= L::kSlots && !wait_on(&bars[L::empty + slot], ph ^ 1u, abort_flag, a.wait_budget)) {
             ok = false;
             return;
           }
@@ -638,7 +773,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       auto push_par = [&](long long u) {
         const int pb = par_fills % kWParBufs;
         if (par_fills >= kWParBufs &&
-            !wait_or_abort(&bars[L::parFree + pb], (par_fills / kWParBufs - 1) & 1, a.status, abort_flag, a.wait_budget)) {
+            !wait_on(&bars[L::parFree + pb], (par_fills / kWParBufs - 1) & 1, abort_flag, a.wait_budget)) {
           ok = false;
           return;
         }
@@ -646,18 +781,25 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         bulk_g2s(par + pb * 384, a.par + u * 384, 1536, &bars[L::parFull + pb]);
         ++par_fills;
       };
-      long long before = 0;
-      for (int f = 0; ok && f < n_tiles; ++f) {
-        const bool first = f == 0 || w.x == 0;
-        const long long u = static_cast<long long>(w.kvh) * a.key_tiles + stored_tile(a, w.tile());
-        if (first && f > 0) push(a.v_tiles + before * (D * 256));
-        if (ok) push_par(u);
+      // in the order of the products
+      WindowWalk wk = w;
+      int fk = 0;
+      auto push_k = [&]() {
+        const long long u = static_cast<long long>(wk.kvh) * a.key_tiles + stored_tile(a, wk.tile());
+        push_par(u);
         if (ok) push(a.k_tiles + u * (D * 256));
-        if (ok && !first) push(a.v_tiles + before * (D * 256));
-        before = u;
+        ++fk;
+        window_step(a, wk);
+      };
+      push_k();
+      if (ok && n_tiles > 1) push_k();
+      for (int f = 0; ok && f < n_tiles; ++f) {
+        const bool early = scores_first<D>(wk.x);
+        if (early && fk < n_tiles) push_k();
+        if (ok) push(a.v_tiles + (static_cast<long long>(w.kvh) * a.key_tiles + stored_tile(a, w.tile())) * (D * 256));
         window_step(a, w);
+        if (ok && !early && fk < n_tiles) push_k();
       }
-      if (ok) push(a.v_tiles + before * (D * 256));
       // copies still in flight (only after an abort) land before the CTA exits
       for (int i = max(0, fills - L::kSlots); i < fills; ++i)
         if (!(skip_one && i == 3))
@@ -666,9 +808,45 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         mbar_wait(&bars[L::parFull + i % kWParBufs], (i / kWParBufs) & 1, a.status, a.wait_budget);
     }
     __syncwarp();
+  } else {
+    // ================================================================ queries: a row tile's when its place is free
+    const int t0 = tid - 32 * kWQWarp;
+    constexpr int CH = D / 8, ROWS = 32 * kWQWarps / CH;  // 16-byte chunks of a row, rows at a time
+    const int ch = t0 % CH;
+    int units = 0;
+    for (int f = 0; f < n_tiles; ++units) {
+      if (units > 0 && !__all_sync(0xffffffffu, wait_on(&bars[L::qFree], (units - 1) & 1, abort_flag, a.wait_budget))) break;
+      int n = t0 / CH, r = 128 * w.t + n, q = r / a.group, g = r - q * a.group;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + static_cast<long long>(w.kvh) * a.group * D + 8 * ch;
+      uint8_t* dst = sm + (ch >> 3) * kPieceBytes;
+#pragma unroll 4
+      for (int i = 0; i < 128 / ROWS; ++i) {
+        const bool real = r < a.n_rows;
+        cp_async16(dst + tc::sw128_off(n, ch & 7), src + (real ? (static_cast<long long>(q) * a.n_q_heads + g) * D : 0), real);
+        n += ROWS;
+        r += ROWS;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k)
+          if (++g == a.group) {
+            g = 0;
+            ++q;
+          }
+      }
+      cp_async_wait();
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[L::qFull]);
+      // The first queries come from before the kernel that makes the tiles, which had them before it let this one start;
+      // this grid's own wait is the other warps'.
+      const int n_unit = min(w.keys.n - w.x, n_tiles - f);
+      f += n_unit;
+      w.x += n_unit - 1;
+      window_step(a, w);
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (tid == 0 && *abort_flag) set_status(a.status, KVQ_DEV_TIMEOUT);
   if (warp == kWMmaWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, L::kTmemCols);
@@ -676,14 +854,13 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
 }
 
 // ============================================================================ joining the parts
-// Block (run, 16 rows).  The run in which a cut row tile ends joins its parts, from the run in which it begins on.
-constexpr int kJoinRows = 16;
-
+// Block (run, 32 columns).  The run in which a cut row tile ends joins its parts, from the run in which it
+// begins on; threads take the places of the attention kernel's softmax threads, as the parts lie.
 template <int D>
-__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ PrefillWindowArgs a, int runs) {
+__global__ void __launch_bounds__(128) window_join_kernel(const __grid_constant__ PrefillWindowArgs a, int runs) {
   grid_dep_wait();
   grid_dep_trigger();
-  const int run = blockIdx.x;
+  const int run = blockIdx.x, o = blockIdx.y, quad = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long f0 = run_start(a, run, runs), f1 = run_start(a, run + 1, runs);
   const WindowWalk w = window_walk_at(a, f0);
   if (w.x == 0 || f0 - w.x + w.keys.n > f1) return;
@@ -691,44 +868,63 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
   int first = run - 1;  // the run in which the row tile begins
   while (run_start(a, first, runs) > start) --first;
   const int first_slot = 2 * first + (run_start(a, first, runs) < start ? 1 : 0);
-  // thread = (row, columns): rows of a warp's lanes side by side, as the parts lie
-  const int row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, r = 128 * w.t + row;
-  if (r >= a.n_rows) return;
-  float m = -INFINITY;
-  bool dropped = false;
-  for (int c = first; c <= run; ++c) {
-    const float2 v = a.part_ml[static_cast<long long>(c == first ? first_slot : 2 * c) * 128 + row];
-    m = fmaxf(m, v.x);
-    dropped |= v.y < 0.0f;
+  auto slot_of = [&](int i) { return static_cast<long long>(i == first ? first_slot : 2 * i); };
+  const int c = lane & 3;
+  float m[4], l[4];
+  bool dropped[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = -INFINITY;
+    l[j] = 0.0f;
+    dropped[j] = false;
   }
-  if (dropped) return;
-  const int qi = r / a.group, h = w.kvh * a.group + (r - qi * a.group);
-  const long long at = (static_cast<long long>(qi) * a.n_q_heads + h) * D;
-  float l = 0.0f;
-  for (int c = first; c <= run; ++c) {
-    const float2 v = a.part_ml[static_cast<long long>(c == first ? first_slot : 2 * c) * 128 + row];
-    if (v.x != -INFINITY || v.y != 0.0f) l += v.y * (v.x == -INFINITY ? 1.0f : fast_exp2(v.x - m));
-  }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  for (int c4 = threadIdx.x / kJoinRows; c4 < D / 4; c4 += 256 / kJoinRows) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = first; c <= run; ++c) {
-      const long long slot = c == first ? first_slot : 2 * c;
-      const float2 v = a.part_ml[slot * 128 + row];
-      if (v.x == -INFINITY && v.y == 0.0f) continue;  // no key of this part is seen
-      const float s = v.x == -INFINITY ? 1.0f : fast_exp2(v.x - m);
-      const float4 x = a.part[(slot * (D / 4) + c4) * 128 + row];
-      o.x = fmaf(x.x, s, o.x);
-      o.y = fmaf(x.y, s, o.y);
-      o.z = fmaf(x.z, s, o.z);
-      o.w = fmaf(x.w, s, o.w);
+  for (int i = first; i <= run; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = a.part_ml[slot_of(i) * 128 + quad * 32 + frag_row(lane, j)];
+      m[j] = fmaxf(m[j], v.x);
+      dropped[j] |= v.y < 0.0f;
     }
-    if (a.out_bf16) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 4 * c4) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 4 * c4) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  float4 acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = first; i <= run; ++i) {
+    float s[4];
+    bool none[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = a.part_ml[slot_of(i) * 128 + quad * 32 + frag_row(lane, j)];
+      none[j] = v.x == -INFINITY && v.y == 0.0f;  // the row sees no key of this part
+      s[j] = v.x == -INFINITY ? 1.0f : fast_exp2(v.x - m[j]);  // (a part of NaN alone has no maximum)
+      if (!none[j]) l[j] = fmaf(v.y, s[j], l[j]);
+    }
+    const float4* src = a.part + ((slot_of(i) * 4 + quad) * (D / 32) + o) * (8 * 32) + lane;  // (o: half of the columns, then 32)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float4 x = src[e * 32];
+      const int ja = (e >> 2) * 2, jb = ja + 1;
+      if (!none[ja]) {
+        acc[e].x = fmaf(x.x, s[ja], acc[e].x);
+        acc[e].y = fmaf(x.y, s[ja], acc[e].y);
+      }
+      if (!none[jb]) {
+        acc[e].z = fmaf(x.z, s[jb], acc[e].z);
+        acc[e].w = fmaf(x.w, s[jb], acc[e].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int rr = 128 * w.t + quad * 32 + frag_row(lane, j), q2 = rr / a.group;
+    if (rr >= a.n_rows || dropped[j]) continue;
+    const float inv = l[j] > 0.0f || l[j] != l[j] ? 1.0f / l[j] : 0.0f;
+    const long long at = (static_cast<long long>(q2) * a.n_q_heads + w.kvh * a.group + (rr - q2 * a.group)) * D + 32 * o + 2 * c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = acc[(j >> 1) * 4 + i];
+      const float x = ((j & 1) ? v.z : v.x) * inv, y = ((j & 1) ? v.w : v.y) * inv;
+      if (a.out_bf16) *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + at + 8 * i) = __floats2bfloat162_rn(x, y);
+      else *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + 8 * i) = make_float2(x, y);
     }
   }
 }
@@ -769,8 +965,8 @@ static cudaError_t launch_prefill_window_d(const PrefillWindowArgs& a, int runs,
   e = launch_pdl(window_attention_kernel<D>, dim3(runs), dim3(kWThreads), L::kAlloc, stream, a);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(runs, 128 / kJoinRows);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(runs, D / 32);
+  cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

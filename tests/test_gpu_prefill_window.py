@@ -55,7 +55,8 @@ def test_windows(kvq, T, history, hq, hkv, d, window, sink):
 @pytest.mark.parametrize("T,history,hq,hkv,d,window,sink", [
     (1, 4000, 24, 4, 256, 1024, 4), (1, 1, 1, 1, 128, 1, 0), (2, 129, 128, 1, 128, 50, 3), (128, 0, 1, 1, 256, 64, 0),
     (129, 127, 1, 1, 128, 127, 1), (1200, 0, 2, 2, 256, 200, 0), (5000, 0, 1, 1, 128, 300, 4), (2047, 333, 4, 1, 128, 1024, 0),
-    (64, 9000, 20, 2, 256, 6000, 300), (3, 20000, 8, 1, 128, 16000, 0), (900, 100, 7, 7, 128, 77, 9), (40, 600, 48, 1, 256, 256, 16)])
+    (300, 333, 32, 8, 128, 100, 0), (500, 100, 8, 8, 128, 150, 4), (260, 500, 24, 8, 256, 60, 130), (700, 0, 10, 5, 256, 130, 1),
+    (2047, 333, 16, 8, 128, 300, 0), (64, 9000, 20, 2, 256, 6000, 300), (3, 20000, 8, 1, 128, 16000, 0), (900, 100, 7, 7, 128, 77, 9), (40, 600, 48, 1, 256, 256, 16)])
 def test_shapes(kvq, T, history, hq, hkv, d, window, sink):
     run(kvq, np.random.default_rng(T), T, history, hq, hkv, d, window, sink)
 
