@@ -60,9 +60,7 @@ struct Pw {
   static constexpr int offRef = offPar + kWParBufs * 3 * 128 * 4;  // [128] the rows' references
   static constexpr int offRed = offRef + 128 * 4;            // [maximum, sum][group][half of the keys][128] a row's two warps
   static constexpr int offSum = offRed + 2 * 2 * 2 * 128 * 4;    // [2][sum, sum, reference][128] what a unit's other group leaves
-  static constexpr int kStageStride = 80;                    // of 32 bf16 columns: no bank conflicts
-  static constexpr int offStage = offSum + 2 * 3 * 128 * 4;  // [warp of a group][32 rows]
-  static constexpr int offBar = offStage + 8 * 32 * kStageStride;
+  static constexpr int offBar = offSum + 2 * 3 * 128 * 4;
   // barriers; those of two are by a tile's parity, so that each has one group on one side
   static constexpr int full = 0, empty = full + kSlots, parFull = empty + kSlots, parFree = parFull + kWParBufs,
                        sFull = parFree + kWParBufs, pFull = sFull + 2, pvDone = pFull + 2, decided = pvDone + 2,
@@ -75,7 +73,7 @@ struct Pw {
   static constexpr uint32_t kOCol = 256, kTmemCols = 512;
   static constexpr uint32_t kPHalf = kOverlay ? 64 : 32;  // columns from a P tile's first half of the keys to its second
   __device__ static uint32_t p_col(int b) { return kOverlay ? 128 * b : 384 + 64 * b; }
-  static_assert(offBar % 8 == 0 && offStage % 16 == 0, "alignment");
+  static_assert(offBar % 8 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
@@ -113,6 +111,26 @@ __device__ __forceinline__ int small_div(int x, uint32_t inv) {
   return inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), inv)) : x;
 }
 
+// Four lanes (c = lane % 4) of four words each: word k of lane c becomes word c of lane k.
+__device__ __forceinline__ void lanes4_transpose(int c, uint32_t (&p)[4]) {
+#pragma unroll
+  for (int b = 1; b < 4; b *= 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & b)) {
+        const bool up = (c & b) != 0;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? p[i] : p[i | b], b);
+        if (up) p[i] = got;
+        else p[i | b] = got;
+      }
+  }
+}
+
+// The lowest min(max(n, 0), 32) bits.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return __funnelshift_rc(0xffffffffu, 0u, 32u - static_cast<uint32_t>(min(n, 32)));
+}
+
 // Row of a quadrant that register pair j of a thread's fragment belongs to (tcgen05.cuh, two loads of 16 lanes).
 __device__ __forceinline__ int frag_row(int lane, int j) { return (j >> 1) * 16 + (j & 1) * 8 + (lane >> 2); }
 
@@ -134,10 +152,10 @@ __host__ __device__ inline RowTileKeys row_tile_keys(int t, int n_rows, int grou
 }
 
 // Whether a row tile's x-th scores, two tiles ahead, are made before the values at hand: not where they wait for those (P in
-// their place) or for new queries.
+// their place) or for new queries, nor where a row tile's result waits for the values.
 template <int D>
 __device__ __forceinline__ bool scores_first(int x) {
-  return !Pw<D>::kOverlay && x != 0;
+  return !Pw<D>::kOverlay && x > 1;
 }
 
 // Place on the line: KV head, row tile, key tile x of its n.
@@ -194,7 +212,7 @@ __device__ __forceinline__ long long run_start(const PrefillWindowArgs& a, int c
 }
 
 // ============================================================================ operand tiles
-// One CTA per (stored tile, KV head): K codes to bf16, rows = keys, piece a = dims 64 a ..; V codes to fp16, rows = dims,
+// Blocks (stored tile, KV head, quarter), two quarters for K and two for V: K codes to bf16, rows = keys, piece a = dims 64 a ..; V codes to fp16, rows = dims,
 // piece kh (D / 128) + dh = keys 64 kh .. of dims 128 dh .. (the layouts of the prefill's operands); each key's factors.
 // Pages that no row sees are not looked at.
 template <int D>
@@ -220,42 +238,49 @@ __global__ void __launch_bounds__(256) window_tiles_kernel(const __grid_constant
   const long long u = static_cast<long long>(kvh) * a.key_tiles + st;
   uint8_t* kdst = a.k_tiles + u * (D * 256);
   uint8_t* vdst = a.v_tiles + u * (D * 256);
-  uint4 raw[D / 32];
+  constexpr int N = D / 64;  // 16-byte loads of a thread
+  const int i0 = tid + 256 * N * (blockIdx.z & 1);
+  uint4 raw[N];
+  if (blockIdx.z < 2) {
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) {  // four adjacent lanes fill one 128-byte row of a piece
-    const int i = tid + 256 * x, n = (i >> 2) & 127, c16 = ((i >> 9) << 2) | (i & 3), page = page_s[n >> 4];
-    raw[x] = make_uint4(0, 0, 0, 0);
-    if (page >= 0 && 128 * tile + n < a.n_keys)
-      raw[x] = __ldg(reinterpret_cast<const uint4*>(
-          a.k + ((static_cast<long long>(page) * a.n_kv_heads + kvh) * (D / 16) + c16) * 256 + (n & 15) * 16));
-  }
+    for (int x = 0; x < N; ++x) {  // four adjacent lanes fill one 128-byte row of a piece
+      const int i = i0 + 256 * x, n = (i >> 2) & 127, c16 = ((i >> 9) << 2) | (i & 3), page = page_s[n >> 4];
+      raw[x] = make_uint4(0, 0, 0, 0);
+      if (page >= 0 && 128 * tile + n < a.n_keys)
+        raw[x] = __ldg(reinterpret_cast<const uint4*>(
+            a.k + ((static_cast<long long>(page) * a.n_kv_heads + kvh) * (D / 16) + c16) * 256 + (n & 15) * 16));
+    }
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) {
-    const int i = tid + 256 * x, n = (i >> 2) & 127, c16 = ((i >> 9) << 2) | (i & 3);
-    uint32_t h[8];
-    widen16_bf16(raw[x], h);
-    uint8_t* piece = kdst + (c16 >> 2) * kPieceBytes;
-    const int cc = (c16 & 3) * 2;
-    sts128(piece + tc::sw128_off(n, cc), make_uint4(h[0], h[1], h[2], h[3]));  // global stores
-    sts128(piece + tc::sw128_off(n, cc + 1), make_uint4(h[4], h[5], h[6], h[7]));
-  }
+    for (int x = 0; x < N; ++x) {
+      const int i = i0 + 256 * x, n = (i >> 2) & 127, c16 = ((i >> 9) << 2) | (i & 3);
+      uint32_t h[8];
+      widen16_bf16(raw[x], h);
+      uint8_t* piece = kdst + (c16 >> 2) * kPieceBytes;
+      const int cc = (c16 & 3) * 2;
+      sts128(piece + tc::sw128_off(n, cc), make_uint4(h[0], h[1], h[2], h[3]));  // global stores
+      sts128(piece + tc::sw128_off(n, cc + 1), make_uint4(h[4], h[5], h[6], h[7]));
+    }
+    if (blockIdx.z == 1) return;
+  } else {
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) {
-    const int i = tid + 256 * x, pl = ((i / (4 * D)) << 2) | (i & 3), d = (i >> 2) % D, page = page_s[pl];
-    raw[x] = make_uint4(0, 0, 0, 0);
-    if (page >= 0)
-      raw[x] = __ldg(reinterpret_cast<const uint4*>(
-          a.v + ((static_cast<long long>(page) * a.n_kv_heads + kvh) * D + d) * KVQ_BLOCK_SIZE));
-  }
+    for (int x = 0; x < N; ++x) {
+      const int i = i0 + 256 * x, pl = ((i / (4 * D)) << 2) | (i & 3), d = (i >> 2) % D, page = page_s[pl];
+      raw[x] = make_uint4(0, 0, 0, 0);
+      if (page >= 0)
+        raw[x] = __ldg(reinterpret_cast<const uint4*>(
+            a.v + ((static_cast<long long>(page) * a.n_kv_heads + kvh) * D + d) * KVQ_BLOCK_SIZE));
+    }
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) {
-    const int i = tid + 256 * x, pl = ((i / (4 * D)) << 2) | (i & 3), d = (i >> 2) % D;
-    uint4 c0, c1;
-    widen16(make_int4(raw[x].x, raw[x].y, raw[x].z, raw[x].w), c0, c1);
-    uint8_t* piece = vdst + ((pl >> 2) * (D / 128) + (d >> 7)) * kPieceBytes;
-    const int cc = (pl & 3) * 2;
-    sts128(piece + tc::sw128_off(d & 127, cc), c0);
-    sts128(piece + tc::sw128_off(d & 127, cc + 1), c1);
+    for (int x = 0; x < N; ++x) {
+      const int i = i0 + 256 * x, pl = ((i / (4 * D)) << 2) | (i & 3), d = (i >> 2) % D;
+      uint4 c0, c1;
+      widen16(make_int4(raw[x].x, raw[x].y, raw[x].z, raw[x].w), c0, c1);
+      uint8_t* piece = vdst + ((pl >> 2) * (D / 128) + (d >> 7)) * kPieceBytes;
+      const int cc = (pl & 3) * 2;
+      sts128(piece + tc::sw128_off(d & 127, cc), c0);
+      sts128(piece + tc::sw128_off(d & 127, cc + 1), c1);
+    }
+    return;
   }
   if (tid < 128) {
     const int page = page_s[tid >> 4];
@@ -401,14 +426,12 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           if (hi0 < 32 || (a.history_len + query(31) + 1 - a.window > k0 && sk < 32)) {  // the same in the warp
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int hi = a.history_len + query(frag_row(lane, j)) + 1 - k0 - 2 * c, lo = hi - a.window, first = min(sk - 2 * c, hi);
-              const unsigned span = static_cast<unsigned>(min(hi, 32)) - static_cast<unsigned>(min(lo, 32));
+              const int hi = a.history_len + query(frag_row(lane, j)) + 1 - k0;
+              const uint32_t seen = (low_bits(hi) & (low_bits(sk) | ~low_bits(hi - a.window))) >> (2 * c);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int n = 8 * (e >> 1) + (e & 1);
-                uint32_t& s = y[(j >> 1) * 16 + 4 * (e >> 1) + 2 * (j & 1) + (e & 1)];
-                if (static_cast<unsigned>(n - min(lo, 32)) >= span && n >= first) s = 0xff800000u;  // -infinity
-              }
+              for (int e = 0; e < 8; ++e)
+                if (!(seen & (1u << (8 * (e >> 1) + (e & 1)))))
+                  y[(j >> 1) * 16 + 4 * (e >> 1) + 2 * (j & 1) + (e & 1)] = 0xff800000u;  // -infinity
             }
           }
 #pragma unroll
@@ -544,106 +567,75 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           arrive(L::sumReady + 4 * (left_sums & 1) + quad);
         }
       } else {
-        // ---- its result: O once its last product is there, with all sums
-        const int f = f_unit + n_unit - 1;
-        await(L::pvDone + group, (f >> 1) & 1);
+        // ---- its result.  All sums:
         if (n_unit > 1) await(L::sumReady + 4 * (left_sums & 1) + quad, (left_sums >> 1) & 1);
-        tc::fence_after_sync();
         float* mine = red + (4 + 2 * group + part) * 128 + quad * 32;
         const float* others = red + (4 + 2 * group + (part ^ 1)) * 128 + quad * 32;
         mine[frag_row(lane, c)] = pick(sum);
         if (pair_or(pair_id, failed)) break;
+        const int slot = 2 * run + (f_unit == 0 ? 0 : 1);
+        float inv[4];
+        int at_row[4];  // where the thread's rows stand in the output, from its query's first on
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sum[j] += others[frag_row(lane, j)];
+          const int row = frag_row(lane, j), qs = small_div(g0 + row, a.group_inv);
+          sum[j] += others[row];
           if (n_unit > 1) {
-            const float at = left[256 + frag_row(lane, j)];
-            sum[j] += (left[frag_row(lane, j)] + left[128 + frag_row(lane, j)]) *
-                      (at == -INFINITY || at == ref[j] ? 1.0f : fast_exp2(at - ref[j]));
+            const float at = left[256 + row];
+            sum[j] += (left[row] + left[128 + row]) * (at == -INFINITY || at == ref[j] ? 1.0f : fast_exp2(at - ref[j]));
           }
+          inv[j] = sum[j] > 0.0f || sum[j] != sum[j] ? __frcp_rn(sum[j]) : 0.0f;
+          at_row[j] = r0 + row < a.n_rows ? (qs * a.n_q_heads + g0 + row - qs * a.group) * D : -1;
         }
-        auto load_o = [&](int o, uint32_t* y) {  // 32 columns of the four rows
+        const long long out0 = (static_cast<long long>(q0) * a.n_q_heads + w.kvh * a.group) * D + part * (D / 2);
+        // O once its last product is there.  (Few instructions: what runs once a row tile comes from far out of the
+        // instruction caches.)
+        await(L::pvDone + group, ((f_unit + n_unit - 1) >> 1) & 1);
+        if (pair_or(pair_id, failed)) break;
+        tc::fence_after_sync();
+        if (!whole_unit && part == 0) ml[(slot & 1) * 128 + quad * 32 + frag_row(lane, c)] = make_float2(pick(ref), pick(sum));
+#pragma unroll 1
+        for (int o = 0; o < D / 64; ++o) {  // 32 columns of the four rows
           const uint32_t at = tmem + L::kOCol + part * (D / 2) + 32 * o;
+          uint32_t y[32];
           tc::ld_16x256b_x4(at + lanes0, y);
           tc::ld_16x256b_x4(at + lanes1, y + 16);
           tc::wait_ld();
-        };
-        auto row_at = [&](int row) {  // where the warp's row stands in the output
-          const int q = query(row), h = w.kvh * a.group + (r0 + row - q * a.group);
-          return (static_cast<long long>(q) * a.n_q_heads + h) * D;
-        };
-        if (whole_unit) {
-          float inv[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) inv[j] = sum[j] > 0.0f || sum[j] != sum[j] ? 1.0f / sum[j] : 0.0f;
-          if (a.out_bf16) {
-            // a warp's 32 rows x 32 columns through shared memory, then 64 bytes of a row at a time
-            uint8_t* tile = sm + L::offStage + (warp & 7) * 32 * L::kStageStride;
-            uint16_t* dst[4];
-            bool real[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              real[i] = r0 + 8 * i + (lane >> 2) < a.n_rows;
-              dst[i] = static_cast<uint16_t*>(a.out) + row_at(8 * i + (lane >> 2)) + part * (D / 2) + 8 * c;
-            }
-#pragma unroll 1
-            for (int o = 0; o < D / 64; ++o) {
-              uint32_t y[32];
-              load_o(o, y);
-              __syncwarp();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {  // pair e: row e / 8, then i, then row
-                const int j = (e >> 3) * 2 + (e & 1), i = (e >> 1) & 3;
-                *reinterpret_cast<__nv_bfloat162*>(tile + frag_row(lane, j) * L::kStageStride + 16 * i + 4 * c) =
-                    __floats2bfloat162_rn(__uint_as_float(y[2 * e]) * inv[j], __uint_as_float(y[2 * e + 1]) * inv[j]);
-              }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (real[i])
-                  *reinterpret_cast<uint4*>(dst[i] + 32 * o) =
-                      *reinterpret_cast<const uint4*>(tile + (8 * i + (lane >> 2)) * L::kStageStride + 16 * c);
-            }
-          } else {
-            float* dst[4];
-            bool real[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              real[j] = r0 + frag_row(lane, j) < a.n_rows;
-              dst[j] = static_cast<float*>(a.out) + row_at(frag_row(lane, j)) + part * (D / 2) + 2 * c;
-            }
-#pragma unroll 1
-            for (int o = 0; o < D / 64; ++o) {
-              uint32_t y[32];
-              load_o(o, y);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int j = (e >> 3) * 2 + (e & 1), i = (e >> 1) & 3;
-                if (real[j])
-                  *reinterpret_cast<float2*>(dst[j] + 32 * o + 8 * i) =
-                      make_float2(__uint_as_float(y[2 * e]) * inv[j], __uint_as_float(y[2 * e + 1]) * inv[j]);
-              }
-            }
+          if (o == D / 64 - 1) {  // the next unit's first product may write O
+            tc::fence_before_sync();
+            arrive(L::oFree);
           }
-        } else {
-          // a part: the numerator as the threads hold it
-          const int slot = 2 * run + (f_unit == 0 ? 0 : 1);
-          float4* dst = a.part + ((static_cast<long long>(slot) * 4 + quad) * 2 + part) * (D / 64 * 8 * 32) + lane;
-#pragma unroll 1
-          for (int o = 0; o < D / 64; ++o) {
-            uint32_t y[32];
-            load_o(o, y);
+          if (!whole_unit) {  // a part: the numerator as the threads hold it
+            float4* dst = a.part + (((static_cast<long long>(slot) * 4 + quad) * 2 + part) * (D / 64) + o) * (8 * 32) + lane;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[(8 * o + e) * 32] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]),
-                                                  __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
+              dst[e * 32] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]), __uint_as_float(y[4 * e + 2]),
+                                        __uint_as_float(y[4 * e + 3]));
+            continue;
           }
-          if (part == 0) ml[(slot & 1) * 128 + quad * 32 + frag_row(lane, c)] = make_float2(pick(ref), pick(sum));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t* v = y + (j >> 1) * 16 + 2 * (j & 1);  // (columns 8 i + 2 c, + 1 at 4 i)
+            auto x = [&](int e) { return __uint_as_float(v[e]) * inv[j]; };
+            if (a.out_bf16) {
+              // four lanes have 8 columns together, four times: each takes one eight, and a row's 64 bytes are written at once
+              uint32_t p[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x(4 * i), x(4 * i + 1));
+                p[i] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              lanes4_transpose(c, p);
+              if (at_row[j] >= 0)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out0 + at_row[j] + 32 * o + 8 * c) =
+                    make_uint4(p[0], p[1], p[2], p[3]);
+            } else if (at_row[j] >= 0) {
+              float* d = static_cast<float*>(a.out) + out0 + at_row[j] + 32 * o + 2 * c;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(x(4 * i), x(4 * i + 1));
+            }
+          }
         }
-      }
-      if (ends_it) {  // O is read, the stage too: the next unit's first product may write O
-        tc::fence_before_sync();
-        arrive(L::oFree);
       }
       if (n_unit > 1) ++left_sums;
       f_unit += n_unit;
@@ -816,21 +808,16 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     int units = 0;
     for (int f = 0; f < n_tiles; ++units) {
       if (units > 0 && !__all_sync(0xffffffffu, wait_on(&bars[L::qFree], (units - 1) & 1, abort_flag, a.wait_budget))) break;
-      int n = t0 / CH, r = 128 * w.t + n, q = r / a.group, g = r - q * a.group;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + static_cast<long long>(w.kvh) * a.group * D + 8 * ch;
+      // every row's address for itself, eight at a time: one warp alone has nothing else to fill the latencies with
+      const int r0 = 128 * w.t, q0 = r0 / a.group, g0 = r0 - q0 * a.group, rows = min(a.n_rows - r0, 128);
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                            (static_cast<long long>(q0) * a.n_q_heads + w.kvh * a.group) * D + 8 * ch;
       uint8_t* dst = sm + (ch >> 3) * kPieceBytes;
-#pragma unroll 4
-      for (int i = 0; i < 128 / ROWS; ++i) {
-        const bool real = r < a.n_rows;
-        cp_async16(dst + tc::sw128_off(n, ch & 7), src + (real ? (static_cast<long long>(q) * a.n_q_heads + g) * D : 0), real);
-        n += ROWS;
-        r += ROWS;
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k)
-          if (++g == a.group) {
-            g = 0;
-            ++q;
-          }
+#pragma unroll 8
+      for (int n = t0 / CH; n < 128; n += ROWS) {
+        const int q = small_div(g0 + n, a.group_inv), g = g0 + n - q * a.group;
+        const bool real = n < rows;
+        cp_async16(dst + tc::sw128_off(n, ch & 7), real ? src + (q * a.n_q_heads + g) * D : src, real);
       }
       cp_async_wait();
       tc::fence_proxy_async_smem();
@@ -960,7 +947,7 @@ static cudaError_t launch_prefill_window_d(const PrefillWindowArgs& a, int runs,
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_attention_kernel<D>), L::kAlloc, done);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(window_tiles_kernel<D>, dim3(a.key_tiles, a.n_kv_heads), dim3(256), 0, stream, a);
+  e = launch_pdl(window_tiles_kernel<D>, dim3(a.key_tiles, a.n_kv_heads, 4), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   e = launch_pdl(window_attention_kernel<D>, dim3(runs), dim3(kWThreads), L::kAlloc, stream, a);
   if (e != cudaSuccess) return e;
