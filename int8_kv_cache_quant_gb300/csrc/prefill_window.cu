@@ -152,10 +152,10 @@ __host__ __device__ inline RowTileKeys row_tile_keys(int t, int n_rows, int grou
 }
 
 // Whether a row tile's x-th scores, two tiles ahead, are made before the values at hand: not where they wait for those (P in
-// their place) or for new queries, nor where a row tile's result waits for the values.
+// their place) or for new queries.
 template <int D>
 __device__ __forceinline__ bool scores_first(int x) {
-  return !Pw<D>::kOverlay && x > 1;
+  return !Pw<D>::kOverlay && x != 0;
 }
 
 // Place on the line: KV head, row tile, key tile x of its n.
@@ -842,76 +842,89 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
 
 // ============================================================================ joining the parts
 // Block (run, 32 columns).  The run in which a cut row tile ends joins its parts, from the run in which it
-// begins on; threads take the places of the attention kernel's softmax threads, as the parts lie.
+// begins on; threads take the places of the attention kernel's softmax threads, as the parts lie, two threads for the four
+// rows of one.  Four parts are fetched at once: one after the other, a part costs two trips to memory (ten parts: 28 us).
 template <int D>
-__global__ void __launch_bounds__(128) window_join_kernel(const __grid_constant__ PrefillWindowArgs a, int runs) {
-  grid_dep_wait();
-  grid_dep_trigger();
-  const int run = blockIdx.x, o = blockIdx.y, quad = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ PrefillWindowArgs a, int runs) {
+  const int run = blockIdx.x, o = blockIdx.y, quad = (threadIdx.x >> 5) & 3, h = threadIdx.x >> 7, lane = threadIdx.x & 31;
   const long long f0 = run_start(a, run, runs), f1 = run_start(a, run + 1, runs);
   const WindowWalk w = window_walk_at(a, f0);
-  if (w.x == 0 || f0 - w.x + w.keys.n > f1) return;
   const long long start = f0 - w.x;
-  int first = run - 1;  // the run in which the row tile begins
-  while (run_start(a, first, runs) > start) --first;
+  // the last run c with run_start(c) <= start: the row tile begins in it
+  const int first = static_cast<int>(((start + 1) * runs - 1) / (a.line * a.n_kv_heads));
   const int first_slot = 2 * first + (run_start(a, first, runs) < start ? 1 : 0);
-  auto slot_of = [&](int i) { return static_cast<long long>(i == first ? first_slot : 2 * i); };
-  const int c = lane & 3;
-  float m[4], l[4];
-  bool dropped[4];
+  grid_dep_wait();
+  grid_dep_trigger();
+  if (w.x == 0 || start + w.keys.n > f1) return;
+  const int c = lane & 3, row0 = quad * 32 + frag_row(lane, 2 * h);  // the thread's rows: row0, row0 + 8
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  bool dropped[2] = {false, false};
+  float4 acc[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    m[j] = -INFINITY;
-    l[j] = 0.0f;
-    dropped[j] = false;
-  }
-  for (int i = first; i <= run; ++i)
+  for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = first; i0 <= run; i0 += 4) {
+    float2 v[4][2];
+    float4 x[4][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 v = a.part_ml[slot_of(i) * 128 + quad * 32 + frag_row(lane, j)];
-      m[j] = fmaxf(m[j], v.x);
-      dropped[j] |= v.y < 0.0f;
+    for (int t = 0; t < 4; ++t) {
+      const long long slot = i0 + t == first ? first_slot : 2 * (i0 + t);
+      const float4* src = a.part + ((slot * 4 + quad) * (D / 32) + o) * (8 * 32) + (4 * h) * 32 + lane;  // (o: half of the columns, then 32)
+      const bool real = i0 + t <= run;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) v[t][j] = real ? a.part_ml[slot * 128 + row0 + 8 * j] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[t][e] = real ? src[e * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  float4 acc[8];
+    float s[4][2];
+    bool none[4][2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = first; i <= run; ++i) {
-    float s[4];
-    bool none[4];
+    for (int j = 0; j < 2; ++j) {
+      const float was = m[j];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 v = a.part_ml[slot_of(i) * 128 + quad * 32 + frag_row(lane, j)];
-      none[j] = v.x == -INFINITY && v.y == 0.0f;  // the row sees no key of this part
-      s[j] = v.x == -INFINITY ? 1.0f : fast_exp2(v.x - m[j]);  // (a part of NaN alone has no maximum)
-      if (!none[j]) l[j] = fmaf(v.y, s[j], l[j]);
-    }
-    const float4* src = a.part + ((slot_of(i) * 4 + quad) * (D / 32) + o) * (8 * 32) + lane;  // (o: half of the columns, then 32)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float4 x = src[e * 32];
-      const int ja = (e >> 2) * 2, jb = ja + 1;
-      if (!none[ja]) {
-        acc[e].x = fmaf(x.x, s[ja], acc[e].x);
-        acc[e].y = fmaf(x.y, s[ja], acc[e].y);
+      for (int t = 0; t < 4; ++t) {
+        m[j] = fmaxf(m[j], v[t][j].x);
+        dropped[j] |= v[t][j].y < 0.0f;
       }
-      if (!none[jb]) {
-        acc[e].z = fmaf(x.z, s[jb], acc[e].z);
-        acc[e].w = fmaf(x.w, s[jb], acc[e].w);
+      const float s0 = was == m[j] || was == -INFINITY ? 1.0f : fast_exp2(was - m[j]);
+      l[j] *= s0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        (j ? acc[e].z : acc[e].x) *= s0;
+        (j ? acc[e].w : acc[e].y) *= s0;
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        none[t][j] = v[t][j].x == -INFINITY && v[t][j].y == 0.0f;  // the row sees no key of this part
+        s[t][j] = v[t][j].x == -INFINITY ? 1.0f : fast_exp2(v[t][j].x - m[j]);  // (a part of NaN alone has no maximum)
+        if (!none[t][j]) l[j] = fmaf(v[t][j].y, s[t][j], l[j]);
       }
     }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!none[t][0]) {
+          acc[e].x = fmaf(x[t][e].x, s[t][0], acc[e].x);
+          acc[e].y = fmaf(x[t][e].y, s[t][0], acc[e].y);
+        }
+        if (!none[t][1]) {
+          acc[e].z = fmaf(x[t][e].z, s[t][1], acc[e].z);
+          acc[e].w = fmaf(x[t][e].w, s[t][1], acc[e].w);
+        }
+      }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int rr = 128 * w.t + quad * 32 + frag_row(lane, j), q2 = rr / a.group;
+  for (int j = 0; j < 2; ++j) {
+    const int rr = 128 * w.t + row0 + 8 * j, q2 = rr / a.group;
     if (rr >= a.n_rows || dropped[j]) continue;
     const float inv = l[j] > 0.0f || l[j] != l[j] ? 1.0f / l[j] : 0.0f;
     const long long at = (static_cast<long long>(q2) * a.n_q_heads + w.kvh * a.group + (rr - q2 * a.group)) * D + 32 * o + 2 * c;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = acc[(j >> 1) * 4 + i];
-      const float x = ((j & 1) ? v.z : v.x) * inv, y = ((j & 1) ? v.w : v.y) * inv;
-      if (a.out_bf16) *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + at + 8 * i) = __floats2bfloat162_rn(x, y);
-      else *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + 8 * i) = make_float2(x, y);
+    for (int e = 0; e < 4; ++e) {
+      const float4 u = acc[e];
+      const float x = (j ? u.z : u.x) * inv, y = (j ? u.w : u.y) * inv;
+      if (a.out_bf16) *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + at + 8 * e) = __floats2bfloat162_rn(x, y);
+      else *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + 8 * e) = make_float2(x, y);
     }
   }
 }
@@ -953,7 +966,7 @@ static cudaError_t launch_prefill_window_d(const PrefillWindowArgs& a, int runs,
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(runs, D / 32);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
