@@ -297,7 +297,7 @@ struct RopeAppendArgs {
   float attn_factor;
   RopeAxes axes;
   unsigned int* status;
-  int q_heads_per_block, q_blocks;  // set by launch_rope_append
+  int q_heads, kv_heads, kv_first;  // of a block, set by launch_rope_append
 };
 cudaError_t launch_rope_append(const RopeAppendArgs& a, int n_sms, cudaStream_t stream);
 

@@ -9,13 +9,19 @@
 // factor cos(2 pi turns) and factor sin(2 pi turns), and
 //     x' = RN(RN(x c) - RN(y s)),   y' = RN(RN(y c) + RN(x s)),
 // then the rule of kvq_quant_write on the fp32 row.  cos_sin_exact below gives those numbers: a table of 256 angles
-// in pairs of fp32 and a short polynomial of what is left, about 50 operations a pair, within 2^-45 of the value, which
+// in pairs of fp32 and a short polynomial of what is left, about 100 instructions a pair, within 2^-45 of the value, which
 // leaves one cos in some 2^19 rounded the other way (and a code only where its quotient lies at a tie as well).
 //
-// Bound: bytes, each row in once, q out once, half a byte out for each byte of k and v in.  A block takes 16 tokens and
-// some query heads, or one KV head; a thread owns one column of a token (8 pairs, two 16-byte words of a row), so its 8 cos and sin serve all
-// its heads and stay in registers.  The 16 tokens are counted from a page boundary where the first token's slot says
-// where one is, so that a chunk's V codes leave a page at a time, 16 bytes a dimension.
+// Bound: bytes, each row in once, q out once, half a byte out for each byte of k and v in; a token's cos and sin cost as many
+// instructions as the rotation of eight heads.  So a block takes 16 tokens and as many heads as leave the GPU full: it makes
+// the cos and sin once, into shared memory, its first query rows on their way meanwhile, and then a thread owns one column
+// of a token (8 pairs, two 16-byte words of a row) for all its heads.  With 8 pairs of cos and sin in each thread's own registers,
+// again for every two heads of a token, 2048 tokens of 24 + 4 + 4 heads of 256 took 18.0 us; so 13.8 us (63 MB: 4.6 TB/s), of
+// which 7 us are instructions to issue (7.7 M warp instructions; 11.5 M before).  One token: 4.3 us in a captured graph.
+// The 16 tokens are counted from a page boundary where the first token's slot says where one is, so that a chunk's V codes
+// leave a page at a time, 16 bytes a dimension.
+#include <algorithm>
+
 #include "kvq_dev.cuh"
 #include "kvq_launch.h"
 #include "quant_rule.cuh"
@@ -110,7 +116,7 @@ __device__ __forceinline__ void cos_sin_exact(unsigned long long t, float f, flo
 }
 
 constexpr int kTokens = 16;  // of a block
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 512;
 
 // A lane's two words of a row, 8 values each; the pair of its frequency i.
 template <bool INTER>
@@ -137,32 +143,59 @@ __device__ __forceinline__ void unpack_words(const uint4& w0, const uint4& w1, f
 
 }  // namespace
 
-// Blocks y < q_blocks: query heads q_heads_per_block * y ..; the others: KV head y - q_blocks.  D / 16 lanes hold a row.
+// Block y: query heads q_heads y .. and, from y = kv_first on, KV heads kv_heads (y - kv_first) ..  First the cos and sin of
+// its tokens, into shared memory; then D / 16 lanes a row, RS rows of each token at a time.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
-  constexpr int LANES = D / 16, ROWS = kAppendThreads / LANES;  // rows the block holds at a time: 16 or 32
-  __shared__ __align__(16) int8_t vs[kTokens][D];
-  __shared__ long long tok_ph[kTokens];  // page * n_kv_heads + head, -1: not written
-  __shared__ int tok_slot[kTokens], tok_seq[kTokens], tok_at[kTokens];
-  const int row = threadIdx.x / LANES, col = threadIdx.x % LANES;
-  const int k = row % kTokens;  // token of the block
-  const bool is_q = static_cast<int>(blockIdx.y) < a.q_blocks;
+__global__ void __launch_bounds__(kAppendThreads, 2) rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
+  constexpr int LANES = D / 16, RS = kAppendThreads / (kTokens * LANES);  // 2 or 4
+  __shared__ __align__(16) float cs_s[2][kTokens][D / 2 + 4];
+  __shared__ __align__(16) int8_t vs[RS / 2][kTokens][D];
+  __shared__ int tok_slot[kTokens], tok_page[kTokens];  // -1: a padding token or none; -1: nothing written to the cache
+  __shared__ bool page_s;
+  const int tid = threadIdx.x, rs = tid / (kTokens * LANES), k = tid / LANES % kTokens, col = tid % LANES;
+  const int h0 = static_cast<int>(blockIdx.y) * a.q_heads, h1 = min(a.n_q_heads, h0 + a.q_heads);
+  const int kv0 = (static_cast<int>(blockIdx.y) - a.kv_first) * a.kv_heads;
+  const int n_kv = kv0 < 0 ? 0 : min(a.n_kv_heads - kv0, a.kv_heads);  // (0 or less: none)
   grid_dep_wait();
   grid_dep_trigger();
   // tokens from a page boundary on (one token more than a whole number of blocks is no reason to shift)
   int shift = 0;
   if (a.n_tokens > kTokens) shift = a.slot[0] & (KVQ_BLOCK_SIZE - 1);
-  const long long tok = static_cast<long long>(blockIdx.x) * kTokens - shift + k;
-  const bool live = tok >= 0 && tok < a.n_tokens;
-  int slot = -1, seq = 0;
-  if (live) {
-    slot = a.slot[tok];
-    if (!is_q) seq = a.seq_idx[tok];
+  const long long base = static_cast<long long>(blockIdx.x) * kTokens - shift;
+  const int lo = base < 0 ? static_cast<int>(-base) : 0, hi = static_cast<int>(min(static_cast<long long>(kTokens), a.n_tokens - base));
+  if (tid < 32) {
+    int slot = -1, seq = 0, page = -1;
+    if (tid >= lo && tid < hi) {
+      slot = a.slot[base + tid];
+      seq = a.seq_idx[base + tid];
+    }
+    if (slot != -1 && n_kv > 0) {
+      unsigned bad = 0;
+      if (seq < 0 || seq >= a.num_seqs) {
+        bad = KVQ_DEV_BAD_SEQ;
+      } else if (slot < 0 || slot / KVQ_BLOCK_SIZE >= a.max_blocks_per_seq) {
+        bad = KVQ_DEV_BAD_POS;
+      } else {
+        page = a.block_table[static_cast<long long>(seq) * a.max_blocks_per_seq + slot / KVQ_BLOCK_SIZE];
+        if (page < 0 || page >= a.num_blocks) {
+          bad = KVQ_DEV_BAD_BLOCK;
+          page = -1;
+        }
+      }
+      if (bad) set_status(a.status, bad);
+    }
+    // whether the tokens fill a page in order: their V codes leave 16 bytes a dimension then
+    const int page0 = __shfl_sync(0xffffffffu, page, 0);
+    const bool fill = __all_sync(0xffffffffu, tid >= kTokens || (page >= 0 && page == page0 && slot % KVQ_BLOCK_SIZE == tid));
+    if (tid < kTokens) {
+      tok_slot[tid] = slot;
+      tok_page[tid] = page;
+      if (tid == 0) page_s = fill;
+    }
   }
-  const bool take = live && slot != -1;  // -1: a padding token
-  const int half = a.rotary_dim / 2, n_rot = half / 8;
-  int e0, e1;
+  const int half = a.rotary_dim / 2, n_live = hi - lo, n_rot = half / 8;
   const bool rotated = col < n_rot;
+  int e0, e1;
   if (rotated) {
     e0 = a.rotary_offset + (INTER ? 16 * col : 8 * col);
     e1 = INTER ? e0 + 8 : e0 + half;
@@ -171,147 +204,144 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const __gri
     e0 = u < a.rotary_offset ? u : u + a.rotary_dim;
     e1 = u + 8 < a.rotary_offset ? u + 8 : u + 8 + a.rotary_dim;
   }
-  const bool is_v = !is_q && ROWS > kTokens && row >= kTokens;  // head_dim 128: K rows and V rows side by side
-  float c[8], s[8];
+  // the first query rows are on their way meanwhile
+  constexpr int IN_FLIGHT = 3;
+  const long long tok = base + k;
+  const uint16_t* q_src = a.q + tok * a.q_stride;
+  uint4 w0[IN_FLIGHT], w1[IN_FLIGHT];
+  auto fetch = [&](int h) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.0f;
-    s[i] = 0.0f;
+    for (int u = 0; u < IN_FLIGHT; ++u)
+      if (h + u * RS < h1 && k >= lo && k < hi) {
+        w0[u] = *reinterpret_cast<const uint4*>(q_src + static_cast<long long>(h + u * RS) * D + e0);
+        w1[u] = *reinterpret_cast<const uint4*>(q_src + static_cast<long long>(h + u * RS) * D + e1);
+      }
+  };
+  fetch(h0 + rs);
+  for (int i = tid; i < n_live * half; i += kAppendThreads) {
+    const int pair = i / n_live, t = lo + (i - pair * n_live), axis = a.axes.map[pair / 16] >> (2 * (pair % 16)) & 3;
+    const int32_t p = a.axes.pos[axis * a.axes.pos_stride + base + t];
+    float c, s;
+    cos_sin_exact(position_bits(p) * __ldg(a.phases + pair), a.attn_factor, c, s);
+    cs_s[0][t][pair] = c;
+    cs_s[1][t][pair] = s;
   }
-  if (rotated && take && !is_v) {
-    int32_t p[kMaxAxes];
-    load_axes(a.axes, tok, p);
-    const uint32_t map = a.axes.map[col / 2] >> (16 * (col % 2));
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      cos_sin_exact(position_bits(axis_position(p, map, i)) * __ldg(a.phases + col * 8 + i), a.attn_factor, c[i], s[i]);
-  }
+  __syncthreads();
 
-  if (is_q) {
-    if (!take) return;
-    constexpr int STEP = ROWS / kTokens, IN_FLIGHT = 4;
-    const int h0 = static_cast<int>(blockIdx.y) * a.q_heads_per_block, h1 = min(a.n_q_heads, h0 + a.q_heads_per_block);
-    const uint16_t* src = a.q + tok * a.q_stride;
+  float c[8], s[8];
+  if (rotated) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 c4 = *reinterpret_cast<const float4*>(&cs_s[0][k][8 * col + 4 * i]);
+      const float4 s4 = *reinterpret_cast<const float4*>(&cs_s[1][k][8 * col + 4 * i]);
+      c[4 * i] = c4.x, c[4 * i + 1] = c4.y, c[4 * i + 2] = c4.z, c[4 * i + 3] = c4.w;
+      s[4 * i] = s4.x, s[4 * i + 1] = s4.y, s[4 * i + 2] = s4.z, s[4 * i + 3] = s4.w;
+    }
+  }
+  const int slot = tok_slot[k], page = tok_page[k], at = slot & (KVQ_BLOCK_SIZE - 1);
+
+  if (slot != -1) {
     uint16_t* dst = a.q_out + tok * a.q_out_stride;
-    for (int h = h0 + row / kTokens; h < h1; h += STEP * IN_FLIGHT) {
-      uint4 w0[IN_FLIGHT], w1[IN_FLIGHT];
+    for (int h = h0 + rs; h < h1; h += RS * IN_FLIGHT) {
+      if (h != h0 + rs) fetch(h);
 #pragma unroll
       for (int u = 0; u < IN_FLIGHT; ++u)
-        if (h + u * STEP < h1) {
-          w0[u] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(h + u * STEP) * D + e0);
-          w1[u] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(h + u * STEP) * D + e1);
-        }
-#pragma unroll
-      for (int u = 0; u < IN_FLIGHT; ++u)
-        if (h + u * STEP < h1) {
+        if (h + u * RS < h1) {
           if (rotated) {
-            float x[16], lo[8], hi[8];
+            float x[16], low[8], high[8];
             unpack_words(w0[u], w1[u], x);
             rotate_words<INTER>(x, c, s);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              lo[i] = x[i];
-              hi[i] = x[8 + i];
+              low[i] = x[i];
+              high[i] = x[8 + i];
             }
-            w0[u] = pack<8>(lo);
-            w1[u] = pack<8>(hi);
+            w0[u] = pack<8>(low);
+            w1[u] = pack<8>(high);
           }
-          *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + u * STEP) * D + e0) = w0[u];
-          *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + u * STEP) * D + e1) = w1[u];
+          *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + u * RS) * D + e0) = w0[u];
+          *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + u * RS) * D + e1) = w1[u];
         }
     }
-    return;
   }
 
-  // ---- one KV head
-  const int kvh = static_cast<int>(blockIdx.y) - a.q_blocks, H = a.n_kv_heads;
-  long long ph = -1;
-  if (take) {
-    unsigned bad = 0;
-    if (seq < 0 || seq >= a.num_seqs) {
-      bad = KVQ_DEV_BAD_SEQ;
-    } else if (slot < 0 || slot / KVQ_BLOCK_SIZE >= a.max_blocks_per_seq) {
-      bad = KVQ_DEV_BAD_POS;
-    } else {
-      const int page = a.block_table[static_cast<long long>(seq) * a.max_blocks_per_seq + slot / KVQ_BLOCK_SIZE];
-      if (page < 0 || page >= a.num_blocks) bad = KVQ_DEV_BAD_BLOCK;
-      else ph = static_cast<long long>(page) * H + kvh;
-    }
-    if (bad && col == 0) set_status(a.status, bad);
-  }
-  const int at = slot & (KVQ_BLOCK_SIZE - 1);
-  if (col == 0 && row < kTokens) {
-    tok_ph[k] = ph;
-    tok_at[k] = at;
-    tok_slot[k] = slot;
-    tok_seq[k] = seq;
-  }
-  const long long src = tok, head = static_cast<long long>(kvh) * D;
-  auto load = [&](const uint16_t* rows, long long stride, float (&x)[16]) {
+  // ---- KV heads, RS / 2 at a time: K rows and V rows side by side
+  const bool is_v = rs & 1, fill = page_s;
+  for (int i0 = 0; i0 < n_kv; i0 += RS / 2) {
+    const bool real = page >= 0 && i0 + rs / 2 < n_kv;
+    const int kvh = kv0 + i0 + rs / 2;
+    const long long ph = static_cast<long long>(page) * a.n_kv_heads + kvh;
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-    if (ph >= 0) {
-      w0 = *reinterpret_cast<const uint4*>(rows + src * stride + head + e0);
-      w1 = *reinterpret_cast<const uint4*>(rows + src * stride + head + e1);
+    if (real) {
+      const uint16_t* src = (is_v ? a.v_new + tok * a.v_stride : a.k_new + tok * a.k_stride) + static_cast<long long>(kvh) * D;
+      w0 = *reinterpret_cast<const uint4*>(src + e0);
+      w1 = *reinterpret_cast<const uint4*>(src + e1);
     }
+    float x[16];
     unpack_words(w0, w1, x);
-  };
-  // every lane of a warp takes part in the rows' maxima
-  if (!is_v) {
-    float x[16];
-    load(a.k_new, a.k_stride, x);
-    if (rotated) rotate_words<INTER>(x, c, s);
+    if (!is_v && rotated) rotate_words<INTER>(x, c, s);
     uint32_t code[4];
-    const float scale = quant_rule_rows_packed<16, LANES>(x, code);
-    if (ph >= 0) {
-      int8_t* page = a.k + ph * (D * KVQ_BLOCK_SIZE);
-      *reinterpret_cast<uint2*>(page + ((e0 / 16) * KVQ_BLOCK_SIZE + at) * 16 + e0 % 16) = make_uint2(code[0], code[1]);
-      *reinterpret_cast<uint2*>(page + ((e1 / 16) * KVQ_BLOCK_SIZE + at) * 16 + e1 % 16) = make_uint2(code[2], code[3]);
-      if (col == 0) a.k_scale[ph * KVQ_BLOCK_SIZE + at] = scale;
+    const float scale = quant_rule_rows_packed<16, LANES>(x, code);  // every lane of a warp takes part in the rows' maxima
+    if (is_v) {
+      *reinterpret_cast<uint2*>(&vs[rs / 2][k][e0]) = make_uint2(code[0], code[1]);
+      *reinterpret_cast<uint2*>(&vs[rs / 2][k][e1]) = make_uint2(code[2], code[3]);
+    } else if (real) {
+      int8_t* dst = a.k + ph * (D * KVQ_BLOCK_SIZE);
+      *reinterpret_cast<uint2*>(dst + ((e0 / 16) * KVQ_BLOCK_SIZE + at) * 16 + e0 % 16) = make_uint2(code[0], code[1]);
+      *reinterpret_cast<uint2*>(dst + ((e1 / 16) * KVQ_BLOCK_SIZE + at) * 16 + e1 % 16) = make_uint2(code[2], code[3]);
     }
-  }
-  if (is_v || ROWS == kTokens) {
-    float x[16];
-    load(a.v_new, a.v_stride, x);
-    uint32_t code[4];
-    const float scale = quant_rule_rows_packed<16, LANES>(x, code);
-    *reinterpret_cast<uint2*>(&vs[k][e0]) = make_uint2(code[0], code[1]);
-    *reinterpret_cast<uint2*>(&vs[k][e1]) = make_uint2(code[2], code[3]);
-    if (ph >= 0 && col == 0) a.v_scale[ph * KVQ_BLOCK_SIZE + at] = scale;
-  }
-  __syncthreads();
-  // The V codes: where the block's tokens fill a page in order, 16 bytes a dimension; else a byte each.
-  bool full = true;
+    if (real && col == 0) (is_v ? a.v_scale : a.k_scale)[ph * KVQ_BLOCK_SIZE + at] = scale;
+    __syncthreads();
+    // The V codes
+    if (fill) {
+      const int b = tid / D, d = tid % D, h = i0 + b;  // (RS / 2 heads of D dimensions: 256 threads)
+      if (b < RS / 2 && h < n_kv) {
+        uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) full = full && tok_ph[i] == tok_ph[0] && tok_at[i] == i;
-  full = full && tok_ph[0] >= 0;
-  if (full) {
-    for (int d = threadIdx.x; d < D; d += kAppendThreads) {
-      uint32_t w[4];
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4)
-        w[q4] = static_cast<uint32_t>(static_cast<uint8_t>(vs[4 * q4][d])) |
-                (static_cast<uint32_t>(static_cast<uint8_t>(vs[4 * q4 + 1][d])) << 8) |
-                (static_cast<uint32_t>(static_cast<uint8_t>(vs[4 * q4 + 2][d])) << 16) |
-                (static_cast<uint32_t>(static_cast<uint8_t>(vs[4 * q4 + 3][d])) << 24);
-      *reinterpret_cast<uint4*>(a.v + (tok_ph[0] * D + d) * KVQ_BLOCK_SIZE) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int q4 = 0; q4 < 4; ++q4)
+          w[q4] = static_cast<uint32_t>(static_cast<uint8_t>(vs[b][4 * q4][d])) |
+                  (static_cast<uint32_t>(static_cast<uint8_t>(vs[b][4 * q4 + 1][d])) << 8) |
+                  (static_cast<uint32_t>(static_cast<uint8_t>(vs[b][4 * q4 + 2][d])) << 16) |
+                  (static_cast<uint32_t>(static_cast<uint8_t>(vs[b][4 * q4 + 3][d])) << 24);
+        *reinterpret_cast<uint4*>(a.v + ((static_cast<long long>(tok_page[0]) * a.n_kv_heads + kv0 + h) * D + d) * KVQ_BLOCK_SIZE) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      for (int it = tid; it < RS / 2 * kTokens * D; it += kAppendThreads) {
+        const int d = it % D, t = it / D % kTokens, b = it / (D * kTokens);
+        if (tok_page[t] >= 0 && i0 + b < n_kv)
+          a.v[((static_cast<long long>(tok_page[t]) * a.n_kv_heads + kv0 + i0 + b) * D + d) * KVQ_BLOCK_SIZE +
+              (tok_slot[t] & (KVQ_BLOCK_SIZE - 1))] = vs[b][t][d];
+      }
     }
-  } else {
-    for (int it = threadIdx.x; it < kTokens * D; it += kAppendThreads) {
-      const int i = it / D, d = it % D;
-      if (tok_ph[i] >= 0) a.v[(tok_ph[i] * D + d) * KVQ_BLOCK_SIZE + tok_at[i]] = vs[i][d];
-    }
+    __syncthreads();
   }
 }
 
+// Heads of a block: all of them share its cos and sin, so as many as leave one and a half blocks an SM; where there are
+// too few tokens for that, query heads and KV heads in blocks of their own.
 template <int D>
 static cudaError_t launch_append_d(RopeAppendArgs a, int n_sms, cudaStream_t stream) {
+  constexpr int RS = kAppendThreads / D;
   const long long groups = a.n_tokens > kTokens ? (static_cast<long long>(a.n_tokens) + KVQ_BLOCK_SIZE - 1 + kTokens - 1) / kTokens : 1;
-  int per = 16;
-  while (per > 256 / D && groups * ((a.n_q_heads + per - 1) / per + a.n_kv_heads) < 4LL * n_sms) per /= 2;
-  a.q_heads_per_block = per;
-  a.q_blocks = (a.n_q_heads + per - 1) / per;
-  if (groups > 0x7fffffffLL || a.q_blocks + a.n_kv_heads > 65535) return cudaErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(groups), a.q_blocks + a.n_kv_heads);
+  const int H = a.n_kv_heads, Hq = a.n_q_heads;
+  long long blocks;
+  if (2 * groups * H >= 3LL * n_sms) {
+    const int cut = static_cast<int>(std::min<long long>(H, (3LL * n_sms + 2 * groups - 1) / (2 * groups)));
+    a.kv_heads = (H + cut - 1) / cut;
+    blocks = (H + a.kv_heads - 1) / a.kv_heads;
+    a.q_heads = static_cast<int>((Hq + blocks - 1) / blocks);
+    a.kv_first = 0;
+  } else {
+    int per = 16;
+    while (per > RS && groups * ((Hq + per - 1) / per + H) < 4LL * n_sms) per /= 2;
+    a.q_heads = per;
+    a.kv_heads = 1;
+    a.kv_first = (Hq + per - 1) / per;
+    blocks = static_cast<long long>(a.kv_first) + H;
+  }
+  if (groups > 0x7fffffffLL || blocks > 65535) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(blocks));
   return a.interleaved ? launch_pdl(rope_append_kernel<D, true>, grid, dim3(kAppendThreads), 0, stream, a)
                        : launch_pdl(rope_append_kernel<D, false>, grid, dim3(kAppendThreads), 0, stream, a);
 }
