@@ -54,6 +54,7 @@ constexpr float kWMinScale = 7.8886091e-31f;  // 2^-100
 template <int D>
 struct Pw {
   static constexpr int kSlots = D == 256 ? 8 : 10;           // pieces in the ring
+  static constexpr int kScoreBufs = D == 256 ? 2 : 3;        // score tiles
   static constexpr int kQBytes = 128 * D * 2;                // Q in pieces of 16 KB
   static constexpr int offRing = kQBytes;
   static constexpr int offPar = offRing + kSlots * kPieceBytes;    // [buf][3][128] fp32
@@ -61,18 +62,17 @@ struct Pw {
   static constexpr int offRed = offRef + 128 * 4;            // [maximum, sum][group][half of the keys][128] a row's two warps
   static constexpr int offSum = offRed + 2 * 2 * 2 * 128 * 4;    // [2][sum, sum, reference][128] what a unit's other group leaves
   static constexpr int offBar = offSum + 2 * 3 * 128 * 4;
-  // barriers; those of two are by a tile's parity, so that each has one group on one side
+  // barriers; a score buffer's tiles have theirs
   static constexpr int full = 0, empty = full + kSlots, parFull = empty + kSlots, parFree = parFull + kWParBufs,
-                       sFull = parFree + kWParBufs, pFull = sFull + 2, pvDone = pFull + 2, decided = pvDone + 2,
+                       sFull = parFree + kWParBufs, pFull = sFull + kScoreBufs, pvDone = pFull + kScoreBufs, decided = pvDone + kScoreBufs,
                        sumReady = decided + 8, qFull = sumReady + 8, qFree = qFull + 1, oFree = qFree + 1,
                        drain = oFree + 1, kNumBars = drain + 1;
   static constexpr int offFlag = offBar + kNumBars * 8;      // abort flag, TMEM base
   static constexpr int kAlloc = offFlag + 16 + 1024;
-  // Tensor memory: two score tiles, O, and at head_dim 128 two P tiles.  At head_dim 256 a P tile takes its score tile's place.
-  static constexpr bool kOverlay = D == 256;
-  static constexpr uint32_t kOCol = 256, kTmemCols = 512;
-  static constexpr uint32_t kPHalf = kOverlay ? 64 : 32;  // columns from a P tile's first half of the keys to its second
-  __device__ static uint32_t p_col(int b) { return kOverlay ? 128 * b : 384 + 64 * b; }
+  // Tensor memory: score tiles and O.  A P tile takes its score tile's place, the first and second half of the keys each
+  // their half's.
+  static constexpr uint32_t kOCol = 128 * kScoreBufs, kTmemCols = 512;
+  static_assert(kOCol + D <= kTmemCols, "tensor memory");
   static_assert(offBar % 8 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
@@ -151,11 +151,11 @@ __host__ __device__ inline RowTileKeys row_tile_keys(int t, int n_rows, int grou
   return r;
 }
 
-// Whether a row tile's x-th scores, two tiles ahead, are made before the values at hand: not where they wait for those (P in
-// their place) or for new queries.
+// Whether a row tile's x-th scores, two tiles ahead, are made before the values at hand: not where they wait for those (two
+// score tiles) or for new queries.
 template <int D>
 __device__ __forceinline__ bool scores_first(int x) {
-  return !Pw<D>::kOverlay && x != 0;
+  return Pw<D>::kScoreBufs > 2 && x != 0;
 }
 
 // Place on the line: KV head, row tile, key tile x of its n.
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       mbar_init(&bars[L::parFull + s], 1);
       mbar_init(&bars[L::parFree + s], 8);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < L::kScoreBufs; ++s) {
       mbar_init(&bars[L::sFull + s], 1);
       mbar_init(&bars[L::pFull + s], 8);
       mbar_init(&bars[L::pvDone + s], 1);
@@ -392,10 +392,11 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       for (int u = (f_unit & 1) == group ? 0 : 1; u < n_unit; u += 2) {
         const int f = f_unit + u, pb = f % kWParBufs, x = w.x + u;
         const int kk = 128 * (x < w.keys.sink ? x : x - w.keys.sink + w.keys.low) + 64 * part;  // the warp's first key
-        const uint32_t tm_s = tmem + 128 * group + 64 * part;
+        const int sb = f % L::kScoreBufs;
+        const uint32_t tm_s = tmem + 128 * sb + 64 * part;
         const float2* kf = reinterpret_cast<const float2*>(par + pb * 384 + 64 * part) + c;
         await(L::parFull + pb, (f / kWParBufs) & 1);
-        await(L::sFull + group, (f >> 1) & 1);
+        await(L::sFull + sb, (f / L::kScoreBufs) & 1);
         tc::fence_after_sync();
         // The scores pass through registers 32 keys at a time, and twice: first they become z, with a row's maximum, and go
         // back.  Loops of few instructions, and many warps at them: a tile unrolled in registers came out of the
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
             arrive(L::decided + 4 * group + quad);
             if (__any_sync(0xffffffffu, moved)) {
               // O holds the products up to tile f - 1 (of this unit: u > 0); half of its columns
-              await(L::pvDone + (group ^ 1), ((f - 1) >> 1) & 1);
+              await(L::pvDone + (f - 1) % L::kScoreBufs, ((f - 1) / L::kScoreBufs) & 1);
               tc::fence_after_sync();
 #pragma unroll 1
               for (int o = 0; o < D / 32; ++o) {  // 16 lanes, 32 columns
@@ -514,11 +515,6 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
             }
           }
         }
-        if (!L::kOverlay && f >= 2) {  // this group's P was read by the product of tile f - 2
-          await(L::pvDone + group, ((f >> 1) - 1) & 1);
-          tc::fence_after_sync();
-        }
-        const uint32_t tm_p = tmem + L::p_col(group) + L::kPHalf * part;  // head_dim 256: where scores were that have been taken
         float nr[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) nr[j] = ref[j] == -INFINITY ? 0.0f : -ref[j];
@@ -540,13 +536,13 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
               (j < 2 ? p0 : p1)[2 * i + (j & 1)] = pack_half2(w0, w1);
             }
           }
-          tc::st_16x128b_x4(tm_p + lanes0 + 16 * k, p0);
-          tc::st_16x128b_x4(tm_p + lanes1 + 16 * k, p1);
+          tc::st_16x128b_x4(tm_s + lanes0 + 16 * k, p0);  // where scores were that have been taken
+          tc::st_16x128b_x4(tm_s + lanes1 + 16 * k, p1);
         }
         arrive(L::parFree + pb);
         tc::wait_st();
         tc::fence_before_sync();
-        arrive(L::pFull + group);
+        arrive(L::pFull + sb);
       }
       if (pair_or(pair_id, failed)) break;
       // ---- the unit's sums: this warp's
@@ -590,7 +586,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         const long long out0 = (static_cast<long long>(q0) * a.n_q_heads + w.kvh * a.group) * D + part * (D / 2);
         // O once its last product is there.  (Few instructions: what runs once a row tile comes from far out of the
         // instruction caches.)
-        await(L::pvDone + group, ((f_unit + n_unit - 1) >> 1) & 1);
+        const int last = f_unit + n_unit - 1;
+        await(L::pvDone + last % L::kScoreBufs, (last / L::kScoreBufs) & 1);
         if (pair_or(pair_id, failed)) break;
         tc::fence_after_sync();
         if (!whole_unit && part == 0) ml[(slot & 1) * 128 + quad * 32 + frag_row(lane, c)] = make_float2(pick(ref), pick(sum));
@@ -661,17 +658,16 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         ph ^= 1u;
       }
     };
-    // S = Q K_f^T, in tile f's score tile: free once the P of tile f - 2 has been made (the caller has waited for it) or, where P
-    // lies in it, multiplied
+    // S = Q K_f^T, in the place of the P of kScoreBufs tiles before, once that is multiplied
     WindowWalk ws = w;  // of the scores
     int fs = 0, s_unit = -1;
     auto scores = [&]() {
-      const int b = fs & 1;
+      const int b = fs % L::kScoreBufs;
       if (fs == 0 || ws.x == 0) {
         ++s_unit;
         if (!await(L::qFull, s_unit & 1)) return;
       }
-      if (L::kOverlay && fs >= 2 && !await(L::pvDone + b, ((fs >> 1) - 1) & 1)) return;
+      if (fs >= L::kScoreBufs && !await(L::pvDone + b, (fs / L::kScoreBufs - 1) & 1)) return;
       const bool last = ws.x + 1 == ws.keys.n;  // of its row tile: Q's place is free then
       for (int qa = 0; qa < NP; ++qa) {
         if (!await(L::full + slot, ph)) return;
@@ -695,7 +691,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     };
     int v_unit = -1;
     auto values = [&](int f) {  // O (+)= P_f V_f
-      const int b = f & 1;
+      const int b = f % L::kScoreBufs;
       const bool first = f == 0 || w.x == 0;
       if (first) ++v_unit;
       if (first && v_unit > 0 && !await(L::oFree, (v_unit - 1) & 1)) return;  // the row tile before has been read
@@ -710,7 +706,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           const uint64_t vd = rd0 + static_cast<uint64_t>((s0 * kPieceBytes) >> 4);
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            tc::mma_f16_ts(tmem + L::kOCol, tmem + L::p_col(b) + L::kPHalf * kh + 8 * s, vd + 2 * s, idesc_pv,
+            tc::mma_f16_ts(tmem + L::kOCol, tmem + 128 * b + 64 * kh + 8 * s, vd + 2 * s, idesc_pv,
                            (first && kh == 0 && s == 0) ? 0u : 1u);
 #pragma unroll
           for (int dh = 0; dh < D / 128; ++dh) tc::commit(&bars[L::empty + s0 + dh]);
@@ -724,10 +720,10 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     scores();
     if (ok && n_tiles > 1) scores();
     for (int f = 0; ok && f < n_tiles; ++f) {
-      if (!await(L::pFull + (f & 1), (f >> 1) & 1)) break;
       const bool early = scores_first<D>(ws.x);
       if (early && fs < n_tiles) scores();
-      if (ok) values(f);
+      if (!ok || !await(L::pFull + f % L::kScoreBufs, (f / L::kScoreBufs) & 1)) break;
+      values(f);
       if (ok && !early && fs < n_tiles) scores();
     }
     // every MMA this warp issued has completed before the CTA releases tensor memory
