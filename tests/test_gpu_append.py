@@ -78,6 +78,15 @@ def test_one_sequence(kvq, T, first, hq, hkv, d, sections, order, ladder, off, i
         ladder, off, inter, packed=T % 2 == 1, stretch=4.0 if T == 31 else 1.0)
 
 
+@pytest.mark.parametrize("T,first,hq,hkv,d,sections", [(3001, 7, 24, 4, 256, [128]), (2500, 0, 7, 3, 128, [24, 20, 20]),
+                                                        (9000, 16, 6, 5, 128, [8, 8]), (5000, 3, 2, 3, 256, [40, 40])])
+def test_long_chunks(kvq, T, first, hq, hkv, d, sections):
+    """Several KV heads a block."""
+    rng = np.random.default_rng(T)
+    table, nb = table_of(rng, [first + T], spare=2)
+    run(kvq, rng, hq, hkv, d, np.zeros(T, np.int32), np.arange(first, first + T, dtype=np.int32), table, nb, sections, packed=True)
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_a_ragged_batch_with_padding(kvq, d):
     """Several sequences' new tokens behind each other, padding between and behind them, slots in any order."""

@@ -178,6 +178,14 @@ def test_rows_that_are_not_finite(kvq):
     assert torch.equal(got[0][keep], want[0][keep])
 
 
+@pytest.mark.parametrize("batch,hkv,d,window", [(20, 8, 128, 1500), (11, 4, 256, 2000), (3, 2, 128, 2100), (70, 8, 128, 300)])
+def test_automatic_splits(kvq, batch, hkv, d, window):
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(window // 2, window + 700, batch)
+    lens[0], lens[1] = window + 700, 1
+    run(kvq, rng, lens, 2 * hkv, hkv, d, 1, window, 4)
+
+
 def test_many_sequences(kvq):
     rng = np.random.default_rng(8)
     lens = rng.integers(1, 700, 200)
