@@ -62,8 +62,10 @@ struct Pw {
   static constexpr int offRed = offRef + 128 * 4;            // [maximum, sum][group][half of the keys][128] a row's two warps
   static constexpr int offSum = offRed + 2 * 2 * 2 * 128 * 4;    // [2][sum, sum, reference][128] what a unit's other group leaves
   static constexpr int offBar = offSum + 2 * 3 * 128 * 4;
-  // barriers; a score buffer's tiles have theirs
-  static constexpr int full = 0, empty = full + kSlots, parFull = empty + kSlots, parFree = parFull + kWParBufs,
+  static constexpr int kTiles = kSlots / (D / 64);           // K or V tiles in the ring
+  static_assert(kSlots % (D / 64) == 0, "whole tiles");
+  // barriers: of the ring's tiles, its pieces, ..; a score buffer's tiles have theirs
+  static constexpr int full = 0, empty = full + kTiles, parFull = empty + kSlots, parFree = parFull + kWParBufs,
                        sFull = parFree + kWParBufs, pFull = sFull + kScoreBufs, pvDone = pFull + kScoreBufs, decided = pvDone + kScoreBufs,
                        sumReady = decided + 8, qFull = sumReady + 8, qFree = qFull + 1, oFree = qFree + 1,
                        drain = oFree + 1, kNumBars = drain + 1;
@@ -324,10 +326,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
 
   if (warp == kWMmaWarp) tc::tmem_alloc(tmem_slot, L::kTmemCols);
   if (tid == 0) {
-    for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(&bars[L::full + s], 1);
-      mbar_init(&bars[L::empty + s], 1);
-    }
+    for (int s = 0; s < L::kTiles; ++s) mbar_init(&bars[L::full + s], NP);
+    for (int s = 0; s < L::kSlots; ++s) mbar_init(&bars[L::empty + s], 1);
     for (int s = 0; s < kWParBufs; ++s) {
       mbar_init(&bars[L::parFull + s], 1);
       mbar_init(&bars[L::parFree + s], 8);
@@ -645,64 +645,61 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     grid_dep_trigger();
     const uint64_t qd0 = tc::sdesc_sw128(smem_u32(sm)), rd0 = tc::sdesc_sw128(smem_u32(ring));
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(128, 128), idesc_pv = tc::idesc_f16_f32(128, D);
-    int slot = 0;
-    uint32_t ph = 0;
+    int tile = 0;  // of the ring's fills
     bool ok = true;
     auto await = [&](int bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, wait_on(&bars[bar], parity, abort_flag, a.wait_budget));
       return ok;
     };
-    auto next_slot = [&]() {
-      if (++slot == L::kSlots) {
-        slot = 0;
-        ph ^= 1u;
-      }
+    // The next tile, before what it is multiplied with, which comes later.  (A tile cut short passes too, after the flag is set.)
+    auto await_tile = [&]() {
+      ok = __all_sync(0xffffffffu, wait_on(&bars[L::full + tile % L::kTiles], (tile / L::kTiles) & 1, abort_flag, a.wait_budget) &&
+                                       !*abort_flag);
+      return ok;
     };
     // S = Q K_f^T, in the place of the P of kScoreBufs tiles before, once that is multiplied
     WindowWalk ws = w;  // of the scores
     int fs = 0, s_unit = -1;
     auto scores = [&]() {
-      const int b = fs % L::kScoreBufs;
+      const int b = fs % L::kScoreBufs, slot = tile % L::kTiles * NP;
+      if (!await_tile()) return;
       if (fs == 0 || ws.x == 0) {
         ++s_unit;
         if (!await(L::qFull, s_unit & 1)) return;
       }
       if (fs >= L::kScoreBufs && !await(L::pvDone + b, (fs / L::kScoreBufs - 1) & 1)) return;
       const bool last = ws.x + 1 == ws.keys.n;  // of its row tile: Q's place is free then
-      for (int qa = 0; qa < NP; ++qa) {
-        if (!await(L::full + slot, ph)) return;
-        if (elect_one()) {
-          tc::fence_after_sync();
-          const uint64_t kd = rd0 + static_cast<uint64_t>((slot * kPieceBytes) >> 4);
+      if (elect_one()) {
+        tc::fence_after_sync();
+#pragma unroll
+        for (int qa = 0; qa < NP; ++qa) {
+          const uint64_t kd = rd0 + static_cast<uint64_t>(((slot + qa) * kPieceBytes) >> 4);
           const uint64_t qd = qd0 + static_cast<uint64_t>((qa * kPieceBytes) >> 4);
 #pragma unroll
           for (int s = 0; s < 4; ++s) tc::mma_f16_ss(tmem + 128 * b, qd + 2 * s, kd + 2 * s, idesc_qk, (qa | s) ? 1u : 0u);
-          tc::commit(&bars[L::empty + slot]);
-          if (qa == NP - 1) {
-            tc::commit(&bars[L::sFull + b]);
-            if (last) tc::commit(&bars[L::qFree]);
-          }
+          tc::commit(&bars[L::empty + slot + qa]);
         }
-        __syncwarp();
-        next_slot();
+        tc::commit(&bars[L::sFull + b]);
+        if (last) tc::commit(&bars[L::qFree]);
       }
+      __syncwarp();
+      ++tile;
       ++fs;
       window_step(a, ws);
     };
     int v_unit = -1;
     auto values = [&](int f) {  // O (+)= P_f V_f
-      const int b = f % L::kScoreBufs;
+      const int b = f % L::kScoreBufs, slot = tile % L::kTiles * NP;
       const bool first = f == 0 || w.x == 0;
+      if (!await_tile()) return;
       if (first) ++v_unit;
       if (first && v_unit > 0 && !await(L::oFree, (v_unit - 1) & 1)) return;  // the row tile before has been read
-      for (int kh = 0; kh < 2; ++kh) {
-        const int s0 = slot;
-        for (int dh = 0; dh < D / 128; ++dh) {
-          if (!await(L::full + slot, ph)) return;
-          next_slot();
-        }
-        if (elect_one()) {
-          tc::fence_after_sync();
+      if (!await(L::pFull + b, (f / L::kScoreBufs) & 1)) return;
+      if (elect_one()) {
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
+          const int s0 = slot + kh * (D / 128);
           const uint64_t vd = rd0 + static_cast<uint64_t>((s0 * kPieceBytes) >> 4);
 #pragma unroll
           for (int s = 0; s < 4; ++s)
@@ -710,10 +707,11 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
                            (first && kh == 0 && s == 0) ? 0u : 1u);
 #pragma unroll
           for (int dh = 0; dh < D / 128; ++dh) tc::commit(&bars[L::empty + s0 + dh]);
-          if (kh == 1) tc::commit(&bars[L::pvDone + b]);
         }
-        __syncwarp();
+        tc::commit(&bars[L::pvDone + b]);
       }
+      __syncwarp();
+      ++tile;
       window_step(a, w);
     };
     // The scores run two tiles ahead of the values: beside tile f's weights, tile f + 1 is with the other group.
@@ -722,8 +720,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     for (int f = 0; ok && f < n_tiles; ++f) {
       const bool early = scores_first<D>(ws.x);
       if (early && fs < n_tiles) scores();
-      if (!ok || !await(L::pFull + f % L::kScoreBufs, (f / L::kScoreBufs) & 1)) break;
-      values(f);
+      if (ok) values(f);
       if (ok && !early && fs < n_tiles) scores();
     }
     // every MMA this warp issued has completed before the CTA releases tensor memory
@@ -740,16 +737,16 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       int slot = 0, fills = 0, par_fills = 0;
       uint32_t ph = 0;
       bool ok = true;
-      const bool skip_one = a.fault == 5 && blockIdx.x == 0;  // test-only: the fourth piece is never copied
+      const bool skip_one = a.fault == 5 && blockIdx.x == 0;  // test-only: the second tile is never copied
       auto push = [&](const uint8_t* src) {
         for (int i = 0; i < NP; ++i) {
           if (fills >= L::kSlots && !wait_on(&bars[L::empty + slot], ph ^ 1u, abort_flag, a.wait_budget)) {
             ok = false;
             return;
           }
-          if (!(skip_one && fills == 3)) {
-            mbar_arrive_expect_tx(&bars[L::full + slot], kPieceBytes);
-            bulk_g2s(ring + slot * kPieceBytes, src + i * kPieceBytes, kPieceBytes, &bars[L::full + slot]);
+          if (!(skip_one && fills / NP == 1)) {
+            mbar_arrive_expect_tx(&bars[L::full + slot / NP], kPieceBytes);
+            bulk_g2s(ring + slot * kPieceBytes, src + i * kPieceBytes, kPieceBytes, &bars[L::full + slot / NP]);
           }
           ++fills;
           if (++slot == L::kSlots) {
@@ -788,10 +785,11 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         window_step(a, w);
         if (ok && !early && fk < n_tiles) push_k();
       }
-      // copies still in flight (only after an abort) land before the CTA exits
-      for (int i = max(0, fills - L::kSlots); i < fills; ++i)
-        if (!(skip_one && i == 3))
-          mbar_wait(&bars[L::full + i % L::kSlots], (i / L::kSlots) & 1, a.status, a.wait_budget);
+      // copies still in flight (only after an abort) land before the CTA exits; of a tile cut short, those that it has
+      for (int p = fills % NP; p != 0 && p < NP; ++p) mbar_arrive(&bars[L::full + slot / NP]);
+      const int tiles = (fills + NP - 1) / NP;
+      for (int i = max(0, tiles - L::kTiles); i < tiles; ++i)
+        if (!(skip_one && i == 1)) mbar_wait(&bars[L::full + i % L::kTiles], (i / L::kTiles) & 1, a.status, a.wait_budget);
       for (int i = max(0, par_fills - kWParBufs); i < par_fills; ++i)
         mbar_wait(&bars[L::parFull + i % kWParBufs], (i / kWParBufs) & 1, a.status, a.wait_budget);
     }
