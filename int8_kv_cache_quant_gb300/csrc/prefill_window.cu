@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::offBar);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::offFlag);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::offFlag + 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the same in its lanes, for the compiler too)
   const int runs = static_cast<int>(gridDim.x), run = static_cast<int>(blockIdx.x);
   const long long f0 = run_start(a, run, runs);
   const int n_tiles = static_cast<int>(run_start(a, run + 1, runs) - f0);
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;  // all columns: from the first
 
   if (warp < kWSoftWarps) {
     // ================================================================ softmax warps
