@@ -153,11 +153,11 @@ __host__ __device__ inline RowTileKeys row_tile_keys(int t, int n_rows, int grou
   return r;
 }
 
-// Whether a row tile's x-th scores, two tiles ahead, are made before the values at hand: not where they wait for those (two
-// score tiles) or for new queries.
+// Whether the scores of tile fs, the x-th of its row tile, come before the values of tile f: two tiles ahead, where they wait neither
+// for those values (two score tiles) nor for new queries; one tile ahead always.
 template <int D>
-__device__ __forceinline__ bool scores_first(int x) {
-  return Pw<D>::kScoreBufs > 2 && x != 0;
+__device__ __forceinline__ bool scores_next(int fs, int f, int n_tiles, int x) {
+  return fs < n_tiles && fs < f + 2 + (Pw<D>::kScoreBufs > 2 && x != 0);
 }
 
 // Place on the line: KV head, row tile, key tile x of its n.
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           }
           // hidden keys: a row at position p sees n < hi, and n >= lo or n < sk, counted from the first of these keys
           const int k0 = kk + 32 * k, sk = a.n_sink - k0, hi0 = a.history_len + q0 + 1 - k0;
-          if (hi0 < 32 || (a.history_len + query(31) + 1 - a.window > k0 && sk < 32)) {  // the same in the warp
+          if (__builtin_expect(hi0 < 32 || (a.history_len + query(31) + 1 - a.window > k0 && sk < 32), 0)) {  // the same in the warp
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int hi = a.history_len + query(frag_row(lane, j)) + 1 - k0;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
             now[j] = refs[quad * 32 + frag_row(lane, j)];
             moved |= now[j] != ref[j] || m[j] > now[j] + kWLazy;
           }
-          if (!__any_sync(0xffffffffu, moved)) {
+          if (__builtin_expect(!__any_sync(0xffffffffu, moved), 1)) {
             arrive(L::decided + 4 * group + quad);
           } else {
             // the other group has moved a reference, or this tile does
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
             pair_or(pair_id, false);  // both have read the references
             if (part == 0) refs[quad * 32 + frag_row(lane, c)] = pick(ref);
             arrive(L::decided + 4 * group + quad);
-            if (__any_sync(0xffffffffu, moved)) {
+            if (__builtin_expect(__any_sync(0xffffffffu, moved), 0)) {
               // O holds the products up to tile f - 1 (of this unit: u > 0); half of its columns
               await(L::pvDone + (f - 1) % L::kScoreBufs, ((f - 1) / L::kScoreBufs) & 1);
               tc::fence_after_sync();
@@ -716,13 +716,9 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       window_step(a, w);
     };
     // The scores run two tiles ahead of the values: beside tile f's weights, tile f + 1 is with the other group.
-    scores();
-    if (ok && n_tiles > 1) scores();
-    for (int f = 0; ok && f < n_tiles; ++f) {
-      const bool early = scores_first<D>(ws.x);
-      if (early && fs < n_tiles) scores();
-      if (ok) values(f);
-      if (ok && !early && fs < n_tiles) scores();
+    for (int f = 0; ok && f < n_tiles;) {
+      if (scores_next<D>(fs, f, n_tiles, ws.x)) scores();
+      else values(f++);
     }
     // every MMA this warp issued has completed before the CTA releases tensor memory
     if (elect_one()) {
@@ -770,21 +766,14 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       // in the order of the products
       WindowWalk wk = w;
       int fk = 0;
-      auto push_k = [&]() {
-        const long long u = static_cast<long long>(wk.kvh) * a.key_tiles + stored_tile(a, wk.tile());
-        push_par(u);
-        if (ok) push(a.k_tiles + u * (D * 256));
-        ++fk;
-        window_step(a, wk);
-      };
-      push_k();
-      if (ok && n_tiles > 1) push_k();
-      for (int f = 0; ok && f < n_tiles; ++f) {
-        const bool early = scores_first<D>(wk.x);
-        if (early && fk < n_tiles) push_k();
-        if (ok) push(a.v_tiles + (static_cast<long long>(w.kvh) * a.key_tiles + stored_tile(a, w.tile())) * (D * 256));
-        window_step(a, w);
-        if (ok && !early && fk < n_tiles) push_k();
+      for (int f = 0; ok && f < n_tiles;) {
+        const bool is_k = scores_next<D>(fk, f, n_tiles, wk.x);
+        WindowWalk& at = is_k ? wk : w;
+        const long long u = static_cast<long long>(at.kvh) * a.key_tiles + stored_tile(a, at.tile());
+        if (is_k) push_par(u);
+        if (ok) push((is_k ? a.k_tiles : a.v_tiles) + u * (D * 256));
+        ++(is_k ? fk : f);
+        window_step(a, at);
       }
       // copies still in flight (only after an abort) land before the CTA exits; of a tile cut short, those that it has
       for (int p = fills % NP; p != 0 && p < NP; ++p) mbar_arrive(&bars[L::full + slot / NP]);
@@ -808,7 +797,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       const uint16_t* src = static_cast<const uint16_t*>(a.q) +
                             (static_cast<long long>(q0) * a.n_q_heads + w.kvh * a.group) * D + 8 * ch;
       uint8_t* dst = sm + (ch >> 3) * kPieceBytes;
-#pragma unroll 8
+#pragma unroll 4
       for (int n = t0 / CH; n < 128; n += ROWS) {
         const int q = small_div(g0 + n, a.group_inv), g = g0 + n - q * a.group;
         const bool real = n < rows;
