@@ -53,19 +53,18 @@ constexpr float kWMinScale = 7.8886091e-31f;  // 2^-100
 
 template <int D>
 struct Pw {
-  static constexpr int kSlots = D == 256 ? 8 : 10;           // pieces in the ring
+  static constexpr int kHalf = D * 128;                      // bytes of half a K tile (of its dims) or V tile (of its keys)
+  static constexpr int kTiles = D == 256 ? 2 : 5;            // K or V tiles in the ring
   static constexpr int kScoreBufs = D == 256 ? 2 : 3;        // score tiles
   static constexpr int kQBytes = 128 * D * 2;                // Q in pieces of 16 KB
   static constexpr int offRing = kQBytes;
-  static constexpr int offPar = offRing + kSlots * kPieceBytes;    // [buf][3][128] fp32
+  static constexpr int offPar = offRing + 2 * kTiles * kHalf;      // [buf][3][128] fp32
   static constexpr int offRef = offPar + kWParBufs * 3 * 128 * 4;  // [128] the rows' references
   static constexpr int offRed = offRef + 128 * 4;            // [maximum, sum][group][half of the keys][128] a row's two warps
   static constexpr int offSum = offRed + 2 * 2 * 2 * 128 * 4;    // [2][sum, sum, reference][128] what a unit's other group leaves
   static constexpr int offBar = offSum + 2 * 3 * 128 * 4;
-  static constexpr int kTiles = kSlots / (D / 64);           // K or V tiles in the ring
-  static_assert(kSlots % (D / 64) == 0, "whole tiles");
-  // barriers: of the ring's tiles, its pieces, ..; a score buffer's tiles have theirs
-  static constexpr int full = 0, empty = full + kTiles, parFull = empty + kSlots, parFree = parFull + kWParBufs,
+  // barriers: of the ring's tiles, their halves, ..; a score buffer's tiles have theirs
+  static constexpr int full = 0, empty = full + kTiles, parFull = empty + 2 * kTiles, parFree = parFull + kWParBufs,
                        sFull = parFree + kWParBufs, pFull = sFull + kScoreBufs, pvDone = pFull + kScoreBufs, decided = pvDone + kScoreBufs,
                        sumReady = decided + 8, qFull = sumReady + 8, qFree = qFull + 1, oFree = qFree + 1,
                        drain = oFree + 1, kNumBars = drain + 1;
@@ -307,7 +306,6 @@ __global__ void __launch_bounds__(256) window_tiles_kernel(const __grid_constant
 template <int D>
 __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __grid_constant__ PrefillWindowArgs a) {
   using L = Pw<D>;
-  constexpr int NP = D / 64;  // pieces of a K or V tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint8_t* ring = sm + L::offRing;
@@ -327,8 +325,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
 
   if (warp == kWMmaWarp) tc::tmem_alloc(tmem_slot, L::kTmemCols);
   if (tid == 0) {
-    for (int s = 0; s < L::kTiles; ++s) mbar_init(&bars[L::full + s], NP);
-    for (int s = 0; s < L::kSlots; ++s) mbar_init(&bars[L::empty + s], 1);
+    for (int s = 0; s < L::kTiles; ++s) mbar_init(&bars[L::full + s], 2);
+    for (int s = 0; s < 2 * L::kTiles; ++s) mbar_init(&bars[L::empty + s], 1);
     for (int s = 0; s < kWParBufs; ++s) {
       mbar_init(&bars[L::parFull + s], 1);
       mbar_init(&bars[L::parFree + s], 8);
@@ -662,7 +660,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     WindowWalk ws = w;  // of the scores
     int fs = 0, s_unit = -1;
     auto scores = [&]() {
-      const int b = fs % L::kScoreBufs, slot = tile % L::kTiles * NP;
+      const int b = fs % L::kScoreBufs, slot = tile % L::kTiles * 2;
       if (!await_tile()) return;
       if (fs == 0 || ws.x == 0) {
         ++s_unit;
@@ -673,12 +671,15 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       if (elect_one()) {
         tc::fence_after_sync();
 #pragma unroll
-        for (int qa = 0; qa < NP; ++qa) {
-          const uint64_t kd = rd0 + static_cast<uint64_t>(((slot + qa) * kPieceBytes) >> 4);
-          const uint64_t qd = qd0 + static_cast<uint64_t>((qa * kPieceBytes) >> 4);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) tc::mma_f16_ss(tmem + 128 * b, qd + 2 * s, kd + 2 * s, idesc_qk, (qa | s) ? 1u : 0u);
-          tc::commit(&bars[L::empty + slot + qa]);
+          for (int i = 0; i < D / 128; ++i) {  // 64 dims
+            const uint64_t kd = rd0 + static_cast<uint64_t>(((slot + h) * L::kHalf + i * kPieceBytes) >> 4);
+            const uint64_t qd = qd0 + static_cast<uint64_t>((h * L::kHalf + i * kPieceBytes) >> 4);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) tc::mma_f16_ss(tmem + 128 * b, qd + 2 * s, kd + 2 * s, idesc_qk, (h | i | s) ? 1u : 0u);
+          }
+          tc::commit(&bars[L::empty + slot + h]);
         }
         tc::commit(&bars[L::sFull + b]);
         if (last) tc::commit(&bars[L::qFree]);
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     };
     int v_unit = -1;
     auto values = [&](int f) {  // O (+)= P_f V_f
-      const int b = f % L::kScoreBufs, slot = tile % L::kTiles * NP;
+      const int b = f % L::kScoreBufs, slot = tile % L::kTiles * 2;
       const bool first = f == 0 || w.x == 0;
       if (!await_tile()) return;
       if (first) ++v_unit;
@@ -700,14 +701,12 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         tc::fence_after_sync();
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh) {
-          const int s0 = slot + kh * (D / 128);
-          const uint64_t vd = rd0 + static_cast<uint64_t>((s0 * kPieceBytes) >> 4);
+          const uint64_t vd = rd0 + static_cast<uint64_t>(((slot + kh) * L::kHalf) >> 4);
 #pragma unroll
           for (int s = 0; s < 4; ++s)
             tc::mma_f16_ts(tmem + L::kOCol, tmem + 128 * b + 64 * kh + 8 * s, vd + 2 * s, idesc_pv,
                            (first && kh == 0 && s == 0) ? 0u : 1u);
-#pragma unroll
-          for (int dh = 0; dh < D / 128; ++dh) tc::commit(&bars[L::empty + s0 + dh]);
+          tc::commit(&bars[L::empty + slot + kh]);
         }
         tc::commit(&bars[L::pvDone + b]);
       }
@@ -727,60 +726,56 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     }
     __syncwarp();
   } else if (warp == kWCopyWarp) {
-    // ================================================================ tile copies
-    if (lane == 0) {
-      grid_dep_wait();
-      grid_dep_trigger();
-      int slot = 0, fills = 0, par_fills = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      const bool skip_one = a.fault == 5 && blockIdx.x == 0;  // test-only: the second tile is never copied
-      auto push = [&](const uint8_t* src) {
-        for (int i = 0; i < NP; ++i) {
-          if (fills >= L::kSlots && !wait_on(&bars[L::empty + slot], ph ^ 1u, abort_flag, a.wait_budget)) {
-            ok = false;
-            return;
-          }
-          if (!(skip_one && fills / NP == 1)) {
-            mbar_arrive_expect_tx(&bars[L::full + slot / NP], kPieceBytes);
-            bulk_g2s(ring + slot * kPieceBytes, src + i * kPieceBytes, kPieceBytes, &bars[L::full + slot / NP]);
-          }
-          ++fills;
-          if (++slot == L::kSlots) {
-            slot = 0;
-            ph ^= 1u;
-          }
+    // ================================================================ tile copies, in the order of the products
+    grid_dep_wait();
+    grid_dep_trigger();
+    const bool skip_one = a.fault == 5 && blockIdx.x == 0;  // test-only: the second tile is never copied
+    WindowWalk wk = w;                                      // of the scores
+    int tile = 0, fk = 0, cut = 0;
+    bool ok = true;
+    auto await = [&](int bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, wait_on(&bars[bar], parity, abort_flag, a.wait_budget));
+      return ok;
+    };
+    for (int f = 0; ok && f < n_tiles; ++tile) {
+      const bool is_k = scores_next<D>(fk, f, n_tiles, wk.x);
+      WindowWalk& at = is_k ? wk : w;
+      const long long u = static_cast<long long>(at.kvh) * a.key_tiles + stored_tile(a, at.tile());
+      window_step(a, at);
+      if (is_k) {
+        const int pb = fk % kWParBufs;
+        if (fk >= kWParBufs && !await(L::parFree + pb, (fk / kWParBufs - 1) & 1)) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bars[L::parFull + pb], 1536);
+          bulk_g2s(par + pb * 384, a.par + u * 384, 1536, &bars[L::parFull + pb]);
         }
-      };
-      auto push_par = [&](long long u) {
-        const int pb = par_fills % kWParBufs;
-        if (par_fills >= kWParBufs &&
-            !wait_on(&bars[L::parFree + pb], (par_fills / kWParBufs - 1) & 1, abort_flag, a.wait_budget)) {
-          ok = false;
-          return;
-        }
-        mbar_arrive_expect_tx(&bars[L::parFull + pb], 1536);
-        bulk_g2s(par + pb * 384, a.par + u * 384, 1536, &bars[L::parFull + pb]);
-        ++par_fills;
-      };
-      // in the order of the products
-      WindowWalk wk = w;
-      int fk = 0;
-      for (int f = 0; ok && f < n_tiles;) {
-        const bool is_k = scores_next<D>(fk, f, n_tiles, wk.x);
-        WindowWalk& at = is_k ? wk : w;
-        const long long u = static_cast<long long>(at.kvh) * a.key_tiles + stored_tile(a, at.tile());
-        if (is_k) push_par(u);
-        if (ok) push((is_k ? a.k_tiles : a.v_tiles) + u * (D * 256));
-        ++(is_k ? fk : f);
-        window_step(a, at);
+        __syncwarp();
+        ++fk;
+      } else {
+        ++f;
       }
-      // copies still in flight (only after an abort) land before the CTA exits; of a tile cut short, those that it has
-      for (int p = fills % NP; p != 0 && p < NP; ++p) mbar_arrive(&bars[L::full + slot / NP]);
-      const int tiles = (fills + NP - 1) / NP;
-      for (int i = max(0, tiles - L::kTiles); i < tiles; ++i)
+      const uint8_t* src = (is_k ? a.k_tiles : a.v_tiles) + u * (2 * L::kHalf);
+      const int slot = tile % L::kTiles * 2;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (tile >= L::kTiles && !await(L::empty + slot + h, (tile / L::kTiles - 1) & 1)) {
+          cut = h;  // the tile has one half
+          break;
+        }
+        if (!(skip_one && tile == 1) && elect_one()) {
+          mbar_arrive_expect_tx(&bars[L::full + slot / 2], L::kHalf);
+          bulk_g2s(ring + (slot + h) * L::kHalf, src + h * L::kHalf, L::kHalf, &bars[L::full + slot / 2]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    // Copies still in flight (only after an abort) land before the CTA exits, those of a tile cut short too.
+    if (lane == 0) {
+      if (cut) mbar_arrive(&bars[L::full + tile++ % L::kTiles]);
+      for (int i = max(0, tile - L::kTiles); i < tile; ++i)
         if (!(skip_one && i == 1)) mbar_wait(&bars[L::full + i % L::kTiles], (i / L::kTiles) & 1, a.status, a.wait_budget);
-      for (int i = max(0, par_fills - kWParBufs); i < par_fills; ++i)
+      for (int i = max(0, fk - kWParBufs); i < fk; ++i)
         mbar_wait(&bars[L::parFull + i % kWParBufs], (i / kWParBufs) & 1, a.status, a.wait_budget);
     }
     __syncwarp();
