@@ -713,10 +713,11 @@ def kvq_decode_step_window_int8kv(cache, k_new, v_new, q, block_table, ctx_lens,
     ctx_p = _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
     n_blocks = block_table.shape[-1]
     table_p = _need(fn, "block_table", block_table, torch.int32, (B, n_blocks), dev)
-    o = _decode_opts(split_rows, 0, force_route, stage1_events, launches)
+    plain = not (split_rows or force_route or stage1_events or launches is not None)
+    o = None if plain else ctypes.byref(_decode_opts(split_rows, 0, force_route, stage1_events, launches))
     ws_p, wbytes = None, 0
     if workspace is None:
-        need = int(lib().kvq_step_window_workspace_bytes(B, nq, Hq, H, int(max_ctx), int(window), int(n_sink), D, ctypes.byref(o)))
+        need = int(lib().kvq_step_window_workspace_bytes(B, nq, Hq, H, int(max_ctx), int(window), int(n_sink), D, o))
         if need:
             workspace = _empty(need, torch.uint8, cache.k.device, stream)
     if workspace is not None:
@@ -724,7 +725,7 @@ def kvq_decode_step_window_int8kv(cache, k_new, v_new, q, block_table, ctx_lens,
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_decode_step_window_int8kv(
         ctypes.byref(c), k_p, v_p, q_p, B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx), float(softmax_scale), int(window),
-        int(n_sink), out_p, ws_p, wbytes, ctypes.byref(o), _stream(stream)))
+        int(n_sink), out_p, ws_p, wbytes, o, _stream(stream)))
     return ret
 
 
