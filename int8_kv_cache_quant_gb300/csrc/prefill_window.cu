@@ -59,15 +59,12 @@ struct Pw {
   static constexpr int kQBytes = 128 * D * 2;                // Q in pieces of 16 KB
   static constexpr int offRing = kQBytes;
   static constexpr int offPar = offRing + 2 * kTiles * kHalf;      // [buf][3][128] fp32
-  static constexpr int offRef = offPar + kWParBufs * 3 * 128 * 4;  // [128] the rows' references
-  static constexpr int offRed = offRef + 128 * 4;            // [maximum, sum][group][half of the keys][128] a row's two warps
-  static constexpr int offSum = offRed + 2 * 2 * 2 * 128 * 4;    // [2][sum, sum, reference][128] what a unit's other group leaves
-  static constexpr int offBar = offSum + 2 * 3 * 128 * 4;
+  static constexpr int offRed = offPar + kWParBufs * 3 * 128 * 4;  // [maximum, sum][quarter of the keys][128] a row's four warps
+  static constexpr int offBar = offRed + 2 * 4 * 128 * 4;
   // barriers: of the ring's tiles, their halves, ..; a score buffer's tiles have theirs
   static constexpr int full = 0, empty = full + kTiles, parFull = empty + 2 * kTiles, parFree = parFull + kWParBufs,
-                       sFull = parFree + kWParBufs, pFull = sFull + kScoreBufs, pvDone = pFull + kScoreBufs, decided = pvDone + kScoreBufs,
-                       sumReady = decided + 8, qFull = sumReady + 8, qFree = qFull + 1, oFree = qFree + 1,
-                       drain = oFree + 1, kNumBars = drain + 1;
+                       sFull = parFree + kWParBufs, pFull = sFull + kScoreBufs, pvDone = pFull + kScoreBufs, qFull = pvDone + kScoreBufs,
+                       qFree = qFull + 1, oFree = qFree + 1, drain = oFree + 1, kNumBars = drain + 1;
   static constexpr int offFlag = offBar + kNumBars * 8;      // abort flag, TMEM base
   static constexpr int kAlloc = offFlag + 16 + 1024;
   // Tensor memory: score tiles and O.  A P tile takes its score tile's place, the first and second half of the keys each
@@ -78,11 +75,11 @@ struct Pw {
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
-// A barrier of two warps that gives them the OR of `pred`: they take the same way.
-__device__ __forceinline__ bool pair_or(int id, bool pred) {
+// A barrier of four warps that gives them the OR of `pred`: they take the same way.
+__device__ __forceinline__ bool rows_or(int id, bool pred) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 64, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(r)
       : "r"(pred ? 1u : 0u), "r"(id)
       : "memory");
@@ -152,11 +149,11 @@ __host__ __device__ inline RowTileKeys row_tile_keys(int t, int n_rows, int grou
   return r;
 }
 
-// Whether the scores of tile fs, the x-th of its row tile, come before the values of tile f: two tiles ahead, where they wait neither
-// for those values (two score tiles) nor for new queries; one tile ahead always.
+// Whether the scores of tile fs, the x-th of its row tile, come before the values of tile f: a tile ahead, two with three score
+// tiles, but none where they wait for new queries, since a row tile's result waits for the values.
 template <int D>
 __device__ __forceinline__ bool scores_next(int fs, int f, int n_tiles, int x) {
-  return fs < n_tiles && fs < f + 2 + (Pw<D>::kScoreBufs > 2 && x != 0);
+  return fs < n_tiles && fs < f + (x == 0 ? 1 : 2 + (Pw<D>::kScoreBufs > 2));
 }
 
 // Place on the line: KV head, row tile, key tile x of its n.
@@ -310,9 +307,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
   uint8_t* sm = align1024(smem_raw);
   uint8_t* ring = sm + L::offRing;
   float* par = reinterpret_cast<float*>(sm + L::offPar);
-  float* refs = reinterpret_cast<float*>(sm + L::offRef);
   float* red = reinterpret_cast<float*>(sm + L::offRed);
-  float* sums = reinterpret_cast<float*>(sm + L::offSum);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::offBar);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::offFlag);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::offFlag + 4);
@@ -329,20 +324,16 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     for (int s = 0; s < 2 * L::kTiles; ++s) mbar_init(&bars[L::empty + s], 1);
     for (int s = 0; s < kWParBufs; ++s) {
       mbar_init(&bars[L::parFull + s], 1);
-      mbar_init(&bars[L::parFree + s], 8);
+      mbar_init(&bars[L::parFree + s], kWSoftWarps);
     }
     for (int s = 0; s < L::kScoreBufs; ++s) {
       mbar_init(&bars[L::sFull + s], 1);
-      mbar_init(&bars[L::pFull + s], 8);
+      mbar_init(&bars[L::pFull + s], kWSoftWarps);
       mbar_init(&bars[L::pvDone + s], 1);
-    }
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(&bars[L::decided + s], 2);
-      mbar_init(&bars[L::sumReady + s], 2);
     }
     mbar_init(&bars[L::qFull], kWQWarps);
     mbar_init(&bars[L::qFree], 1);
-    mbar_init(&bars[L::oFree], 8);
+    mbar_init(&bars[L::oFree], kWSoftWarps);
     mbar_init(&bars[L::drain], 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -354,8 +345,9 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
 
   if (warp < kWSoftWarps) {
     // ================================================================ softmax warps
-    // Two groups of eight warps take turns at the tiles; of a group a warp has the rows 32 quad .. and half of the keys.
-    const int quad = warp & 3, part = (warp >> 2) & 1, group = warp >> 3, c = lane & 3, pair_id = 1 + 4 * group + quad;
+    // A warp has the rows 32 quad .. and a quarter of a tile's keys, 32: a thread four rows, frag_row(lane, j), and eight keys,
+    // 8 i + 2 c and the one after it.
+    const int quad = warp & 3, part = warp >> 2, c = lane & 3, rows_id = 1 + quad;
     const uint32_t lanes0 = static_cast<uint32_t>(quad * 32) << 16, lanes1 = lanes0 + (16u << 16);
     bool failed = false;
     auto await = [&](int bar, uint32_t parity) {
@@ -366,6 +358,11 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       if (lane == 0) mbar_arrive(&bars[bar]);
     };
     auto pick = [&](const float (&x)[4]) { return c < 2 ? (c == 0 ? x[0] : x[1]) : (c == 2 ? x[2] : x[3]); };  // x[c]
+    float* red_max = red + quad * 32 + frag_row(lane, c);  // of a row of the thread's; its quarters 128 apart
+    auto all_max = [&](int j) {                            // of the four warps
+      const float* r = red + quad * 32 + frag_row(lane, j);
+      return fmaxf(fmaxf(r[0], r[128]), fmaxf(r[256], r[384]));
+    };
     grid_dep_wait();  // the tiles come from the kernel before
     grid_dep_trigger();
     float2* ml = a.part_ml + static_cast<long long>(run) * 256;
@@ -373,12 +370,11 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       ml[quad * 32 + lane] = make_float2(-INFINITY, -1.0f);
       ml[128 + quad * 32 + lane] = make_float2(-INFINITY, -1.0f);
     }
-    int f_unit = 0, left_sums = 0;
+    int f_unit = 0;
     while (f_unit < n_tiles) {
-      // ---- a unit: the key tiles of row tile w.t that belong to this run.  The thread has four rows, frag_row(lane, j).
+      // ---- a unit: the key tiles of row tile w.t that belong to this run
       const int n_unit = min(w.keys.n - w.x, n_tiles - f_unit);
       const bool whole_unit = w.x == 0 && n_unit == w.keys.n;
-      const bool ends_it = ((f_unit + n_unit - 1) & 1) == group;  // this group has the unit's last tile, and writes its result
       const int r0 = 128 * w.t + quad * 32, q0 = r0 / a.group, g0 = r0 - q0 * a.group;  // the warp's first row: query, head
       auto query = [&](int row) { return q0 + small_div(g0 + row, a.group_inv); };       // of the warp's row
       float ref[4];
@@ -388,163 +384,127 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         ref[j] = -INFINITY;
         l[j] = mk2(0.f, 0.f);
       }
-      for (int u = (f_unit & 1) == group ? 0 : 1; u < n_unit; u += 2) {
-        const int f = f_unit + u, pb = f % kWParBufs, x = w.x + u;
-        const int kk = 128 * (x < w.keys.sink ? x : x - w.keys.sink + w.keys.low) + 64 * part;  // the warp's first key
-        const int sb = f % L::kScoreBufs;
-        const uint32_t tm_s = tmem + 128 * sb + 64 * part;
-        const float2* kf = reinterpret_cast<const float2*>(par + pb * 384 + 64 * part) + c;
+      for (int u = 0; u < n_unit; ++u) {
+        const int f = f_unit + u, pb = f % kWParBufs, x = w.x + u, sb = f % L::kScoreBufs;
+        const int k0 = 128 * (x < w.keys.sink ? x : x - w.keys.sink + w.keys.low) + 32 * part;  // the warp's first key
+        const uint32_t tm_s = tmem + 128 * sb + 32 * part, tm_p = tmem + 128 * sb + 16 * part;
+        const float2* kf = reinterpret_cast<const float2*>(par + pb * 384 + 32 * part) + c;
         await(L::parFull + pb, (f / kWParBufs) & 1);
         await(L::sFull + sb, (f / L::kScoreBufs) & 1);
         tc::fence_after_sync();
-        // The scores pass through registers 32 keys at a time, and twice: first they become z, with a row's maximum, and go
-        // back.  Loops of few instructions, and many warps at them: a tile unrolled in registers came out of the
-        // instruction caches at a third of the speed.
-        float m[4];
+        uint32_t y[32];
+        tc::ld_16x256b_x4(tm_s + lanes0, y);
+        tc::ld_16x256b_x4(tm_s + lanes1, y + 16);
+        tc::wait_ld();
+        // z
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m[j] = -INFINITY;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          uint32_t y[32];
-          tc::ld_16x256b_x4(tm_s + lanes0 + 32 * k, y);
-          tc::ld_16x256b_x4(tm_s + lanes1 + 32 * k, y + 16);
-          tc::wait_ld();
-          // z of the four rows' keys 8 i + 2 c (and the one after it)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 k2 = kf[16 * k + 4 * i], l2 = kf[64 + 16 * k + 4 * i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
-              const f2 z = fma2(mk2(__uint_as_float(s[0]), __uint_as_float(s[1])), mk2(k2.x, k2.y), mk2(l2.x, l2.y));
-              s[0] = __float_as_uint(lo2(z));
-              s[1] = __float_as_uint(hi2(z));
-            }
-          }
-          // hidden keys: a row at position p sees n < hi, and n >= lo or n < sk, counted from the first of these keys
-          const int k0 = kk + 32 * k, sk = a.n_sink - k0, hi0 = a.history_len + q0 + 1 - k0;
-          if (__builtin_expect(hi0 < 32 || (a.history_len + query(31) + 1 - a.window > k0 && sk < 32), 0)) {  // the same in the warp
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int hi = a.history_len + query(frag_row(lane, j)) + 1 - k0;
-              const uint32_t seen = (low_bits(hi) & (low_bits(sk) | ~low_bits(hi - a.window))) >> (2 * c);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (!(seen & (1u << (8 * (e >> 1) + (e & 1)))))
-                  y[(j >> 1) * 16 + 4 * (e >> 1) + 2 * (j & 1) + (e & 1)] = 0xff800000u;  // -infinity
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
-              m[j] = fmax3(m[j], __uint_as_float(s[0]), __uint_as_float(s[1]));
-            }
-          tc::st_16x256b_x4(tm_s + lanes0 + 32 * k, y);
-          tc::st_16x256b_x4(tm_s + lanes1 + 32 * k, y + 16);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 1));
-          m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 2));
-        }
-        float* mine = red + (2 * group + part) * 128 + quad * 32;
-        const float* others = red + (2 * group + (part ^ 1)) * 128 + quad * 32;
-        mine[frag_row(lane, c)] = pick(m);
-        tc::wait_st();
-        if (pair_or(pair_id, failed)) {
-          failed = true;
-          break;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], others[frag_row(lane, j)]);
-        // The rows' references, decided tile by tile: the other group's warp with these rows has decided for the tile before.
-        if (f > 0) await(L::decided + 4 * (group ^ 1) + quad, ((f - 1) >> 1) & 1);
-        bool moved = false;
-        if (u == 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) ref[j] = m[j];
-          if (part == 0) refs[quad * 32 + frag_row(lane, c)] = pick(ref);
-          arrive(L::decided + 4 * group + quad);
-        } else {
-          float now[4];
+        for (int i = 0; i < 4; ++i) {
+          const float2 k2 = kf[4 * i], l2 = kf[64 + 4 * i];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            now[j] = refs[quad * 32 + frag_row(lane, j)];
-            moved |= now[j] != ref[j] || m[j] > now[j] + kWLazy;
-          }
-          if (__builtin_expect(!__any_sync(0xffffffffu, moved), 1)) {
-            arrive(L::decided + 4 * group + quad);
-          } else {
-            // the other group has moved a reference, or this tile does
-            float scale[4];
-            moved = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // (from -infinity there is nothing in l, but NaN, which stays)
-              const float s = ref[j] == now[j] || ref[j] == -INFINITY ? 1.0f : fast_exp2(ref[j] - now[j]);
-              ref[j] = now[j];
-              scale[j] = 1.0f;
-              if (m[j] > now[j] + kWLazy) {
-                scale[j] = now[j] == -INFINITY ? 0.0f : fast_exp2(now[j] - m[j]);
-                ref[j] = m[j];
-                moved = true;
-              }
-              l[j] = mul2(l[j], mk2(s * scale[j], s * scale[j]));
-            }
-            pair_or(pair_id, false);  // both have read the references
-            if (part == 0) refs[quad * 32 + frag_row(lane, c)] = pick(ref);
-            arrive(L::decided + 4 * group + quad);
-            if (__builtin_expect(__any_sync(0xffffffffu, moved), 0)) {
-              // O holds the products up to tile f - 1 (of this unit: u > 0); half of its columns
-              await(L::pvDone + (f - 1) % L::kScoreBufs, ((f - 1) / L::kScoreBufs) & 1);
-              tc::fence_after_sync();
-#pragma unroll 1
-              for (int o = 0; o < D / 32; ++o) {  // 16 lanes, 32 columns
-                const uint32_t at = tmem + (o & 1 ? lanes1 : lanes0) + L::kOCol + part * (D / 2) + 32 * (o >> 1);
-                const float sa = o & 1 ? scale[2] : scale[0], sb = o & 1 ? scale[3] : scale[1];
-                uint32_t y[16];
-                tc::ld_16x256b_x4(at, y);
-                tc::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * (e & 2 ? sb : sa));
-                tc::st_16x256b_x4(at, y);
-              }
-            }
+            uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
+            const f2 z = fma2(mk2(__uint_as_float(s[0]), __uint_as_float(s[1])), mk2(k2.x, k2.y), mk2(l2.x, l2.y));
+            s[0] = __float_as_uint(lo2(z));
+            s[1] = __float_as_uint(hi2(z));
           }
         }
-        float nr[4];
+        // hidden keys: a row at position p sees n < hi, and n >= lo or n < sk, counted from the first of these keys
+        const int sk = a.n_sink - k0, hi0 = a.history_len + q0 + 1 - k0;
+        if (__builtin_expect(hi0 < 32 || (a.history_len + query(31) + 1 - a.window > k0 && sk < 32), 0)) {  // the same in the warp
 #pragma unroll
-        for (int j = 0; j < 4; ++j) nr[j] = ref[j] == -INFINITY ? 0.0f : -ref[j];
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          uint32_t y[32], p0[8], p1[8];
-          tc::ld_16x256b_x4(tm_s + lanes0 + 32 * k, y);
-          tc::ld_16x256b_x4(tm_s + lanes1 + 32 * k, y + 16);
-          tc::wait_ld();
+          for (int j = 0; j < 4; ++j) {
+            const int hi = a.history_len + query(frag_row(lane, j)) + 1 - k0;
+            const uint32_t seen = (low_bits(hi) & (low_bits(sk) | ~low_bits(hi - a.window))) >> (2 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (!(seen & (1u << (8 * (e >> 1) + (e & 1)))))
+                y[(j >> 1) * 16 + 4 * (e >> 1) + 2 * (j & 1) + (e & 1)] = 0xff800000u;  // -infinity
+          }
+        }
+        float m[4];
+        bool over = failed || u == 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          m[j] = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 i2 = kf[128 + 16 * k + 4 * i];
+            const uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
+            m[j] = fmax3(m[j], __uint_as_float(s[0]), __uint_as_float(s[1]));
+          }
+          over |= m[j] > ref[j] + kWLazy;
+        }
+        // All scores are in registers, and P may take their place; and does a row's maximum exceed its reference?
+        tc::fence_before_sync();
+        over = rows_or(rows_id, over);
+        tc::fence_after_sync();
+        if (__builtin_expect(over, 0)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
-              const f2 v = add2(mk2(__uint_as_float(s[0]), __uint_as_float(s[1])), mk2(nr[j], nr[j]));
-              const float w0 = fast_exp2(lo2(v)), w1 = fast_exp2(hi2(v));
-              l[j] = fma2(mk2(w0, w1), mk2(i2.x, i2.y), l[j]);
-              (j < 2 ? p0 : p1)[2 * i + (j & 1)] = pack_half2(w0, w1);
+          for (int j = 0; j < 4; ++j) {
+            m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 1));
+            m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 2));
+          }
+          red_max[128 * part] = pick(m);
+          if (rows_or(rows_id, failed)) {
+            failed = true;
+            break;
+          }
+          bool moved = false;
+          float scale[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            m[j] = all_max(j);
+            scale[j] = 1.0f;
+            if (u == 0 || m[j] > ref[j] + kWLazy) {
+              // (from -infinity there is nothing in l and O, but NaN, which stays)
+              if (ref[j] != -INFINITY) {
+                scale[j] = fast_exp2(ref[j] - m[j]);
+                moved = true;
+              }
+              ref[j] = m[j];
+              l[j] = mul2(l[j], mk2(scale[j], scale[j]));
             }
           }
-          tc::st_16x128b_x4(tm_s + lanes0 + 16 * k, p0);  // where scores were that have been taken
-          tc::st_16x128b_x4(tm_s + lanes1 + 16 * k, p1);
+          rows_or(rows_id, false);  // the maxima are read
+          if (__any_sync(0xffffffffu, moved)) {
+            // O holds the products up to tile f - 1 (of this unit: u > 0); a quarter of its columns
+            await(L::pvDone + (f - 1) % L::kScoreBufs, ((f - 1) / L::kScoreBufs) & 1);
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int o = 0; o < D / 64; ++o) {  // 16 lanes, 32 columns
+              const uint32_t at = tmem + (o & 1 ? lanes1 : lanes0) + L::kOCol + part * (D / 4) + 32 * (o >> 1);
+              const float sa = o & 1 ? scale[2] : scale[0], sb2 = o & 1 ? scale[3] : scale[1];
+              uint32_t t[16];
+              tc::ld_16x256b_x4(at, t);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * (e & 2 ? sb2 : sa));
+              tc::st_16x256b_x4(at, t);
+            }
+          }
         }
+        uint32_t p0[8], p1[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 i2 = kf[128 + 4 * i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
+            const float nr = ref[j] == -INFINITY ? 0.0f : -ref[j];
+            const f2 v = add2(mk2(__uint_as_float(s[0]), __uint_as_float(s[1])), mk2(nr, nr));
+            const float w0 = fast_exp2(lo2(v)), w1 = fast_exp2(hi2(v));
+            l[j] = fma2(mk2(w0, w1), mk2(i2.x, i2.y), l[j]);
+            (j < 2 ? p0 : p1)[2 * i + (j & 1)] = pack_half2(w0, w1);
+          }
+        }
+        tc::st_16x128b_x4(tm_p + lanes0, p0);
+        tc::st_16x128b_x4(tm_p + lanes1, p1);
         arrive(L::parFree + pb);
         tc::wait_st();
         tc::fence_before_sync();
         arrive(L::pFull + sb);
       }
-      if (pair_or(pair_id, failed)) break;
-      // ---- the unit's sums: this warp's
+      if (rows_or(rows_id, failed)) break;
+      // ---- the unit's sums: this warp's, then all four's
       float sum[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -552,88 +512,69 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
         sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
       }
-      float* left = sums + (left_sums & 1) * 384 + quad * 32;
-      if (!ends_it) {
-        if (n_unit > 1) {
-          // left for the group that has the last tile, which may still have the sums before these to take: two places, two
-          // barriers (the ones before those it took before it decided for its tile of the row tile between)
-          left[128 * part + frag_row(lane, c)] = pick(sum);
-          if (part == 0) left[256 + frag_row(lane, c)] = pick(ref);
-          arrive(L::sumReady + 4 * (left_sums & 1) + quad);
+      red_max[512 + 128 * part] = pick(sum);
+      rows_or(rows_id, false);
+      const int slot = 2 * run + (f_unit == 0 ? 0 : 1);
+      float inv[4];
+      int at_row[4];  // where the thread's rows stand in the output, from its query's first on
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = frag_row(lane, j), qs = small_div(g0 + row, a.group_inv);
+        const float* r = red + 512 + quad * 32 + row;
+        sum[j] = (r[0] + r[128]) + (r[256] + r[384]);
+        inv[j] = sum[j] > 0.0f || sum[j] != sum[j] ? __frcp_rn(sum[j]) : 0.0f;
+        at_row[j] = r0 + row < a.n_rows ? (qs * a.n_q_heads + g0 + row - qs * a.group) * D : -1;
+      }
+      const long long out0 = (static_cast<long long>(q0) * a.n_q_heads + w.kvh * a.group) * D + part * (D / 4);
+      // O once its last product is there.  (Few instructions: what runs once a row tile comes from far out of the
+      // instruction caches.)
+      const int last = f_unit + n_unit - 1;
+      await(L::pvDone + last % L::kScoreBufs, (last / L::kScoreBufs) & 1);
+      if (rows_or(rows_id, failed)) break;
+      tc::fence_after_sync();
+      if (!whole_unit && part == 0) ml[(slot & 1) * 128 + quad * 32 + frag_row(lane, c)] = make_float2(pick(ref), pick(sum));
+#pragma unroll 1
+      for (int o = 0; o < D / 128; ++o) {  // 32 columns of the four rows
+        const uint32_t at = tmem + L::kOCol + part * (D / 4) + 32 * o;
+        uint32_t y[32];
+        tc::ld_16x256b_x4(at + lanes0, y);
+        tc::ld_16x256b_x4(at + lanes1, y + 16);
+        tc::wait_ld();
+        if (o == D / 128 - 1) {  // the next unit's first product may write O
+          tc::fence_before_sync();
+          arrive(L::oFree);
         }
-      } else {
-        // ---- its result.  All sums:
-        if (n_unit > 1) await(L::sumReady + 4 * (left_sums & 1) + quad, (left_sums >> 1) & 1);
-        float* mine = red + (4 + 2 * group + part) * 128 + quad * 32;
-        const float* others = red + (4 + 2 * group + (part ^ 1)) * 128 + quad * 32;
-        mine[frag_row(lane, c)] = pick(sum);
-        if (pair_or(pair_id, failed)) break;
-        const int slot = 2 * run + (f_unit == 0 ? 0 : 1);
-        float inv[4];
-        int at_row[4];  // where the thread's rows stand in the output, from its query's first on
+        if (!whole_unit) {  // a part: the numerator as the threads hold it
+          float4* dst = a.part + (((static_cast<long long>(slot) * 4 + quad) * 4 + part) * (D / 128) + o) * (8 * 32) + lane;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e * 32] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]), __uint_as_float(y[4 * e + 2]),
+                                      __uint_as_float(y[4 * e + 3]));
+          continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int row = frag_row(lane, j), qs = small_div(g0 + row, a.group_inv);
-          sum[j] += others[row];
-          if (n_unit > 1) {
-            const float at = left[256 + row];
-            sum[j] += (left[row] + left[128 + row]) * (at == -INFINITY || at == ref[j] ? 1.0f : fast_exp2(at - ref[j]));
-          }
-          inv[j] = sum[j] > 0.0f || sum[j] != sum[j] ? __frcp_rn(sum[j]) : 0.0f;
-          at_row[j] = r0 + row < a.n_rows ? (qs * a.n_q_heads + g0 + row - qs * a.group) * D : -1;
-        }
-        const long long out0 = (static_cast<long long>(q0) * a.n_q_heads + w.kvh * a.group) * D + part * (D / 2);
-        // O once its last product is there.  (Few instructions: what runs once a row tile comes from far out of the
-        // instruction caches.)
-        const int last = f_unit + n_unit - 1;
-        await(L::pvDone + last % L::kScoreBufs, (last / L::kScoreBufs) & 1);
-        if (pair_or(pair_id, failed)) break;
-        tc::fence_after_sync();
-        if (!whole_unit && part == 0) ml[(slot & 1) * 128 + quad * 32 + frag_row(lane, c)] = make_float2(pick(ref), pick(sum));
-#pragma unroll 1
-        for (int o = 0; o < D / 64; ++o) {  // 32 columns of the four rows
-          const uint32_t at = tmem + L::kOCol + part * (D / 2) + 32 * o;
-          uint32_t y[32];
-          tc::ld_16x256b_x4(at + lanes0, y);
-          tc::ld_16x256b_x4(at + lanes1, y + 16);
-          tc::wait_ld();
-          if (o == D / 64 - 1) {  // the next unit's first product may write O
-            tc::fence_before_sync();
-            arrive(L::oFree);
-          }
-          if (!whole_unit) {  // a part: the numerator as the threads hold it
-            float4* dst = a.part + (((static_cast<long long>(slot) * 4 + quad) * 2 + part) * (D / 64) + o) * (8 * 32) + lane;
+          const uint32_t* v = y + (j >> 1) * 16 + 2 * (j & 1);  // (columns 8 i + 2 c, + 1 at 4 i)
+          auto x = [&](int e) { return __uint_as_float(v[e]) * inv[j]; };
+          if (a.out_bf16) {
+            // four lanes have 8 columns together, four times: each takes one eight, and a row's 64 bytes are written at once
+            uint32_t p[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e * 32] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]), __uint_as_float(y[4 * e + 2]),
-                                        __uint_as_float(y[4 * e + 3]));
-            continue;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t* v = y + (j >> 1) * 16 + 2 * (j & 1);  // (columns 8 i + 2 c, + 1 at 4 i)
-            auto x = [&](int e) { return __uint_as_float(v[e]) * inv[j]; };
-            if (a.out_bf16) {
-              // four lanes have 8 columns together, four times: each takes one eight, and a row's 64 bytes are written at once
-              uint32_t p[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x(4 * i), x(4 * i + 1));
-                p[i] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-              lanes4_transpose(c, p);
-              if (at_row[j] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out0 + at_row[j] + 32 * o + 8 * c) =
-                    make_uint4(p[0], p[1], p[2], p[3]);
-            } else if (at_row[j] >= 0) {
-              float* d = static_cast<float*>(a.out) + out0 + at_row[j] + 32 * o + 2 * c;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(x(4 * i), x(4 * i + 1));
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x(4 * i), x(4 * i + 1));
+              p[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
+            lanes4_transpose(c, p);
+            if (at_row[j] >= 0)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out0 + at_row[j] + 32 * o + 8 * c) =
+                  make_uint4(p[0], p[1], p[2], p[3]);
+          } else if (at_row[j] >= 0) {
+            float* d = static_cast<float*>(a.out) + out0 + at_row[j] + 32 * o + 2 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(x(4 * i), x(4 * i + 1));
           }
         }
       }
-      if (n_unit > 1) ++left_sums;
       f_unit += n_unit;
       w.x += n_unit - 1;
       window_step(a, w);
@@ -704,7 +645,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           const uint64_t vd = rd0 + static_cast<uint64_t>(((slot + kh) * L::kHalf) >> 4);
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            tc::mma_f16_ts(tmem + L::kOCol, tmem + 128 * b + 64 * kh + 8 * s, vd + 2 * s, idesc_pv,
+            tc::mma_f16_ts(tmem + L::kOCol, tmem + 128 * b + 32 * kh + 8 * s, vd + 2 * s, idesc_pv,
                            (first && kh == 0 && s == 0) ? 0u : 1u);
           tc::commit(&bars[L::empty + slot + kh]);
         }
