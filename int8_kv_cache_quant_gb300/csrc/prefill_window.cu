@@ -498,10 +498,10 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
         }
         tc::st_16x128b_x4(tm_p + lanes0, p0);
         tc::st_16x128b_x4(tm_p + lanes1, p1);
-        arrive(L::parFree + pb);
         tc::wait_st();
         tc::fence_before_sync();
         arrive(L::pFull + sb);
+        arrive(L::parFree + pb);
       }
       if (rows_or(rows_id, failed)) break;
       // ---- the unit's sums: this warp's, then all four's
