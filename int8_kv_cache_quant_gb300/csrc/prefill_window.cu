@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
 // begins on; threads take the places of the attention kernel's softmax threads, as the parts lie, two threads for the four
 // rows of one.  Four parts are fetched at once: one after the other, a part costs two trips to memory (ten parts: 28 us).
 template <int D>
-__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ PrefillWindowArgs a, int runs) {
+__global__ void __launch_bounds__(256, 5) window_join_kernel(const __grid_constant__ PrefillWindowArgs a, int runs) {
   const int run = blockIdx.x, o = blockIdx.y, quad = (threadIdx.x >> 5) & 3, h = threadIdx.x >> 7, lane = threadIdx.x & 31;
   const long long f0 = run_start(a, run, runs), f1 = run_start(a, run + 1, runs);
   const WindowWalk w = window_walk_at(a, f0);
@@ -782,11 +782,11 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
   float4 acc[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = first; i0 <= run; i0 += 4) {
-    float2 v[4][2];
-    float4 x[4][4];
+  for (int i0 = first; i0 <= run; i0 += 2) {
+    float2 v[2][2];
+    float4 x[2][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 2; ++t) {
       const long long slot = i0 + t == first ? first_slot : 2 * (i0 + t);
       const float4* src = a.part + ((slot * 4 + quad) * (D / 32) + o) * (8 * 32) + (4 * h) * 32 + lane;  // (o: half of the columns, then 32)
       const bool real = i0 + t <= run;
@@ -795,13 +795,13 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[t][e] = real ? src[e * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    float s[4][2];
-    bool none[4][2];
+    float s[2][2];
+    bool none[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float was = m[j];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 2; ++t) {
         m[j] = fmaxf(m[j], v[t][j].x);
         dropped[j] |= v[t][j].y < 0.0f;
       }
@@ -813,14 +813,14 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
         (j ? acc[e].w : acc[e].y) *= s0;
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 2; ++t) {
         none[t][j] = v[t][j].x == -INFINITY && v[t][j].y == 0.0f;  // the row sees no key of this part
         s[t][j] = v[t][j].x == -INFINITY ? 1.0f : fast_exp2(v[t][j].x - m[j]);  // (a part of NaN alone has no maximum)
         if (!none[t][j]) l[j] = fmaf(v[t][j].y, s[t][j], l[j]);
       }
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (!none[t][0]) {
@@ -864,8 +864,9 @@ PrefillWindowPlan prefill_window_plan(int n_tokens, int n_q_heads, int n_kv_head
   p.key_tiles = p.sink_tiles + (history_len + n_tokens - 1) / 128 - p.first_tile + 1;
   for (int t = 0; t < p.row_tiles; ++t) p.line += row_tile_keys(t, n_rows, group, history_len, window, n_sink).n;
   const long long pairs = p.line * n_kv_heads;
-  p.runs = static_cast<int>(std::min<long long>(pairs, std::min(n_sms, kWMaxRuns)));
-  const long long max_runs = std::min<long long>(pairs, kWMaxRuns), tiles = static_cast<long long>(n_kv_heads) * p.key_tiles;
+  // (two tiles a run at least: a part costs more to write and to join than a tile; 80 pairs, one | two a run: 21.0 | 18.6 us)
+  p.runs = static_cast<int>(std::min<long long>(std::max(1LL, pairs / 2), std::min(n_sms, kWMaxRuns)));
+  const long long max_runs = std::min<long long>(std::max(1LL, pairs / 2), kWMaxRuns), tiles = static_cast<long long>(n_kv_heads) * p.key_tiles;
   p.off_v = tiles * head_dim * 256;
   p.off_par = 2 * p.off_v;
   p.off_ml = p.off_par + tiles * 1536;

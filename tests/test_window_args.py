@@ -96,7 +96,7 @@ def prompt_tiles(T, hq, hkv, hist, window, sink):
     (300, 8, 8, 5000, 77, 20000, 128), (33, 24, 4, 5000, 2 ** 31 - 1, 2 ** 31 - 1, 256)])
 def test_prompt_workspace(L, T, hq, hkv, hist, window, sink, d):
     pairs, tiles = prompt_tiles(T, hq, hkv, hist, window, sink)
-    runs = min(160, pairs * hkv)
+    runs = min(160, max(1, pairs * hkv // 2))  # of two tile pairs at least
     want = hkv * tiles * (4 * 128 * d + 1536) + runs * 2 * 128 * (d + 2) * 4
     assert k.kvq_prefill_window_workspace_bytes(T, hq, hkv, hist, window, sink, d) == want
     kw = dict(c=cache(d=d, hkv=hkv), n=T, hq=hq, hist=hist, nb=-(-(hist + T) // 16), w=window, sink=sink)
