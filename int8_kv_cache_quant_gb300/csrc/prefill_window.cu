@@ -22,17 +22,29 @@
 // the order of the line, so that the same call gives the same bits; one that lies within a run is written at once.
 //
 // A CTA's warps:
-//   warps 0-7  softmax: rows 32 (w % 4) .. of the tile (the lanes of tensor memory that the warp can reach), half of its keys
-//   warp 8     MMA issue and tensor-memory allocation
-//   warp 9     tile copies: a ring of 16 KB pieces in the order the MMAs take them, and the keys' factors
-// Tensor memory: S (128 columns) | P, two buffers of 64 | O (head_dim).  S is one buffer: its threads hold it in
-// registers and free it before they work on it, so that the next Q K^T runs meanwhile.  P in tensor memory leaves the
-// shared memory to Q and the K/V tiles.
-// A softmax thread holds four rows x 16 keys of its warp's 32 x 64 (tcgen05.ld.16x256b), not one row x 64: with a row a
-// thread every thread needs all keys' factors, 512 bytes a load of the 128 that shared memory gives a cycle, 1500 cycles
-// a tile; so it is a quarter of that, for two shuffles a row in the maximum.
-// The next row tile's queries are on their way while the last tile of this one is worked on, and the products go on
-// through the change: the next Q K^T runs while the output is written.
+//   warps 0-15   softmax: rows 32 (w % 4) .. of the tile (the lanes of tensor memory that the warp can reach), a quarter of
+//                its keys
+//   warp 16      MMA issue and tensor-memory allocation
+//   warp 17      tile copies, a ring of half tiles in the order the MMAs take them, and the keys' factors
+//   warps 18-19  the next row tile's queries, while the last tiles of this one are worked on
+// Tensor memory: three score tiles of 128 columns (two at head_dim 256) and O.  P takes its score tile's place, so that shared
+// memory is left to Q and the K/V tiles and the scores run two tiles ahead of the values (one at head_dim 256).
+// A softmax thread holds four rows x 8 keys (tcgen05.ld.16x256b), not one row x 32: a row a thread would need all keys'
+// factors in every thread.  The scores stay in registers from the maximum to the weights; whether a row's maximum exceeds its
+// reference is one barrier of the row's four warps, and only then do they exchange maxima.
+//
+// What bounds it, and what it was measured at.  2048 queries behind 30720 keys, W = 4096, 24 / 4 heads of 256: 178 us (206 GFLOP:
+// 1.16 PFLOP/s), the tensor cores busy for 60 % of the attention's 161 us: a tile's P waits for its scores and these for
+// the values two tiles before, since O leaves tensor memory room for two score tiles.  2047 queries, W = 1024, 32 / 8 heads of 128:
+// 58.4 us (30 GFLOP), the softmax and each row tile's end: its last values, its output, the next queries (5000 of 30000
+// cycles).  33 queries, 24 / 4 heads of 256: 17.5 us, three launches of latencies.
+// Instruction fetch decides more than arithmetic here: 20 warps in six roles run from the same caches.  2047 queries, us:
+// with a softmax tile unrolled twice 71 against 63; product and copy code in one place each instead of three 59 against 63;
+// the queries' loop eight times unrolled 64, four times 62; the MMA warp's operands not provably uniform 69 against 63.
+// Other shapes that were built and were slower, us (2047 queries | 32K chunk): eight softmax warps and one score tile
+// 104 | 314; two groups of eight that take turns at the tiles 58.6 | 193; scores and values issued by two warps 81 | 238 against
+// 74 | 220; pairs of CTAs that share an MMA (cta_group::2, each half of a tile's K and V) 70 | 235 against 64 | 197; parts
+// joined by whoever writes the second 63 | 183 against 59 | 181; half of the bytes copied is no faster (L2 is not the limit).
 #include <algorithm>
 
 #include "kvq_dev.cuh"
@@ -67,8 +79,7 @@ struct Pw {
                        qFree = qFull + 1, oFree = qFree + 1, drain = oFree + 1, kNumBars = drain + 1;
   static constexpr int offFlag = offBar + kNumBars * 8;      // abort flag, TMEM base
   static constexpr int kAlloc = offFlag + 16 + 1024;
-  // Tensor memory: score tiles and O.  A P tile takes its score tile's place, the first and second half of the keys each
-  // their half's.
+  // Tensor memory: score tiles and O.  A P tile takes the first half of its score tile's place.
   static constexpr uint32_t kOCol = 128 * kScoreBufs, kTmemCols = 512;
   static_assert(kOCol + D <= kTmemCols, "tensor memory");
   static_assert(offBar % 8 == 0, "alignment");
@@ -763,7 +774,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
 // ============================================================================ joining the parts
 // Block (run, 32 columns).  The run in which a cut row tile ends joins its parts, from the run in which it
 // begins on; threads take the places of the attention kernel's softmax threads, as the parts lie, two threads for the four
-// rows of one.  Four parts are fetched at once: one after the other, a part costs two trips to memory (ten parts: 28 us).
+// rows of one.  Two parts are fetched at once, five blocks an SM; one part after the other 28 us for ten parts, four at once and
+// three blocks an SM 4 us more for the chunk of 32K.
 template <int D>
 __global__ void __launch_bounds__(256, 5) window_join_kernel(const __grid_constant__ PrefillWindowArgs a, int runs) {
   const int run = blockIdx.x, o = blockIdx.y, quad = (threadIdx.x >> 5) & 3, h = threadIdx.x >> 7, lane = threadIdx.x & 31;
@@ -864,7 +876,8 @@ PrefillWindowPlan prefill_window_plan(int n_tokens, int n_q_heads, int n_kv_head
   p.key_tiles = p.sink_tiles + (history_len + n_tokens - 1) / 128 - p.first_tile + 1;
   for (int t = 0; t < p.row_tiles; ++t) p.line += row_tile_keys(t, n_rows, group, history_len, window, n_sink).n;
   const long long pairs = p.line * n_kv_heads;
-  // (two tiles a run at least: a part costs more to write and to join than a tile; 80 pairs, one | two a run: 21.0 | 18.6 us)
+  // (two tiles a run at least: a part costs more to write and to join than a tile; 80 pairs, one | two | three a run: 21.0 |
+  // 18.6 | 22.2 us)
   p.runs = static_cast<int>(std::min<long long>(std::max(1LL, pairs / 2), std::min(n_sms, kWMaxRuns)));
   const long long max_runs = std::min<long long>(std::max(1LL, pairs / 2), kWMaxRuns), tiles = static_cast<long long>(n_kv_heads) * p.key_tiles;
   p.off_v = tiles * head_dim * 256;

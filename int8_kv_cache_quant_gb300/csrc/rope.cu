@@ -21,7 +21,9 @@
 //
 // With several axes (kvq_rope_axes_bf16: time, height and width of a patch) a frequency takes the position of its own
 // axis: a thread loads a token's positions (four at most) and picks one for each of its pairs by two bits of the
-// call's arguments, so that the map costs no load.  The inverse has the sine's sign turned.
+// call's arguments, so that the map costs no load.  The inverse has the sine's sign turned.  4095 tokens x (32 + 8) heads of 128, two
+// axes (84 MB): 11.3 us, 7.4 TB/s, the outputs staying in L2; 2048 x (24 + 4) heads of 256, three axes, 128 dims rotated
+// (59 MB): 9.9 us, 5.9 TB/s; one token 2.0 us, a launch.
 #include <type_traits>
 
 #include "kvq_dev.cuh"
