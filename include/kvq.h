@@ -692,8 +692,8 @@ size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, i
  *   workspace      : device, >= kvq_prefill_window_workspace_bytes(...), 16-byte aligned; its contents on entry do not matter
  * A key on a page outside the pool is skipped (KVQ_DEV_BAD_BLOCK); a row that sees no key, or scores -infinity alone, gives
  * zeros.  If a bounded wait runs out (KVQ_DEV_TIMEOUT), the rows concerned are not written.
- * KVQ_ERR_UNSUPPORTED when the GQA group exceeds 1024, the rows n_tokens * (n_q_heads / n_kv_heads) or the keys reach 2^30, or
- * the pairs of 128-row and 128-key tiles of all KV heads 2^35.
+ * KVQ_ERR_UNSUPPORTED when the GQA group exceeds 1024, a token's n_q_heads * head_dim reaches 2^24, the rows n_tokens *
+ * (n_q_heads / n_kv_heads) or the keys reach 2^30, or the pairs of 128-row and 128-key tiles of all KV heads 2^35.
  */
 int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_t n_tokens, int32_t n_q_heads,
                                    int32_t history_len, const int32_t* block_table_row, int32_t n_blocks_row,
@@ -811,7 +811,7 @@ int kvq_debug_stream_floor(const kvq_cache* cache, int32_t batch, const int32_t*
  * does not issue the copy of its second page, with mode 2 the producer of prefill attention CTA 0
  * does not issue its fourth piece, with mode 3 the sparse CTA of (query 0, KV head 0) does not
  * issue the copies of its second chunk, with mode 4 the first CTA of the chunk weights' row pass does not
- * announce its first key tile, with mode 5 the first CTA of the windowed prefill does not issue its fourth piece
+ * announce its first key tile, with mode 5 the first CTA of the windowed prefill does not issue its second tile's copies
  * (mode 0: no injection).  No copy is left in flight:
  * the consumer's wait runs out, the kernel sets KVQ_DEV_TIMEOUT, waits (bounded) for the copies it
  * did issue, drops that CTA's result (decode single route: zero output rows; split route: an empty

@@ -1103,15 +1103,16 @@ int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_
   if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
   if (static_cast<long long>(history_len) + n_tokens > static_cast<long long>(n_blocks_row) * KVQ_BLOCK_SIZE)
     return KVQ_ERR_INVALID_ARG;
-  if (H > 65535 || n_q_heads / H > 1024 || !prefill_window_sizes_ok(n_tokens, n_q_heads, H, history_len)) return KVQ_ERR_UNSUPPORTED;
+  // (the kernel counts the elements of 128 queries' rows in 32 bits)
+  if (H > 65535 || n_q_heads / H > 1024 || n_q_heads >= (1 << 24) / D || !prefill_window_sizes_ok(n_tokens, n_q_heads, H, history_len))
+    return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out) || !aligned4(block_table_row)) return KVQ_ERR_MISALIGNED;
   if (!workspace) return KVQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
-  const kvq::PrefillWindowPlan size = prefill_window_plan_of(n_tokens, n_q_heads, H, history_len, window, n_sink, D, 1);
-  if (workspace_bytes < static_cast<size_t>(size.bytes)) return KVQ_ERR_WORKSPACE;
   const int sms = device_sm_count();
+  const kvq::PrefillWindowPlan p = prefill_window_plan_of(n_tokens, n_q_heads, H, history_len, window, n_sink, D, std::max(sms, 1));
+  if (workspace_bytes < static_cast<size_t>(p.bytes)) return KVQ_ERR_WORKSPACE;
   if (sms <= 0) return KVQ_ERR_CUDA;
-  const kvq::PrefillWindowPlan p = prefill_window_plan_of(n_tokens, n_q_heads, H, history_len, window, n_sink, D, sms);
   kvq::PrefillWindowArgs a{};
   a.k = cache->k;
   a.v = cache->v;

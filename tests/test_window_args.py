@@ -69,6 +69,7 @@ def prompt(L, c=None, q=A, n=10, hq=24, hist=20, bt=A, nb=8, scale=0.1, w=50, si
     (INVALID, dict(hq=26)), (INVALID, dict(hist=-1)), (INVALID, dict(nb=0)), (INVALID, dict(nb=1)), (INVALID, dict(w=0)),
     (INVALID, dict(w=-5)), (INVALID, dict(sink=-1)), (INVALID, dict(scale=0.0)), (INVALID, dict(scale=-0.1)), (INVALID, dict(scale=NAN)),
     (INVALID, dict(scale=INF)), (UNSUPPORTED, dict(kind=2)), (UNSUPPORTED, dict(kind=-1)),
+    (UNSUPPORTED, dict(c=cache(hkv=64), hq=65536)), (WORKSPACE, dict(c=cache(hkv=64), hq=65536 - 64, ws=None)),
     (UNSUPPORTED, dict(c=cache(hkv=1), hq=1025)), (WORKSPACE, dict(c=cache(hkv=1), hq=1024, ws=None)),
     (UNSUPPORTED, dict(n=1 << 28, hist=0, nb=1 << 24)), (UNSUPPORTED, dict(hist=(1 << 30) - 10, nb=1 << 27)),
     (UNSUPPORTED, dict(n=1 << 25, hist=1 << 29, nb=1 << 26)), (UNSUPPORTED, dict(c=cache(hkv=65536), hq=65536)),
