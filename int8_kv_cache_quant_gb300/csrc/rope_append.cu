@@ -318,15 +318,17 @@ __global__ void __launch_bounds__(kAppendThreads, 2) rope_append_kernel(const __
   }
 }
 
-// Heads of a block: all of them share its cos and sin, so as many as leave one and a half blocks an SM; where there are
-// too few tokens for that, query heads and KV heads in blocks of their own.
+// Heads of a block: all of them share its cos and sin, so as many as leave one and a half blocks an SM, and from half a
+// block an SM on a KV head and its query heads at least.  Where there are fewer tokens, query heads and KV heads in blocks of their own.
+// So | always together | apart up to three blocks an SM, us: 64 sequences' tokens, 8 KV heads of 128 5.2 | 5.6 | 5.2; 64 tokens of
+// one sequence, 4 heads of 256 5.3 | 6.3 | 5.3; 200 sequences 6.3 | 6.3 | 7.2; 512 tokens of one 6.5 | 6.5 | 10.1.
 template <int D>
 static cudaError_t launch_append_d(RopeAppendArgs a, int n_sms, cudaStream_t stream) {
   constexpr int RS = kAppendThreads / D;
   const long long groups = a.n_tokens > kTokens ? (static_cast<long long>(a.n_tokens) + KVQ_BLOCK_SIZE - 1 + kTokens - 1) / kTokens : 1;
   const int H = a.n_kv_heads, Hq = a.n_q_heads;
   long long blocks;
-  if (2 * groups * H >= 3LL * n_sms) {
+  if (2 * groups * H >= n_sms) {
     const int cut = static_cast<int>(std::min<long long>(H, (3LL * n_sms + 2 * groups - 1) / (2 * groups)));
     a.kv_heads = (H + cut - 1) / cut;
     blocks = (H + a.kv_heads - 1) / a.kv_heads;
@@ -334,7 +336,7 @@ static cudaError_t launch_append_d(RopeAppendArgs a, int n_sms, cudaStream_t str
     a.kv_first = 0;
   } else {
     int per = 16;
-    while (per > RS && groups * ((Hq + per - 1) / per + H) < 4LL * n_sms) per /= 2;
+    while (per > RS && groups * ((Hq + per - 1) / per + H) < 2LL * n_sms) per /= 2;
     a.q_heads = per;
     a.kv_heads = 1;
     a.kv_first = (Hq + per - 1) / per;
