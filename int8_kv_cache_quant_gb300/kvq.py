@@ -451,7 +451,7 @@ def kvq_attn_decode_int8kv_noalloc(cache, q, block_table, ctx_lens, max_ctx, sof
 def kvq_debug_fault_inject(mode, wait_budget_cycles=0):
     """Test entry point of the failure path (see kvq.h): mode 0 none, 1 a decode stage-1 copy left
     un-issued, 2 a prefill piece left un-issued, 3 a sparse chunk left un-issued, 4 a key tile of the chunk
-    weights not announced, 5 a piece of the windowed prefill left un-issued; every bounded wait gives up after wait_budget_cycles (<= 0: the default)."""
+    weights not announced, 5 a tile of the windowed prefill left un-issued; every bounded wait gives up after wait_budget_cycles (<= 0: the default)."""
     _fit("kvq_debug_fault_inject", mode)
     _check("kvq_debug_fault_inject", lib().kvq_debug_fault_inject(int(mode), int(wait_budget_cycles)))
 
@@ -544,6 +544,8 @@ def kvq_attn_prefill_window_int8kv(cache, q, history_len, block_table_row, softm
     if workspace is None:
         need = kvq_prefill_window_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), int(window), int(n_sink), D)
     workspace, wbytes = _ws(workspace, need, q.device, stream)
+    if workspace.get_device() != dev:
+        _elsewhere(fn, "the workspace", workspace)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_attn_prefill_window_int8kv(
         ctypes.byref(c), q_p, T, Hq, int(history_len), table_p, n_blocks, float(softmax_scale), int(window), int(n_sink), out_p,
@@ -721,7 +723,9 @@ def kvq_decode_step_window_int8kv(cache, k_new, v_new, q, block_table, ctx_lens,
         if need:
             workspace = _empty(need, torch.uint8, cache.k.device, stream)
     if workspace is not None:
-        ws_p, wbytes = _p(workspace), workspace.numel() * workspace.element_size()
+        if workspace.get_device() != dev:
+            _elsewhere(fn, "the workspace", workspace)
+        ws_p, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_decode_step_window_int8kv(
         ctypes.byref(c), k_p, v_p, q_p, B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx), float(softmax_scale), int(window),

@@ -209,3 +209,22 @@ def test_host_tensors_are_refused(monkeypatch):
         k.kvq_rope_axes_bf16(x, None, pos, plan, q_out=x)
     with pytest.raises(ValueError):
         k.kvq_rope_append_int8kv(k.KVCache(2, 4, 128, device="cpu"), None, x, x, pos, plan, pos, pos, pos.view(1, 2))
+
+
+def test_a_workspace_on_another_device_is_refused(monkeypatch):
+    import torch
+
+    class Elsewhere:
+        device = "cuda:7"
+        get_device = staticmethod(lambda: 7)
+        numel = staticmethod(lambda: 1 << 30)
+        element_size = staticmethod(lambda: 1)
+
+    monkeypatch.setattr(k.kvq, "_current_device", lambda: -1)  # what tensors of the host say
+    cache = k.KVCache(4, 2, 128, device="cpu")
+    q, row = torch.zeros((3, 4, 128), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="workspace"):
+        k.kvq_attn_prefill_window_int8kv(cache, q, 5, row, 0.1, 16, out=torch.empty_like(q), workspace=Elsewhere())
+    with pytest.raises(ValueError, match="workspace"):
+        k.kvq_decode_step_window_int8kv(cache, None, None, q, row.repeat(3, 1), torch.ones(3, dtype=torch.int32), 40, 0.1, 16,
+                                        out=torch.empty((3, 4, 128)), workspace=Elsewhere())
