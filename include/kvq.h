@@ -90,6 +90,7 @@ int32_t kvq_device_accessible(const void* p);
 #define KVQ_DEV_TIMEOUT 0x4u   /* a bounded mbarrier wait ran out; the CTA returned early */
 #define KVQ_DEV_BAD_CELL 0x8u  /* a sparse cell index is negative or past the mapped range */
 #define KVQ_DEV_BAD_SEQ 0x10u  /* a seq_idx is outside [0, num_seqs) */
+#define KVQ_DEV_BAD_SCALE 0x20u /* a V scale is past what the call takes (kvq_attn_prefill_window_int8kv) */
 
 typedef struct kvq_cache {
   int8_t* k;          /* device, layout above */
@@ -680,9 +681,10 @@ size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, i
  * over those keys.  Scores from the bf16 queries and the int8 codes as in decode (q is not quantised; a row whose
  * sum of |q code| passes fp32's range, elements near 1e34, is infinite), statistics and sums in fp32 in a fixed order (the
  * same call gives the same bits); the softmax weights, times the V scales, go into the second product as fp16 (2^-11
- * relative), and the output is rounded once: bf16, or fp32, which then shows the weights' rounding.  V scales below 2^-100
- * count as 2^-100.  The chunk's own K/V must already be in the cache (kvq_rope_append_int8kv, kvq_quant_write); history_len
- * may be 0.
+ * relative), and the output is rounded once: bf16, or fp32, which then shows the weights' rounding.  The chunk's own K/V must
+ * already be in the cache (kvq_rope_append_int8kv, kvq_quant_write); history_len may be 0.
+ * V scales below 2^-60 count as 2^-60 (a row of zeros stays zeros).  Where a query sees a key whose V scale is above 2^40, elements
+ * near 10^14, the call sets KVQ_DEV_BAD_SCALE: beside such a scale, keys with scales near 2^-60 may be missing in the softmax's sum.
  *   q              : device bf16 [n_tokens][n_q_heads][head_dim]
  *   block_table_row: device int32 [n_blocks_row], covering history_len + n_tokens keys; entries of pages that no query
  *                    sees are not read

@@ -6,8 +6,13 @@
 //     out = sum_t 2^s[t] v_scale[t] v_code[t] / sum_t 2^s[t].
 // The V scale goes into the exponent: z[t] = s[t] + log2 v_scale[t], w[t] = 2^(z[t] - r) with one reference r a row, so that
 //     out = sum_t w[t] v_code[t] / sum_t w[t] / v_scale[t],
-// one exponential a score, weights that fit fp16 whatever the V scales are, and no second maximum.  r is the largest z
-// of the row's first tile and moves only when a tile exceeds it by 2^8, so that the accumulator is hardly ever scaled again.
+// one exponential a score, weights that fit fp16 whatever the V scales are, and no second maximum.  r is 7 less than the largest z
+// of the row's first tile and moves only when a tile's z is more than 15 above it, so that the accumulator is hardly ever scaled again:
+// weights are at most 2^15, the half of fp16's range that is left above its largest reference weight, 2^7.
+// The one statistic has a price.  Factors of two to the -126 and less are 0, in the sum too, where a weight stands for w / v_scale: a
+// key whose V scale is 2^-k of another's is lost from 126 - k octaves below that one's score on.  So V scales count as 2^-60
+// at least (rows of zeros have 0), and past 2^40 they are reported: between the two, a key that is lost has less than
+// 2^-26 of the largest probability.  A second statistic, of the scores alone, would be a second exponential a score.
 //
 // Operands.  Codes are exact in 16-bit floats: the scores take the bf16 queries as they are and the K codes in bf16
 // (every product exact, fp32 sums); the weights go in as fp16, rounded to 11 bits (2^-11 relative: the one rounding
@@ -59,9 +64,11 @@ namespace {
 constexpr int kWSoftWarps = 16, kWMmaWarp = kWSoftWarps, kWCopyWarp = kWMmaWarp + 1, kWQWarp = kWCopyWarp + 1, kWQWarps = 2;
 constexpr int kWThreads = 32 * (kWQWarp + kWQWarps);
 constexpr int kWParBufs = 4;
-constexpr float kWLazy = 8.0f;  // a tile may exceed its row's reference by 2^8
-// V scales below this count as this: their codes' share of an output, at most 127 * 2^-100, is lost in any other
-constexpr float kWMinScale = 7.8886091e-31f;  // 2^-100
+// A row's largest weight when its reference is set, and what a later tile's may come to before it moves, in octaves: within
+// fp16's 2^16, and as far from where weights become subnormal, 2^-14, as that leaves.
+constexpr float kWLift = 7.0f, kWMost = kWLift + 8.0f;
+// The V scales that a weight and its sum take (above).
+constexpr float kWMinScale = 0x1p-60f, kWMaxScale = 0x1p40f;
 
 template <int D>
 struct Pw {
@@ -298,6 +305,8 @@ __global__ void __launch_bounds__(256) window_tiles_kernel(const __grid_constant
       const long long at = (static_cast<long long>(page) * a.n_kv_heads + kvh) * KVQ_BLOCK_SIZE + (tid & 15);
       kf = a.k_scale[at] * a.c2;
       float vs = a.v_scale[at];
+      const int key = 128 * tile + tid;
+      if (vs > kWMaxScale && (key > a.history_len - a.window || key < a.n_sink)) set_status(a.status, KVQ_DEV_BAD_SCALE);
       if (vs < kWMinScale) vs = kWMinScale;
       lv = log2f(vs);
       // (finite: 0 times it is 0 for the rows that do not see the key; the others have its infinity or NaN from lv)
@@ -442,7 +451,7 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
             const uint32_t* s = y + (j >> 1) * 16 + 4 * i + 2 * (j & 1);
             m[j] = fmax3(m[j], __uint_as_float(s[0]), __uint_as_float(s[1]));
           }
-          over |= m[j] > ref[j] + kWLazy;
+          over |= m[j] > ref[j] + kWMost;
         }
         // All scores are in registers, and P may take their place; and does a row's maximum exceed its reference?
         tc::fence_before_sync();
@@ -465,7 +474,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
           for (int j = 0; j < 4; ++j) {
             m[j] = all_max(j);
             scale[j] = 1.0f;
-            if (u == 0 || m[j] > ref[j] + kWLazy) {
+            if (u == 0 || m[j] > ref[j] + kWMost) {
+              m[j] -= kWLift;
               // (from -infinity there is nothing in l and O, but NaN, which stays)
               if (ref[j] != -INFINITY) {
                 scale[j] = fast_exp2(ref[j] - m[j]);

@@ -23,7 +23,7 @@ _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape or option",
            3: "device pointer not 16-byte aligned", 4: "workspace missing or too small",
            5: "CUDA launch or runtime error"}
 
-DEV_BAD_BLOCK, DEV_BAD_POS, DEV_TIMEOUT, DEV_BAD_CELL, DEV_BAD_SEQ = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_BAD_BLOCK, DEV_BAD_POS, DEV_TIMEOUT, DEV_BAD_CELL, DEV_BAD_SEQ, DEV_BAD_SCALE = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 
 
 class KvqError(RuntimeError):
