@@ -680,9 +680,10 @@ size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, i
  *   out[i][h] = sum_t softmax_t(s) * v^[t],  s[t] = softmax_scale * q[i][h] . k^[t]
  * over those keys.  Scores from the bf16 queries and the int8 codes as in decode (q is not quantised; a row whose
  * sum of |q code| passes fp32's range, elements near 1e34, is infinite), statistics and sums in fp32 in a fixed order (the
- * same call gives the same bits); the softmax weights, times the V scales, go into the second product as fp16 (2^-11
- * relative), and the output is rounded once: bf16, or fp32, which then shows the weights' rounding.  The chunk's own K/V must
- * already be in the cache (kvq_rope_append_int8kv, kvq_quant_write); history_len may be 0.
+ * same call gives the same bits).  The softmax weights, times the V scales, go into the second product as fp16, off by
+ * 2^-11 of themselves, or by 2^-32 of the row's largest where that is more; the output is rounded once: bf16, or fp32, which
+ * then shows the weights' rounding.  The chunk's own K/V must already be in the cache (kvq_rope_append_int8kv,
+ * kvq_quant_write); history_len may be 0.
  * V scales below 2^-60 count as 2^-60 (a row of zeros stays zeros).  Where a query sees a key whose V scale is above 2^40, elements
  * near 10^14, the call sets KVQ_DEV_BAD_SCALE: beside such a scale, keys with scales near 2^-60 may be missing in the softmax's sum.
  *   q              : device bf16 [n_tokens][n_q_heads][head_dim]

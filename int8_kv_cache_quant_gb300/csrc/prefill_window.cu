@@ -15,8 +15,8 @@
 // 2^-26 of the largest probability.  A second statistic, of the scores alone, would be a second exponential a score.
 //
 // Operands.  Codes are exact in 16-bit floats: the scores take the bf16 queries as they are and the K codes in bf16
-// (every product exact, fp32 sums); the weights go in as fp16, rounded to 11 bits (2^-11 relative: the one rounding
-// before the output's), against V codes in fp16.  A pass before the attention widens the tiles of 128 keys that any
+// (every product exact, fp32 sums); the weights go in as fp16, rounded to 11 bits (2^-11 relative, or 2^-25 where they are
+// below 2^-14, which is 2^-32 of a row's largest: the one rounding before the output's), against V codes in fp16.  A pass before the attention widens the tiles of 128 keys that any
 // row sees, once for all row tiles and heads, into the byte image of the operands, and leaves each key's factors.
 //
 // Rows.  The rows of a KV head are r = i G + g (G heads a group): a tile of 128 rows is a run of 128 / G queries, so that

@@ -86,3 +86,29 @@ def test_a_scale_past_the_range_is_reported(kvq, large):
         pool.vs[table[0, key // 16], 1, key % 16] = large
         kvq.kvq_attn_prefill_window_int8kv(pool.to_gpu(kvq), q, 290, row, 0.1, 50, 4)
         assert kvq.kvq_device_status() == flags, key
+
+
+@pytest.mark.parametrize("octaves", [0.6, 12.3, 18.7, 22.4, 25.6, 29.5])
+def test_small_weights(kvq, octaves):
+    """One key far above the others, all of whose weights are the same, in dims where it has a code of 0: a weight goes in as fp16, off
+    by 2^-11 of itself or 2^-32 of the row's largest."""
+    import torch
+    rng = np.random.default_rng(4)
+    d, n, scale = 128, 1000, 0.125
+    table, nb = table_of(rng, [n])
+    pool = R.Pool.random(rng, nb, 1, d)
+    pool.vs[:], pool.ks[:], pool.k[:] = 1.0, 1.0, 0
+    page, at = keys_of(table, n)
+    top = 200
+    pool.k[page[top], 0, 0, at[top], 0], pool.ks[page[top], 0, at[top]] = 64, octaves * np.log(2) / (64 * scale)
+    pool.v[page[top], 0, ::2, at[top]] = 0
+    q = torch.ones((1, 4, d), dtype=torch.bfloat16, device="cuda")
+    out = kvq.kvq_attn_prefill_window_int8kv(pool.to_gpu(kvq), q, n - 1, dev(table[0]), scale, 5000, out_dtype=torch.float32)
+    ref, _ = WR.prompt(pool, table[0], np.ones((1, 4, d)), n - 1, 5000, 0, scale)
+    v = np.abs(pool.rows(table[0], n)[1][0])
+    p = np.where(np.arange(n) == top, 1.0, 2.0 ** -octaves)
+    p /= p.sum()
+    # the score: two factors' roundings and the sum's, 2^-22 of it in octaves; weights, sum and quotient some steps more
+    rel = np.log(2) * octaves * 2.0 ** -22 + 2.0 ** -20 + n * 2.0 ** -24
+    tol = (p @ v) * rel + np.maximum(2.0 ** -11 * p, 2.0 ** -32 * p.max()) @ v
+    assert (np.abs(out.cpu().numpy() - ref) <= tol).all()
