@@ -1062,8 +1062,9 @@ int kvq_attn_prefill_int8(const kvq_cache* cache, const void* q, int32_t n_token
   return KVQ_OK;
 }
 
-// Rows, keys and tile pairs are counted in 32 bits, a tile of them ahead.
-static bool prefill_window_sizes_ok(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len) {
+// Rows, keys, tile pairs and the elements of 128 queries' rows are counted in 32 bits, a tile of them ahead.
+static bool prefill_window_sizes_ok(int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t history_len, int32_t head_dim) {
+  if (n_kv_heads > 65535 || n_q_heads / n_kv_heads > 1024 || n_q_heads >= (1 << 24) / head_dim) return false;
   constexpr long long kMost = 1LL << 30;
   const long long rows = static_cast<long long>(n_tokens) * (n_q_heads / n_kv_heads), keys = static_cast<long long>(history_len) + n_tokens;
   if (rows >= kMost || keys >= kMost) return false;
@@ -1083,7 +1084,7 @@ size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, i
                                           int32_t window, int32_t n_sink, int32_t head_dim) {
   if (n_tokens <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || history_len < 0 || window <= 0 || n_sink < 0) return 0;
   if (n_q_heads % n_kv_heads != 0 || (head_dim != 128 && head_dim != 256)) return 0;
-  if (!prefill_window_sizes_ok(n_tokens, n_q_heads, n_kv_heads, history_len)) return 0;
+  if (!prefill_window_sizes_ok(n_tokens, n_q_heads, n_kv_heads, history_len, head_dim)) return 0;
   return static_cast<size_t>(
       prefill_window_plan_of(n_tokens, n_q_heads, n_kv_heads, history_len, window, n_sink, head_dim, 1).bytes);
 }
@@ -1103,9 +1104,7 @@ int kvq_attn_prefill_window_int8kv(const kvq_cache* cache, const void* q, int32_
   if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
   if (static_cast<long long>(history_len) + n_tokens > static_cast<long long>(n_blocks_row) * KVQ_BLOCK_SIZE)
     return KVQ_ERR_INVALID_ARG;
-  // (the kernel counts the elements of 128 queries' rows in 32 bits)
-  if (H > 65535 || n_q_heads / H > 1024 || n_q_heads >= (1 << 24) / D || !prefill_window_sizes_ok(n_tokens, n_q_heads, H, history_len))
-    return KVQ_ERR_UNSUPPORTED;
+  if (!prefill_window_sizes_ok(n_tokens, n_q_heads, H, history_len, D)) return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out) || !aligned4(block_table_row)) return KVQ_ERR_MISALIGNED;
   if (!workspace) return KVQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KVQ_ERR_MISALIGNED;
