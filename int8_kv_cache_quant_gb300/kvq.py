@@ -631,24 +631,22 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
     fp32 shaped like q."""
     _fit("kvq_decode_step_accum_int8kv", max_ctx)
     fn = "kvq_decode_step_accum_int8kv"
-    squeeze = q.dim() == 3
-    if squeeze:
-        q = q[:, None]
-    B, nq, Hq, D = q.shape
-    if out is None:
-        out = _new_out((B, nq, Hq, D), q, stream)
-        ret = out[:, 0] if squeeze else out
+    shape, H, dev = q.shape, cache.n_kv_heads, _current_device()
+    if len(shape) == 3:  # one token
+        (B, Hq, D), nq = shape, 1
+        rows = B, H, D
     else:
-        ret = out
-    H, dev = cache.n_kv_heads, _current_device()
-    for name, t, dtype, n in (("q", q, torch.bfloat16, B * nq * Hq * D), ("out", out, torch.float32, B * nq * Hq * D),
-                              ("k_new", k_new, torch.bfloat16, B * nq * H * D),
-                              ("v_new", v_new, torch.bfloat16, B * nq * H * D)):
-        if t is not None:
-            if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-                raise ValueError("%s: %s must be a contiguous %s tensor of %d elements" % (fn, name, dtype, n))
-            if t.get_device() != dev and t.is_cuda:  # host memory: zero-copy, checked by _hp
-                _elsewhere(fn, name, t)
+        B, nq, Hq, D = shape
+        rows = B, nq, H, D
+    if out is None:
+        out = _new_out(shape, q, stream)
+    q_p = _step_rows(fn, "q", q, torch.bfloat16, None, dev)
+    out_p = _step_rows(fn, "out", out, torch.float32, shape, dev)
+    k_p = v_p = None
+    if k_new is not None:
+        k_p = _step_rows(fn, "k_new", k_new, torch.bfloat16, rows, dev)
+    if v_new is not None:
+        v_p = _step_rows(fn, "v_new", v_new, torch.bfloat16, rows, dev)
     if D != cache.head_dim:
         raise ValueError("%s: q has head_dim %d, the cache %d" % (fn, D, cache.head_dim))
     ctx_p = _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
@@ -672,10 +670,9 @@ def kvq_decode_step_accum_int8kv(cache, k_new, v_new, q, block_table, ctx_lens, 
     workspace, wbytes = _ws(workspace, need, cache.k.device, stream)
     c = _cache_struct(fn, cache, dev)
     _check(fn, lib().kvq_decode_step_accum_int8kv(
-        ctypes.byref(c), _hp(k_new), _hp(v_new), _hp(q), B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx),
-        float(softmax_scale), _hp(out), acc_p, stride, slot_pos_p, pos_p, _p(workspace), wbytes, ctypes.byref(o),
-        _stream(stream)))
-    return ret
+        ctypes.byref(c), k_p, v_p, q_p, B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx), float(softmax_scale), out_p, acc_p,
+        stride, slot_pos_p, pos_p, _p(workspace), wbytes, ctypes.byref(o), _stream(stream)))
+    return out
 
 
 def kvq_step_window_workspace_bytes(batch, n_new, n_q_heads, n_kv_heads, max_ctx, window, n_sink, head_dim, split_rows=0,
@@ -692,24 +689,23 @@ def kvq_decode_step_window_int8kv(cache, k_new, v_new, q, block_table, ctx_lens,
     sees keys t <= p with t > p - window or t < n_sink.  Returns out fp32 shaped like q."""
     fn = "kvq_decode_step_window_int8kv"
     _fit(fn, max_ctx, window, n_sink)
-    squeeze = q.dim() == 3
-    if squeeze:
-        q = q[:, None]
-    B, nq, Hq, D = q.shape
-    if out is None:
-        out = _new_out((B, nq, Hq, D), q, stream)
-        ret = out[:, 0] if squeeze else out
+    shape, H, dev = q.shape, cache.n_kv_heads, _current_device()
+    if len(shape) == 3:  # one token
+        (B, Hq, D), nq = shape, 1
+        rows = B, H, D
     else:
-        ret = out
-    H, dev = cache.n_kv_heads, _current_device()
-    q_p = _step_rows(fn, "q", q, torch.bfloat16, B * nq * Hq * D, dev)
-    out_p = _step_rows(fn, "out", out, torch.float32, B * nq * Hq * D, dev)
+        B, nq, Hq, D = shape
+        rows = B, nq, H, D
+    if out is None:
+        out = _new_out(shape, q, stream)
+    q_p = _step_rows(fn, "q", q, torch.bfloat16, None, dev)
+    out_p = _step_rows(fn, "out", out, torch.float32, shape, dev)
     k_p = v_p = None
     if k_new is not None or v_new is not None:
         if k_new is None or v_new is None:
             raise ValueError("%s: k_new and v_new go together" % fn)
-        k_p = _step_rows(fn, "k_new", k_new, torch.bfloat16, B * nq * H * D, dev)
-        v_p = _step_rows(fn, "v_new", v_new, torch.bfloat16, B * nq * H * D, dev)
+        k_p = _step_rows(fn, "k_new", k_new, torch.bfloat16, rows, dev)
+        v_p = _step_rows(fn, "v_new", v_new, torch.bfloat16, rows, dev)
     if D != cache.head_dim:
         raise ValueError("%s: q has head_dim %d, the cache %d" % (fn, D, cache.head_dim))
     ctx_p = _need(fn, "ctx_lens", ctx_lens, torch.int32, (B,), dev)
@@ -730,13 +726,15 @@ def kvq_decode_step_window_int8kv(cache, k_new, v_new, q, block_table, ctx_lens,
     _check(fn, lib().kvq_decode_step_window_int8kv(
         ctypes.byref(c), k_p, v_p, q_p, B, nq, Hq, table_p, n_blocks, ctx_p, int(max_ctx), float(softmax_scale), int(window),
         int(n_sink), out_p, ws_p, wbytes, o, _stream(stream)))
-    return ret
+    return out
 
 
-def _step_rows(fn, name, t, dtype, n, dev):
-    """Pointer of n contiguous elements on the current device, or in mapped page-locked host memory (zero-copy)."""
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s: %s must be a contiguous %s tensor of %d elements" % (fn, name, dtype, n))
+def _step_rows(fn, name, t, dtype, shape, dev):
+    """Pointer of contiguous rows in the order of `shape` (its dims may be merged; None: any) on the current device, or in
+    mapped page-locked host memory (zero-copy)."""
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape and not _merged(t.shape, shape)):
+        raise ValueError("%s: %s must be a contiguous %s tensor of shape %s (got %s %s)" %
+                         (fn, name, dtype, list(shape or t.shape), t.dtype, list(t.shape)))
     if t.get_device() != dev:
         if t.is_cuda:
             _elsewhere(fn, name, t)
@@ -1004,6 +1002,20 @@ def kvq_rope_append_int8kv(cache, q, k_new, v_new, pos, plan, seq_idx, slot, blo
         n_axes, plan.phases.data_ptr(), plan.axis_of, plan.rotary_dim, int(rotary_offset), int(layout), plan.attn_factor,
         _stream(stream)))
     return q_out if q is not None else None
+
+
+def _merged(got, shape):
+    """Whether a shape is `shape` with neighbouring dims merged, or dims of 1 put in: the same elements in the same order."""
+    places, n = {1}, 1
+    for x in reversed(shape):
+        n *= x
+        places.add(n)
+    m = 1
+    for x in reversed(got):
+        m *= x
+        if m not in places:
+            return False
+    return m == n
 
 
 def _heads(fn, name, t, T, D, dev):
