@@ -91,7 +91,7 @@ struct WindowMap {
 __host__ __device__ inline WindowMap window_map(int ctx, int nq, int window, int n_sink) {
   WindowMap m;
   m.sink_pages = n_sink / KVQ_BLOCK_SIZE + (n_sink % KVQ_BLOCK_SIZE != 0);
-  const int low = ctx - nq - window + 1;  // the first key of the first row's window
+  const int low = (ctx >= nq ? ctx - nq + 1 : 0) - window;  // the first key of the first row's window (no row's: below 0)
   m.skipped = low > 0 && low / KVQ_BLOCK_SIZE > m.sink_pages ? low / KVQ_BLOCK_SIZE - m.sink_pages : 0;
   return m;
 }
