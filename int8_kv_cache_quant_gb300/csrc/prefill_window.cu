@@ -38,18 +38,21 @@
 // factors in every thread.  The scores stay in registers from the maximum to the weights; whether a row's maximum exceeds its
 // reference is one barrier of the row's four warps, and only then do they exchange maxima.
 //
-// What bounds it, and what it was measured at.  2048 queries behind 30720 keys, W = 4096, 24 / 4 heads of 256: 178 us (206 GFLOP:
-// 1.16 PFLOP/s), the tensor cores busy for 60 % of the attention's 161 us: a tile's P waits for its scores and these for
-// the values two tiles before, since O leaves tensor memory room for two score tiles.  2047 queries, W = 1024, 32 / 8 heads of 128:
-// 58.4 us (30 GFLOP), the softmax and each row tile's end: its last values, its output, the next queries (5000 of 30000
-// cycles).  33 queries, 24 / 4 heads of 256: 17.5 us, three launches of latencies.
+// What bounds it, and what it was measured at.  2048 queries behind 30720 keys, W = 4096, 24 / 4 heads of 256: 177 us (206 GFLOP:
+// 1.16 PFLOP/s), the tensor cores busy for 60 % of the attention's 161 us.  A tile has 2048 cycles of products and takes 3660
+// (86 tiles a CTA): its P waits for its scores and these for the values two tiles before, since O leaves tensor memory
+// room for two score tiles; and its operands are 128 KB, whose copies from L2 weigh as well (half of the bytes, the rest
+// zeros: 165 us against 179 in the same build).  2047 queries, W = 1024, 32 / 8 heads of 128: 58.1 us (30 GFLOP), 27.4
+// tiles and 3.4 row tiles' ends a CTA: the softmax and those ends, about 5000 cycles each for the last values, the output and the
+// next queries; half of the bytes is no faster there (60.9 against 58.9).  33 queries, 24 / 4 heads of 256: 17.5 us, three
+// launches of latencies.
 // Instruction fetch decides more than arithmetic here: 20 warps in six roles run from the same caches.  2047 queries, us:
 // with a softmax tile unrolled twice 71 against 63; product and copy code in one place each instead of three 59 against 63;
 // the queries' loop eight times unrolled 64, four times 62; the MMA warp's operands not provably uniform 69 against 63.
 // Other shapes that were built and were slower, us (2047 queries | 32K chunk): eight softmax warps and one score tile
 // 104 | 314; two groups of eight that take turns at the tiles 58.6 | 193; scores and values issued by two warps 81 | 238 against
 // 74 | 220; pairs of CTAs that share an MMA (cta_group::2, each half of a tile's K and V) 70 | 235 against 64 | 197; parts
-// joined by whoever writes the second 63 | 183 against 59 | 181; half of the bytes copied is no faster (L2 is not the limit).
+// joined by whoever writes the second 63 | 183 against 59 | 181.
 #include <algorithm>
 
 #include "kvq_dev.cuh"
@@ -236,6 +239,8 @@ __global__ void __launch_bounds__(256) window_tiles_kernel(const __grid_constant
   const int kvh = blockIdx.y, tid = threadIdx.x;
   const int st = blockIdx.x, tile = st < a.sink_tiles ? st : st - a.sink_tiles + a.first_tile;
   __shared__ int page_s[8];
+  // The wait stays ahead of the trigger: the attention kernel's query warps read q without a wait of their own, and what the
+  // stream did before this launch is there by then only because every block of it has waited.
   grid_dep_wait();
   grid_dep_trigger();
   if (tid < 8) {
@@ -676,7 +681,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       ++tile;
       window_step(a, w);
     };
-    // The scores run two tiles ahead of the values: beside tile f's weights, tile f + 1 is with the other group.
+    // The scores run ahead of the values, one tile with two score tiles and two with three (scores_next): while the softmax
+    // warps are at tile f, the scores of the next are made, and the values of the one before.
     for (int f = 0; ok && f < n_tiles;) {
       if (scores_next<D>(fs, f, n_tiles, ws.x)) scores();
       else values(f++);
@@ -749,7 +755,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
     int units = 0;
     for (int f = 0; f < n_tiles; ++units) {
       if (units > 0 && !__all_sync(0xffffffffu, wait_on(&bars[L::qFree], (units - 1) & 1, abort_flag, a.wait_budget))) break;
-      // every row's address for itself, eight at a time: one warp alone has nothing else to fill the latencies with
+      // every row's address for itself, four rows of a thread on their way: two warps alone have nothing else to fill the
+      // latencies with
       const int r0 = 128 * w.t, q0 = r0 / a.group, g0 = r0 - q0 * a.group, rows = min(a.n_rows - r0, 128);
       const uint16_t* src = static_cast<const uint16_t*>(a.q) +
                             (static_cast<long long>(q0) * a.n_q_heads + w.kvh * a.group) * D + 8 * ch;
@@ -764,8 +771,8 @@ __global__ void __launch_bounds__(kWThreads, 1) window_attention_kernel(const __
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[L::qFull]);
-      // The first queries come from before the kernel that makes the tiles, which had them before it let this one start;
-      // this grid's own wait is the other warps'.
+      // The first queries come from before the kernel that makes the tiles, which waits for them before it lets this one
+      // start (window_tiles_kernel); this grid's own wait is the other warps'.
       const int n_unit = min(w.keys.n - w.x, n_tiles - f);
       f += n_unit;
       w.x += n_unit - 1;

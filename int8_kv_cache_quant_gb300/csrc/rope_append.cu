@@ -17,7 +17,8 @@
 // the cos and sin once, into shared memory, its first query rows on their way meanwhile, and then a thread owns one column
 // of a token (8 pairs, two 16-byte words of a row) for all its heads.  With 8 pairs of cos and sin in each thread's own registers,
 // again for every two heads of a token, 2048 tokens of 24 + 4 + 4 heads of 256 took 18.0 us; so 13.8 us (63 MB: 4.6 TB/s), of
-// which 7 us are instructions to issue (7.7 M warp instructions; 11.5 M before).  One token: 4.3 us in a captured graph.
+// which 7 us are instructions to issue (7.7 M warp instructions; 11.5 M before).  Two blocks an SM leave a thread 64 registers, 36
+// bytes of which are spilled beside the three rows on their way.  One token: 4.3 us in a captured graph.
 // The 16 tokens are counted from a page boundary where the first token's slot says where one is, so that a chunk's V codes
 // leave a page at a time, 16 bytes a dimension.
 #include <algorithm>
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) rope_append_kernel(const __
   const int n_kv = kv0 < 0 ? 0 : min(a.n_kv_heads - kv0, a.kv_heads);  // (0 or less: none)
   grid_dep_wait();
   grid_dep_trigger();
-  // tokens from a page boundary on (one token more than a whole number of blocks is no reason to shift)
+  // more than one block: tokens from a page boundary on, as the first token's slot has it
   int shift = 0;
   if (a.n_tokens > kTokens) shift = a.slot[0] & (KVQ_BLOCK_SIZE - 1);
   const long long base = static_cast<long long>(blockIdx.x) * kTokens - shift;

@@ -1,5 +1,5 @@
 // tile_dev.cuh — device helpers shared by the kernels that stream operand tiles to the 5th-generation
-// tensor core (prefill.cu, chunk_weights.cu): packed fp32 pairs, widening of int8 codes, power-of-two
+// tensor core (prefill.cu, chunk_weights.cu, prefill_window.cu): packed fp32 pairs, widening of int8 codes, power-of-two
 // row scales, and bounded waits that give up together.
 #pragma once
 
