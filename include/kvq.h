@@ -691,7 +691,8 @@ size_t kvq_prefill_window_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, i
  *                    sees are not read
  *   softmax_scale  : finite and > 0
  *   window         : > 0;  n_sink : >= 0
- *   out            : device [n_tokens][n_q_heads][head_dim] of out_type, KVQ_OUT_BF16 or KVQ_OUT_FP32
+ *   out            : device [n_tokens][n_q_heads][head_dim] of out_type, KVQ_OUT_BF16 or KVQ_OUT_FP32; not over q, rows of
+ *                    which are read after others are written
  *   workspace      : device, >= kvq_prefill_window_workspace_bytes(...), 16-byte aligned; its contents on entry do not matter
  * A key on a page outside the pool is skipped (KVQ_DEV_BAD_BLOCK); a row that sees no key, or scores -infinity alone, gives
  * zeros.  If a bounded wait runs out (KVQ_DEV_TIMEOUT), the rows concerned are not written.

@@ -540,6 +540,9 @@ def kvq_attn_prefill_window_int8kv(cache, q, history_len, block_table_row, softm
     if out is None:
         out = _result((T, Hq, D), kind, q.device, stream)
     out_p = _need(fn, "out", out, kind, (T, Hq, D), dev)
+    n = T * Hq * D
+    if out_p < q_p + 2 * n and q_p < out_p + (4 if kind is torch.float32 else 2) * n:
+        raise ValueError("%s: out overlaps q" % fn)
     need = 0
     if workspace is None:
         need = kvq_prefill_window_workspace_bytes(T, Hq, cache.n_kv_heads, int(history_len), int(window), int(n_sink), D)
