@@ -893,7 +893,7 @@ class RopeAxes:
     __slots__ = ("phases", "axis_of", "attn_factor", "n_axes", "rotary_dim")
 
     def __init__(self, phases, axis_of, attn_factor=1.0):
-        self.phases, self.axis_of, self.attn_factor = phases, bytes(axis_of), float(attn_factor)
+        self.phases, self.axis_of, self.attn_factor = phases, bytes(list(axis_of)), float(attn_factor)
         self.n_axes, self.rotary_dim = max(self.axis_of, default=0) + 1, 2 * len(self.axis_of)
         if phases.dtype is not torch.int64 or tuple(phases.shape) != (len(self.axis_of),) or not phases.is_contiguous():
             raise ValueError("RopeAxes: phases must be a contiguous int64 tensor [%d]" % len(self.axis_of))
