@@ -7,8 +7,8 @@
 // The V scale goes into the exponent: z[t] = s[t] + log2 v_scale[t], w[t] = 2^(z[t] - r) with one reference r a row, so that
 //     out = sum_t w[t] v_code[t] / sum_t w[t] / v_scale[t],
 // one exponential a score, weights that fit fp16 whatever the V scales are, and no second maximum.  r is 7 less than the largest z
-// of the row's first tile and moves only when a tile's z is more than 15 above it, so that the accumulator is hardly ever scaled again:
-// weights are at most 2^15, the half of fp16's range that is left above its largest reference weight, 2^7.
+// of the row's first tile and moves only when a tile's z is more than 15 above it, so that the accumulator is hardly ever scaled
+// again: a row's largest weight is between 2^7 and 2^15, within fp16's 2^16 and far from where its numbers become subnormal.
 // The one statistic has a price.  Factors of two to the -126 and less are 0, in the sum too, where a weight stands for w / v_scale: a
 // key whose V scale is 2^-k of another's is lost from 126 - k octaves below that one's score on.  So V scales count as 2^-60
 // at least (rows of zeros have 0), and past 2^40 they are reported: between the two, a key that is lost has less than
